@@ -592,6 +592,212 @@ int kda_ckpt_flush(const kda_pool* pool, const kda_ckpt_plane* plane, const int3
 int kda_ckpt_load(const kda_pool* pool, const kda_ckpt_plane* plane, const int32_t* slots,
                   const int32_t* entries, int32_t n, int32_t* dev_status, uint32_t flags, void* stream);
 
+/*
+ * The paged key/value cache in 4-bit blocks: the cache of the full attention
+ * layers that stand between KDA layers.  A value is code * scale * k_scale
+ * (keys) or v_scale (values): codes are e2m1, one e4m3 scale serves 16
+ * neighbouring channels of a token's head (9/16 byte a value).  A page holds
+ * page_tokens tokens of every head:
+ *   page p, head h, 16 tokens from 16 b: base + p * page_stride +
+ *       (h * page_tokens / 16 + b) * 18 * dim bytes, 18 * dim bytes long:
+ *   [0, 8 dim)        key codes [token][dim / 2], two channels a byte, the even one in the low nibble
+ *   [8 dim, 16 dim)   value codes: byte j of the dim / 2 bytes of token w, with c = dim / 16, at
+ *                     (w / 8) 64 c + (j / c * 4 + w % 8 / 2) 2 c + (w % 2) c + j % c
+ *   [16 dim, 17 dim)  key scales [token][dim / 16]
+ *   [17 dim, 18 dim)  value scales: group i of token w at (i * 4 + w % 8 / 2) * 4 + w / 8 * 2 + w % 2
+ * (the order in which the attention kernel's tensor-core fragments take
+ * them).  Pages need no initial value: what was never appended is never read
+ * as a value.  (The pages of pull request 2945, Performance, count a key/value
+ * pool in blocks of 128 tokens; its format is this library's own.)
+ */
+typedef struct kda_kv4_cache {
+    void* base;           /* device, 16-byte aligned */
+    int32_t page_tokens;  /* 16 .. 65536, a multiple of 16 */
+    int32_t heads;        /* key/value heads */
+    int32_t dim;          /* channels of a head: 64 or 128 */
+    int32_t reserved;     /* 0 */
+    int64_t num_pages;
+    int64_t page_stride;  /* bytes, >= kda_kv4_page_bytes, a multiple of 16 */
+    float k_scale;        /* > 0; 1 unless keys or values leave the range of code * scale (2^-10 .. 2688) */
+    float v_scale;
+} kda_kv4_cache;
+
+/* Bytes of one page.  KDA_ERR_SHAPE for a shape that a cache cannot have. */
+int kda_kv4_page_bytes(int32_t page_tokens, int32_t heads, int32_t dim, int64_t* bytes);
+
+/*
+ * Arguments of kda_kv4_append (device pointers; optional ones may be NULL).
+ * Request r owns tokens cu_seqlens[r] .. cu_seqlens[r+1] - 1 of k and v (or
+ * r * max_t .. with cu_seqlens NULL); its token j goes to position
+ * ctx_len[r] + j: page page_table[r][position / page_tokens].  A negative
+ * position is padding: nothing is stored, its rows of k_out and v_out are
+ * zero (ctx_len[r] = -T_r pads a whole request).
+ * Keys are rotated on the way, channels below rot_dim, by the row of cos and
+ * sin at the token's position, in fp32:
+ *   interleaved 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1);
+ *   x_a <- x_a cos_i - x_b sin_i,  x_b <- x_b cos_i + x_a sin_i.
+ * A group of 16 values t (x / k_scale or x / v_scale) is rounded as
+ *   scale = e4m3(max |t| / 6), code = e2m1(t / scale), to nearest even, at
+ *   most 448 and 6; a group that holds a NaN or an infinity reads back as NaN.
+ * k_out and v_out receive the values that the cache then stands for, rounded
+ * to out_dtype: attention over a prompt's own tokens can run on the values
+ * that later steps will see.
+ */
+typedef struct kda_kv4_append_args {
+    int32_t n;                  /* requests */
+    int32_t total;              /* packed tokens: rows of k, v, k_out, v_out */
+    int32_t max_t;              /* most tokens of any request */
+    int32_t dtype;              /* of k and v: KDA_F32, KDA_F16 or KDA_BF16 */
+    int32_t table_cols;         /* columns of page_table */
+    int32_t rot_dim;            /* 0 .. dim, a multiple of 32 */
+    int32_t interleaved;        /* 0 or 1 */
+    int32_t rope_rows;          /* rows of cos and sin */
+    int32_t out_dtype;          /* of k_out and v_out */
+    int32_t reserved;           /* 0 */
+    int64_t k_stride;           /* elements from one token to the next, >= heads * dim, a multiple of 16 bytes */
+    int64_t v_stride;
+    const int32_t* cu_seqlens;  /* [n + 1] or NULL */
+    const int32_t* page_table;  /* [n][table_cols] */
+    const int32_t* ctx_len;     /* [n]: tokens in the cache before this call */
+    const void* k;              /* [total] rows of [heads][dim], 16-byte aligned */
+    const void* v;
+    const float* cos;           /* [rope_rows][rot_dim / 2], 16-byte aligned, or NULL with rot_dim 0 */
+    const float* sin;
+    void* k_out;                /* [total][heads][dim], 16-byte aligned, or NULL */
+    void* v_out;
+} kda_kv4_append_args;
+
+/*
+ * Appends a step's keys and values (see kda_kv4_append_args); cache and args
+ * are host pointers.  Host checks: KDA_ERR_NULL, _DTYPE_UNSUPPORTED, _SHAPE
+ * (the cache, strides, rot_dim, total inconsistent with n and max_t, a table
+ * of 2^31 tokens or more), _ALIGN, _ARG (negative counts, reserved fields,
+ * scales that are not positive numbers, flags other than KDA_LAUNCH_PDL).
+ * Device checks (in *dev_status, that token skipped): KDA_ERR_ARG for token
+ * offsets outside 0 .. max_t and for a position past the page table or the
+ * rotation rows, KDA_ERR_SLOT_RANGE for a page id outside [0, num_pages).
+ * Two tokens of one call must not share a position of a page.
+ */
+int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, int32_t* dev_status,
+                   uint32_t flags, void* stream);
+
+/*
+ * Arguments of kda_kv4_attend: the attention of a decode or speculative step
+ * over the cache, after the step's own keys and values were appended.  Token j
+ * of request r (packed as for kda_kv4_append, at most KDA_KV4_MAX_TOKENS a
+ * request) stands at position ctx_len[r] + j and sees the keys at positions
+ * up to its own, with window > 0 the last `window` of them:
+ *   o = sum_p softmax_p(scale * rot(q) . K_p) V_p;
+ * query head h reads key/value head h / (h_q / heads).  Queries are rotated
+ * like the keys (rot_dim 0: not at all).  A row that sees no key (a negative
+ * position) is zero.  o has q's dtype.
+ */
+#define KDA_KV4_MAX_TOKENS 16
+#define KDA_KV4_WORKSPACE_BYTES (20 << 20)
+typedef struct kda_kv4_attend_args {
+    int32_t n;                  /* requests */
+    int32_t total;              /* packed tokens: rows of q and o */
+    int32_t max_t;              /* most tokens of any request, <= KDA_KV4_MAX_TOKENS */
+    int32_t dtype;              /* of q and o: KDA_F32, KDA_F16 or KDA_BF16 */
+    int32_t table_cols;         /* columns of page_table */
+    int32_t rot_dim;            /* 0 .. dim, a multiple of 32 */
+    int32_t interleaved;        /* 0 or 1 */
+    int32_t rope_rows;          /* rows of cos and sin */
+    int32_t h_q;                /* query heads, a multiple of the cache's heads */
+    int32_t window;             /* 0: every earlier key */
+    float scale;                /* 0: 1 / sqrt(dim) */
+    int32_t reserved;           /* 0 */
+    int64_t q_stride;           /* elements from one token to the next, >= h_q * dim */
+    const int32_t* cu_seqlens;  /* [n + 1] or NULL */
+    const int32_t* page_table;  /* [n][table_cols] */
+    const int32_t* ctx_len;     /* [n]: tokens in the cache before this step's */
+    const void* q;              /* [total] rows of [h_q][dim] */
+    const float* cos;           /* [rope_rows][rot_dim / 2] or NULL with rot_dim 0 */
+    const float* sin;
+    void* o;                    /* [total][h_q][dim], 16-byte aligned (output) */
+    void* workspace;            /* device, 16-byte aligned, zeroed once before its first call; one call at a time */
+    int64_t workspace_bytes;    /* >= KDA_KV4_WORKSPACE_BYTES, whatever the sizes */
+} kda_kv4_attend_args;
+
+/*
+ * Attention over the cache (see kda_kv4_attend_args); cache and args are host
+ * pointers.  The call leaves the workspace ready for the next one (in any
+ * stream order); calls that may run at the same time need one each.  Results
+ * do not depend on the order in which the GPU runs its parts.  Host checks as
+ * for kda_kv4_append, and KDA_ERR_SHAPE for h_q, max_t and a small workspace,
+ * KDA_ERR_ARG for a negative window or a scale that is not finite.  Device
+ * checks (in *dev_status): KDA_ERR_ARG for token offsets outside 0 .. max_t
+ * (that request is skipped) and for positions past the page table or the
+ * rotation rows (its rows are zero); KDA_ERR_SLOT_RANGE for a page id outside
+ * [0, num_pages) (its tokens are not seen); KDA_ERR_TIMEOUT.
+ */
+int kda_kv4_attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, int32_t* dev_status,
+                   uint32_t flags, void* stream);
+
+/*
+ * The norm and output gate behind the recurrence, per head:
+ *   y = weight * o / sqrt(mean(o^2) + eps) * act(gate)
+ * (activation 0: the gate itself, 1: sigmoid, 2: SiLU; gate NULL: no factor).
+ * dim is the head's V; fp32 arithmetic, y rounded to nearest even.
+ */
+typedef struct kda_head_norm_args {
+    int32_t total;        /* tokens */
+    int32_t heads;
+    int32_t dim;          /* 8 .. 256, a multiple of 8 */
+    int32_t o_dtype;      /* KDA_F32, KDA_F16 or KDA_BF16 */
+    int32_t dtype;        /* of gate and y */
+    int32_t activation;
+    float eps;            /* >= 0 */
+    int32_t reserved;     /* 0 */
+    int64_t gate_stride;  /* elements from one token's gate to the next, >= heads * dim, a multiple of 16 bytes */
+    const void* o;        /* [total][heads][dim]; every buffer 16-byte aligned */
+    const void* gate;     /* [total] rows of [heads][dim], or NULL */
+    const float* weight;  /* [dim] */
+    void* y;              /* [total][heads][dim] (output; may be o when the dtypes agree) */
+} kda_head_norm_args;
+int kda_head_norm(const kda_head_norm_args* args, uint32_t flags, void* stream);
+
+/*
+ * The norms before and after a block with its gate and residual scale, in one
+ * pass over the token's row: the block's output y becomes the new residual,
+ * and that the next block's input,
+ *   z = w_post * y / sqrt(mean(y^2) + eps)       (w_post NULL: z = y)
+ *   h = residual_scale * residual + branch_scale * scale * act(gate) * z
+ *   x = w_pre * h / sqrt(mean(h^2) + eps)        (w_pre NULL: no weight)
+ * residual_out = h (may be residual itself), rounded; x is computed from the
+ * unrounded h.  scale [hidden] and gate may be NULL (1); x NULL: only h.
+ * y NULL: only x = norm of the residual (before the first block).  Any
+ * addresses of whole elements; 16-byte aligned rows run faster.
+ */
+#define KDA_BLOCK_NORM_MAX 16384
+typedef struct kda_block_norm_args {
+    int32_t total;            /* tokens */
+    int32_t hidden;           /* 1 .. KDA_BLOCK_NORM_MAX */
+    int32_t dtype;            /* of y, gate and x: KDA_F32, KDA_F16 or KDA_BF16 */
+    int32_t residual_dtype;   /* KDA_F32 or dtype */
+    int32_t activation;       /* of the gate, as for kda_head_norm */
+    float eps;                /* >= 0 */
+    float residual_scale;
+    float branch_scale;
+    int64_t y_stride;         /* elements from one token to the next, >= hidden */
+    int64_t gate_stride;
+    const void* residual;     /* [total][hidden] */
+    const void* y;            /* [total] rows of [hidden], or NULL */
+    const void* gate;         /* [total] rows of [hidden], or NULL */
+    const float* w_post;      /* [hidden] or NULL */
+    const float* scale;       /* [hidden] or NULL */
+    const float* w_pre;       /* [hidden] or NULL */
+    void* residual_out;       /* [total][hidden] (output) */
+    void* x;                  /* [total][hidden] (output) or NULL */
+} kda_block_norm_args;
+
+/*
+ * Both norms' host checks: KDA_ERR_NULL, _DTYPE_UNSUPPORTED, _SHAPE (heads,
+ * dim, hidden, strides), _ALIGN, _ARG (negative total, activation, eps,
+ * reserved, flags other than KDA_LAUNCH_PDL).  total == 0 is a no-op.
+ */
+int kda_block_norm(const kda_block_norm_args* args, uint32_t flags, void* stream);
+
 /* A static, human-readable string for a kda_status code. */
 const char* kda_strerror(int32_t code);
 

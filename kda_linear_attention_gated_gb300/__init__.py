@@ -26,11 +26,13 @@ __all__ = ["KdaError", "KdaLibrary", "PoolDesc", "build", "lib_path",
            "KDA_ERR_DTYPE_MISMATCH", "KDA_ERR_DTYPE_UNSUPPORTED", "KDA_ERR_LAYERS_DISAGREE",
            "KDA_ERR_SHAPE", "KDA_ERR_ALIGN", "KDA_ERR_LAUNCH", "KDA_ERR_SLOT_RANGE",
            "KDA_ERR_ARG", "KDA_ERR_TIMEOUT", "KDA_ERR_LAYOUT", "KDA_LAUNCH_PDL", "KDA_LAUNCH_PDL_EARLY_STATE",
-           "KDA_LAUNCH_TEST_WITHHOLD_STATE", "EXPORTED_SYMBOLS"]
+           "KDA_LAUNCH_TEST_WITHHOLD_STATE", "KDA_KV4_WORKSPACE_BYTES", "KDA_KV4_MAX_TOKENS", "KDA_BLOCK_NORM_MAX",
+           "EXPORTED_SYMBOLS"]
 
 KDA_F32, KDA_F16, KDA_BF16 = 0, 1, 2
 KDA_LAUNCH_PDL, KDA_LAUNCH_PDL_EARLY_STATE = 1, 2
 KDA_LAUNCH_TEST_WITHHOLD_STATE = 1 << 30  # test hook of the timeout path (include/kda.h)
+KDA_KV4_WORKSPACE_BYTES, KDA_KV4_MAX_TOKENS, KDA_BLOCK_NORM_MAX = 20 << 20, 16, 16384
 (KDA_OK, KDA_ERR_NULL, KDA_ERR_DTYPE_MISMATCH, KDA_ERR_DTYPE_UNSUPPORTED,
  KDA_ERR_LAYERS_DISAGREE, KDA_ERR_SHAPE, KDA_ERR_ALIGN, KDA_ERR_LAUNCH,
  KDA_ERR_SLOT_RANGE, KDA_ERR_ARG, KDA_ERR_TIMEOUT, KDA_ERR_LAYOUT) = range(12)
@@ -39,7 +41,9 @@ EXPORTED_SYMBOLS = ("kda_build_state_dtype", "kda_pool_check", "kda_state_bytes"
                     "kda_decode_step", "kda_spec_verify", "kda_step", "kda_prefill", "kda_prefill_workspace_bytes",
                     "kda_prefill_chunked", "kda_prefill_chunked_noalloc", "kda_conv_step", "kda_decode_conv_step",
                     "kda_step_conv",
-                    "kda_layout_id", "kda_ckpt_flush", "kda_ckpt_load", "kda_stage_host", "kda_strerror")
+                    "kda_layout_id", "kda_ckpt_flush", "kda_ckpt_load", "kda_stage_host",
+                    "kda_kv4_page_bytes", "kda_kv4_append", "kda_kv4_attend", "kda_head_norm", "kda_block_norm",
+                    "kda_strerror")
 
 
 class KdaError(RuntimeError):
@@ -115,6 +119,46 @@ class HostCopy(ctypes.Structure):
     _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("bytes", ctypes.c_int64)]
 
 
+class Kv4CacheDesc(ctypes.Structure):
+    """Mirror of ``struct kda_kv4_cache`` (include/kda.h)."""
+    _fields_ = [("base", ctypes.c_void_p), ("page_tokens", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("reserved", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Kv4AppendArgs(ctypes.Structure):
+    """Mirror of ``struct kda_kv4_append_args`` (include/kda.h)."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("n", "total", "max_t", "dtype", "table_cols", "rot_dim", "interleaved",
+                                              "rope_rows", "out_dtype", "reserved")] + \
+               [("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)] + \
+               [(f, ctypes.c_void_p) for f in ("cu_seqlens", "page_table", "ctx_len", "k", "v", "cos", "sin", "k_out",
+                                               "v_out")]
+
+
+class Kv4AttendArgs(ctypes.Structure):
+    """Mirror of ``struct kda_kv4_attend_args`` (include/kda.h)."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("n", "total", "max_t", "dtype", "table_cols", "rot_dim", "interleaved",
+                                              "rope_rows", "h_q", "window")] + \
+               [("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("q_stride", ctypes.c_int64)] + \
+               [(f, ctypes.c_void_p) for f in ("cu_seqlens", "page_table", "ctx_len", "q", "cos", "sin", "o",
+                                               "workspace")] + [("workspace_bytes", ctypes.c_int64)]
+
+
+class HeadNormArgs(ctypes.Structure):
+    """Mirror of ``struct kda_head_norm_args`` (include/kda.h)."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("total", "heads", "dim", "o_dtype", "dtype", "activation")] + \
+               [("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("gate_stride", ctypes.c_int64)] + \
+               [(f, ctypes.c_void_p) for f in ("o", "gate", "weight", "y")]
+
+
+class BlockNormArgs(ctypes.Structure):
+    """Mirror of ``struct kda_block_norm_args`` (include/kda.h)."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("total", "hidden", "dtype", "residual_dtype", "activation")] + \
+               [(f, ctypes.c_float) for f in ("eps", "residual_scale", "branch_scale")] + \
+               [("y_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64)] + \
+               [(f, ctypes.c_void_p) for f in ("residual", "y", "gate", "w_post", "scale", "w_pre", "residual_out", "x")]
+
+
 class CkptPlaneDesc(ctypes.Structure):
     """Mirror of ``struct kda_ckpt_plane`` (include/kda.h)."""
     _fields_ = [("base", ctypes.c_void_p), ("layout_id", ctypes.c_uint32), ("reserved", ctypes.c_int32),
@@ -139,6 +183,19 @@ def pool_desc(pool) -> PoolDesc:
     return PoolDesc(pool.data_ptr(), _dtype_code(pool.dtype), hv, k, v, ns, pool.stride(0))
 
 
+def kv4_cache_desc(pages, k_scale=1.0, v_scale=1.0) -> Kv4CacheDesc:
+    """Descriptor of a uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor whose pages are dense."""
+    if pages.dim() != 4 or pages.element_size() != 1 or pages.is_floating_point() or not pages.is_cuda:
+        raise ValueError("a 4-bit cache is a CUDA uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor")
+    num, heads, blocks, size = pages.shape
+    if pages.stride(3) != 1 or pages.stride(2) != size or pages.stride(1) != blocks * size:
+        raise ValueError("the [heads, page_tokens / 16, 18 * dim] part of a 4-bit cache must be dense")
+    dim, rest = divmod(size, 18)
+    if rest:
+        raise ValueError(f"the last dimension of a 4-bit cache is 18 * dim bytes, not {size}")
+    return Kv4CacheDesc(pages.data_ptr(), 16 * blocks, heads, dim, 0, num, pages.stride(0), k_scale, v_scale)
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -155,6 +212,52 @@ def _expect(name, t, shape, dtypes) -> None:
         raise ValueError(f"{name} must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _expect_rows(name, t, shape, dtype) -> int:
+    """As _expect for a tensor whose rows (its inner dimensions) are dense but may lie apart: the stride between them."""
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {tuple(shape)} {dtype} on CUDA")
+    if t.is_contiguous():
+        width = 1
+        for d in shape[1:]:
+            width *= d
+        return width
+    inner = 1
+    for d in range(len(shape) - 1, 0, -1):
+        if t.stride(d) != inner:
+            raise ValueError(f"{name}: the dimensions behind the first must be dense")
+        inner *= shape[d]
+    return t.stride(0)
+
+
+def _tokens(cu_seqlens, max_t, n, total) -> int:
+    """The most tokens of a request of a packed batch (see kda_step)."""
+    if cu_seqlens is None:
+        return (total // n if n else 0) if max_t is None else int(max_t)
+    _expect("cu_seqlens", cu_seqlens, (n + 1,), (_torch().int32,))
+    if max_t is None:
+        raise ValueError("max_t is required with cu_seqlens")
+    return int(max_t)
+
+
+def _rotation(cos, sin) -> tuple[int, int]:
+    """(rot_dim, rows) of a pair of fp32 [rows, rot_dim / 2] tables."""
+    if cos is None and sin is None:
+        return 0, 0
+    if cos is None or sin is None:
+        raise ValueError("cos and sin are given together")
+    if cos.dim() != 2:
+        raise ValueError("cos and sin are [rows, rot_dim / 2] tensors")
+    f32 = (_torch().float32,)
+    _expect("cos", cos, cos.shape, f32)
+    _expect("sin", sin, cos.shape, f32)
+    return 2 * cos.shape[1], cos.shape[0]
+
+
+def _torch():
+    import torch
+    return torch
 
 
 _libs: dict[bool, ctypes.CDLL] = {}
@@ -210,6 +313,15 @@ def _load(state16: bool) -> ctypes.CDLL:
             fn.argtypes = [P, ctypes.POINTER(CkptPlaneDesc), vp, vp, i32, vp, u32, vp]
         lib.kda_stage_host.restype = ctypes.c_int
         lib.kda_stage_host.argtypes = [ctypes.POINTER(HostCopy), i32, u32, vp]
+        lib.kda_kv4_page_bytes.restype = ctypes.c_int
+        lib.kda_kv4_page_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(ctypes.c_int64)]
+        C = ctypes.POINTER(Kv4CacheDesc)
+        for fn, args in ((lib.kda_kv4_append, Kv4AppendArgs), (lib.kda_kv4_attend, Kv4AttendArgs)):
+            fn.restype = ctypes.c_int
+            fn.argtypes = [C, ctypes.POINTER(args), vp, u32, vp]
+        for fn, args in ((lib.kda_head_norm, HeadNormArgs), (lib.kda_block_norm, BlockNormArgs)):
+            fn.restype = ctypes.c_int
+            fn.argtypes = [ctypes.POINTER(args), u32, vp]
         lib.kda_strerror.restype = ctypes.c_char_p
         lib.kda_strerror.argtypes = [i32]
         _libs[state16] = lib
@@ -618,3 +730,117 @@ class KdaLibrary:
                                                      _workspace[1], _ptr(status), flags, self._stream(stream)),
                         "kda_prefill_chunked")
 
+    # -- the operators around the recurrence ---------------------------------
+    def kda_kv4_page_bytes(self, page_tokens, heads, dim) -> int:
+        """Bytes of a page of the 4-bit cache: heads * page_tokens / 16 * 18 * dim."""
+        out = ctypes.c_int64(0)
+        self._check(self.lib.kda_kv4_page_bytes(page_tokens, heads, dim, ctypes.byref(out)), "kda_kv4_page_bytes")
+        return out.value
+
+    def kda_kv4_append_raw(self, cache: Kv4CacheDesc, args: Kv4AppendArgs, status, stream, flags=0) -> int:
+        return self.lib.kda_kv4_append(ctypes.byref(cache), ctypes.byref(args), status, flags, stream)
+
+    def kda_kv4_append(self, pages, page_table, ctx_len, k, v, status, cu_seqlens=None, max_t=None, cos=None, sin=None,
+                       interleaved=False, k_scale=1.0, v_scale=1.0, k_out=None, v_out=None, stream=None, flags=0) -> None:
+        """Appends k, v [total, heads, dim] (rows may lie apart) to the 4-bit
+        cache pages [num_pages, heads, page_tokens / 16, 18 * dim], keys
+        rotated by cos, sin [rows, rot_dim / 2] (see kda_kv4_append_args in
+        include/kda.h): page_table [N, cols], ctx_len [N] the tokens in the
+        cache before the call; k_out, v_out receive the values as stored."""
+        torch = _torch()
+        cache = kv4_cache_desc(pages, k_scale, v_scale)
+        n, total = int(page_table.shape[0]), int(k.shape[0])
+        shape = (total, cache.heads, cache.dim)
+        max_t = _tokens(cu_seqlens, max_t, n, total)
+        rot, rows = _rotation(cos, sin)
+        i32 = (torch.int32,)
+        _expect("page_table", page_table, (n, page_table.shape[-1]), i32)
+        _expect("ctx_len", ctx_len, (n,), i32)
+        _expect("status", status, (1,), i32)
+        ks, vs = _expect_rows("k", k, shape, k.dtype), _expect_rows("v", v, shape, k.dtype)
+        out = None
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
+                _expect(name, t, shape, (out or t.dtype,))
+                out = t.dtype
+        args = Kv4AppendArgs(n, total, max_t, _dtype_code(k.dtype), page_table.shape[1], rot, int(bool(interleaved)), rows,
+                             0 if out is None else _dtype_code(out), 0, ks, vs, _ptr(cu_seqlens), page_table.data_ptr(),
+                             ctx_len.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(cos), _ptr(sin), _ptr(k_out), _ptr(v_out))
+        self._check(self.kda_kv4_append_raw(cache, args, status.data_ptr(), self._stream(stream), flags), "kda_kv4_append")
+
+    def kda_kv4_attend_raw(self, cache: Kv4CacheDesc, args: Kv4AttendArgs, status, stream, flags=0) -> int:
+        return self.lib.kda_kv4_attend(ctypes.byref(cache), ctypes.byref(args), status, flags, stream)
+
+    def kda_kv4_attend(self, pages, page_table, ctx_len, q, o, workspace, status, cu_seqlens=None, max_t=None, cos=None,
+                       sin=None, interleaved=False, window=0, scale=None, k_scale=1.0, v_scale=1.0, stream=None,
+                       flags=0) -> None:
+        """Attention of a decode or speculative step over the 4-bit cache (see
+        kda_kv4_attend_args in include/kda.h): q [total, h_q, dim] (rows may
+        lie apart), o alike and dense, ctx_len [N] the tokens in the cache
+        before the step's own; workspace: KDA_KV4_WORKSPACE_BYTES bytes,
+        zeroed once."""
+        torch = _torch()
+        cache = kv4_cache_desc(pages, k_scale, v_scale)
+        n, total, h_q = int(page_table.shape[0]), int(q.shape[0]), int(q.shape[1])
+        shape = (total, h_q, cache.dim)
+        max_t = _tokens(cu_seqlens, max_t, n, total)
+        rot, rows = _rotation(cos, sin)
+        i32 = (torch.int32,)
+        _expect("page_table", page_table, (n, page_table.shape[-1]), i32)
+        _expect("ctx_len", ctx_len, (n,), i32)
+        _expect("status", status, (1,), i32)
+        qs = _expect_rows("q", q, shape, q.dtype)
+        _expect("o", o, shape, (q.dtype,))
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if scale is not None and scale == 0:
+            raise ValueError("scale must not be zero")
+        args = Kv4AttendArgs(n, total, max_t, _dtype_code(q.dtype), page_table.shape[1], rot, int(bool(interleaved)), rows, h_q,
+                             int(window), 0.0 if scale is None else float(scale), 0, qs, _ptr(cu_seqlens),
+                             page_table.data_ptr(), ctx_len.data_ptr(), q.data_ptr(), _ptr(cos), _ptr(sin), o.data_ptr(),
+                             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        self._check(self.kda_kv4_attend_raw(cache, args, status.data_ptr(), self._stream(stream), flags), "kda_kv4_attend")
+
+    def kda_head_norm(self, o, weight, y, gate=None, activation=1, eps=1e-6, stream=None, flags=0) -> None:
+        """y = weight * o / rms(o) * act(gate) over the heads of o [total,
+        heads, dim] (see kda_head_norm_args in include/kda.h): gate
+        [total, heads, dim] of y's dtype (rows may lie apart), weight fp32
+        [dim]; activation 0 none, 1 sigmoid, 2 SiLU."""
+        torch = _torch()
+        total, heads, dim = o.shape
+        _expect("o", o, (total, heads, dim), (o.dtype,))
+        _expect("y", y, (total, heads, dim), (y.dtype,))
+        _expect("weight", weight, (dim,), (torch.float32,))
+        gs = heads * dim if gate is None else _expect_rows("gate", gate, (total, heads, dim), y.dtype)
+        args = HeadNormArgs(total, heads, dim, _dtype_code(o.dtype), _dtype_code(y.dtype), int(activation), eps, 0, gs,
+                            o.data_ptr(), _ptr(gate), weight.data_ptr(), y.data_ptr())
+        self._check(self.lib.kda_head_norm(ctypes.byref(args), flags, self._stream(stream)), "kda_head_norm")
+
+    def kda_block_norm(self, residual, y, residual_out, w_post=None, gate=None, activation=1, scale=None, w_pre=None, x=None,
+                       residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None, flags=0) -> None:
+        """The norms around a block with its gate and residual scale (see
+        kda_block_norm_args in include/kda.h): residual, residual_out
+        [total, hidden] (fp32 or y's dtype; may be one tensor), y, gate
+        [total, hidden] (rows may lie apart), x [total, hidden]; w_post,
+        scale, w_pre fp32 [hidden].  y None: x is the norm of the residual."""
+        torch = _torch()
+        total, hidden = residual.shape
+        typed = x if y is None else y
+        if typed is None:
+            raise ValueError("y or x is required")
+        _expect("residual", residual, (total, hidden), (residual.dtype,))
+        ys = gs = hidden
+        if y is not None:
+            ys = _expect_rows("y", y, (total, hidden), y.dtype)
+            _expect("residual_out", residual_out, (total, hidden), (residual.dtype,))
+        if gate is not None:
+            gs = _expect_rows("gate", gate, (total, hidden), typed.dtype)
+        if x is not None:
+            _expect("x", x, (total, hidden), (typed.dtype,))
+        for name, w in (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)):
+            if w is not None:
+                _expect(name, w, (hidden,), (torch.float32,))
+        args = BlockNormArgs(total, hidden, _dtype_code(typed.dtype), _dtype_code(residual.dtype), int(activation), eps,
+                             residual_scale, branch_scale, ys, gs, residual.data_ptr(), _ptr(y), _ptr(gate), _ptr(w_post),
+                             _ptr(scale), _ptr(w_pre), _ptr(residual_out), _ptr(x))
+        self._check(self.lib.kda_block_norm(ctypes.byref(args), flags, self._stream(stream)), "kda_block_norm")

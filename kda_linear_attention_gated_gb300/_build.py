@@ -22,7 +22,8 @@ INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_DIR = os.path.join(PKG_DIR, "lib")
 SOURCES = [os.path.join(CSRC, f) for f in ("kda_api.cu", "kda_common.cuh", "kda_decode_tma.cuh",
                                           "kda_verify_tma.cuh", "kda_conv.cuh", "kda_ckpt.cuh",
-                                          "kda_prefill_chunk.cuh", "kda_stage.cuh")] + [os.path.join(INCLUDE, "kda.h")]
+                                          "kda_prefill_chunk.cuh", "kda_stage.cuh", "kda_host.cuh",
+                                          "kda_layer_api.cu", "kda_kv4.cuh", "kda_norm.cuh")] + [os.path.join(INCLUDE, "kda.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -49,7 +50,8 @@ def nvcc_command(state16: bool, out: str, extra: list[str] | None = None) -> lis
     return [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17",
             "-Xcompiler", "-fPIC", "-shared", "-cudart", "shared",
             f"-I{INCLUDE}", f"-DKDA_STATE16={int(bool(state16))}",
-            *(extra or []), os.path.join(CSRC, "kda_api.cu"), "-o", out]
+            *(extra or []), os.path.join(CSRC, "kda_api.cu"),
+            os.path.join(CSRC, "kda_layer_api.cu"), "-o", out]
 
 
 def _build_one(state16: bool, force: bool) -> str:

@@ -19,6 +19,7 @@
 #include <utility>
 
 #include "kda.h"
+#include "kda_host.cuh"
 #include "kda_decode_tma.cuh"
 #include "kda_verify_tma.cuh"
 #include "kda_conv.cuh"
@@ -106,17 +107,6 @@ static constexpr int kBuildDtype = KDA_F32;
 
 namespace {
 
-int elem_size(int32_t dtype) {
-    switch (dtype) {
-        case KDA_F32: return 4;
-        case KDA_F16: return 2;
-        case KDA_BF16: return 2;
-        default: return 0;
-    }
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // Shape, alignment and dtype of one pool, without the build-dtype rule.
 int check_pool_self(const kda_pool* p) {
     if (p == nullptr) return KDA_ERR_NULL;
@@ -177,30 +167,6 @@ int make_pool_map(const kda_pool* pool, int bv, CUtensorMap* map) {
     return r == CUDA_SUCCESS ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
-// Resident CTAs per SM of `kernel` with `smem` dynamic bytes (also raises the
-// kernel's dynamic shared-memory limit); cached per (kernel, device).
-int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, int* sms) {
-    static std::mutex mu;
-    static std::map<std::pair<const void*, int>, std::pair<int, int>> cache;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_LAUNCH;
-    std::lock_guard<std::mutex> lock(mu);
-    auto it = cache.find({kernel, dev});
-    if (it == cache.end()) {
-        int occ = 0, count = 0;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-                cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) != cudaSuccess ||
-            cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            occ < 1)
-            return KDA_ERR_LAUNCH;
-        it = cache.emplace(std::make_pair(kernel, dev), std::make_pair(occ, count)).first;
-    }
-    *blocks_per_sm = it->second.first;
-    *sms = it->second.second;
-    return KDA_OK;
-}
-
 // The scratch of kda_prefill_chunked_noalloc: a file-scope device array, so
 // that the call allocates nothing.  Its address is looked up once per device.
 static __device__ __align__(256) float g_prefill_scratch[KDA_PREFILL_SCRATCH_BYTES / 4];
@@ -218,16 +184,6 @@ void* prefill_scratch() {
         it = addr.emplace(dev, p).first;
     }
     return it->second;
-}
-
-// Programmatic dependent launch attribute when the caller asked for it.
-void set_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, uint32_t flags) {
-    if (flags & KDA_LAUNCH_PDL) {
-        attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr->val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
 }
 
 // The prefill scan pass with WPC column blocks of 16 value columns per CTA,

@@ -1,0 +1,978 @@
+// The paged key/value cache in 4-bit blocks of the attention layers that stand
+// between KDA layers: appending (rotation and rounding on the way) and the
+// attention of a decode or speculative step over it.
+//
+// Format.  A value is code * scale * (the cache's k_scale or v_scale): codes
+// are e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 with a sign), one e4m3 scale serves 16
+// neighbouring channels of a token's head.  Sixteen tokens of one head make a
+// block of 18 D bytes, contiguous, which one bulk copy moves:
+//   [0, 8 D)       key codes, [token][D / 2], two channels a byte (low nibble first)
+//   [8 D, 16 D)    value codes in the order a warp's mma fragments take them
+//   [16 D, 17 D)   key scales, [token][D / 16]
+//   [17 D, 18 D)   value scales, fragment order
+// Value order: lane (g, t) of a warp (g = lane / 4, t = lane % 4) multiplies
+// tokens 2t, 2t + 1, 2t + 8, 2t + 9 by channels g D / 8 .. (g + 1) D / 8 - 1,
+// so its D / 16 code bytes of token 2t and of token 2t + 1 are neighbours, and
+// the four lanes of a g follow each other: every read is one 16-byte (D = 128)
+// word a lane, in lane order.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+template <int D> struct Kv4 {
+    static constexpr int CB = D / 16;        // code bytes of a token in one lane's channels; also scale groups
+    static constexpr int NG = D / 16;        // 16-channel groups
+    static constexpr int KC = 0, VC = 8 * D, KS = 16 * D, VS = 17 * D;
+    static constexpr int BLOCK = 18 * D;     // bytes of a block
+};
+
+// Places inside a block of token `w` (0..15).
+template <int D> __device__ __forceinline__ int kv4_v_code(int w, int g) {
+    return Kv4<D>::VC + (w >> 3) * (64 * Kv4<D>::CB) + (g * 4 + ((w & 7) >> 1)) * (2 * Kv4<D>::CB) + (w & 1) * Kv4<D>::CB;
+}
+template <int D> __device__ __forceinline__ int kv4_v_scale(int w, int grp) {
+    return Kv4<D>::VS + (grp * 4 + ((w & 7) >> 1)) * 4 + (w >> 3) * 2 + (w & 1);
+}
+
+// Element loads from a typed buffer (kda_dtype codes 0 fp32, 1 fp16, 2 bf16).
+__device__ __forceinline__ float ld_elem(const void* p, int64_t i, int dtype) {
+    if (dtype == 0) return static_cast<const float*>(p)[i];
+    if (dtype == 1) return __half2float(static_cast<const __half*>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// Four elements to a typed buffer, rounded to nearest even; i a multiple of 4
+// of a 16-byte aligned buffer.
+__device__ __forceinline__ void st_elem4(void* p, int64_t i, int dtype, float a, float b, float c, float d) {
+    if (dtype == 0) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
+    } else if (dtype == 1) {
+        const __half2 x = __floats2half2_rn(a, b), y = __floats2half2_rn(c, d);
+        *reinterpret_cast<uint2*>(static_cast<__half*>(p) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+}
+
+// PTX conversions of the 4- and 8-bit types (two values an instruction).
+__device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ uint32_t cvt_f32_e4m3(float x) {  // to nearest even, at most 448
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n\tcvt.u32.u16 %0, h;\n\t}"
+        : "=r"(r) : "f"(x), "f"(0.f));
+    return r & 0xffu;
+}
+// Eight e2m1 codes from eight floats, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t cvt_f32x8_e2m1(const float* y) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r) : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return r;
+}
+// The four bytes of a word, two codes each, as f16 pairs.
+__device__ __forceinline__ void cvt_e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// threadIdx.x read again, where a value kept across the main loop would cost a register.
+__device__ __forceinline__ int tid_again() {
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    return t;
+}
+// As mma_16816_f16, free to be scheduled among its neighbours.
+__device__ __forceinline__ void kv4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2f(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// Append
+// ---------------------------------------------------------------------------
+struct Kv4AppendParams {
+    uint8_t* pages;
+    int64_t num_pages, page_stride;      // bytes
+    int page_tokens, heads;
+    int n, total, max_t, dtype, cols, rot, inter, rope_rows;
+    int64_t k_stride, v_stride;          // elements between tokens
+    const int32_t *cu, *table, *ctx;
+    const void *k, *v;
+    const float *cos, *sin;
+    void *k_out, *v_out;
+    int out_dtype;
+    float inv_k, inv_v, k_scale, v_scale;
+    int32_t* status;
+};
+
+constexpr int KV4_APPEND_THREADS = 256;
+
+// Sixteen elements at element index i, 16-byte loads (the host checks the
+// alignment of base and stride).
+__device__ __forceinline__ void ld_elem16(const void* p, int64_t i, int dtype, float (&x)[16]) {
+    if (dtype == 0) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = __ldg(q + j);
+            x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+        }
+        return;
+    }
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint4 v = __ldg(q + j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 f;
+            if (dtype == 1) f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
+            x[8 * j + 2 * e] = f.x;
+            x[8 * j + 2 * e + 1] = f.y;
+        }
+    }
+}
+
+// Eight tokens a CTA, four 16-channel groups of each a warp at a time: a
+// warp's loads are whole 128-byte lines of a token (16-bit inputs), its key
+// codes whole 32-byte sectors, and its value codes 64 contiguous bytes when the
+// eight tokens fill half a block.  A thread rounds one group: in fp32
+//   t = x / scale of the cache (as a product with the reciprocal, 1 by default),
+//   s = e4m3(max|t| / 6), code = e2m1(t / s), each rounded to nearest even;
+// the two quotients are IEEE divisions, so that a value half way between two
+// codes stays half way.  A group that holds a NaN or an infinity gets a NaN
+// scale: it reads back as NaN.  Rotation in fp32, products and sums rounded
+// one by one (no fused multiply-add).
+template <int D>
+__global__ void __launch_bounds__(KV4_APPEND_THREADS) kda_kv4_append_kernel(const Kv4AppendParams p) {
+    constexpr int NG = Kv4<D>::NG, GQ = NG / 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+    const int tok = (int)blockIdx.x * 8 + (lane >> 2);
+    // the request that owns the token: the number of requests that end at or before it
+    int r;
+    if (p.cu == nullptr) {
+        r = tok / p.max_t;
+    } else {
+        r = 0;
+        for (int b = 0; b < p.n; b += 32) {
+            const int32_t end = b + lane < p.n ? __ldg(p.cu + b + lane + 1) : 0x7fffffff;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = __popc(__ballot_sync(0xffffffffu, end <= (int)blockIdx.x * 8 + j));
+                if (j == (lane >> 2)) r += c;
+            }
+        }
+    }
+    if (tok >= p.total) return;
+    int pos = -1;
+    uint8_t* blk = nullptr;   // the token's block of head 0
+    int where = 0;
+    if (r < p.n) {
+        const int tok0 = p.cu ? __ldg(p.cu + r) : r * p.max_t;
+        const int t = (p.cu ? __ldg(p.cu + r + 1) : tok0 + p.max_t) - tok0;
+        const int64_t at = (int64_t)__ldg(p.ctx + r) + (tok - tok0);
+        if (tok0 < 0 || tok < tok0 || t > p.max_t ||
+            (at >= 0 && (at >= (int64_t)p.cols * p.page_tokens || (p.rot && at >= p.rope_rows)))) {
+            atomicCAS(p.status, 0, STATUS_ARG);
+        } else if (at >= 0) {
+            const int pg = (int)at / p.page_tokens, in = (int)at - pg * p.page_tokens;
+            const int32_t id = __ldg(p.table + (int64_t)r * p.cols + pg);
+            if (id < 0 || id >= p.num_pages) {
+                atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
+            } else {
+                pos = (int)at;
+                where = in & 15;
+                blk = p.pages + (int64_t)id * p.page_stride + (int64_t)(in >> 4) * Kv4<D>::BLOCK;
+            }
+        }
+    } else {
+        atomicCAS(p.status, 0, STATUS_ARG);
+    }
+    const int64_t head_bytes = (int64_t)(p.page_tokens >> 4) * Kv4<D>::BLOCK;
+    const int items = p.heads * 2 * GQ;
+    for (int it = (int)blockIdx.y * 8 + warp; it < items; it += 8 * (int)gridDim.y) {
+        const int kv = it / GQ & 1, h = it / (2 * GQ), grp = (it % GQ) * 4 + (lane & 3);
+        const bool is_v = kv != 0;
+        void* out = is_v ? p.v_out : p.k_out;
+        float x[16];
+        if (pos >= 0) {
+            const void* src = is_v ? p.v : p.k;
+            const int64_t base = (int64_t)tok * (is_v ? p.v_stride : p.k_stride) + h * D;
+            ld_elem16(src, base + grp * 16, p.dtype, x);
+            if (!is_v && grp * 16 < p.rot) {
+                const int half = p.rot >> 1;
+                const float* cs = p.cos + (int64_t)pos * half;
+                const float* sn = p.sin + (int64_t)pos * half;
+                if (p.inter) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float c = __ldg(cs + grp * 8 + j), s = __ldg(sn + grp * 8 + j);
+                        const float a = x[2 * j], b = x[2 * j + 1];
+                        x[2 * j] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+                        x[2 * j + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+                    }
+                } else {
+                    const bool first = grp * 16 < half;
+                    const int i = first ? grp * 16 : grp * 16 - half;
+                    float y[16];
+                    ld_elem16(src, base + (first ? i + half : i), p.dtype, y);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float c = __ldg(cs + i + j), s = __ldg(sn + i + j);
+                        x[j] = first ? __fsub_rn(__fmul_rn(x[j], c), __fmul_rn(y[j], s))
+                                     : __fadd_rn(__fmul_rn(x[j], c), __fmul_rn(y[j], s));
+                    }
+                }
+            }
+            const float inv = is_v ? p.inv_v : p.inv_k;
+            uint32_t amax = 0;  // bit patterns of |t| order like the values, NaN above infinity
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                x[j] = __fmul_rn(x[j], inv);
+                amax = max(amax, __float_as_uint(x[j]) & 0x7fffffffu);
+            }
+            const bool fine = amax < 0x7f800000u;
+            const uint32_t s8 = fine ? cvt_f32_e4m3(__fdiv_rn(__uint_as_float(amax), 6.0f)) : 0x7fu;
+            const uint32_t sh = cvt_e4m3x2_f16x2(s8);
+            const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                x[j] = !fine ? 0.f : s > 0.f ? __fdiv_rn(x[j], s) : copysignf(0.f, x[j]);
+            const uint2 c = make_uint2(cvt_f32x8_e2m1(x), cvt_f32x8_e2m1(x + 8));
+            uint8_t* b = blk + h * head_bytes;
+            if (!is_v) {
+                *reinterpret_cast<uint2*>(b + Kv4<D>::KC + where * (D / 2) + grp * 8) = c;
+                b[Kv4<D>::KS + where * NG + grp] = (uint8_t)s8;
+            } else {
+                if constexpr (D == 128) {
+                    *reinterpret_cast<uint2*>(b + kv4_v_code<D>(where, grp)) = c;
+                } else {
+                    *reinterpret_cast<uint32_t*>(b + kv4_v_code<D>(where, 2 * grp)) = c.x;
+                    *reinterpret_cast<uint32_t*>(b + kv4_v_code<D>(where, 2 * grp + 1)) = c.y;
+                }
+                b[kv4_v_scale<D>(where, grp)] = (uint8_t)s8;
+            }
+            if (out != nullptr) {
+                uint32_t q[8];
+                cvt_e2m1x8_f16(c.x, *reinterpret_cast<uint32_t(*)[4]>(q));
+                cvt_e2m1x8_f16(c.y, *reinterpret_cast<uint32_t(*)[4]>(q + 4));
+                const float g = is_v ? p.v_scale : p.k_scale;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
+                    x[2 * j] = f.x * s * g;       // code * scale is exact; one rounding for g != 1
+                    x[2 * j + 1] = f.y * s * g;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = 0.f;
+        }
+        if (out != nullptr) {
+            const int64_t o = ((int64_t)tok * p.heads + h) * D + grp * 16;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) st_elem4(out, o + j, p.out_dtype, x[j], x[j + 1], x[j + 2], x[j + 3]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Attend
+// ---------------------------------------------------------------------------
+struct Kv4AttendParams {
+    const uint8_t* pages;
+    int64_t num_pages, page_stride;      // bytes
+    int page_tokens, heads;
+    int n, total, max_t, dtype, cols, rot, inter, rope_rows, h_q, grp, window;
+    int64_t q_stride;                    // elements between tokens
+    const int32_t *cu, *table, *ctx;
+    const void* q;
+    const float *cos, *sin;
+    void* o;
+    float scale_log2, v_scale;           // softmax scale * k_scale * log2(e)
+    int32_t* counters;                   // [gridDim.x], zero between calls
+    float* partials;                     // [2 gridDim.x][KV4_ROWS][D + 2]
+    int32_t* status;
+};
+
+constexpr int KV4_WARPS = 8, KV4_THREADS = KV4_WARPS * 32;
+constexpr int KV4_ROWS = 16;             // rows of an mma tile
+constexpr int KV4_STAGES = 4;            // blocks a warp has in flight
+constexpr int KV4_MIN_BLOCKS = 8;        // least blocks of a CTA's share: one a warp
+constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
+constexpr int KV4_AHEAD = 16;            // blocks whose pages a warp looks up at a time
+constexpr float KV4_SLACK = 8.f;         // the running maximum may lag by this many powers of two
+
+template <int D> struct Kv4Smem {
+    static constexpr int RING = KV4_WARPS * KV4_STAGES * Kv4<D>::BLOCK;
+    static constexpr int MERGE = KV4_WARPS * 8 * D * 4;
+    // a row of queries in 16-byte pieces (w, t) of lane t's channels 8 w .. 8 w + 7; the pitch keeps a
+    // quarter-warp's reads (two rows, four t) on different banks
+    static constexpr int QPITCH = D + 32;                    // halves
+    static constexpr int Q = KV4_ROWS * QPITCH * 2;
+    static constexpr int ML = KV4_WARPS * KV4_ROWS * 2 * 4;
+    static constexpr int OFF_MERGE = RING, OFF_Q = OFF_MERGE + MERGE, OFF_ML = OFF_Q + Q,
+                         OFF_ROW = OFF_ML + ML,              // row factors [16]
+                         OFF_BAR = OFF_ROW + KV4_ROWS * 4,   // [warps][stages] barriers
+                         OFF_PLAN = OFF_BAR + KV4_WARPS * KV4_STAGES * 8,
+                         OFF_WALK = OFF_PLAN + 128,          // [warps][2] Kv4Walk
+                         OFF_AHEAD = OFF_WALK + KV4_WARPS * 2 * 80,   // [warps][KV4_AHEAD] byte offsets of blocks
+                         BYTES = OFF_AHEAD + KV4_WARPS * KV4_AHEAD * 8;
+    static_assert(BYTES <= 115712, "two CTAs an SM");
+};
+
+// One request's part of the work: its tokens, and the blocks of 16 keys that
+// any of its queries can see.
+struct Kv4Req {
+    int tok0, t, ctx, first, nblk, tiles, err;
+};
+
+__device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, int rows) {
+    Kv4Req q;
+    q.err = 0;
+    q.tok0 = p.cu ? __ldg(p.cu + r) : r * p.max_t;
+    q.t = (p.cu ? __ldg(p.cu + r + 1) : q.tok0 + p.max_t) - q.tok0;
+    q.ctx = __ldg(p.ctx + r);
+    q.first = q.nblk = 0;
+    if (q.tok0 < 0 || q.t < 0 || q.t > p.max_t || (int64_t)q.tok0 + q.t > p.total) {
+        q.err = STATUS_ARG;
+        q.tok0 = q.t = 0;
+    }
+    q.tiles = (q.t * p.grp + rows - 1) / rows;
+    const int64_t end = (int64_t)q.ctx + q.t;
+    if (q.t > 0 && end > 0) {
+        if (end > (int64_t)p.cols * p.page_tokens || (p.rot && end > p.rope_rows)) {
+            q.err = STATUS_ARG;
+        } else {
+            if (p.window > 0) q.first = max(0, max(q.ctx, 0) - p.window + 1) >> 4;
+            q.nblk = (int)((end + 15) >> 4) - q.first;
+        }
+    }
+    return q;
+}
+
+// A walk over a CTA's share of the flattened list of (request, head, row tile,
+// block): each step is the part of one (request, head, row tile) in the share.
+struct Kv4Walk {
+    int64_t left;        // blocks of the share not yet taken
+    int r, off;          // request, blocks of it already taken
+    Kv4Req q;
+    int seg, b0, b1;     // the current step: head * tiles + tile, blocks [b0, b1)
+    int b, used;         // (fetching) this warp's next block, its place among those looked up
+    __device__ __forceinline__ bool next(const Kv4AttendParams& p, int rows) {
+        if (left <= 0) return false;
+        while (off >= q.nblk * q.tiles * p.heads) {
+            if (++r >= p.n) return false;
+            q = kv4_request(p, r, rows);
+            off = 0;
+        }
+        seg = off / q.nblk;
+        b0 = off - seg * q.nblk;
+        const int take = (int)min((int64_t)(q.nblk - b0), left);
+        b1 = b0 + take;
+        off += take;
+        left -= take;
+        return true;
+    }
+};
+
+// Attention over the cache, one pass with a running maximum and sum.
+//
+// Rows.  The query heads of one key/value head and the request's tokens make
+// the rows of an mma tile (m16n8k16, fp16 operands, fp32 sums); keys are the
+// columns.  A code times its scale has at most 6 significant bits, so keys and
+// values are exact in fp16.  Queries are scaled by a power of two a row to
+// below 1 and rounded to fp16.  SPLIT: a tile has 8 rows, and its other 8 hold
+// the fp16 remainders of the first (queries and probabilities alike; the sums
+// of both are added), so that products carry 22 bits at no extra cost: for
+// fp16 and fp32 queries, and whenever 8 rows are enough.  Otherwise (bf16,
+// more than 8 rows) a tile has 16 rows whose queries and probabilities are
+// rounded to 11 bits, an eighth of the bf16 output's own rounding.
+//
+// Channel order.  A product over channels may take them in any order, so lane
+// (g, t) takes channels t D / 4 .. of key g: 16 contiguous code bytes (D =
+// 128), and at most two scales.
+//
+// Split.  All (request, head, tile, block) are one list, cut evenly over the
+// CTAs whatever the lengths; a CTA's warps take its blocks in turn, each with
+// its own ring of bulk copies, and join at the end of a part.  Parts of one
+// (request, head, tile) in several CTAs go to the workspace, and the CTA that
+// arrives last joins them in order (results do not depend on who that is).
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv4AttendParams p) {
+    using F = Kv4<D>;
+    using SM = Kv4Smem<D>;
+    constexpr int ROWS = SPLIT ? 8 : 16;      // real rows of a tile
+    constexpr int NT = D / 8;                 // n tiles of the output
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    uint8_t* ring = smem + warp * (KV4_STAGES * F::BLOCK);
+    float* merge = reinterpret_cast<float*>(smem + SM::OFF_MERGE);
+    __half* qbuf = reinterpret_cast<__half*>(smem + SM::OFF_Q);
+    float* ml = reinterpret_cast<float*>(smem + SM::OFF_ML);          // [warp][16] m, then l
+    float* rowf = reinterpret_cast<float*>(smem + SM::OFF_ROW);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::OFF_BAR) + warp * KV4_STAGES;
+    int64_t* plan = reinterpret_cast<int64_t*>(smem + SM::OFF_PLAN);  // warp sums [8], r0 and off0, -, share, its start, its length
+    int* plan_i = reinterpret_cast<int*>(plan + 8);
+
+    if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < KV4_STAGES; ++s) mbar_init(bars + s, 1);
+        fence_mbar_init();
+    }
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+
+    // ---- the share of this CTA ----
+    const int cnt = (p.n + KV4_THREADS - 1) / KV4_THREADS;
+    int64_t mine = 0;
+    bool empty = false;
+    for (int r = tid * cnt; r < min(p.n, (tid + 1) * cnt); ++r) {
+        const Kv4Req q = kv4_request(p, r, ROWS);
+        mine += (int64_t)q.nblk * q.tiles * p.heads;
+        empty |= q.t > 0 && q.nblk == 0;
+        if (q.err && blockIdx.x == 0) atomicCAS(p.status, 0, q.err);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) plan[warp] = incl;
+    const bool any_empty = __syncthreads_or(empty);
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < KV4_WARPS; ++w) {
+        const int64_t s = plan[w];
+        if (w < warp) before += s;
+        total += s;
+    }
+    const int64_t per = max((int64_t)KV4_MIN_BLOCKS, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t lo = per * blockIdx.x;
+    before += incl - mine;
+    if (mine > 0 && before <= lo && lo < before + mine) {
+        int r = tid * cnt;
+        int64_t off = lo - before;
+        for (;; ++r) {
+            const Kv4Req q = kv4_request(p, r, ROWS);
+            const int64_t c = (int64_t)q.nblk * q.tiles * p.heads;
+            if (off < c) break;
+            off -= c;
+        }
+        plan_i[0] = r;
+        plan_i[1] = (int)off;
+    }
+    __syncthreads();
+    if (any_empty) {  // requests without a visible key: zero rows
+        for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
+            const Kv4Req q = kv4_request(p, r, ROWS);
+            if (q.nblk > 0) continue;
+            const int64_t base = (int64_t)q.tok0 * p.h_q * D;
+            for (int64_t i = tid * 4; i < (int64_t)q.t * p.h_q * D; i += KV4_THREADS * 4)
+                st_elem4(p.o, base + i, p.dtype, 0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    if (lo >= total) return;
+    if (tid == 0) {  // kept for the joins
+        plan[10] = per;
+        plan[11] = lo;
+        plan[12] = min(per, total - lo);
+    }
+
+    // what is being fetched, what is being worked on: a warp's own, in shared
+    // memory (read seldom; the registers go to the accumulators)
+    Kv4Walk& put = reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK)[2 * warp];
+    Kv4Walk& get = reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK)[2 * warp + 1];
+    static_assert(sizeof(Kv4Walk) <= 80, "Kv4Smem::OFF_WALK");
+    if (lane == 0) {
+        put.r = plan_i[0];
+        put.off = plan_i[1];
+        put.left = min(per, total - lo);
+        put.q = kv4_request(p, put.r, ROWS);
+        put.b0 = put.b1 = put.b = put.seg = 0;
+        get = put;
+    }
+    __syncwarp();
+    auto step = [&](Kv4Walk& w) {   // lane 0 walks, all lanes see it
+        int ok = 0;
+        __syncwarp();
+        if (lane == 0) ok = w.next(p, ROWS);
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
+
+    const int bpp = p.page_tokens >> 4;
+    int64_t* ahead = reinterpret_cast<int64_t*>(smem + SM::OFF_AHEAD) + warp * KV4_AHEAD;
+    // one register of flags: bits 0.. the slots' phase parities, 8.. slots whose page was bad, MORE
+    // to fetch, ALIVE until a wait runs out
+    constexpr uint32_t MORE = 1u << 16, ALIVE = 1u << 17;
+    uint32_t flags = MORE | ALIVE;
+
+    // Fetches this warp's next block into a slot.
+    auto fetch = [&](uint32_t slot) {
+        if (!(flags & MORE)) return;
+        while (put.b >= put.b1) {
+            if (!step(put)) {
+                flags &= ~MORE;
+                return;
+            }
+            if (lane == 0) {
+                put.b = put.b0 + warp;
+                put.used = KV4_AHEAD;
+            }
+            __syncwarp();
+        }
+        if (put.used == KV4_AHEAD) {
+            const int mine = put.b + KV4_WARPS * lane;
+            if (lane < KV4_AHEAD && mine < put.b1) {
+                const int b = put.q.first + mine, pg = b / bpp;
+                const int page = __ldg(p.table + (int64_t)put.r * p.cols + pg);
+                ahead[lane] = page < 0 || page >= p.num_pages
+                                  ? -1
+                                  : (int64_t)page * p.page_stride + ((int64_t)(put.seg / put.q.tiles) * bpp + (b - pg * bpp)) * F::BLOCK;
+            }
+            __syncwarp();
+            if (lane == 0) put.used = 0;
+            __syncwarp();
+        }
+        const int64_t off = ahead[put.used];
+        __syncwarp();
+        if (lane == 0) {
+            ++put.used;
+            put.b += KV4_WARPS;
+        }
+        if (off < 0) {
+            flags |= 256u << slot;
+            if (lane == 0) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
+        } else {
+            flags &= ~(256u << slot);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bars + slot, F::BLOCK);
+                bulk_load(ring + slot * F::BLOCK, p.pages + off, F::BLOCK, bars + slot);
+            }
+        }
+        __syncwarp();
+    };
+#pragma unroll 1
+    for (int s = 0; s < KV4_STAGES; ++s) fetch(s);
+    uint32_t slot = 0;                  // the slot to work on, and then to fetch into
+
+    // the current tile's first row, a row's position and the tile's last one: worked out where
+    // they are needed, not kept in registers
+    auto first_row = [&]() { return get.seg % get.q.tiles * ROWS; };
+    auto row_pos = [&](int i) { return get.q.ctx + (first_row() + i) / p.grp; };
+    auto last_row_pos = [&]() { return get.q.ctx + min(get.q.t - 1, (first_row() + ROWS - 1) / p.grp); };
+
+    while (step(get)) {
+        {
+        const int h = get.seg / get.q.tiles, i0 = first_row();
+        const int live = min(ROWS, get.q.t * p.grp - i0);
+        // ---- queries: rotate, scale, round; one row a warp at a time ----
+        for (int i = warp; i < ROWS; i += KV4_WARPS) {
+            constexpr int E = D / 32;
+            float x[E];
+            float factor = 0.f;
+            const int j = (i0 + i) / p.grp;
+            const int pos = get.q.ctx + j;
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = 0.f;
+            if (i < live && pos >= 0) {
+                const int64_t base = (int64_t)(get.q.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + (i0 + i) - j * p.grp) * D;
+                const int half = p.rot >> 1;
+                float amax = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int d = lane * E + e;
+                    x[e] = ld_elem(p.q, base + d, p.dtype);
+                    if (d < p.rot) {
+                        int c, o;
+                        bool first;
+                        if (p.inter) { c = d >> 1; first = (d & 1) == 0; o = d ^ 1; }
+                        else { first = d < half; c = first ? d : d - half; o = first ? d + half : c; }
+                        const float y = ld_elem(p.q, base + o, p.dtype);
+                        const float cs = __ldg(p.cos + (int64_t)pos * half + c), sn = __ldg(p.sin + (int64_t)pos * half + c);
+                        x[e] = first ? x[e] * cs - y * sn : x[e] * cs + y * sn;
+                    }
+                    amax = fmaxf(amax, fabsf(x[e]));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                // 2^-k with amax 2^-k in [1/2, 1); the factor below 2^-100 and the infinite stay as they are
+                const int k = amax > 1e-30f && amax < 3e38f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
+                factor = p.scale_log2 * exp2f((float)k);
+                const float down = exp2f((float)-k);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] *= down;
+            }
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const __half2 hi = __floats2half2_rn(x[e], x[e + 1]);
+                const int d = lane * E + e, at = (d % (D / 4) / 8 * 4 + d / (D / 4)) * 8 + d % 8;
+                *reinterpret_cast<__half2*>(qbuf + i * SM::QPITCH + at) = hi;
+                if constexpr (SPLIT) {
+                    const float2 f = __half22float2(hi);
+                    *reinterpret_cast<__half2*>(qbuf + (i + 8) * SM::QPITCH + at) =
+                        __floats2half2_rn(x[e] - f.x, x[e + 1] - f.y);
+                }
+            }
+            if (lane == 0) rowf[i] = factor;
+        }
+        }
+        __syncthreads();
+        // query fragments: eight channels of row g and of row g + 8, two k steps, a piece.  D = 64
+        // keeps them in registers; D = 128 reads them again for each block (32 registers more would spill)
+        const uint4* qa = reinterpret_cast<const uint4*>(qbuf + g * SM::QPITCH) + t;
+        const uint4* qb = qa + 8 * SM::QPITCH / 8;
+        constexpr bool QREG = D == 64;
+        uint4 qra[QREG ? D / 32 : 1], qrb[QREG ? D / 32 : 1];
+        if constexpr (QREG) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                qra[w] = qa[w * 4];
+                qrb[w] = qb[w * 4];
+            }
+        }
+        constexpr int NR = SPLIT ? 1 : 2;     // real rows a lane holds
+        float m[NR], l[NR];
+#pragma unroll
+        for (int a = 0; a < NR; ++a) {
+            m[a] = -INFINITY;
+            l[a] = 0.f;
+        }
+        // blocks that every row of the tile sees whole: [see0, see1)
+        const int see1 = (row_pos(0) + 1) >> 4;
+        const int see0 = p.window > 0 ? (max(0, last_row_pos() - p.window + 1) + 15) >> 4 : 0;
+        float acc[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+
+#pragma unroll 1
+        for (int b = get.b0 + warp; b < get.b1; b += KV4_WARPS) {
+            bool use = (flags & ALIVE) && !(flags & 256u << slot);
+            if (use) {
+                use = mbar_wait(bars + slot, flags >> slot & 1u);
+                if (use) {
+                    flags ^= 1u << slot;
+                } else {
+                    flags &= ~(MORE | ALIVE);
+                    if (lane == 0) atomicCAS(p.status, 0, STATUS_TIMEOUT);
+                }
+            }
+            if (use) {
+                const uint8_t* B = ring + slot * F::BLOCK;
+                float s[2][4];
+                // ---- scores of keys g (n tile 0) and g + 8 (n tile 1) ----
+                uint32_t code[2][D / 32], sc[2][2];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                    const int key = nt * 8 + g;
+                    if constexpr (D == 128) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(B + F::KC + key * 64 + t * 16);
+                        code[nt][0] = w.x; code[nt][1] = w.y; code[nt][2] = w.z; code[nt][3] = w.w;
+                        const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(B + F::KS + key * 8 + 2 * t));
+                        sc[nt][0] = __byte_perm(two, two, 0x1010);
+                        sc[nt][1] = __byte_perm(two, two, 0x3232);
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(B + F::KC + key * 32 + t * 8);
+                        code[nt][0] = w.x; code[nt][1] = w.y;
+                        const uint32_t two = cvt_e4m3x2_f16x2(B[F::KS + key * 4 + t]);
+                        sc[nt][0] = sc[nt][1] = __byte_perm(two, two, 0x1010);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    const uint4 a = QREG ? qra[w % (QREG ? D / 32 : 1)] : qa[w * 4], b2 = QREG ? qrb[w % (QREG ? D / 32 : 1)] : qb[w * 4];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        uint32_t k[4];
+                        cvt_e2m1x8_f16(code[nt][w], k);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) k[e] = hmul2_u32(k[e], sc[nt][w / 2]);
+                        kv4_mma(s[nt], a.x, b2.x, a.y, b2.y, k[0], k[1]);
+                        kv4_mma(s[nt], a.z, b2.z, a.w, b2.w, k[2], k[3]);
+                    }
+                }
+                // ---- running softmax; column of s[nt][e]: key nt * 8 + 2 t + (e & 1) ----
+                const int blk = get.q.first + b;
+                const bool masked = blk < see0 || blk >= see1;
+                float x[NR][4];
+                uint32_t pf[4];
+                bool grow = false;
+                float top[NR];
+#pragma unroll
+                for (int a = 0; a < NR; ++a) {
+                    const float c = rowf[g + 8 * a];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            x[a][nt * 2 + e] = (SPLIT ? s[nt][e] + s[nt][2 + e] : s[nt][2 * a + e]) * c;
+                    if (masked) {
+                        const int pos = row_pos(g + 8 * a);
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = blk * 16 + nt * 8 + 2 * t + e;
+                                if (key > pos || (p.window > 0 && key <= pos - p.window)) x[a][nt * 2 + e] = -INFINITY;
+                            }
+                    }
+                    top[a] = fmaxf(fmaxf(x[a][0], x[a][1]), fmaxf(x[a][2], x[a][3]));
+                    top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 1));
+                    top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 2));
+                    grow |= top[a] > m[a] + KV4_SLACK;
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int a = 0; a < NR; ++a) {
+                        if (top[a] > m[a]) {
+                            const float f = ex2f(m[a] - top[a]);
+                            m[a] = top[a];
+                            l[a] *= f;
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {
+                                acc[j][2 * a] *= f;
+                                acc[j][2 * a + 1] *= f;
+                                if constexpr (SPLIT) { acc[j][2] *= f; acc[j][3] *= f; }
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < NR; ++a) {
+                    const float mu = m[a] == -INFINITY ? 0.f : m[a];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[a][e] = ex2f(x[a][e] - mu);
+                    l[a] += (x[a][0] + x[a][1]) + (x[a][2] + x[a][3]);
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const __half2 hi = __floats2half2_rn(x[a][2 * nt], x[a][2 * nt + 1]);
+                        pf[2 * nt + a] = *reinterpret_cast<const uint32_t*>(&hi);
+                        if constexpr (SPLIT) {
+                            const float2 f = __half22float2(hi);
+                            const __half2 lo2 = __floats2half2_rn(x[a][2 * nt] - f.x, x[a][2 * nt + 1] - f.y);
+                            pf[2 * nt + 1] = *reinterpret_cast<const uint32_t*>(&lo2);
+                        }
+                    }
+                }
+                // ---- values ----
+                uint32_t vs4;
+                if constexpr (D == 128) vs4 = *reinterpret_cast<const uint32_t*>(B + F::VS + lane * 4);
+                else vs4 = *reinterpret_cast<const uint32_t*>(B + F::VS + ((g >> 1) * 4 + t) * 4);
+                if (masked) {
+                    // A token that some row does not see may hold anything, and 0 * NaN is NaN:
+                    // scales behind the end become 0, and so do NaN ones, whose channels of the
+                    // rows that do see them are then set by hand (a rare path).
+                    bool nan = false;
+                    const int last_pos = last_row_pos();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = blk * 16 + (e >> 1) * 8 + 2 * t + (e & 1);
+                        const bool bad = (vs4 >> (8 * e) & 0x7fu) == 0x7fu;
+                        if (key > last_pos || bad) vs4 &= ~(0xffu << (8 * e));
+                        nan |= bad && key <= last_pos;
+                    }
+                    if (__any_sync(0xffffffffu, nan)) {
+                        uint32_t hit = 0;
+#pragma unroll 1
+                        for (int i = 0; i < 32; ++i) {
+                            const int w = i >> 1, key = blk * 16 + w;
+                            if ((B[kv4_v_scale<D>(w, (2 * t + (i & 1)) * (D / 8) / 16)] & 0x7f) != 0x7f) continue;
+#pragma unroll
+                            for (int a = 0; a < NR; ++a) {
+                                const int pos = row_pos(g + 8 * a);
+                                if (key <= pos && (p.window <= 0 || key > pos - p.window)) hit |= 1u << (2 * a + (i & 1));
+                            }
+                        }
+#pragma unroll
+                        for (int a = 0; a < 2 * NR; ++a)
+                            if (hit >> a & 1u)
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) acc[j][a] = NAN;
+                    }
+                }
+                const uint32_t sv[2] = {cvt_e4m3x2_f16x2(vs4 & 0xffffu), cvt_e4m3x2_f16x2(vs4 >> 16)};
+                uint32_t vc[2][2][D / 64];          // [half][token of the pair][word]
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint8_t* V = B + F::VC + hf * (64 * F::CB) + lane * (2 * F::CB);
+                    if constexpr (D == 128) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(V);
+                        vc[hf][0][0] = w.x; vc[hf][0][1] = w.y; vc[hf][1][0] = w.z; vc[hf][1][1] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(V);
+                        vc[hf][0][0] = w.x; vc[hf][1][0] = w.y;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w) {
+                    uint32_t even[2], odd[2];   // codes of tokens 2t (low nibbles) and 2t + 1 by even and odd channels
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t A = vc[hf][0][w], C = vc[hf][1][w];
+                        even[hf] = (A & 0x0f0f0f0fu) | (C << 4 & 0xf0f0f0f0u);
+                        odd[hf] = (A >> 4 & 0x0f0f0f0fu) | (C & 0xf0f0f0f0u);
+                    }
+#pragma unroll
+                    for (int par = 0; par < 2; ++par) {
+                        uint32_t v0[4], v1[4];
+                        cvt_e2m1x8_f16(par ? odd[0] : even[0], v0);
+                        cvt_e2m1x8_f16(par ? odd[1] : even[1], v1);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            kv4_mma(acc[8 * w + 2 * e + par], pf[0], pf[1], pf[2], pf[3],
+                                    hmul2_u32(v0[e], sv[0]), hmul2_u32(v1[e], sv[1]));
+                    }
+                }
+            }
+            __syncwarp();
+            fetch(slot);
+            slot = slot + 1 == KV4_STAGES ? 0 : slot + 1;
+        }
+
+        // ---- the warps' sums of this part, joined in warp order ----
+        const int h = get.seg / get.q.tiles, i0 = first_row(), live = min(ROWS, get.q.t * p.grp - i0);
+        const bool whole = get.b0 == 0 && get.b1 == get.q.nblk;
+        float* part = p.partials + (int64_t)(2 * blockIdx.x + (get.b0 == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
+#pragma unroll
+        for (int a = 0; a < NR; ++a) {
+            l[a] += __shfl_xor_sync(0xffffffffu, l[a], 1);
+            l[a] += __shfl_xor_sync(0xffffffffu, l[a], 2);
+            if (t == 0) {
+                ml[(warp * KV4_ROWS + g + 8 * a) * 2] = m[a];
+                ml[(warp * KV4_ROWS + g + 8 * a) * 2 + 1] = l[a];
+            }
+        }
+        auto join = [&](int row, int d, float4 o, float M, float L) {
+            const int j = (i0 + row) / p.grp;
+            const int64_t out = ((int64_t)(get.q.tok0 + j) * p.h_q + h * p.grp + (i0 + row) - j * p.grp) * D + d;
+            const float f = L == 0.f ? 0.f : p.v_scale / L;
+            if (L == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+            st_elem4(p.o, out, p.dtype, o.x * f, o.y * f, o.z * f, o.w * f);
+        };
+        constexpr int CH = D / 4;             // 16-byte pieces of a row
+#pragma unroll
+        for (int a = 0; a < NR; ++a) {
+            if (8 * a < live) {
+                if (a > 0) __syncthreads();
+                if (g + 8 * a < live) {
+                    float* row = merge + (warp * 8 + g) * D;
+#pragma unroll
+                    for (int k = 0; k < CH / 4; ++k) {
+                        // this lane's channels t D / 4 + 4 k ..: column 2t of n tiles 4k .., then column 2t + 1
+                        const int col = k >= CH / 8, j = (k % (CH / 8)) * 4;
+                        float4 o;
+                        o.x = SPLIT ? acc[j][col] + acc[j][2 + col] : acc[j][2 * a + col];
+                        o.y = SPLIT ? acc[j + 1][col] + acc[j + 1][2 + col] : acc[j + 1][2 * a + col];
+                        o.z = SPLIT ? acc[j + 2][col] + acc[j + 2][2 + col] : acc[j + 2][2 * a + col];
+                        o.w = SPLIT ? acc[j + 3][col] + acc[j + 3][2 + col] : acc[j + 3][2 * a + col];
+                        const int chunk = (t * (CH / 4) + k) ^ ((t * 2 + (g & 1)) & 7);
+                        *reinterpret_cast<float4*>(row + chunk * 4) = o;
+                    }
+                }
+                __syncthreads();
+                const int tid2 = tid_again(), row = tid2 / CH, ch = tid2 % CH;
+                if (row < 8 && row + 8 * a < live) {
+                    const int sw = ch ^ ((ch / (CH / 4) * 2 + (row & 1)) & 7);
+                    float M = -INFINITY, L = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < KV4_WARPS; ++w) M = fmaxf(M, ml[(w * KV4_ROWS + row + 8 * a) * 2]);
+#pragma unroll 2
+                    for (int w = 0; w < KV4_WARPS; ++w) {
+                        const float mw = ml[(w * KV4_ROWS + row + 8 * a) * 2], lw = ml[(w * KV4_ROWS + row + 8 * a) * 2 + 1];
+                        // no key seen: nothing to add (a NaN sum stays one)
+                        const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : ex2f(mw - M);
+                        if (f != 0.f) {
+                            const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * D + sw * 4);
+                            L += f * lw;
+                            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+                        }
+                    }
+                    if (whole) {
+                        join(row + 8 * a, ch * 4, o, M, L);
+                    } else {
+                        __stcg(reinterpret_cast<float4*>(part + (row + 8 * a) * D + ch * 4), o);
+                        if (ch == 0) __stcg(reinterpret_cast<float2*>(part + KV4_ROWS * D) + row + 8 * a, make_float2(M, L));
+                    }
+                }
+            }
+        }
+        if (!whole) {
+            // CTAs that share this (request, head, tile), from its place in the list
+            const int64_t seg0 = plan[11] + plan[12] - get.left - get.b1, share = plan[10];
+            const int c0 = (int)(seg0 / share), c1 = (int)((seg0 + get.q.nblk - 1) / share);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int old = atomicAdd(p.counters + c0, 1);
+                if (old == c1 - c0) p.counters[c0] = 0;
+                plan_i[0] = old == c1 - c0;
+                __threadfence();
+            }
+            __syncthreads();
+            if (plan_i[0]) {
+                const int tid2 = tid_again(), ch = tid2 % CH;
+                for (int row = tid2 / CH; row < live; row += KV4_THREADS / CH) {
+                    auto slot = [&](int cta) {
+                        return p.partials + (int64_t)(2 * cta + (cta == c0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
+                    };
+                    float M = -INFINITY, L = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + KV4_ROWS * D + 2 * row));
+#pragma unroll 4
+                    for (int k = c0; k <= c1; ++k) {
+                        const float* s = slot(k);
+                        const float2 x = __ldcg(reinterpret_cast<const float2*>(s + KV4_ROWS * D) + row);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D + ch * 4));
+                        const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2f(x.x - M);
+                        if (f != 0.f) {
+                            L += f * x.y;
+                            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+                        }
+                    }
+                    join(row, ch * 4, o, M, L);
+                }
+            }
+        }
+    }
+    // after a wait that ran out: the copies still in flight end (or time out) before the CTA does
+    if (!(flags & ALIVE)) {
+        for (int s = 0; s < KV4_STAGES; ++s)
+            if (!(flags & 256u << s)) (void)mbar_wait(bars + s, flags >> s & 1u);
+    }
+}
+
+}  // namespace kda
