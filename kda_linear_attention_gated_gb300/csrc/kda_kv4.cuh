@@ -17,6 +17,8 @@
 // word a lane, in lane order.
 #pragma once
 
+#include <cfloat>
+
 #include "kda_common.cuh"
 
 namespace kda {
@@ -93,6 +95,13 @@ __device__ __forceinline__ void cvt_e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
 __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Transposes an 8 x 8 matrix of 16-bit elements held two a lane (row lane / 4,
+// columns 2 (lane % 4) ..).
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 // threadIdx.x read again, where a value kept across the main loop would cost a register.
 __device__ __forceinline__ int tid_again() {
@@ -325,36 +334,46 @@ struct Kv4AttendParams {
     int32_t* status;
 };
 
-constexpr int KV4_WARPS = 8, KV4_THREADS = KV4_WARPS * 32;
-constexpr int KV4_ROWS = 16;             // rows of an mma tile
-constexpr int KV4_STAGES = 4;            // blocks a warp has in flight
-constexpr int KV4_MIN_BLOCKS = 8;        // least blocks of a CTA's share: one a warp
+// What the columns of a query tile hold, see kda_kv4_attend_kernel.
+constexpr int KV4_8 = 0, KV4_REST = 1, KV4_16 = 2;
+constexpr int KV4_ROWS = 16;             // most rows of a tile
+constexpr int KV4_KEYS = 32;             // keys of a unit of work: two blocks
+constexpr int KV4_PART = 8;              // what beginning and ending a part costs a CTA, in units
 constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
-constexpr int KV4_AHEAD = 16;            // blocks whose pages a warp looks up at a time
+constexpr int KV4_AHEAD = 16;            // units whose pages a warp looks up at a time: lanes 2 i, 2 i + 1 a block each
 constexpr float KV4_SLACK = 8.f;         // the running maximum may lag by this many powers of two
 
-template <int D> struct Kv4Smem {
-    static constexpr int RING = KV4_WARPS * KV4_STAGES * Kv4<D>::BLOCK;
-    static constexpr int MERGE = KV4_WARPS * 8 * D * 4;
+// Warps of a CTA (two CTAs an SM) and units that each has in flight: as many
+// warps as the registers of a mode allow.
+template <int D, int MODE> struct Kv4Shape {
+    static constexpr int WARPS = MODE == KV4_16 || (MODE == KV4_REST && D == 128) ? 6 : 8, THREADS = WARPS * 32;
+    static constexpr int STAGES = WARPS == 6 ? 3 : 2;
+    static constexpr int ROWS = MODE == KV4_16 ? 16 : 8;
+    static constexpr int MIN_SHARE = KV4_PART + WARPS;   // least share of a CTA: a unit a warp
+};
+
+template <int D, int MODE> struct Kv4Smem {
+    static constexpr int WARPS = Kv4Shape<D, MODE>::WARPS, STAGES = Kv4Shape<D, MODE>::STAGES;
+    static constexpr int RING = WARPS * STAGES * 2 * Kv4<D>::BLOCK;
+    static constexpr int MERGE = WARPS * 8 * D * 4;
     // a row of queries in 16-byte pieces (w, t) of lane t's channels 8 w .. 8 w + 7; the pitch keeps a
     // quarter-warp's reads (two rows, four t) on different banks
     static constexpr int QPITCH = D + 32;                    // halves
     static constexpr int Q = KV4_ROWS * QPITCH * 2;
-    static constexpr int ML = KV4_WARPS * KV4_ROWS * 2 * 4;
+    static constexpr int ML = WARPS * KV4_ROWS * 2 * 4;
     static constexpr int OFF_MERGE = RING, OFF_Q = OFF_MERGE + MERGE, OFF_ML = OFF_Q + Q,
                          OFF_ROW = OFF_ML + ML,              // row factors [16]
                          OFF_BAR = OFF_ROW + KV4_ROWS * 4,   // [warps][stages] barriers
-                         OFF_PLAN = OFF_BAR + KV4_WARPS * KV4_STAGES * 8,
+                         OFF_PLAN = OFF_BAR + WARPS * STAGES * 8,
                          OFF_WALK = OFF_PLAN + 128,          // [warps][2] Kv4Walk
-                         OFF_AHEAD = OFF_WALK + KV4_WARPS * 2 * 80,   // [warps][KV4_AHEAD] byte offsets of blocks
-                         BYTES = OFF_AHEAD + KV4_WARPS * KV4_AHEAD * 8;
+                         BYTES = OFF_WALK + WARPS * 2 * 80;
     static_assert(BYTES <= 115712, "two CTAs an SM");
 };
 
-// One request's part of the work: its tokens, and the blocks of 16 keys that
+// One request's part of the work: its tokens, and the units of 32 keys that
 // any of its queries can see.
 struct Kv4Req {
-    int tok0, t, ctx, first, nblk, tiles, err;
+    int tok0, t, ctx, first, units, tiles, err;
 };
 
 __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, int rows) {
@@ -363,7 +382,7 @@ __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, i
     q.tok0 = p.cu ? __ldg(p.cu + r) : r * p.max_t;
     q.t = (p.cu ? __ldg(p.cu + r + 1) : q.tok0 + p.max_t) - q.tok0;
     q.ctx = __ldg(p.ctx + r);
-    q.first = q.nblk = 0;
+    q.first = q.units = 0;
     if (q.tok0 < 0 || q.t < 0 || q.t > p.max_t || (int64_t)q.tok0 + q.t > p.total) {
         q.err = STATUS_ARG;
         q.tok0 = q.t = 0;
@@ -374,75 +393,95 @@ __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, i
         if (end > (int64_t)p.cols * p.page_tokens || (p.rot && end > p.rope_rows)) {
             q.err = STATUS_ARG;
         } else {
-            if (p.window > 0) q.first = max(0, max(q.ctx, 0) - p.window + 1) >> 4;
-            q.nblk = (int)((end + 15) >> 4) - q.first;
+            if (p.window > 0) q.first = max(0, max(q.ctx, 0) - p.window + 1) / KV4_KEYS;
+            q.units = (int)((end + KV4_KEYS - 1) / KV4_KEYS) - q.first;
         }
     }
     return q;
 }
 
-// A walk over a CTA's share of the flattened list of (request, head, row tile,
-// block): each step is the part of one (request, head, row tile) in the share.
+// Cost of a request: each (head, row tile) its units, behind KV4_PART for its
+// beginning and end.
+__device__ __forceinline__ int64_t kv4_cost(const Kv4Req& q, int heads) {
+    return q.units > 0 ? (int64_t)(q.units + KV4_PART) * q.tiles * heads : 0;
+}
+
+// A walk over a CTA's share of the flattened list of costs: each step is the
+// part of one (request, head, row tile) whose units lie in the share.
 struct Kv4Walk {
-    int64_t left;        // blocks of the share not yet taken
-    int r, off;          // request, blocks of it already taken
+    int64_t left;        // of the share, not yet taken
+    int64_t off;         // of request r, already taken
+    int r;
     Kv4Req q;
-    int seg, b0, b1;     // the current step: head * tiles + tile, blocks [b0, b1)
-    int b, used;         // (fetching) this warp's next block, its place among those looked up
+    int seg, b0, b1;     // the current step: head * tiles + tile, units [b0, b1)
+    int b;               // (fetching) this warp's next unit not looked up
     __device__ __forceinline__ bool next(const Kv4AttendParams& p, int rows) {
-        if (left <= 0) return false;
-        while (off >= q.nblk * q.tiles * p.heads) {
-            if (++r >= p.n) return false;
-            q = kv4_request(p, r, rows);
-            off = 0;
-        }
-        seg = off / q.nblk;
-        b0 = off - seg * q.nblk;
-        const int take = (int)min((int64_t)(q.nblk - b0), left);
-        b1 = b0 + take;
-        off += take;
-        left -= take;
+        do {
+            if (left <= 0) return false;
+            while (off >= kv4_cost(q, p.heads)) {
+                if (++r >= p.n) return false;
+                q = kv4_request(p, r, rows);
+                off = 0;
+            }
+            const int each = q.units + KV4_PART;
+            seg = (int)(off / each);
+            const int u = (int)(off - (int64_t)seg * each);
+            const int take = (int)min((int64_t)(each - u), left);
+            b0 = max(0, u - KV4_PART);
+            b1 = max(0, u + take - KV4_PART);
+            off += take;
+            left -= take;
+        } while (b0 == b1);
         return true;
     }
 };
 
 // Attention over the cache, one pass with a running maximum and sum.
 //
-// Rows.  The query heads of one key/value head and the request's tokens make
-// the rows of an mma tile (m16n8k16, fp16 operands, fp32 sums); keys are the
-// columns.  A code times its scale has at most 6 significant bits, so keys and
-// values are exact in fp16.  Queries are scaled by a power of two a row to
-// below 1 and rounded to fp16.  SPLIT: a tile has 8 rows, and its other 8 hold
-// the fp16 remainders of the first (queries and probabilities alike; the sums
-// of both are added), so that products carry 22 bits at no extra cost: for
-// fp16 and fp32 queries, and whenever 8 rows are enough.  Otherwise (bf16,
-// more than 8 rows) a tile has 16 rows whose queries and probabilities are
-// rounded to 11 bits, an eighth of the bf16 output's own rounding.
+// Operands.  Keys and values are the A operand of the mma (m16n8k16, fp16,
+// fp32 sums): S^T = K Q^T with 16 keys by 8 query rows, and O^T += V^T P^T with
+// 16 channels by 8 rows; the 8 rows are the query heads of one key/value head
+// and the request's tokens.  A code times its scale has at most 6 significant
+// bits, so keys and values are exact in fp16.  Queries are scaled by a power of
+// two a row to below 1 and rounded to fp16.  MODE says what B operands each
+// decoded A operand meets:
+//   KV4_8     8 rows, queries and probabilities rounded to 11 bits, an eighth of
+//             the output's own rounding: bf16 queries with up to 8 rows
+//   KV4_REST  8 rows, and again with the fp16 remainders of queries and of
+//             probabilities into the same sums, so that products carry 22
+//             bits: fp16 and fp32 queries
+//   KV4_16    two times 8 rows as KV4_8: bf16 queries with more
+// P leaves the first product with keys along the lane's rows and enters the
+// second with keys along its columns: two 8 x 8 transposes a block.
 //
 // Channel order.  A product over channels may take them in any order, so lane
 // (g, t) takes channels t D / 4 .. of key g: 16 contiguous code bytes (D =
 // 128), and at most two scales.
 //
-// Split.  All (request, head, tile, block) are one list, cut evenly over the
-// CTAs whatever the lengths; a CTA's warps take its blocks in turn, each with
+// Split.  All (request, head, tile, unit) are one list, cut evenly over the
+// CTAs whatever the lengths; a CTA's warps take its units in turn, each with
 // its own ring of bulk copies, and join at the end of a part.  Parts of one
 // (request, head, tile) in several CTAs go to the workspace, and the CTA that
 // arrives last joins them in order (results do not depend on who that is).
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv4AttendParams p) {
+template <int D, int MODE>
+__global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_kernel(const Kv4AttendParams p) {
     using F = Kv4<D>;
-    using SM = Kv4Smem<D>;
-    constexpr int ROWS = SPLIT ? 8 : 16;      // real rows of a tile
-    constexpr int NT = D / 8;                 // n tiles of the output
+    using SM = Kv4Smem<D, MODE>;
+    using SH = Kv4Shape<D, MODE>;
+    constexpr int KV4_WARPS = SH::WARPS, KV4_THREADS = SH::THREADS, KV4_STAGES = SH::STAGES;
+    constexpr bool SPLIT = MODE == KV4_REST;
+    constexpr int ROWS = SH::ROWS;            // rows of a tile
+    constexpr int MT = D / 16;                // m tiles of the output
+    constexpr int NB = MODE == KV4_16 ? 2 : 1;   // sets of 8 rows
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    uint8_t* ring = smem + warp * (KV4_STAGES * F::BLOCK);
+    uint8_t* ring = smem + warp * (KV4_STAGES * 2 * F::BLOCK);
     float* merge = reinterpret_cast<float*>(smem + SM::OFF_MERGE);
     __half* qbuf = reinterpret_cast<__half*>(smem + SM::OFF_Q);
     float* ml = reinterpret_cast<float*>(smem + SM::OFF_ML);          // [warp][16] m, then l
     float* rowf = reinterpret_cast<float*>(smem + SM::OFF_ROW);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::OFF_BAR) + warp * KV4_STAGES;
-    int64_t* plan = reinterpret_cast<int64_t*>(smem + SM::OFF_PLAN);  // warp sums [8], r0 and off0, -, share, its start, its length
+    int64_t* plan = reinterpret_cast<int64_t*>(smem + SM::OFF_PLAN);  // warp sums [8], first request, its offset, share, its start, its length
     int* plan_i = reinterpret_cast<int*>(plan + 8);
 
     if (lane == 0) {
@@ -459,8 +498,8 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
     bool empty = false;
     for (int r = tid * cnt; r < min(p.n, (tid + 1) * cnt); ++r) {
         const Kv4Req q = kv4_request(p, r, ROWS);
-        mine += (int64_t)q.nblk * q.tiles * p.heads;
-        empty |= q.t > 0 && q.nblk == 0;
+        mine += kv4_cost(q, p.heads);
+        empty |= q.t > 0 && q.units == 0;
         if (q.err && blockIdx.x == 0) atomicCAS(p.status, 0, q.err);
     }
     int64_t incl = mine;
@@ -478,7 +517,7 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
         if (w < warp) before += s;
         total += s;
     }
-    const int64_t per = max((int64_t)KV4_MIN_BLOCKS, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t per = max((int64_t)SH::MIN_SHARE, (total + gridDim.x - 1) / gridDim.x);
     const int64_t lo = per * blockIdx.x;
     before += incl - mine;
     if (mine > 0 && before <= lo && lo < before + mine) {
@@ -486,18 +525,18 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
         int64_t off = lo - before;
         for (;; ++r) {
             const Kv4Req q = kv4_request(p, r, ROWS);
-            const int64_t c = (int64_t)q.nblk * q.tiles * p.heads;
+            const int64_t c = kv4_cost(q, p.heads);
             if (off < c) break;
             off -= c;
         }
         plan_i[0] = r;
-        plan_i[1] = (int)off;
+        plan[9] = off;
     }
     __syncthreads();
     if (any_empty) {  // requests without a visible key: zero rows
         for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
             const Kv4Req q = kv4_request(p, r, ROWS);
-            if (q.nblk > 0) continue;
+            if (q.units > 0) continue;
             const int64_t base = (int64_t)q.tok0 * p.h_q * D;
             for (int64_t i = tid * 4; i < (int64_t)q.t * p.h_q * D; i += KV4_THREADS * 4)
                 st_elem4(p.o, base + i, p.dtype, 0.f, 0.f, 0.f, 0.f);
@@ -517,7 +556,7 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
     static_assert(sizeof(Kv4Walk) <= 80, "Kv4Smem::OFF_WALK");
     if (lane == 0) {
         put.r = plan_i[0];
-        put.off = plan_i[1];
+        put.off = plan[9];
         put.left = min(per, total - lo);
         put.q = kv4_request(p, put.r, ROWS);
         put.b0 = put.b1 = put.b = put.seg = 0;
@@ -532,56 +571,59 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
     };
 
     const int bpp = p.page_tokens >> 4;
-    int64_t* ahead = reinterpret_cast<int64_t*>(smem + SM::OFF_AHEAD) + warp * KV4_AHEAD;
-    // one register of flags: bits 0.. the slots' phase parities, 8.. slots whose page was bad, MORE
-    // to fetch, ALIVE until a wait runs out
+    // one register of flags: bits 0.. the slots' phase parities, 8.. two bits a slot, its blocks
+    // that were not fetched, MORE to fetch, ALIVE until a wait runs out
     constexpr uint32_t MORE = 1u << 16, ALIVE = 1u << 17;
     uint32_t flags = MORE | ALIVE;
+    const uint8_t* from = nullptr;      // lanes 2 i and 2 i + 1: the two blocks of the i-th unit looked up
+    uint32_t there = 0;                 // blocks that are there, from the next unit's on
+    int looked = 0;                     // units looked up and not yet fetched
 
-    // Fetches this warp's next block into a slot.
+    // Looks up the pages of this warp's next units; false behind the last.
+    auto look = [&]() {
+        while (put.b >= put.b1) {
+            if (!step(put)) return false;
+            if (lane == 0) put.b = put.b0 + warp;
+            __syncwarp();
+        }
+        const int first = put.b, mine = first + KV4_WARPS * (lane >> 1);
+        bool ok = false;
+        const int b = (put.q.first + mine) * 2 + (lane & 1);
+        if (mine < put.b1 && b * 16 < put.q.ctx + put.q.t) {     // a request's last unit may be one block
+            const int pg = b / bpp, page = __ldg(p.table + (int64_t)put.r * p.cols + pg);
+            ok = page >= 0 && page < p.num_pages;
+            if (!ok) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
+            from = p.pages + (int64_t)page * p.page_stride + ((int64_t)(put.seg / put.q.tiles) * bpp + (b - pg * bpp)) * F::BLOCK;
+        }
+        there = __ballot_sync(0xffffffffu, ok);
+        looked = min(KV4_AHEAD, (put.b1 - first + KV4_WARPS - 1) / KV4_WARPS);
+        // the next unit's lanes are 0 and 1 until fetch() turns the lanes
+        __syncwarp();
+        if (lane == 0) put.b = first + KV4_WARPS * looked;
+        __syncwarp();
+        return true;
+    };
+    int turn = 0;                       // lane of the next unit's first block
+    // Fetches this warp's next unit into a slot.
     auto fetch = [&](uint32_t slot) {
         if (!(flags & MORE)) return;
-        while (put.b >= put.b1) {
-            if (!step(put)) {
+        if (looked == 0) {
+            turn = 0;
+            if (!look()) {
                 flags &= ~MORE;
                 return;
             }
-            if (lane == 0) {
-                put.b = put.b0 + warp;
-                put.used = KV4_AHEAD;
-            }
-            __syncwarp();
         }
-        if (put.used == KV4_AHEAD) {
-            const int mine = put.b + KV4_WARPS * lane;
-            if (lane < KV4_AHEAD && mine < put.b1) {
-                const int b = put.q.first + mine, pg = b / bpp;
-                const int page = __ldg(p.table + (int64_t)put.r * p.cols + pg);
-                ahead[lane] = page < 0 || page >= p.num_pages
-                                  ? -1
-                                  : (int64_t)page * p.page_stride + ((int64_t)(put.seg / put.q.tiles) * bpp + (b - pg * bpp)) * F::BLOCK;
-            }
-            __syncwarp();
-            if (lane == 0) put.used = 0;
-            __syncwarp();
+        const uint32_t two = there & 3u;
+        flags = (flags & ~(3u << (8 + 2 * slot))) | (two ^ 3u) << (8 + 2 * slot);
+        const int mine = lane - turn;
+        if ((mine & ~1) == 0) {         // the copies may complete before they are expected: the phase waits for the arrival
+            if (mine == 0 && two != 0) mbar_arrive_expect_tx(bars + slot, two == 3u ? 2 * F::BLOCK : F::BLOCK);
+            if (two >> mine & 1u) bulk_load(ring + (2 * slot + mine) * F::BLOCK, from, F::BLOCK, bars + slot);
         }
-        const int64_t off = ahead[put.used];
-        __syncwarp();
-        if (lane == 0) {
-            ++put.used;
-            put.b += KV4_WARPS;
-        }
-        if (off < 0) {
-            flags |= 256u << slot;
-            if (lane == 0) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
-        } else {
-            flags &= ~(256u << slot);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bars + slot, F::BLOCK);
-                bulk_load(ring + slot * F::BLOCK, p.pages + off, F::BLOCK, bars + slot);
-            }
-        }
-        __syncwarp();
+        there >>= 2;
+        turn += 2;
+        --looked;
     };
 #pragma unroll 1
     for (int s = 0; s < KV4_STAGES; ++s) fetch(s);
@@ -601,7 +643,7 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
         for (int i = warp; i < ROWS; i += KV4_WARPS) {
             constexpr int E = D / 32;
             float x[E];
-            float factor = 0.f;
+            float factor = 1.f;   // of a row of zeros (not 0: a masked score times it stays -infinity)
             const int j = (i0 + i) / p.grp;
             const int pos = get.q.ctx + j;
 #pragma unroll
@@ -629,8 +671,8 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
                 for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 // 2^-k with amax 2^-k in [1/2, 1); the factor below 2^-100 and the infinite stay as they are
                 const int k = amax > 1e-30f && amax < 3e38f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
-                factor = p.scale_log2 * exp2f((float)k);
-                const float down = exp2f((float)-k);
+                factor = fmaxf(1e-30f, fabsf(p.scale_log2) * exp2f((float)k));
+                const float down = p.scale_log2 < 0.f ? -exp2f((float)-k) : exp2f((float)-k);   // the factor itself is not negative
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] *= down;
             }
@@ -649,36 +691,38 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
         }
         }
         __syncthreads();
-        // query fragments: eight channels of row g and of row g + 8, two k steps, a piece.  D = 64
-        // keeps them in registers; D = 128 reads them again for each block (32 registers more would spill)
-        const uint4* qa = reinterpret_cast<const uint4*>(qbuf + g * SM::QPITCH) + t;
-        const uint4* qb = qa + 8 * SM::QPITCH / 8;
-        constexpr bool QREG = D == 64;
-        uint4 qra[QREG ? D / 32 : 1], qrb[QREG ? D / 32 : 1];
-        if constexpr (QREG) {
+        // query fragments of row g and of row g + 8: eight channels, two k steps, a piece
+        uint4 qa[D / 32], qb[MODE == KV4_8 ? 1 : D / 32];
+        {
+            const uint4* qr = reinterpret_cast<const uint4*>(qbuf + g * SM::QPITCH) + t;
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                qra[w] = qa[w * 4];
-                qrb[w] = qb[w * 4];
+            for (int w = 0; w < D / 32; ++w) qa[w] = qr[w * 4];
+            if constexpr (MODE != KV4_8) {
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) qb[w] = qr[8 * SM::QPITCH / 8 + w * 4];
             }
         }
-        constexpr int NR = SPLIT ? 1 : 2;     // real rows a lane holds
-        float m[NR], l[NR];
+        // this lane's rows: 8 n + 2 t and the next, index 2 n + e
+        float m[2 * NB], l[2 * NB];
 #pragma unroll
-        for (int a = 0; a < NR; ++a) {
-            m[a] = -INFINITY;
+        for (int a = 0; a < 2 * NB; ++a) {
+            m[a] = -FLT_MAX;    // finite: nothing below is infinity minus infinity
             l[a] = 0.f;
         }
-        // blocks that every row of the tile sees whole: [see0, see1)
-        const int see1 = (row_pos(0) + 1) >> 4;
-        const int see0 = p.window > 0 ? (max(0, last_row_pos() - p.window + 1) + 15) >> 4 : 0;
-        float acc[NT][4];
+        auto row_of = [&](int a) { return 8 * (a >> 1) + 2 * t + (a & 1); };
+        // units that every row of the tile sees whole: [see0, see1)
+        const int see1 = (row_pos(0) + 1) / KV4_KEYS;
+        const int see0 = p.window > 0 ? (max(0, last_row_pos() - p.window + 1) + KV4_KEYS - 1) / KV4_KEYS : 0;
+        // sums of channels g D / 8 + 2 i (elements 0, 1: the lane's rows) and the next (2, 3)
+        float acc[NB][MT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.f;
 
 #pragma unroll 1
-        for (int b = get.b0 + warp; b < get.b1; b += KV4_WARPS) {
-            bool use = (flags & ALIVE) && !(flags & 256u << slot);
+        for (int unit = get.q.first + get.b0 + warp, end = get.q.first + get.b1; unit < end; unit += KV4_WARPS) {
+            bool use = (flags & ALIVE) && (flags >> (8 + 2 * slot) & 3u) != 3u;
             if (use) {
                 use = mbar_wait(bars + slot, flags >> slot & 1u);
                 if (use) {
@@ -689,170 +733,174 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
                 }
             }
             if (use) {
-                const uint8_t* B = ring + slot * F::BLOCK;
-                float s[2][4];
-                // ---- scores of keys g (n tile 0) and g + 8 (n tile 1) ----
-                uint32_t code[2][D / 32], sc[2][2];
+                const uint8_t* B = ring + slot * (2 * F::BLOCK);
+                // ---- scores: s[blk][n][..] of keys 16 blk + g (0, 1) and g + 8 (2, 3) with the lane's rows ----
+                float s[2][NB][4];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-                    const int key = nt * 8 + g;
-                    if constexpr (D == 128) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(B + F::KC + key * 64 + t * 16);
-                        code[nt][0] = w.x; code[nt][1] = w.y; code[nt][2] = w.z; code[nt][3] = w.w;
-                        const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(B + F::KS + key * 8 + 2 * t));
-                        sc[nt][0] = __byte_perm(two, two, 0x1010);
-                        sc[nt][1] = __byte_perm(two, two, 0x3232);
-                    } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(B + F::KC + key * 32 + t * 8);
-                        code[nt][0] = w.x; code[nt][1] = w.y;
-                        const uint32_t two = cvt_e4m3x2_f16x2(B[F::KS + key * 4 + t]);
-                        sc[nt][0] = sc[nt][1] = __byte_perm(two, two, 0x1010);
+                for (int blk = 0; blk < 2; ++blk) {
+                    const uint8_t* K = B + blk * F::BLOCK;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) s[blk][n][0] = s[blk][n][1] = s[blk][n][2] = s[blk][n][3] = 0.f;
+                    uint32_t code[2][D / 32], sc[2][2];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int key = hf * 8 + g;
+                        if constexpr (D == 128) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(K + F::KC + key * 64 + t * 16);
+                            code[hf][0] = w.x; code[hf][1] = w.y; code[hf][2] = w.z; code[hf][3] = w.w;
+                            const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(K + F::KS + key * 8 + 2 * t));
+                            sc[hf][0] = __byte_perm(two, two, 0x1010);
+                            sc[hf][1] = __byte_perm(two, two, 0x3232);
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2*>(K + F::KC + key * 32 + t * 8);
+                            code[hf][0] = w.x; code[hf][1] = w.y;
+                            const uint32_t two = cvt_e4m3x2_f16x2(K[F::KS + key * 4 + t]);
+                            sc[hf][0] = sc[hf][1] = __byte_perm(two, two, 0x1010);
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) {
+                        uint32_t k0[4], k1[4];
+                        cvt_e2m1x8_f16(code[0][w], k0);
+                        cvt_e2m1x8_f16(code[1][w], k1);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            k0[e] = hmul2_u32(k0[e], sc[0][w / 2]);
+                            k1[e] = hmul2_u32(k1[e], sc[1][w / 2]);
+                        }
+                        kv4_mma(s[blk][0], k0[0], k1[0], k0[1], k1[1], qa[w].x, qa[w].y);
+                        if constexpr (MODE != KV4_8) kv4_mma(s[blk][NB - 1], k0[0], k1[0], k0[1], k1[1], qb[w].x, qb[w].y);
+                        kv4_mma(s[blk][0], k0[2], k1[2], k0[3], k1[3], qa[w].z, qa[w].w);
+                        if constexpr (MODE != KV4_8) kv4_mma(s[blk][NB - 1], k0[2], k1[2], k0[3], k1[3], qb[w].z, qb[w].w);
                     }
                 }
+                // ---- running softmax ----
+                const uint32_t miss = flags >> (8 + 2 * slot) & 3u;
+                const bool masked = unit < see0 || unit >= see1 || miss != 0;
+                if (masked) {
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    const uint4 a = QREG ? qra[w % (QREG ? D / 32 : 1)] : qa[w * 4], b2 = QREG ? qrb[w % (QREG ? D / 32 : 1)] : qb[w * 4];
+                    for (int a = 0; a < 2 * NB; ++a) {
+                        const int pos = row_pos(row_of(a));
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        uint32_t k[4];
-                        cvt_e2m1x8_f16(code[nt][w], k);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) k[e] = hmul2_u32(k[e], sc[nt][w / 2]);
-                        kv4_mma(s[nt], a.x, b2.x, a.y, b2.y, k[0], k[1]);
-                        kv4_mma(s[nt], a.z, b2.z, a.w, b2.w, k[2], k[3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = unit * KV4_KEYS + i * 8 + g;
+                            if (key > pos || (p.window > 0 && key <= pos - p.window) || (miss >> (i >> 1) & 1u))
+                                s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
+                        }
                     }
                 }
-                // ---- running softmax; column of s[nt][e]: key nt * 8 + 2 t + (e & 1) ----
-                const int blk = get.q.first + b;
-                const bool masked = blk < see0 || blk >= see1;
-                float x[NR][4];
-                uint32_t pf[4];
+                float top[2 * NB];
                 bool grow = false;
-                float top[NR];
 #pragma unroll
-                for (int a = 0; a < NR; ++a) {
-                    const float c = rowf[g + 8 * a];
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            x[a][nt * 2 + e] = (SPLIT ? s[nt][e] + s[nt][2 + e] : s[nt][2 * a + e]) * c;
-                    if (masked) {
-                        const int pos = row_pos(g + 8 * a);
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = blk * 16 + nt * 8 + 2 * t + e;
-                                if (key > pos || (p.window > 0 && key <= pos - p.window)) x[a][nt * 2 + e] = -INFINITY;
-                            }
-                    }
-                    top[a] = fmaxf(fmaxf(x[a][0], x[a][1]), fmaxf(x[a][2], x[a][3]));
-                    top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 1));
-                    top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 2));
+                for (int a = 0; a < 2 * NB; ++a) {
+                    const int n = a >> 1, e = a & 1;
+                    top[a] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e])) * rowf[row_of(a)];
                     grow |= top[a] > m[a] + KV4_SLACK;
                 }
+                // rarely: a score above the running maximum by more than its slack
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                    for (int a = 0; a < NR; ++a) {
+                    for (int a = 0; a < 2 * NB; ++a) {
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], o));
                         if (top[a] > m[a]) {
                             const float f = ex2f(m[a] - top[a]);
                             m[a] = top[a];
                             l[a] *= f;
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                acc[j][2 * a] *= f;
-                                acc[j][2 * a + 1] *= f;
-                                if constexpr (SPLIT) { acc[j][2] *= f; acc[j][3] *= f; }
+                            for (int j = 0; j < MT; ++j) {
+                                acc[a >> 1][j][a & 1] *= f;
+                                acc[a >> 1][j][2 + (a & 1)] *= f;
                             }
                         }
                     }
                 }
+                uint32_t pf[2][NB][2], pr[SPLIT ? 2 : 1][2];   // B fragments of the probabilities, of their remainders
 #pragma unroll
-                for (int a = 0; a < NR; ++a) {
-                    const float mu = m[a] == -INFINITY ? 0.f : m[a];
+                for (int n = 0; n < NB; ++n) {
+                    const float c0 = rowf[row_of(2 * n)], c1 = rowf[row_of(2 * n + 1)];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[a][e] = ex2f(x[a][e] - mu);
-                    l[a] += (x[a][0] + x[a][1]) + (x[a][2] + x[a][3]);
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const __half2 hi = __floats2half2_rn(x[a][2 * nt], x[a][2 * nt + 1]);
-                        pf[2 * nt + a] = *reinterpret_cast<const uint32_t*>(&hi);
+                    for (int i = 0; i < 4; ++i) {
+                        const float x0 = ex2f(fmaf(s[i >> 1][n][2 * (i & 1)], c0, -m[2 * n]));
+                        const float x1 = ex2f(fmaf(s[i >> 1][n][2 * (i & 1) + 1], c1, -m[2 * n + 1]));
+                        l[2 * n] += x0;
+                        l[2 * n + 1] += x1;
+                        const __half2 hi = __floats2half2_rn(x0, x1);
+                        pf[i >> 1][n][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&hi));
                         if constexpr (SPLIT) {
                             const float2 f = __half22float2(hi);
-                            const __half2 lo2 = __floats2half2_rn(x[a][2 * nt] - f.x, x[a][2 * nt + 1] - f.y);
-                            pf[2 * nt + 1] = *reinterpret_cast<const uint32_t*>(&lo2);
+                            const __half2 rest = __floats2half2_rn(x0 - f.x, x1 - f.y);
+                            pr[i >> 1][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&rest));
                         }
                     }
                 }
                 // ---- values ----
-                uint32_t vs4;
-                if constexpr (D == 128) vs4 = *reinterpret_cast<const uint32_t*>(B + F::VS + lane * 4);
-                else vs4 = *reinterpret_cast<const uint32_t*>(B + F::VS + ((g >> 1) * 4 + t) * 4);
-                if (masked) {
-                    // A token that some row does not see may hold anything, and 0 * NaN is NaN:
-                    // scales behind the end become 0, and so do NaN ones, whose channels of the
-                    // rows that do see them are then set by hand (a rare path).
-                    bool nan = false;
-                    const int last_pos = last_row_pos();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = blk * 16 + (e >> 1) * 8 + 2 * t + (e & 1);
-                        const bool bad = (vs4 >> (8 * e) & 0x7fu) == 0x7fu;
-                        if (key > last_pos || bad) vs4 &= ~(0xffu << (8 * e));
-                        nan |= bad && key <= last_pos;
-                    }
-                    if (__any_sync(0xffffffffu, nan)) {
-                        uint32_t hit = 0;
-#pragma unroll 1
-                        for (int i = 0; i < 32; ++i) {
-                            const int w = i >> 1, key = blk * 16 + w;
-                            if ((B[kv4_v_scale<D>(w, (2 * t + (i & 1)) * (D / 8) / 16)] & 0x7f) != 0x7f) continue;
+                for (int blk = 0; blk < 2; ++blk) {
+                    const uint8_t* W = B + blk * F::BLOCK;
+                    const int grp = g * (D / 8) / 16;       // the lane's channels are of one scale group
+                    uint32_t vs4 = *reinterpret_cast<const uint32_t*>(W + F::VS + (grp * 4 + t) * 4);
+                    if (masked) {
+                        // A token that some row does not see may hold anything, and 0 * NaN is NaN:
+                        // scales behind the end become 0, and so do NaN ones, whose channels of the
+                        // rows that do see them are then set by hand (a rare path).
+                        const int key0 = unit * KV4_KEYS + blk * 16, to = (miss >> blk & 1u) ? -1 : last_row_pos();
+                        bool nan = false;
 #pragma unroll
-                            for (int a = 0; a < NR; ++a) {
-                                const int pos = row_pos(g + 8 * a);
-                                if (key <= pos && (p.window <= 0 || key > pos - p.window)) hit |= 1u << (2 * a + (i & 1));
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + (e >> 1) * 8 + 2 * t + (e & 1);
+                            const bool bad = (vs4 >> (8 * e) & 0x7fu) == 0x7fu;
+                            if (key > to || bad) vs4 &= ~(0xffu << (8 * e));
+                            nan |= bad && key <= to;
                         }
+                        if (__any_sync(0xffffffffu, nan)) {
+                            uint32_t hit = 0;
+#pragma unroll 1
+                            for (int w = 0; w < 16; ++w) {
+                                if ((W[kv4_v_scale<D>(w, grp)] & 0x7f) != 0x7f || key0 + w > to) continue;
 #pragma unroll
-                        for (int a = 0; a < 2 * NR; ++a)
-                            if (hit >> a & 1u)
+                                for (int a = 0; a < 2 * NB; ++a) {
+                                    const int pos = row_pos(row_of(a));
+                                    if (key0 + w <= pos && (p.window <= 0 || key0 + w > pos - p.window)) hit |= 1u << a;
+                                }
+                            }
 #pragma unroll
-                                for (int j = 0; j < NT; ++j) acc[j][a] = NAN;
+                            for (int a = 0; a < 2 * NB; ++a)
+                                if (hit >> a & 1u)
+#pragma unroll
+                                    for (int j = 0; j < MT; ++j) acc[a >> 1][j][a & 1] = acc[a >> 1][j][2 + (a & 1)] = NAN;
+                        }
                     }
-                }
-                const uint32_t sv[2] = {cvt_e4m3x2_f16x2(vs4 & 0xffffu), cvt_e4m3x2_f16x2(vs4 >> 16)};
-                uint32_t vc[2][2][D / 64];          // [half][token of the pair][word]
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint8_t* V = B + F::VC + hf * (64 * F::CB) + lane * (2 * F::CB);
-                    if constexpr (D == 128) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(V);
-                        vc[hf][0][0] = w.x; vc[hf][0][1] = w.y; vc[hf][1][0] = w.z; vc[hf][1][1] = w.w;
-                    } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(V);
-                        vc[hf][0][0] = w.x; vc[hf][1][0] = w.y;
-                    }
-                }
-#pragma unroll
-                for (int w = 0; w < D / 64; ++w) {
-                    uint32_t even[2], odd[2];   // codes of tokens 2t (low nibbles) and 2t + 1 by even and odd channels
+                    const uint32_t sv[2] = {cvt_e4m3x2_f16x2(vs4 & 0xffffu), cvt_e4m3x2_f16x2(vs4 >> 16)};
+                    uint32_t vc[2][2][D / 64];          // [half][token of the pair][word]
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const uint32_t A = vc[hf][0][w], C = vc[hf][1][w];
-                        even[hf] = (A & 0x0f0f0f0fu) | (C << 4 & 0xf0f0f0f0u);
-                        odd[hf] = (A >> 4 & 0x0f0f0f0fu) | (C & 0xf0f0f0f0u);
+                        const uint8_t* V = W + F::VC + hf * (64 * F::CB) + lane * (2 * F::CB);
+                        if constexpr (D == 128) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(V);
+                            vc[hf][0][0] = w.x; vc[hf][0][1] = w.y; vc[hf][1][0] = w.z; vc[hf][1][1] = w.w;
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2*>(V);
+                            vc[hf][0][0] = w.x; vc[hf][1][0] = w.y;
+                        }
                     }
 #pragma unroll
-                    for (int par = 0; par < 2; ++par) {
-                        uint32_t v0[4], v1[4];
-                        cvt_e2m1x8_f16(par ? odd[0] : even[0], v0);
-                        cvt_e2m1x8_f16(par ? odd[1] : even[1], v1);
+                    for (int w = 0; w < D / 64; ++w) {
+                        uint32_t ev[2][4], od[2][4];   // pairs (token 2t, token 2t + 1) of the even and of the odd channels
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            kv4_mma(acc[8 * w + 2 * e + par], pf[0], pf[1], pf[2], pf[3],
-                                    hmul2_u32(v0[e], sv[0]), hmul2_u32(v1[e], sv[1]));
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const uint32_t A = vc[hf][0][w], C = vc[hf][1][w];
+                            cvt_e2m1x8_f16((A & 0x0f0f0f0fu) | (C << 4 & 0xf0f0f0f0u), ev[hf]);
+                            cvt_e2m1x8_f16((A >> 4 & 0x0f0f0f0fu) | (C & 0xf0f0f0f0u), od[hf]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t a0 = hmul2_u32(ev[0][e], sv[0]), a1 = hmul2_u32(od[0][e], sv[0]);
+                            const uint32_t a2 = hmul2_u32(ev[1][e], sv[1]), a3 = hmul2_u32(od[1][e], sv[1]);
+#pragma unroll
+                            for (int n = 0; n < NB; ++n) kv4_mma(acc[n][4 * w + e], a0, a1, a2, a3, pf[blk][n][0], pf[blk][n][1]);
+                            if constexpr (SPLIT) kv4_mma(acc[0][4 * w + e], a0, a1, a2, a3, pr[blk][0], pr[blk][1]);
+                        }
                     }
                 }
             }
@@ -862,16 +910,17 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
         }
 
         // ---- the warps' sums of this part, joined in warp order ----
+        __syncwarp();
         const int h = get.seg / get.q.tiles, i0 = first_row(), live = min(ROWS, get.q.t * p.grp - i0);
-        const bool whole = get.b0 == 0 && get.b1 == get.q.nblk;
-        float* part = p.partials + (int64_t)(2 * blockIdx.x + (get.b0 == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
+        const bool whole = get.b0 == 0 && get.b1 == get.q.units;
+        float* part = p.partials + (2 * blockIdx.x + (get.b0 == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
 #pragma unroll
-        for (int a = 0; a < NR; ++a) {
-            l[a] += __shfl_xor_sync(0xffffffffu, l[a], 1);
-            l[a] += __shfl_xor_sync(0xffffffffu, l[a], 2);
-            if (t == 0) {
-                ml[(warp * KV4_ROWS + g + 8 * a) * 2] = m[a];
-                ml[(warp * KV4_ROWS + g + 8 * a) * 2 + 1] = l[a];
+        for (int a = 0; a < 2 * NB; ++a) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[a] += __shfl_xor_sync(0xffffffffu, l[a], o);
+            if (g == 0) {
+                ml[(warp * KV4_ROWS + row_of(a)) * 2] = m[a];
+                ml[(warp * KV4_ROWS + row_of(a)) * 2 + 1] = l[a];
             }
         }
         auto join = [&](int row, int d, float4 o, float M, float L) {
@@ -883,42 +932,35 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
         };
         constexpr int CH = D / 4;             // 16-byte pieces of a row
 #pragma unroll
-        for (int a = 0; a < NR; ++a) {
+        for (int a = 0; a < NB; ++a) {
             if (8 * a < live) {
                 if (a > 0) __syncthreads();
-                if (g + 8 * a < live) {
-                    float* row = merge + (warp * 8 + g) * D;
+                // a row's 16-byte pieces, each at its place xor (row / 2) % 4: eight lanes' stores fall on
+                // different banks
+                const int tid3 = tid_again(), g3 = (tid3 & 31) >> 2, t3 = tid3 & 3;
 #pragma unroll
-                    for (int k = 0; k < CH / 4; ++k) {
-                        // this lane's channels t D / 4 + 4 k ..: column 2t of n tiles 4k .., then column 2t + 1
-                        const int col = k >= CH / 8, j = (k % (CH / 8)) * 4;
-                        float4 o;
-                        o.x = SPLIT ? acc[j][col] + acc[j][2 + col] : acc[j][2 * a + col];
-                        o.y = SPLIT ? acc[j + 1][col] + acc[j + 1][2 + col] : acc[j + 1][2 * a + col];
-                        o.z = SPLIT ? acc[j + 2][col] + acc[j + 2][2 + col] : acc[j + 2][2 * a + col];
-                        o.w = SPLIT ? acc[j + 3][col] + acc[j + 3][2 + col] : acc[j + 3][2 * a + col];
-                        const int chunk = (t * (CH / 4) + k) ^ ((t * 2 + (g & 1)) & 7);
-                        *reinterpret_cast<float4*>(row + chunk * 4) = o;
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    float* row = merge + ((tid3 >> 5) * 8 + 2 * t3 + e) * D;
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k)
+                        *reinterpret_cast<float4*>(row + ((g3 * (D / 32) + k) ^ t3) * 4) =
+                            make_float4(acc[a][2 * k][e], acc[a][2 * k][2 + e], acc[a][2 * k + 1][e], acc[a][2 * k + 1][2 + e]);
                 }
                 __syncthreads();
-                const int tid2 = tid_again(), row = tid2 / CH, ch = tid2 % CH;
-                if (row < 8 && row + 8 * a < live) {
-                    const int sw = ch ^ ((ch / (CH / 4) * 2 + (row & 1)) & 7);
-                    float M = -INFINITY, L = 0.f;
+                const int tid2 = tid_again(), ch = tid2 % CH;
+                for (int row = tid2 / CH; row < min(8, live - 8 * a); row += KV4_THREADS / CH) {
+                    const int sw = ch ^ (row >> 1 & 3);
+                    float M = -FLT_MAX, L = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < KV4_WARPS; ++w) M = fmaxf(M, ml[(w * KV4_ROWS + row + 8 * a) * 2]);
 #pragma unroll 2
                     for (int w = 0; w < KV4_WARPS; ++w) {
                         const float mw = ml[(w * KV4_ROWS + row + 8 * a) * 2], lw = ml[(w * KV4_ROWS + row + 8 * a) * 2 + 1];
-                        // no key seen: nothing to add (a NaN sum stays one)
-                        const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : ex2f(mw - M);
-                        if (f != 0.f) {
-                            const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * D + sw * 4);
-                            L += f * lw;
-                            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
-                        }
+                        const float f = ex2f(mw - M);   // a warp that saw no key: sums of 0 (a NaN stays one)
+                        const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * D + sw * 4);
+                        L += f * lw;
+                        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
                     }
                     if (whole) {
                         join(row + 8 * a, ch * 4, o, M, L);
@@ -931,8 +973,8 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
         }
         if (!whole) {
             // CTAs that share this (request, head, tile), from its place in the list
-            const int64_t seg0 = plan[11] + plan[12] - get.left - get.b1, share = plan[10];
-            const int c0 = (int)(seg0 / share), c1 = (int)((seg0 + get.q.nblk - 1) / share);
+            const int64_t first = plan[11] + plan[12] - get.left - get.b1, share = plan[10];   // unit of block 0
+            const int c0 = (int)(first / share), c1 = (int)((first + get.q.units - 1) / share);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -943,27 +985,43 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
             }
             __syncthreads();
             if (plan_i[0]) {
-                const int tid2 = tid_again(), ch = tid2 % CH;
-                for (int row = tid2 / CH; row < live; row += KV4_THREADS / CH) {
-                    auto slot = [&](int cta) {
-                        return p.partials + (int64_t)(2 * cta + (cta == c0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
-                    };
-                    float M = -INFINITY, L = 0.f;
+                // every part's maximum and sum of each row, weights from them, then the rows in
+                // NGRP groups of parts at a time; merge holds the groups' sums, ring is not free
+                const int tid2 = tid_again(), np = c1 - c0 + 1, cta0 = 2 * c0 + tid_again() - tid2;
+                auto slot = [&](int k) {
+                    return p.partials + (cta0 + 2 * k + (k == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
+                };
+                constexpr int NGRP = KV4_THREADS / CH;   // thread groups, each a whole row wide
+                const int ch = tid2 % CH, grp = tid2 / CH;
+#pragma unroll 1
+                for (int row = 0; row < live; ++row) {
+                    float M = -FLT_MAX;
+                    for (int k = tid2 & 31; k < np; k += 32) M = fmaxf(M, __ldcg(slot(k) + KV4_ROWS * D + 2 * row));
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
+                    float L = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-                    for (int k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + KV4_ROWS * D + 2 * row));
-#pragma unroll 4
-                    for (int k = c0; k <= c1; ++k) {
+                    for (int k = grp; k < np; k += NGRP) {
                         const float* s = slot(k);
                         const float2 x = __ldcg(reinterpret_cast<const float2*>(s + KV4_ROWS * D) + row);
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D + ch * 4));
-                        const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2f(x.x - M);
-                        if (f != 0.f) {
-                            L += f * x.y;
-                            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
-                        }
+                        const float f = ex2f(x.x - M);
+                        L += f * x.y;
+                        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
                     }
-                    join(row, ch * 4, o, M, L);
+                    __syncthreads();
+                    reinterpret_cast<float4*>(merge)[tid2] = o;
+                    if (ch == 0) ml[grp] = L;
+                    __syncthreads();
+                    if (tid2 < CH) {
+                        for (int k = 1; k < min(NGRP, np); ++k) {
+                            const float4 v = reinterpret_cast<const float4*>(merge)[k * CH + tid2];
+                            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                            L += ml[k];
+                        }
+                        join(row, ch * 4, o, M, L);
+                    }
                 }
             }
         }
@@ -971,7 +1029,7 @@ __global__ void __launch_bounds__(KV4_THREADS, 2) kda_kv4_attend_kernel(const Kv
     // after a wait that ran out: the copies still in flight end (or time out) before the CTA does
     if (!(flags & ALIVE)) {
         for (int s = 0; s < KV4_STAGES; ++s)
-            if (!(flags & 256u << s)) (void)mbar_wait(bars + s, flags >> s & 1u);
+            if ((flags >> (8 + 2 * s) & 3u) != 3u) (void)mbar_wait(bars + s, flags >> s & 1u);
     }
 }
 

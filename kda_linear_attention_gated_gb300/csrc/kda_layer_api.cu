@@ -52,19 +52,19 @@ int check_common_pointers(const kda_kv4_cache* c, const Common& g, const int32_t
     return KDA_OK;
 }
 
-template <int D, bool SPLIT>
+template <int D, int MODE>
 int launch_attend(kda::Kv4AttendParams& prm, int64_t list, uint32_t flags, cudaStream_t stream) {
-    auto kernel = kda::kda_kv4_attend_kernel<D, SPLIT>;
+    auto kernel = kda::kda_kv4_attend_kernel<D, MODE>;
     int occ = 0, sms = 0;
-    const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::KV4_THREADS, kda::Kv4Smem<D>::BYTES, &occ, &sms);
+    const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::Kv4Shape<D, MODE>::THREADS, kda::Kv4Smem<D, MODE>::BYTES, &occ, &sms);
     if (rc != KDA_OK) return rc;
-    // every CTA resident, and none without a block for each of its warps
+    // every CTA resident, and none without a unit for each of its warps
     int64_t grid = std::min<int64_t>((int64_t)occ * sms, kda::KV4_MAX_CTAS);
-    grid = std::max<int64_t>(1, std::min(grid, (list + kda::KV4_MIN_BLOCKS - 1) / kda::KV4_MIN_BLOCKS));
+    grid = std::max<int64_t>(1, std::min(grid, list / kda::Kv4Shape<D, MODE>::WARPS + 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3(kda::KV4_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = kda::Kv4Smem<D>::BYTES;
+    cfg.blockDim = dim3(kda::Kv4Shape<D, MODE>::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = kda::Kv4Smem<D, MODE>::BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     set_pdl(cfg, &attr, flags);
@@ -200,12 +200,12 @@ int kda_kv4_attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, 
     if (g.h_q < 1 || g.h_q % cache->heads != 0 || g.max_t > KDA_KV4_MAX_TOKENS || g.q_stride < (int64_t)g.h_q * cache->dim)
         return KDA_ERR_SHAPE;
     const int grp = g.h_q / cache->heads;
-    // rows of a tile: 8 with remainders, unless bf16 queries have more (kda_kv4.cuh)
-    const bool split = g.dtype != KDA_BF16 || (int64_t)g.max_t * grp <= 8;
-    const int rows = split ? 8 : 16;
-    const int64_t blocks = ((int64_t)g.table_cols * cache->page_tokens + 15) / 16;
+    // rows of a tile and their rounding (kda_kv4.cuh)
+    const int mode = g.dtype != KDA_BF16 ? kda::KV4_REST : (int64_t)g.max_t * grp <= 8 ? kda::KV4_8 : kda::KV4_16;
+    const int rows = mode == kda::KV4_16 ? 16 : 8;
+    const int64_t units = ((int64_t)g.table_cols * cache->page_tokens + kda::KV4_KEYS - 1) / kda::KV4_KEYS;
     const int64_t tiles = ((int64_t)g.max_t * grp + rows - 1) / rows;
-    if (blocks * tiles * cache->heads > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if (tiles * cache->heads > 0x7fffffffLL) return KDA_ERR_SHAPE;
     if (g.n == 0 || g.total == 0 || g.max_t == 0) return KDA_OK;
     rc = check_common_pointers(cache, c, dev_status);
     if (rc != KDA_OK) return rc;
@@ -244,11 +244,16 @@ int kda_kv4_attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, 
     prm.partials = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + kda::KV4_MAX_CTAS * sizeof(int32_t));
     prm.status = dev_status;
     static_assert(kda::KV4_MAX_CTAS * (4 + 2 * kda::KV4_ROWS * (128 + 2) * 4) <= KDA_KV4_WORKSPACE_BYTES, "workspace");
-    const int64_t list = std::min<int64_t>(blocks * tiles * cache->heads * g.n, 1LL << 40);
+    const int64_t list = units * std::min<int64_t>(tiles * cache->heads * g.n, 1 << 20);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    using namespace kda;
     if (cache->dim == 128)
-        return split ? launch_attend<128, true>(prm, list, flags, st) : launch_attend<128, false>(prm, list, flags, st);
-    return split ? launch_attend<64, true>(prm, list, flags, st) : launch_attend<64, false>(prm, list, flags, st);
+        return mode == KV4_8 ? launch_attend<128, KV4_8>(prm, list, flags, st)
+               : mode == KV4_16 ? launch_attend<128, KV4_16>(prm, list, flags, st)
+                                : launch_attend<128, KV4_REST>(prm, list, flags, st);
+    return mode == KV4_8 ? launch_attend<64, KV4_8>(prm, list, flags, st)
+           : mode == KV4_16 ? launch_attend<64, KV4_16>(prm, list, flags, st)
+                            : launch_attend<64, KV4_REST>(prm, list, flags, st);
 }
 
 int kda_head_norm(const kda_head_norm_args* args, uint32_t flags, void* stream) {

@@ -269,7 +269,7 @@ def run_attend(lib, heads, grp, dim, page, ctx, lens, dtype, rot, inter, window=
     assert status.item() == 0
     assert not ws[:2048].any(), "the workspace's counters are not back at zero"
     want, err, big, top = ref.attend(cache, ctx, lens, q, cos, sin, inter, window, scale, ks, vs)
-    split = dtype != BF16 or max(lens) * grp <= 8
+    split = dtype != BF16      # bf16 queries and probabilities are rounded to 11 bits, others keep remainders
     got = o.cpu().double()
     lim = ref.attend_tolerance(want, err, big, top, dtype, split)
     assert torch.equal(got.isnan(), want.isnan())
