@@ -707,11 +707,11 @@ typedef struct kda_kv4_attend_args {
     int32_t window;             /* 0: every earlier key */
     float scale;                /* 0: 1 / sqrt(dim) */
     int32_t reserved;           /* 0 */
-    int64_t q_stride;           /* elements from one token to the next, >= h_q * dim */
+    int64_t q_stride;           /* elements from one token to the next, >= h_q * dim, a multiple of 16 bytes */
     const int32_t* cu_seqlens;  /* [n + 1] or NULL */
     const int32_t* page_table;  /* [n][table_cols] */
     const int32_t* ctx_len;     /* [n]: tokens in the cache before this step's */
-    const void* q;              /* [total] rows of [h_q][dim] */
+    const void* q;              /* [total] rows of [h_q][dim], 16-byte aligned */
     const float* cos;           /* [rope_rows][rot_dim / 2] or NULL with rot_dim 0 */
     const float* sin;
     void* o;                    /* [total][h_q][dim], 16-byte aligned (output) */

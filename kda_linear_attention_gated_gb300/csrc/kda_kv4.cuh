@@ -38,11 +38,40 @@ template <int D> __device__ __forceinline__ int kv4_v_scale(int w, int grp) {
     return Kv4<D>::VS + (grp * 4 + ((w & 7) >> 1)) * 4 + (w >> 3) * 2 + (w & 1);
 }
 
-// Element loads from a typed buffer (kda_dtype codes 0 fp32, 1 fp16, 2 bf16).
-__device__ __forceinline__ float ld_elem(const void* p, int64_t i, int dtype) {
-    if (dtype == 0) return static_cast<const float*>(p)[i];
-    if (dtype == 1) return __half2float(static_cast<const __half*>(p)[i]);
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+// Typed buffers are kda_dtype codes: 0 fp32, 1 fp16, 2 bf16.
+// N (1, 2 or 4) neighbouring elements from a multiple of N of a 16-byte aligned buffer.
+template <int N, int M> __device__ __forceinline__ void ld_elems(const void* p, int64_t i, int dtype, float (&x)[M]) {
+    static_assert(N <= M && (N == 1 || N == 2 || N == 4), "elements");
+    if (dtype == 0) {
+        const float* f = static_cast<const float*>(p) + i;
+        if constexpr (N == 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(f));
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        } else if constexpr (N == 2) {
+            const float2 v = __ldg(reinterpret_cast<const float2*>(f));
+            x[0] = v.x; x[1] = v.y;
+        } else {
+            x[0] = __ldg(f);
+        }
+        return;
+    }
+    const uint16_t* h = static_cast<const uint16_t*>(p) + i;
+    uint32_t w[2];
+    if constexpr (N == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(h));
+        w[0] = v.x; w[1] = v.y;
+    } else if constexpr (N == 2) {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(h));
+    } else {
+        w[0] = __ldg(h);
+    }
+#pragma unroll
+    for (int k = 0; k < (N + 1) / 2; ++k) {
+        const float2 f = dtype == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k]))
+                                    : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+        x[2 * k] = f.x;
+        if constexpr (N > 1) x[2 * k + 1] = f.y;
+    }
 }
 
 // Four elements to a typed buffer, rounded to nearest even; i a multiple of 4
@@ -338,7 +367,7 @@ struct Kv4AttendParams {
 constexpr int KV4_8 = 0, KV4_REST = 1, KV4_16 = 2;
 constexpr int KV4_ROWS = 16;             // most rows of a tile
 constexpr int KV4_KEYS = 32;             // keys of a unit of work: two blocks
-constexpr int KV4_PART = 8;              // what beginning and ending a part costs a CTA, in units
+constexpr int KV4_PART = 16;             // what beginning and ending a part costs a CTA, in units
 constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
 constexpr int KV4_AHEAD = 16;            // units whose pages a warp looks up at a time: lanes 2 i, 2 i + 1 a block each
 constexpr float KV4_SLACK = 8.f;         // the running maximum may lag by this many powers of two
@@ -349,7 +378,9 @@ template <int D, int MODE> struct Kv4Shape {
     static constexpr int WARPS = MODE == KV4_16 || (MODE == KV4_REST && D == 128) ? 6 : 8, THREADS = WARPS * 32;
     static constexpr int STAGES = WARPS == 6 ? 3 : 2;
     static constexpr int ROWS = MODE == KV4_16 ? 16 : 8;
-    static constexpr int MIN_SHARE = KV4_PART + WARPS;   // least share of a CTA: a unit a warp
+    // A cut in a (request, head, row tile) leaves at least FIRST (a unit a warp behind the fixed
+    // cost) before it and LAST after it, or it moves to that end; FIRST + LAST is the least share.
+    static constexpr int FIRST = KV4_PART + WARPS, LAST = WARPS;
 };
 
 template <int D, int MODE> struct Kv4Smem {
@@ -365,8 +396,8 @@ template <int D, int MODE> struct Kv4Smem {
                          OFF_ROW = OFF_ML + ML,              // row factors [16]
                          OFF_BAR = OFF_ROW + KV4_ROWS * 4,   // [warps][stages] barriers
                          OFF_PLAN = OFF_BAR + WARPS * STAGES * 8,
-                         OFF_WALK = OFF_PLAN + 128,          // [warps][2] Kv4Walk
-                         BYTES = OFF_WALK + WARPS * 2 * 80;
+                         OFF_WALK = OFF_PLAN + 128,          // [warps][2] Kv4Walk, the first state
+                         BYTES = OFF_WALK + (WARPS * 2 + 1) * 80;
     static_assert(BYTES <= 115712, "two CTAs an SM");
 };
 
@@ -402,16 +433,15 @@ __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, i
 
 // Cost of a request: each (head, row tile) its units, behind KV4_PART for its
 // beginning and end.
-__device__ __forceinline__ int64_t kv4_cost(const Kv4Req& q, int heads) {
-    return q.units > 0 ? (int64_t)(q.units + KV4_PART) * q.tiles * heads : 0;
+__device__ __forceinline__ int kv4_cost(const Kv4Req& q, int heads) {
+    return q.units > 0 ? (q.units + KV4_PART) * q.tiles * heads : 0;   // the host bounds it by the page table
 }
 
 // A walk over a CTA's share of the flattened list of costs: each step is the
 // part of one (request, head, row tile) whose units lie in the share.
 struct Kv4Walk {
     int64_t left;        // of the share, not yet taken
-    int64_t off;         // of request r, already taken
-    int r;
+    int r, off;          // request, and what is taken of it
     Kv4Req q;
     int seg, b0, b1;     // the current step: head * tiles + tile, units [b0, b1)
     int b;               // (fetching) this warp's next unit not looked up
@@ -424,8 +454,8 @@ struct Kv4Walk {
                 off = 0;
             }
             const int each = q.units + KV4_PART;
-            seg = (int)(off / each);
-            const int u = (int)(off - (int64_t)seg * each);
+            seg = off / each;
+            const int u = off - seg * each;
             const int take = (int)min((int64_t)(each - u), left);
             b0 = max(0, u - KV4_PART);
             b1 = max(0, u + take - KV4_PART);
@@ -481,8 +511,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     float* ml = reinterpret_cast<float*>(smem + SM::OFF_ML);          // [warp][16] m, then l
     float* rowf = reinterpret_cast<float*>(smem + SM::OFF_ROW);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::OFF_BAR) + warp * KV4_STAGES;
-    int64_t* plan = reinterpret_cast<int64_t*>(smem + SM::OFF_PLAN);  // warp sums [8], first request, its offset, share, its start, its length
-    int* plan_i = reinterpret_cast<int*>(plan + 8);
+    int64_t* plan = reinterpret_cast<int64_t*>(smem + SM::OFF_PLAN);  // warp sums [8], the cuts [2], -, the even share
+    int* plan_i = reinterpret_cast<int*>(plan + 11);                  // a flag
 
     if (lane == 0) {
 #pragma unroll
@@ -492,15 +522,16 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
 
-    // ---- the share of this CTA ----
+    // ---- the share of this CTA: the list between two cuts ----
     const int cnt = (p.n + KV4_THREADS - 1) / KV4_THREADS;
     int64_t mine = 0;
     bool empty = false;
+    Kv4Req own;      // of a thread with one request
     for (int r = tid * cnt; r < min(p.n, (tid + 1) * cnt); ++r) {
-        const Kv4Req q = kv4_request(p, r, ROWS);
-        mine += kv4_cost(q, p.heads);
-        empty |= q.t > 0 && q.units == 0;
-        if (q.err && blockIdx.x == 0) atomicCAS(p.status, 0, q.err);
+        own = kv4_request(p, r, ROWS);
+        mine += kv4_cost(own, p.heads);
+        empty |= own.t > 0 && own.units == 0;
+        if (own.err && blockIdx.x == 0) atomicCAS(p.status, 0, own.err);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -517,20 +548,37 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         if (w < warp) before += s;
         total += s;
     }
-    const int64_t per = max((int64_t)SH::MIN_SHARE, (total + gridDim.x - 1) / gridDim.x);
-    const int64_t lo = per * blockIdx.x;
     before += incl - mine;
-    if (mine > 0 && before <= lo && lo < before + mine) {
-        int r = tid * cnt;
-        int64_t off = lo - before;
-        for (;; ++r) {
-            const Kv4Req q = kv4_request(p, r, ROWS);
-            const int64_t c = kv4_cost(q, p.heads);
-            if (off < c) break;
-            off -= c;
+    const int64_t even = total <= 0x7fffffff ? (int64_t)(((unsigned)total + gridDim.x - 1) / gridDim.x)
+                                             : (total + gridDim.x - 1) / gridDim.x;
+    const int64_t per = max((int64_t)(SH::FIRST + SH::LAST), even);
+    Kv4Walk& start = reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK)[2 * KV4_WARPS];
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const int64_t cut = per * (blockIdx.x + k);
+        if (cut >= total) {
+            if (tid == 0) plan[8 + k] = total;
+        } else if (before <= cut && cut < before + mine) {
+            int r = tid * cnt, off = 0;
+            int64_t at = cut - before;
+            Kv4Req q = own;
+            for (;; ++r) {
+                if (cnt > 1) q = kv4_request(p, r, ROWS);
+                const int c = kv4_cost(q, p.heads);
+                if (at < c) break;
+                at -= c;
+            }
+            off = (int)at;
+            const int each = q.units + KV4_PART, u = off % each;
+            const int move = u < SH::FIRST ? -u : each - u < SH::LAST ? each - u : 0;
+            plan[8 + k] = cut + move;
+            if (k == 0) {
+                start.r = r;
+                start.off = off + move;
+                start.q = q;
+                start.b0 = start.b1 = start.b = start.seg = 0;
+            }
         }
-        plan_i[0] = r;
-        plan[9] = off;
     }
     __syncthreads();
     if (any_empty) {  // requests without a visible key: zero rows
@@ -542,12 +590,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 st_elem4(p.o, base + i, p.dtype, 0.f, 0.f, 0.f, 0.f);
         }
     }
-    if (lo >= total) return;
-    if (tid == 0) {  // kept for the joins
-        plan[10] = per;
-        plan[11] = lo;
-        plan[12] = min(per, total - lo);
-    }
+    if (plan[8] >= plan[9]) return;
+    if (tid == 0) plan[10] = per;       // kept for the joins
 
     // what is being fetched, what is being worked on: a warp's own, in shared
     // memory (read seldom; the registers go to the accumulators)
@@ -555,12 +599,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     Kv4Walk& get = reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK)[2 * warp + 1];
     static_assert(sizeof(Kv4Walk) <= 80, "Kv4Smem::OFF_WALK");
     if (lane == 0) {
-        put.r = plan_i[0];
-        put.off = plan[9];
-        put.left = min(per, total - lo);
-        put.q = kv4_request(p, put.r, ROWS);
-        put.b0 = put.b1 = put.b = put.seg = 0;
-        get = put;
+        Kv4Walk w = start;
+        w.left = plan[9] - plan[8];
+        put = w;
+        get = w;
     }
     __syncwarp();
     auto step = [&](Kv4Walk& w) {   // lane 0 walks, all lanes see it
@@ -639,55 +681,73 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         {
         const int h = get.seg / get.q.tiles, i0 = first_row();
         const int live = min(ROWS, get.q.t * p.grp - i0);
-        // ---- queries: rotate, scale, round; one row a warp at a time ----
-        for (int i = warp; i < ROWS; i += KV4_WARPS) {
-            constexpr int E = D / 32;
-            float x[E];
-            float factor = 1.f;   // of a row of zeros (not 0: a masked score times it stays -infinity)
-            const int j = (i0 + i) / p.grp;
-            const int pos = get.q.ctx + j;
+        // ---- queries: rotate, scale, round; R rows a warp, all their loads first ----
+        constexpr int E = D / 32, R = (ROWS + KV4_WARPS - 1) / KV4_WARPS;
+        const int d = lane * E, half = p.rot >> 1;
+        const bool first = d < half, turned = d < p.rot;
+        float x[R][E], y[R][E], cs[R][E], sn[R][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = 0.f;
-            if (i < live && pos >= 0) {
-                const int64_t base = (int64_t)(get.q.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + (i0 + i) - j * p.grp) * D;
-                const int half = p.rot >> 1;
-                float amax = 0.f;
+        for (int k = 0; k < R; ++k) {
+            const int i = warp + k * KV4_WARPS, j = (i0 + i) / p.grp, pos = get.q.ctx + j;
+            const bool on = i < live && pos >= 0;
+            const int64_t base = (int64_t)(get.q.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + (i0 + i) - j * p.grp) * D;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int d = lane * E + e;
-                    x[e] = ld_elem(p.q, base + d, p.dtype);
-                    if (d < p.rot) {
-                        int c, o;
-                        bool first;
-                        if (p.inter) { c = d >> 1; first = (d & 1) == 0; o = d ^ 1; }
-                        else { first = d < half; c = first ? d : d - half; o = first ? d + half : c; }
-                        const float y = ld_elem(p.q, base + o, p.dtype);
-                        const float cs = __ldg(p.cos + (int64_t)pos * half + c), sn = __ldg(p.sin + (int64_t)pos * half + c);
-                        x[e] = first ? x[e] * cs - y * sn : x[e] * cs + y * sn;
+            for (int e = 0; e < E; ++e) {
+                x[k][e] = y[k][e] = sn[k][e] = 0.f;
+                cs[k][e] = 1.f;
+            }
+            if (on) ld_elems<E>(p.q, base + d, p.dtype, x[k]);
+            if (on && turned) {
+                const int64_t row = (int64_t)pos * half;
+                if (p.inter) {
+                    ld_elems<E / 2>(p.cos, row + d / 2, 0, cs[k]);
+                    ld_elems<E / 2>(p.sin, row + d / 2, 0, sn[k]);
+                } else {
+                    ld_elems<E>(p.q, base + (first ? d + half : d - half), p.dtype, y[k]);
+                    ld_elems<E>(p.cos, row + (first ? d : d - half), 0, cs[k]);
+                    ld_elems<E>(p.sin, row + (first ? d : d - half), 0, sn[k]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int i = warp + k * KV4_WARPS;
+            if (turned) {
+                if (p.inter) {
+#pragma unroll
+                    for (int e = E / 2 - 1; e >= 0; --e) {
+                        const float a = x[k][2 * e], b = x[k][2 * e + 1];
+                        x[k][2 * e] = a * cs[k][e] - b * sn[k][e];
+                        x[k][2 * e + 1] = b * cs[k][e] + a * sn[k][e];
                     }
-                    amax = fmaxf(amax, fabsf(x[e]));
-                }
+                } else {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                // 2^-k with amax 2^-k in [1/2, 1); the factor below 2^-100 and the infinite stay as they are
-                const int k = amax > 1e-30f && amax < 3e38f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
-                factor = fmaxf(1e-30f, fabsf(p.scale_log2) * exp2f((float)k));
-                const float down = p.scale_log2 < 0.f ? -exp2f((float)-k) : exp2f((float)-k);   // the factor itself is not negative
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[e] *= down;
-            }
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const __half2 hi = __floats2half2_rn(x[e], x[e + 1]);
-                const int d = lane * E + e, at = (d % (D / 4) / 8 * 4 + d / (D / 4)) * 8 + d % 8;
-                *reinterpret_cast<__half2*>(qbuf + i * SM::QPITCH + at) = hi;
-                if constexpr (SPLIT) {
-                    const float2 f = __half22float2(hi);
-                    *reinterpret_cast<__half2*>(qbuf + (i + 8) * SM::QPITCH + at) =
-                        __floats2half2_rn(x[e] - f.x, x[e + 1] - f.y);
+                    for (int e = 0; e < E; ++e) x[k][e] = x[k][e] * cs[k][e] + (first ? -y[k][e] : y[k][e]) * sn[k][e];
                 }
             }
-            if (lane == 0) rowf[i] = factor;
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // 2^-z with amax 2^-z in [1/2, 1); rows of nothing, below 1e-30 or infinite stay as they are
+            const int z = amax > 1e-30f && amax < 3e38f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
+            // the factor is positive (not 0: a masked score times it stays -infinity), queries take the sign
+            const float down = __uint_as_float((uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u));
+            if (i < ROWS) {
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float u = x[k][e] * down, v = x[k][e + 1] * down;
+                    const __half2 hi = __floats2half2_rn(u, v);
+                    const int dd = d + e, at = (dd % (D / 4) / 8 * 4 + dd / (D / 4)) * 8 + dd % 8;
+                    *reinterpret_cast<__half2*>(qbuf + i * SM::QPITCH + at) = hi;
+                    if constexpr (SPLIT) {
+                        const float2 f = __half22float2(hi);
+                        *reinterpret_cast<__half2*>(qbuf + (i + 8) * SM::QPITCH + at) = __floats2half2_rn(u - f.x, v - f.y);
+                    }
+                }
+                if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
+            }
         }
         }
         __syncthreads();
@@ -972,12 +1032,13 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             }
         }
         if (!whole) {
-            // CTAs that share this (request, head, tile), from its place in the list
-            const int64_t first = plan[11] + plan[12] - get.left - get.b1, share = plan[10];   // unit of block 0
-            const int c0 = (int)(first / share), c1 = (int)((first + get.q.units - 1) / share);
-            __threadfence();
+            // CTAs that share this (request, head, tile): those between the cuts that stayed inside it
+            const int64_t seg0 = plan[9] - get.left - get.b1 - KV4_PART, share = plan[10];
+            const int c0 = (int)((seg0 + SH::FIRST + share - 1) / share) - 1;
+            const int c1 = (int)((seg0 + get.q.units + KV4_PART - SH::LAST) / share);
             __syncthreads();
             if (tid == 0) {
+                __threadfence();        // the CTA's stores, ordered before by the barrier
                 const int old = atomicAdd(p.counters + c0, 1);
                 if (old == c1 - c0) p.counters[c0] = 0;
                 plan_i[0] = old == c1 - c0;
@@ -985,43 +1046,47 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             }
             __syncthreads();
             if (plan_i[0]) {
-                // every part's maximum and sum of each row, weights from them, then the rows in
-                // NGRP groups of parts at a time; merge holds the groups' sums, ring is not free
-                const int tid2 = tid_again(), np = c1 - c0 + 1, cta0 = 2 * c0 + tid_again() - tid2;
+                // Thread groups a row wide; where there are more groups than rows, several share a
+                // row's parts and their sums meet in shared memory.
+                constexpr int GROUPS = KV4_THREADS / CH;
+                const int tid2 = tid_again(), np = c1 - c0 + 1, ch = tid2 % CH, grp = tid2 / CH;
+                const int share = max(1, GROUPS / live), rows = GROUPS / share;   // groups of a row, rows at a time
                 auto slot = [&](int k) {
-                    return p.partials + (cta0 + 2 * k + (k == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
+                    return p.partials + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
                 };
-                constexpr int NGRP = KV4_THREADS / CH;   // thread groups, each a whole row wide
-                const int ch = tid2 % CH, grp = tid2 / CH;
 #pragma unroll 1
-                for (int row = 0; row < live; ++row) {
-                    float M = -FLT_MAX;
-                    for (int k = tid2 & 31; k < np; k += 32) M = fmaxf(M, __ldcg(slot(k) + KV4_ROWS * D + 2 * row));
-#pragma unroll
-                    for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
-                    float L = 0.f;
+                for (int row0 = 0; row0 < live; row0 += rows) {
+                    const int row = row0 + grp / share, kk = grp % share;
+                    const bool on = grp < rows * share && row < live;
+                    float M = -FLT_MAX, L = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = ch; k < np; k += CH)
+                        if (on) M = fmaxf(M, __ldcg(slot(k) + KV4_ROWS * D + 2 * row));
+#pragma unroll
+                    for (int o2 = CH / 2; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
+                    if (on) {
 #pragma unroll 4
-                    for (int k = grp; k < np; k += NGRP) {
-                        const float* s = slot(k);
-                        const float2 x = __ldcg(reinterpret_cast<const float2*>(s + KV4_ROWS * D) + row);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D + ch * 4));
-                        const float f = ex2f(x.x - M);
-                        L += f * x.y;
-                        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
-                    }
-                    __syncthreads();
-                    reinterpret_cast<float4*>(merge)[tid2] = o;
-                    if (ch == 0) ml[grp] = L;
-                    __syncthreads();
-                    if (tid2 < CH) {
-                        for (int k = 1; k < min(NGRP, np); ++k) {
-                            const float4 v = reinterpret_cast<const float4*>(merge)[k * CH + tid2];
-                            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-                            L += ml[k];
+                        for (int k = kk; k < np; k += share) {
+                            const float* s = slot(k);
+                            const float2 x = __ldcg(reinterpret_cast<const float2*>(s + KV4_ROWS * D) + row);
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D + ch * 4));
+                            const float f = ex2f(x.x - M);
+                            L += f * x.y;
+                            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
                         }
-                        join(row, ch * 4, o, M, L);
                     }
+                    if (share > 1) {
+                        __syncthreads();
+                        reinterpret_cast<float4*>(merge)[tid2] = o;
+                        if (ch == 0) ml[grp] = L;
+                        __syncthreads();
+                        for (int k = 1; k < share && kk == 0; ++k) {
+                            const float4 v = reinterpret_cast<const float4*>(merge)[tid2 + k * CH];
+                            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                            L += ml[grp + k];
+                        }
+                    }
+                    if (on && kk == 0) join(row, ch * 4, o, M, L);
                 }
             }
         }

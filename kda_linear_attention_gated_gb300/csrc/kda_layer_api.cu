@@ -205,12 +205,12 @@ int kda_kv4_attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, 
     const int rows = mode == kda::KV4_16 ? 16 : 8;
     const int64_t units = ((int64_t)g.table_cols * cache->page_tokens + kda::KV4_KEYS - 1) / kda::KV4_KEYS;
     const int64_t tiles = ((int64_t)g.max_t * grp + rows - 1) / rows;
-    if (tiles * cache->heads > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if ((units + kda::KV4_PART) * tiles * cache->heads > 0x7fffffffLL) return KDA_ERR_SHAPE;
     if (g.n == 0 || g.total == 0 || g.max_t == 0) return KDA_OK;
     rc = check_common_pointers(cache, c, dev_status);
     if (rc != KDA_OK) return rc;
     if (!g.q || !g.o || !g.workspace) return KDA_ERR_NULL;
-    if (!aligned(g.q, es) || !aligned(g.o, 16) || !aligned(g.workspace, 16)) return KDA_ERR_ALIGN;
+    if (!aligned(g.q, 16) || g.q_stride * es % 16 != 0 || !aligned(g.o, 16) || !aligned(g.workspace, 16)) return KDA_ERR_ALIGN;
     if (g.workspace_bytes < KDA_KV4_WORKSPACE_BYTES) return KDA_ERR_SHAPE;
     kda::Kv4AttendParams prm;
     prm.pages = static_cast<const uint8_t*>(cache->base);
