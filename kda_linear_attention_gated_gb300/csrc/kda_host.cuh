@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 
 #include "kda.h"
@@ -24,14 +25,14 @@ int elem_size(int32_t dtype) {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Resident CTAs per SM of `kernel` with `smem` dynamic bytes (also raises the
-// kernel's dynamic shared-memory limit); cached per (kernel, device).
+// kernel's dynamic shared-memory limit); cached per (kernel, device, threads).
 int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, int* sms) {
     static std::mutex mu;
-    static std::map<std::pair<const void*, int>, std::pair<int, int>> cache;
+    static std::map<std::tuple<const void*, int, int>, std::pair<int, int>> cache;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_LAUNCH;
     std::lock_guard<std::mutex> lock(mu);
-    auto it = cache.find({kernel, dev});
+    auto it = cache.find({kernel, dev, threads});
     if (it == cache.end()) {
         int occ = 0, count = 0;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -40,7 +41,7 @@ int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, 
             cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             occ < 1)
             return KDA_ERR_LAUNCH;
-        it = cache.emplace(std::make_pair(kernel, dev), std::make_pair(occ, count)).first;
+        it = cache.emplace(std::make_tuple(kernel, dev, threads), std::make_pair(occ, count)).first;
     }
     *blocks_per_sm = it->second.first;
     *sms = it->second.second;

@@ -199,19 +199,91 @@ __device__ __forceinline__ void ld_elem16(const void* p, int64_t i, int dtype, f
     }
 }
 
-// Eight tokens a CTA, four 16-channel groups of each a warp at a time: a
-// warp's loads are whole 128-byte lines of a token (16-bit inputs), its key
-// codes whole 32-byte sectors, and its value codes 64 contiguous bytes when the
-// eight tokens fill half a block.  A thread rounds one group: in fp32
+// Rounds a group of 16 channels: the two words of codes and the scale byte.  In fp32
 //   t = x / scale of the cache (as a product with the reciprocal, 1 by default),
-//   s = e4m3(max|t| / 6), code = e2m1(t / s), each rounded to nearest even;
-// the two quotients are IEEE divisions, so that a value half way between two
-// codes stays half way.  A group that holds a NaN or an infinity gets a NaN
-// scale: it reads back as NaN.  Rotation in fp32, products and sums rounded
-// one by one (no fused multiply-add).
+//   s = e4m3(max|t| / 6), code = e2m1(t / s), each rounded to nearest even.
+// The quotients are those of IEEE division, so that a value half way between
+// two codes stays half way: max / 6 is one, and t / s is the product with the
+// rounded reciprocal, corrected once by its exact remainder (Markstein, IBM
+// Journal of Research and Development 34, 1990; s has four bits and lies in
+// 2^-9 .. 448; below 1/4 of a code, where the remainder may underflow, the code
+// is 0 either way).  A group that holds a NaN or an infinity gets a NaN scale:
+// it reads back as NaN.
+__device__ __forceinline__ uint32_t kv4_round(float* x, float inv, uint2& code) {
+    uint32_t amax = 0;  // bit patterns of |t| order like the values, NaN above infinity
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        x[j] = __fmul_rn(x[j], inv);
+        amax = max(amax, __float_as_uint(x[j]) & 0x7fffffffu);
+    }
+    const bool fine = amax < 0x7f800000u;
+    const uint32_t s8 = fine ? cvt_f32_e4m3(__fdiv_rn(__uint_as_float(amax), 6.0f)) : 0x7fu;
+    const uint32_t sh = cvt_e4m3x2_f16x2(s8);
+    const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
+    const float rs = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float q = x[j] * rs;
+        x[j] = copysignf(fmaf(fmaf(-q, s, x[j]), rs, q), x[j]);
+    }
+    code = fine ? make_uint2(cvt_f32x8_e2m1(x), cvt_f32x8_e2m1(x + 8)) : make_uint2(0u, 0u);
+    return s8;
+}
+
+// The 16 values that codes and a scale byte stand for, times g, to a typed
+// buffer at element i.  code * scale has six significant bits: whole in fp16.
+__device__ __forceinline__ void kv4_values(void* out, int64_t i, int dtype, uint2 code, uint32_t s8, float g) {
+    uint32_t q[8];
+    cvt_e2m1x8_f16(code.x, *reinterpret_cast<uint32_t(*)[4]>(q));
+    cvt_e2m1x8_f16(code.y, *reinterpret_cast<uint32_t(*)[4]>(q + 4));
+    const uint32_t sh = cvt_e4m3x2_f16x2(s8), s2 = __byte_perm(sh, sh, 0x1010);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = hmul2_u32(q[j], s2);
+    if (dtype == 1 && g == 1.f) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__half*>(out) + i);
+        o[0] = make_uint4(q[0], q[1], q[2], q[3]);
+        o[1] = make_uint4(q[4], q[5], q[6], q[7]);
+        return;
+    }
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
+        x[2 * j] = f.x * g;
+        x[2 * j + 1] = f.y * g;
+    }
+    if (dtype == 2) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + i);
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) st_elem4(out, i + j, dtype, x[j], x[j + 1], x[j + 2], x[j + 3]);
+}
+
+__device__ __forceinline__ void kv4_turn(float& a, float& b, float c, float s) {
+    const float u = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    a = u;
+}
+
+// Eight tokens a CTA, a whole head of each a warp at a time (two heads of 64
+// channels).  A lane rounds two groups of 16 channels: of keys those that the
+// rotation pairs, so that every key and every table entry is loaded once.  A
+// warp's loads are whole 128-byte lines of a token (16-bit inputs), its key
+// codes whole 32-byte sectors, and its value codes 64 contiguous bytes when
+// the eight tokens fill half a block.  Rotation in fp32, products and sums
+// rounded one by one (no fused multiply-add).
 template <int D>
 __global__ void __launch_bounds__(KV4_APPEND_THREADS) kda_kv4_append_kernel(const Kv4AppendParams p) {
-    constexpr int NG = Kv4<D>::NG, GQ = NG / 4;
+    constexpr int NG = Kv4<D>::NG, NP = NG / 2, HW = 4 / NP;     // groups and pairs of a head, heads of a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
@@ -257,89 +329,66 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS) kda_kv4_append_kernel(cons
         atomicCAS(p.status, 0, STATUS_ARG);
     }
     const int64_t head_bytes = (int64_t)(p.page_tokens >> 4) * Kv4<D>::BLOCK;
-    const int items = p.heads * 2 * GQ;
+    // this lane's two groups: those of a rotated pair of halves, else neighbours
+    const int i = (lane & 3) % NP, half = p.rot >> 1, rg = p.rot >> 4;
+    const bool halves = !p.inter && 2 * i < rg;
+    const int grp[2] = {halves ? i : 2 * i, halves ? i + (rg >> 1) : 2 * i + 1};
+    const int items = (p.heads + HW - 1) / HW * 2;
     for (int it = (int)blockIdx.y * 8 + warp; it < items; it += 8 * (int)gridDim.y) {
-        const int kv = it / GQ & 1, h = it / (2 * GQ), grp = (it % GQ) * 4 + (lane & 3);
-        const bool is_v = kv != 0;
+        const bool is_v = (it & 1) != 0;
+        const int h = (it >> 1) * HW + (lane & 3) / NP;
+        if (h >= p.heads) continue;
         void* out = is_v ? p.v_out : p.k_out;
-        float x[16];
-        if (pos >= 0) {
-            const void* src = is_v ? p.v : p.k;
-            const int64_t base = (int64_t)tok * (is_v ? p.v_stride : p.k_stride) + h * D;
-            ld_elem16(src, base + grp * 16, p.dtype, x);
-            if (!is_v && grp * 16 < p.rot) {
-                const int half = p.rot >> 1;
-                const float* cs = p.cos + (int64_t)pos * half;
-                const float* sn = p.sin + (int64_t)pos * half;
-                if (p.inter) {
+        const int64_t row = ((int64_t)tok * p.heads + h) * D;
+        if (pos < 0) {
+            if (out != nullptr)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float c = __ldg(cs + grp * 8 + j), s = __ldg(sn + grp * 8 + j);
-                        const float a = x[2 * j], b = x[2 * j + 1];
-                        x[2 * j] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-                        x[2 * j + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-                    }
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) st_elem4(out, row + grp[k] * 16 + j, p.out_dtype, 0.f, 0.f, 0.f, 0.f);
+            continue;
+        }
+        float x[2][16];
+        const void* src = is_v ? p.v : p.k;
+        const int64_t base = (int64_t)tok * (is_v ? p.v_stride : p.k_stride) + h * D;
+        ld_elem16(src, base + grp[0] * 16, p.dtype, x[0]);
+        ld_elem16(src, base + grp[1] * 16, p.dtype, x[1]);
+        if (!is_v && 2 * i < rg) {
+            const float* cs = p.cos + (int64_t)pos * half;
+            const float* sn = p.sin + (int64_t)pos * half;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float c[4], s[4];
+                const int e0 = 16 * i + 4 * q;      // table entries of the pair's 16 angles
+                ld_elems<4>(cs, e0, 0, c);
+                ld_elems<4>(sn, e0, 0, s);
+                if (!p.inter) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) kv4_turn(x[0][4 * q + j], x[1][4 * q + j], c[j], s[j]);
                 } else {
-                    const bool first = grp * 16 < half;
-                    const int i = first ? grp * 16 : grp * 16 - half;
-                    float y[16];
-                    ld_elem16(src, base + (first ? i + half : i), p.dtype, y);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float c = __ldg(cs + i + j), s = __ldg(sn + i + j);
-                        x[j] = first ? __fsub_rn(__fmul_rn(x[j], c), __fmul_rn(y[j], s))
-                                     : __fadd_rn(__fmul_rn(x[j], c), __fmul_rn(y[j], s));
-                    }
+                    for (int j = 0; j < 4; ++j) kv4_turn(x[q >> 1][8 * (q & 1) + 2 * j], x[q >> 1][8 * (q & 1) + 2 * j + 1], c[j], s[j]);
                 }
             }
-            const float inv = is_v ? p.inv_v : p.inv_k;
-            uint32_t amax = 0;  // bit patterns of |t| order like the values, NaN above infinity
+        }
+        uint8_t* b = blk + h * head_bytes;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                x[j] = __fmul_rn(x[j], inv);
-                amax = max(amax, __float_as_uint(x[j]) & 0x7fffffffu);
-            }
-            const bool fine = amax < 0x7f800000u;
-            const uint32_t s8 = fine ? cvt_f32_e4m3(__fdiv_rn(__uint_as_float(amax), 6.0f)) : 0x7fu;
-            const uint32_t sh = cvt_e4m3x2_f16x2(s8);
-            const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                x[j] = !fine ? 0.f : s > 0.f ? __fdiv_rn(x[j], s) : copysignf(0.f, x[j]);
-            const uint2 c = make_uint2(cvt_f32x8_e2m1(x), cvt_f32x8_e2m1(x + 8));
-            uint8_t* b = blk + h * head_bytes;
+        for (int k = 0; k < 2; ++k) {
+            uint2 c;
+            const uint32_t s8 = kv4_round(x[k], is_v ? p.inv_v : p.inv_k, c);
             if (!is_v) {
-                *reinterpret_cast<uint2*>(b + Kv4<D>::KC + where * (D / 2) + grp * 8) = c;
-                b[Kv4<D>::KS + where * NG + grp] = (uint8_t)s8;
+                *reinterpret_cast<uint2*>(b + Kv4<D>::KC + where * (D / 2) + grp[k] * 8) = c;
+                b[Kv4<D>::KS + where * NG + grp[k]] = (uint8_t)s8;
             } else {
                 if constexpr (D == 128) {
-                    *reinterpret_cast<uint2*>(b + kv4_v_code<D>(where, grp)) = c;
+                    *reinterpret_cast<uint2*>(b + kv4_v_code<D>(where, grp[k])) = c;
                 } else {
-                    *reinterpret_cast<uint32_t*>(b + kv4_v_code<D>(where, 2 * grp)) = c.x;
-                    *reinterpret_cast<uint32_t*>(b + kv4_v_code<D>(where, 2 * grp + 1)) = c.y;
+                    *reinterpret_cast<uint32_t*>(b + kv4_v_code<D>(where, 2 * grp[k])) = c.x;
+                    *reinterpret_cast<uint32_t*>(b + kv4_v_code<D>(where, 2 * grp[k] + 1)) = c.y;
                 }
-                b[kv4_v_scale<D>(where, grp)] = (uint8_t)s8;
+                b[kv4_v_scale<D>(where, grp[k])] = (uint8_t)s8;
             }
-            if (out != nullptr) {
-                uint32_t q[8];
-                cvt_e2m1x8_f16(c.x, *reinterpret_cast<uint32_t(*)[4]>(q));
-                cvt_e2m1x8_f16(c.y, *reinterpret_cast<uint32_t(*)[4]>(q + 4));
-                const float g = is_v ? p.v_scale : p.k_scale;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
-                    x[2 * j] = f.x * s * g;       // code * scale is exact; one rounding for g != 1
-                    x[2 * j + 1] = f.y * s * g;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.f;
-        }
-        if (out != nullptr) {
-            const int64_t o = ((int64_t)tok * p.heads + h) * D + grp * 16;
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) st_elem4(out, o + j, p.out_dtype, x[j], x[j + 1], x[j + 2], x[j + 3]);
+            if (out != nullptr) kv4_values(out, row + grp[k] * 16, p.out_dtype, c, s8, is_v ? p.v_scale : p.k_scale);
         }
     }
 }

@@ -84,24 +84,28 @@ cudaError_t launch_head_norm_t(const cudaLaunchConfig_t& cfg, const kda::HeadNor
     }
 }
 
+// Rows in turn over CTAs that all fit the card at once.
+template <typename T, typename R, int NV>
+cudaError_t launch_block_norm_rows(cudaLaunchConfig_t& cfg, const kda::BlockNormParams& prm, int units) {
+    auto kernel = kda::kda_block_norm_kernel<T, R, NV>;
+    const int threads = ((units + NV - 1) / NV + 31) / 32 * 32;
+    int occ = 0, sms = 0;
+    if (occupancy(reinterpret_cast<const void*>(kernel), threads, 0, &occ, &sms) != KDA_OK) return cudaErrorUnknown;
+    cfg.gridDim = dim3((unsigned)std::min(prm.total, occ * sms));
+    cfg.blockDim = dim3(threads);
+    return cudaLaunchKernelEx(&cfg, kernel, prm);
+}
+
 template <typename T, typename R>
 cudaError_t launch_block_norm(cudaLaunchConfig_t& cfg, const kda::BlockNormParams& prm, bool vec) {
-    const int units = vec ? prm.hidden / 8 : prm.hidden;
-    auto threads = [&](int nv) { return ((units + nv - 1) / nv + 31) / 32 * 32; };
-    if (vec) {
-        if (units <= 1024) {
-            cfg.blockDim = dim3(threads(1));
-            return cudaLaunchKernelEx(&cfg, kda::kda_block_norm_kernel<T, R, 8, 1>, prm);
-        }
-        cfg.blockDim = dim3(threads(2));
-        return cudaLaunchKernelEx(&cfg, kda::kda_block_norm_kernel<T, R, 8, 2>, prm);
-    }
-    if (units <= 4096) {
-        cfg.blockDim = dim3(threads(4));
-        return cudaLaunchKernelEx(&cfg, kda::kda_block_norm_kernel<T, R, 1, 4>, prm);
-    }
-    cfg.blockDim = dim3(threads(16));
-    return cudaLaunchKernelEx(&cfg, kda::kda_block_norm_kernel<T, R, 1, 16>, prm);
+    const int units = prm.hidden / 8;
+    if (vec && units <= 512) return launch_block_norm_rows<T, R, 1>(cfg, prm, units);
+    if (vec && units <= 1024) return launch_block_norm_rows<T, R, 2>(cfg, prm, units);
+    const int nv = prm.hidden <= 4096 ? 4 : 16;
+    cfg.gridDim = dim3((unsigned)prm.total);
+    cfg.blockDim = dim3(((prm.hidden + nv - 1) / nv + 31) / 32 * 32);
+    return nv == 4 ? cudaLaunchKernelEx(&cfg, kda::kda_block_norm_any_kernel<T, R, 4>, prm)
+                   : cudaLaunchKernelEx(&cfg, kda::kda_block_norm_any_kernel<T, R, 16>, prm);
 }
 
 }  // namespace
@@ -171,7 +175,7 @@ int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, 
     prm.inv_v = 1.0f / cache->v_scale;
     prm.status = dev_status;
     // eight tokens a CTA; few tokens share their heads out over more CTAs
-    const int tokens = (int)(((int64_t)g.total + 7) / 8), items = cache->heads * 2 * (cache->dim / 64);
+    const int tokens = (int)(((int64_t)g.total + 7) / 8), items = cache->dim == 128 ? cache->heads * 2 : (cache->heads + 1) / 2 * 2;
     const int parts = std::max(1, std::min((items + 7) / 8, 608 / tokens));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tokens, (unsigned)parts, 1);

@@ -8,7 +8,7 @@
 
 namespace kda {
 
-// Eight elements <-> fp32 registers by 16-byte accesses.
+// Eight elements -> fp32 registers by 16-byte accesses.
 template <typename T> __device__ __forceinline__ void ld8(const T* p, float (&x)[8]) {
     if constexpr (sizeof(T) == 4) {
         const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
@@ -127,93 +127,192 @@ __device__ __forceinline__ float block_sum(float x, float* part, int warps) {
     return s;
 }
 
+// Eight elements as loaded: 16 bytes, or 32 of fp32.
+template <typename T> struct Raw8 { uint4 v[sizeof(T) / 2]; };
+template <typename T> __device__ __forceinline__ Raw8<T> raw8(const T* p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    return r;
+}
+template <typename T> __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 4) {
+                x[4 * i + e] = __uint_as_float(w[e]);
+            } else {
+                float2 f;
+                if constexpr (__is_same(T, __half)) f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
+                x[2 * e] = f.x;
+                x[2 * e + 1] = f.y;
+            }
+        }
+    }
+}
+
 // h = a residual + b scale act(gate) [w_post y / rms(y)]; x = w_pre h / rms(h).
-// A CTA a row at a time; a thread keeps NV vectors of VEC channels of the row
-// in registers across both sums, so memory is touched once.
-template <typename T, typename R, int VEC, int NV>
-__global__ void __launch_bounds__(1024, NV > 8 ? 0 : 1) kda_block_norm_kernel(const BlockNormParams p) {
+// Bound by memory: every element of a row is read and written once, the row
+// stays in registers across both sums.  A CTA takes rows in turn, its threads
+// NV vectors of eight channels each; the weights stay in registers for all its
+// rows (reading them again for every row is half as many bytes again, from
+// L2), and the next row is on its way while a row is summed up (but for two
+// vectors of fp32, which fill the registers).
+template <typename T, typename R, int NV>
+__global__ void __launch_bounds__(512) kda_block_norm_kernel(const BlockNormParams p) {
+    constexpr bool AHEAD = NV == 1 || sizeof(T) == 2;
     __shared__ float part[2][32];
     const int nt = blockDim.x, warps = nt >> 5;
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
     const float inv = 1.f / (float)p.hidden;
-    for (int row = blockIdx.x; row < p.total; row += gridDim.x) {
-        const R* res = static_cast<const R*>(p.residual) + (int64_t)row * p.hidden;
-        float h[NV][VEC], z[NV][VEC];
-        float s = 0.f;
+    bool on[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) on[i] = (i * nt + (int)threadIdx.x) * 8 < p.hidden;
+    float wb[NV][8], wq[NV][8];      // weights of the branch, of the next block's input
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (!on[i]) continue;
+        const int c = (i * nt + (int)threadIdx.x) * 8;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            wb[i][e] = p.branch_scale;
+            wq[i][e] = 1.f;
+        }
+        if (p.w_post != nullptr) {
+            widen8(raw8(p.w_post + c), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wb[i][e] *= f[e];
+        }
+        if (p.scale != nullptr) {
+            widen8(raw8(p.scale + c), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wb[i][e] *= f[e];
+        }
+        if (p.w_pre != nullptr) widen8(raw8(p.w_pre + c), wq[i]);
+    }
+    Raw8<T> y[NV], gate[NV];
+    Raw8<R> res[NV];
+    auto load = [&](int row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + (int)threadIdx.x) * VEC;
+            const int c = (i * nt + (int)threadIdx.x) * 8;
+            if (!on[i]) continue;
+            res[i] = raw8(static_cast<const R*>(p.residual) + (int64_t)row * p.hidden + c);
+            if (p.y != nullptr) y[i] = raw8(static_cast<const T*>(p.y) + (int64_t)row * p.y_stride + c);
+            if (p.gate != nullptr) gate[i] = raw8(static_cast<const T*>(p.gate) + (int64_t)row * p.gate_stride + c);
+        }
+    };
+    int row = blockIdx.x;
+    if (AHEAD && row < p.total) load(row);
+    for (; row < p.total; row += gridDim.x) {
+        if (!AHEAD) load(row);
+        float z[NV][8], h[NV][8], s = 0.f;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) h[i][e] = z[i][e] = 0.f;
-            if (c < p.hidden) {
-                if constexpr (VEC == 8) ld8(res + c, h[i]);
-                if (p.y != nullptr) {
-                    const T* y = static_cast<const T*>(p.y) + (int64_t)row * p.y_stride + c;
-                    if constexpr (VEC == 8) ld8(y, z[i]);
-                    else z[i][0] = to_f32(y[0]);
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[i][e] = h[i][e] = 0.f;
+            if (!on[i]) continue;
+            widen8(res[i], h[i]);
+            if (p.y != nullptr) {
+                widen8(y[i], z[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(z[i][e], z[i][e], s);
+                if (p.gate != nullptr) {
+                    float f[8];
+                    widen8(gate[i], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[i][e] *= gate_act(f[e], p.act);
                 }
             }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s = fmaf(z[i][e], z[i][e], s);
         }
+        const int next = row + gridDim.x;
+        if (AHEAD && next < p.total) load(next);
         float r = 1.f;
         if (p.w_post != nullptr) r = rsqrtf(block_sum(s, part[0], warps) * inv + p.eps);
         s = 0.f;
-        if constexpr (VEC == 1) {  // late: with up to 16 channels a thread, both rows at once would not fit its registers
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = i * nt + (int)threadIdx.x;
-                if (c < p.hidden) h[i][0] = to_f32(res[c]);
-            }
-        }
         if (p.y != nullptr) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * nt + (int)threadIdx.x) * VEC;
-                if (c < p.hidden) {
-                    float gt[VEC];
-                    if (p.gate != nullptr) {
-                        const T* g = static_cast<const T*>(p.gate) + (int64_t)row * p.gate_stride + c;
-                        if constexpr (VEC == 8) ld8(g, gt);
-                        else gt[0] = to_f32(g[0]);
-                    }
+                if (!on[i]) continue;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        float v = z[i][e] * r * p.branch_scale;
-                        if (p.w_post != nullptr) v *= __ldg(p.w_post + c + e);
-                        if (p.scale != nullptr) v *= __ldg(p.scale + c + e);
-                        if (p.gate != nullptr) v *= gate_act(gt[e], p.act);
-                        h[i][e] = fmaf(p.residual_scale, h[i][e], v);
-                    }
-                    R* out = static_cast<R*>(p.residual_out) + (int64_t)row * p.hidden + c;
-                    if constexpr (VEC == 8) st8(out, h[i]);
-                    else out[0] = from_f32<R>(h[i][0]);
+                for (int e = 0; e < 8; ++e) {
+                    h[i][e] = fmaf(p.residual_scale, h[i][e], z[i][e] * r * wb[i][e]);
+                    s = fmaf(h[i][e], h[i][e], s);
                 }
+                st8(static_cast<R*>(p.residual_out) + (int64_t)row * p.hidden + (i * nt + (int)threadIdx.x) * 8, h[i]);
             }
-        }
-        if (p.x != nullptr) {
+        } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s = fmaf(h[i][e], h[i][e], s);
+                for (int e = 0; e < 8; ++e) s = fmaf(h[i][e], h[i][e], s);
+        }
+        if (p.x != nullptr) {
             r = rsqrtf(block_sum(s, part[1], warps) * inv + p.eps);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * nt + (int)threadIdx.x) * VEC;
-                if (c < p.hidden) {
+                if (!on[i]) continue;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        h[i][e] *= r;
-                        if (p.w_pre != nullptr) h[i][e] *= __ldg(p.w_pre + c + e);
-                    }
-                    T* out = static_cast<T*>(p.x) + (int64_t)row * p.hidden + c;
-                    if constexpr (VEC == 8) st8(out, h[i]);
-                    else out[0] = from_f32<T>(h[i][0]);
-                }
+                for (int e = 0; e < 8; ++e) h[i][e] *= r * wq[i][e];
+                st8(static_cast<T*>(p.x) + (int64_t)row * p.hidden + (i * nt + (int)threadIdx.x) * 8, h[i]);
             }
         }
         if ((p.w_post == nullptr) != (p.x == nullptr)) __syncthreads();  // one buffer only: the next row writes it again
+    }
+}
+
+// The same for rows that do not start on 16 bytes, are no multiple of eight
+// channels wide, or wider than 8192: one channel an access, NV of them a thread; the weights come
+// from L1.  Row after row of an odd width is still contiguous, so a warp's
+// loads are whole lines.
+template <typename T, typename R, int NV>
+__global__ void __launch_bounds__(1024, NV > 8 ? 0 : 1) kda_block_norm_any_kernel(const BlockNormParams p) {
+    __shared__ float part[2][32];
+    const int nt = blockDim.x, warps = nt >> 5;
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+    const float inv = 1.f / (float)p.hidden;
+    const int row = blockIdx.x;
+    float h[NV], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * nt + (int)threadIdx.x;
+        h[i] = c < p.hidden && p.y != nullptr ? to_f32(static_cast<const T*>(p.y)[(int64_t)row * p.y_stride + c]) : 0.f;
+        s = fmaf(h[i], h[i], s);
+    }
+    float r = 1.f;
+    if (p.w_post != nullptr) r = rsqrtf(block_sum(s, part[0], warps) * inv + p.eps);
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * nt + (int)threadIdx.x;
+        if (c >= p.hidden) continue;
+        const float old = to_f32(static_cast<const R*>(p.residual)[(int64_t)row * p.hidden + c]);
+        if (p.y != nullptr) {
+            float w = p.branch_scale;
+            if (p.w_post != nullptr) w *= __ldg(p.w_post + c);
+            if (p.scale != nullptr) w *= __ldg(p.scale + c);
+            if (p.gate != nullptr) h[i] *= gate_act(to_f32(static_cast<const T*>(p.gate)[(int64_t)row * p.gate_stride + c]), p.act);
+            h[i] = fmaf(p.residual_scale, old, h[i] * r * w);
+            static_cast<R*>(p.residual_out)[(int64_t)row * p.hidden + c] = from_f32<R>(h[i]);
+        } else {
+            h[i] = old;
+        }
+        s = fmaf(h[i], h[i], s);
+    }
+    if (p.x == nullptr) return;
+    r = rsqrtf(block_sum(s, part[1], warps) * inv + p.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * nt + (int)threadIdx.x;
+        if (c >= p.hidden) continue;
+        const float w = p.w_pre != nullptr ? __ldg(p.w_pre + c) : 1.f;
+        static_cast<T*>(p.x)[(int64_t)row * p.hidden + c] = from_f32<T>(h[i] * r * w);
     }
 }
 
