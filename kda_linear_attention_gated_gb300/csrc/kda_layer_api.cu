@@ -90,7 +90,9 @@ cudaError_t launch_block_norm_rows(cudaLaunchConfig_t& cfg, const kda::BlockNorm
     auto kernel = kda::kda_block_norm_kernel<T, R, NV>;
     const int threads = ((units + NV - 1) / NV + 31) / 32 * 32;
     int occ = 0, sms = 0;
-    if (occupancy(reinterpret_cast<const void*>(kernel), threads, 0, &occ, &sms) != KDA_OK) return cudaErrorUnknown;
+    const size_t smem = kda::block_norm_smem<T, R, NV>(threads);
+    if (occupancy(reinterpret_cast<const void*>(kernel), threads, smem, &occ, &sms) != KDA_OK) return cudaErrorUnknown;
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = dim3((unsigned)std::min(prm.total, occ * sms));
     cfg.blockDim = dim3(threads);
     return cudaLaunchKernelEx(&cfg, kernel, prm);
@@ -289,7 +291,7 @@ int kda_head_norm(const kda_head_norm_args* args, uint32_t flags, void* stream) 
     prm.eps = g.eps;
     int lpr_log2 = 0;
     while ((8 << lpr_log2) < g.dim) ++lpr_log2;
-    const int64_t per = kda::HEAD_NORM_THREADS >> lpr_log2, ctas = (prm.rows + per - 1) / per;
+    const int64_t per = (kda::HEAD_NORM_THREADS >> lpr_log2) * kda::HEAD_NORM_ROWS, ctas = (prm.rows + per - 1) / per;
     if (ctas > 0x7fffffffLL) return KDA_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
