@@ -444,9 +444,9 @@ template <int D, int MODE> struct Kv4Smem {
     static constexpr int OFF_MERGE = RING, OFF_Q = OFF_MERGE + MERGE, OFF_ML = OFF_Q + Q,
                          OFF_ROW = OFF_ML + ML,              // row factors [16]
                          OFF_BAR = OFF_ROW + KV4_ROWS * 4,   // [warps][stages] barriers
-                         OFF_PLAN = OFF_BAR + WARPS * STAGES * 8,
-                         OFF_WALK = OFF_PLAN + 128,          // [warps][2] Kv4Walk, the first state
-                         BYTES = OFF_WALK + (WARPS * 2 + 1) * 80;
+                         OFF_FLAG = OFF_BAR + WARPS * STAGES * 8,
+                         OFF_WALK = OFF_FLAG + 16,           // [warps][3] Kv4Walk
+                         BYTES = OFF_WALK + WARPS * 3 * 96;
     static_assert(BYTES <= 115712, "two CTAs an SM");
 };
 
@@ -490,6 +490,7 @@ __device__ __forceinline__ int kv4_cost(const Kv4Req& q, int heads) {
 // part of one (request, head, row tile) whose units lie in the share.
 struct Kv4Walk {
     int64_t left;        // of the share, not yet taken
+    int64_t end, even;   // where the share ends in the list; an even share
     int r, off;          // request, and what is taken of it
     Kv4Req q;
     int seg, b0, b1;     // the current step: head * tiles + tile, units [b0, b1)
@@ -560,8 +561,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     float* ml = reinterpret_cast<float*>(smem + SM::OFF_ML);          // [warp][16] m, then l
     float* rowf = reinterpret_cast<float*>(smem + SM::OFF_ROW);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::OFF_BAR) + warp * KV4_STAGES;
-    int64_t* plan = reinterpret_cast<int64_t*>(smem + SM::OFF_PLAN);  // warp sums [8], the cuts [2], -, the even share
-    int* plan_i = reinterpret_cast<int*>(plan + 11);                  // a flag
+    volatile int* last_to_come = reinterpret_cast<int*>(smem + SM::OFF_FLAG);
 
     if (lane == 0) {
 #pragma unroll
@@ -571,66 +571,63 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
 
-    // ---- the share of this CTA: the list between two cuts ----
-    const int cnt = (p.n + KV4_THREADS - 1) / KV4_THREADS;
+    // what is being fetched, what comes next, what is being worked on: a warp's own, in shared
+    // memory (read seldom; the registers go to the accumulators)
+    static_assert(sizeof(Kv4Walk) <= 96, "Kv4Smem::OFF_WALK");
+    auto walk = [&](int i) -> Kv4Walk& { return *reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK + (3 * warp + i) * 96); };
+    Kv4Walk &put = walk(0), &get = walk(1), &cur = walk(2);
+
+    // ---- the share of this CTA: the list between two cuts; every warp finds it for itself ----
+    const int cnt = (p.n + 31) / 32;
     int64_t mine = 0;
     bool empty = false;
-    Kv4Req own;      // of a thread with one request
-    for (int r = tid * cnt; r < min(p.n, (tid + 1) * cnt); ++r) {
+    Kv4Req own;      // of a lane with one request
+#pragma unroll 2
+    for (int r = lane * cnt; r < min(p.n, (lane + 1) * cnt); ++r) {
         own = kv4_request(p, r, ROWS);
         mine += kv4_cost(own, p.heads);
         empty |= own.t > 0 && own.units == 0;
-        if (own.err && blockIdx.x == 0) atomicCAS(p.status, 0, own.err);
+        if (own.err && blockIdx.x == 0 && warp == 0) atomicCAS(p.status, 0, own.err);
     }
-    int64_t incl = mine;
+    int64_t before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+        const int64_t up = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += up;
     }
-    if (lane == 31) plan[warp] = incl;
-    const bool any_empty = __syncthreads_or(empty);
-    int64_t total = 0, before = 0;
+    const int64_t total = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    const int64_t even = max((int64_t)(SH::FIRST + SH::LAST),
+                             total <= 0x7fffffff ? (int64_t)(((unsigned)total + gridDim.x - 1) / gridDim.x)
+                                                 : (total + gridDim.x - 1) / gridDim.x);
+    int64_t cut[2];
 #pragma unroll
-    for (int w = 0; w < KV4_WARPS; ++w) {
-        const int64_t s = plan[w];
-        if (w < warp) before += s;
-        total += s;
-    }
-    before += incl - mine;
-    const int64_t even = total <= 0x7fffffff ? (int64_t)(((unsigned)total + gridDim.x - 1) / gridDim.x)
-                                             : (total + gridDim.x - 1) / gridDim.x;
-    const int64_t per = max((int64_t)(SH::FIRST + SH::LAST), even);
-    Kv4Walk& start = reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK)[2 * KV4_WARPS];
-#pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-        const int64_t cut = per * (blockIdx.x + k);
-        if (cut >= total) {
-            if (tid == 0) plan[8 + k] = total;
-        } else if (before <= cut && cut < before + mine) {
-            int r = tid * cnt, off = 0;
-            int64_t at = cut - before;
+        cut[k] = even * (blockIdx.x + k);
+        const bool here = before <= cut[k] && cut[k] < before + mine;
+        if (here) {
+            int64_t at = cut[k] - before;
             Kv4Req q = own;
+            int r = lane * cnt;
             for (;; ++r) {
                 if (cnt > 1) q = kv4_request(p, r, ROWS);
                 const int c = kv4_cost(q, p.heads);
                 if (at < c) break;
                 at -= c;
             }
-            off = (int)at;
-            const int each = q.units + KV4_PART, u = off % each;
+            const int each = q.units + KV4_PART, u = (int)at % each;
             const int move = u < SH::FIRST ? -u : each - u < SH::LAST ? each - u : 0;
-            plan[8 + k] = cut + move;
+            cut[k] += move;
             if (k == 0) {
-                start.r = r;
-                start.off = off + move;
-                start.q = q;
-                start.b0 = start.b1 = start.b = start.seg = 0;
+                get.r = r;
+                get.off = (int)at + move;
+                get.q = q;
             }
         }
+        const uint32_t who = __ballot_sync(0xffffffffu, here);
+        cut[k] = who ? __shfl_sync(0xffffffffu, cut[k], __ffs(who) - 1) : total;
     }
-    __syncthreads();
-    if (any_empty) {  // requests without a visible key: zero rows
+    if (__any_sync(0xffffffffu, empty)) {  // requests without a visible key: zero rows
         for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
             const Kv4Req q = kv4_request(p, r, ROWS);
             if (q.units > 0) continue;
@@ -639,27 +636,102 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 st_elem4(p.o, base + i, p.dtype, 0.f, 0.f, 0.f, 0.f);
         }
     }
-    if (plan[8] >= plan[9]) return;
-    if (tid == 0) plan[10] = per;       // kept for the joins
-
-    // what is being fetched, what is being worked on: a warp's own, in shared
-    // memory (read seldom; the registers go to the accumulators)
-    Kv4Walk& put = reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK)[2 * warp];
-    Kv4Walk& get = reinterpret_cast<Kv4Walk*>(smem + SM::OFF_WALK)[2 * warp + 1];
-    static_assert(sizeof(Kv4Walk) <= 80, "Kv4Smem::OFF_WALK");
-    if (lane == 0) {
-        Kv4Walk w = start;
-        w.left = plan[9] - plan[8];
-        put = w;
-        get = w;
-    }
+    if (cut[0] >= cut[1]) return;
     __syncwarp();
+    if (lane == 0) {
+        get.left = cut[1] - cut[0];
+        get.end = cut[1];
+        get.even = even;
+    }
     auto step = [&](Kv4Walk& w) {   // lane 0 walks, all lanes see it
         int ok = 0;
         __syncwarp();
         if (lane == 0) ok = w.next(p, ROWS);
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
+
+    // ---- queries: R rows a warp; loaded ahead, then rotated, scaled and rounded ----
+    constexpr int E = D / 32, R = (ROWS + KV4_WARPS - 1) / KV4_WARPS;
+    float x[R][E], y[R][E], cs[R][E], sn[R][E];
+    auto load_q = [&]() {
+        const int d = lane * E, half = p.rot >> 1, h = get.seg / get.q.tiles, i0 = (get.seg - h * get.q.tiles) * ROWS;
+        const bool first = d < half;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int i = i0 + warp + k * KV4_WARPS, j = i / p.grp, pos = get.q.ctx + j;
+            const int64_t base = (int64_t)(get.q.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + i - j * p.grp) * D;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                x[k][e] = y[k][e] = sn[k][e] = 0.f;
+                cs[k][e] = 1.f;
+            }
+            if (i - i0 >= ROWS || j >= get.q.t || pos < 0) continue;
+            ld_elems<E>(p.q, base + d, p.dtype, x[k]);
+            if (d < p.rot) {
+                const int64_t row = (int64_t)pos * half;
+                if (p.inter) {
+                    ld_elems<E / 2>(p.cos, row + d / 2, 0, cs[k]);
+                    ld_elems<E / 2>(p.sin, row + d / 2, 0, sn[k]);
+                } else {
+                    ld_elems<E>(p.q, base + (first ? d + half : d - half), p.dtype, y[k]);
+                    ld_elems<E>(p.cos, row + (first ? d : d - half), 0, cs[k]);
+                    ld_elems<E>(p.sin, row + (first ? d : d - half), 0, sn[k]);
+                }
+            }
+        }
+    };
+    auto store_q = [&]() {
+        const int d = lane * E;
+        const bool first = d < p.rot >> 1;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int i = warp + k * KV4_WARPS;
+            if (d < p.rot) {
+                if (p.inter) {
+#pragma unroll
+                    for (int e = E / 2 - 1; e >= 0; --e) {
+                        const float a = x[k][2 * e], b = x[k][2 * e + 1];
+                        x[k][2 * e] = a * cs[k][e] - b * sn[k][e];
+                        x[k][2 * e + 1] = b * cs[k][e] + a * sn[k][e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[k][e] = x[k][e] * cs[k][e] + (first ? -y[k][e] : y[k][e]) * sn[k][e];
+                }
+            }
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // 2^-z with amax 2^-z in [1/2, 1); rows of nothing, below 1e-30 or past 1e37 stay as they are
+            const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
+            // the factor is positive (not 0: a masked score times it stays -infinity), queries take the sign
+            const float down = __uint_as_float((uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u));
+            if (i < ROWS) {
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float u = x[k][e] * down, v = x[k][e + 1] * down;
+                    const __half2 hi = __floats2half2_rn(u, v);
+                    const int dd = d + e, at = (dd % (D / 4) / 8 * 4 + dd / (D / 4)) * 8 + dd % 8;
+                    *reinterpret_cast<__half2*>(qbuf + i * SM::QPITCH + at) = hi;
+                    if constexpr (SPLIT) {
+                        const float2 f = __half22float2(hi);
+                        *reinterpret_cast<__half2*>(qbuf + (i + 8) * SM::QPITCH + at) = __floats2half2_rn(u - f.x, v - f.y);
+                    }
+                }
+                if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
+            }
+        }
+    };
+    bool have = step(get);
+    if (have) load_q();
+    if (lane == 0) {
+        put = get;
+        put.b = have ? get.b0 + warp : 0;
+        if (!have) put.b1 = 0;
+    }
+    __syncwarp();
 
     const int bpp = p.page_tokens >> 4;
     // one register of flags: bits 0.. the slots' phase parities, 8.. two bits a slot, its blocks
@@ -722,83 +794,18 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 
     // the current tile's first row, a row's position and the tile's last one: worked out where
     // they are needed, not kept in registers
-    auto first_row = [&]() { return get.seg % get.q.tiles * ROWS; };
-    auto row_pos = [&](int i) { return get.q.ctx + (first_row() + i) / p.grp; };
-    auto last_row_pos = [&]() { return get.q.ctx + min(get.q.t - 1, (first_row() + ROWS - 1) / p.grp); };
+    auto first_row = [&]() { return cur.seg % cur.q.tiles * ROWS; };
+    auto row_pos = [&](int i) { return cur.q.ctx + (first_row() + i) / p.grp; };
+    auto last_row_pos = [&]() { return cur.q.ctx + min(cur.q.t - 1, (first_row() + ROWS - 1) / p.grp); };
 
-    while (step(get)) {
-        {
-        const int h = get.seg / get.q.tiles, i0 = first_row();
-        const int live = min(ROWS, get.q.t * p.grp - i0);
-        // ---- queries: rotate, scale, round; R rows a warp, all their loads first ----
-        constexpr int E = D / 32, R = (ROWS + KV4_WARPS - 1) / KV4_WARPS;
-        const int d = lane * E, half = p.rot >> 1;
-        const bool first = d < half, turned = d < p.rot;
-        float x[R][E], y[R][E], cs[R][E], sn[R][E];
+    while (have) {
+        store_q();
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int i = warp + k * KV4_WARPS, j = (i0 + i) / p.grp, pos = get.q.ctx + j;
-            const bool on = i < live && pos >= 0;
-            const int64_t base = (int64_t)(get.q.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + (i0 + i) - j * p.grp) * D;
+        for (int k = 0; k < R; ++k)      // not to be kept: the next part loads its own
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                x[k][e] = y[k][e] = sn[k][e] = 0.f;
-                cs[k][e] = 1.f;
-            }
-            if (on) ld_elems<E>(p.q, base + d, p.dtype, x[k]);
-            if (on && turned) {
-                const int64_t row = (int64_t)pos * half;
-                if (p.inter) {
-                    ld_elems<E / 2>(p.cos, row + d / 2, 0, cs[k]);
-                    ld_elems<E / 2>(p.sin, row + d / 2, 0, sn[k]);
-                } else {
-                    ld_elems<E>(p.q, base + (first ? d + half : d - half), p.dtype, y[k]);
-                    ld_elems<E>(p.cos, row + (first ? d : d - half), 0, cs[k]);
-                    ld_elems<E>(p.sin, row + (first ? d : d - half), 0, sn[k]);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int i = warp + k * KV4_WARPS;
-            if (turned) {
-                if (p.inter) {
-#pragma unroll
-                    for (int e = E / 2 - 1; e >= 0; --e) {
-                        const float a = x[k][2 * e], b = x[k][2 * e + 1];
-                        x[k][2 * e] = a * cs[k][e] - b * sn[k][e];
-                        x[k][2 * e + 1] = b * cs[k][e] + a * sn[k][e];
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[k][e] = x[k][e] * cs[k][e] + (first ? -y[k][e] : y[k][e]) * sn[k][e];
-                }
-            }
-            float amax = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // 2^-z with amax 2^-z in [1/2, 1); rows of nothing, below 1e-30 or infinite stay as they are
-            const int z = amax > 1e-30f && amax < 3e38f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
-            // the factor is positive (not 0: a masked score times it stays -infinity), queries take the sign
-            const float down = __uint_as_float((uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u));
-            if (i < ROWS) {
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float u = x[k][e] * down, v = x[k][e + 1] * down;
-                    const __half2 hi = __floats2half2_rn(u, v);
-                    const int dd = d + e, at = (dd % (D / 4) / 8 * 4 + dd / (D / 4)) * 8 + dd % 8;
-                    *reinterpret_cast<__half2*>(qbuf + i * SM::QPITCH + at) = hi;
-                    if constexpr (SPLIT) {
-                        const float2 f = __half22float2(hi);
-                        *reinterpret_cast<__half2*>(qbuf + (i + 8) * SM::QPITCH + at) = __floats2half2_rn(u - f.x, v - f.y);
-                    }
-                }
-                if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
-            }
-        }
-        }
+            for (int e = 0; e < E; ++e) x[k][e] = y[k][e] = cs[k][e] = sn[k][e] = 0.f;
+        __syncwarp();
+        if (lane == 0) cur = get;
         __syncthreads();
         // query fragments of row g and of row g + 8: eight channels, two k steps, a piece
         uint4 qa[D / 32], qb[MODE == KV4_8 ? 1 : D / 32];
@@ -830,7 +837,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             for (int j = 0; j < MT; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.f;
 
 #pragma unroll 1
-        for (int unit = get.q.first + get.b0 + warp, end = get.q.first + get.b1; unit < end; unit += KV4_WARPS) {
+        for (int unit = cur.q.first + cur.b0 + warp, end = cur.q.first + cur.b1; unit < end; unit += KV4_WARPS) {
             bool use = (flags & ALIVE) && (flags >> (8 + 2 * slot) & 3u) != 3u;
             if (use) {
                 use = mbar_wait(bars + slot, flags >> slot & 1u);
@@ -1020,9 +1027,9 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 
         // ---- the warps' sums of this part, joined in warp order ----
         __syncwarp();
-        const int h = get.seg / get.q.tiles, i0 = first_row(), live = min(ROWS, get.q.t * p.grp - i0);
-        const bool whole = get.b0 == 0 && get.b1 == get.q.units;
-        float* part = p.partials + (2 * blockIdx.x + (get.b0 == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
+        const int h = cur.seg / cur.q.tiles, i0 = first_row(), live = min(ROWS, cur.q.t * p.grp - i0);
+        const bool whole = cur.b0 == 0 && cur.b1 == cur.q.units;
+        float* part = p.partials + (2 * blockIdx.x + (cur.b0 == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
 #pragma unroll
         for (int a = 0; a < 2 * NB; ++a) {
 #pragma unroll
@@ -1034,7 +1041,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         }
         auto join = [&](int row, int d, float4 o, float M, float L) {
             const int j = (i0 + row) / p.grp;
-            const int64_t out = ((int64_t)(get.q.tok0 + j) * p.h_q + h * p.grp + (i0 + row) - j * p.grp) * D + d;
+            const int64_t out = ((int64_t)(cur.q.tok0 + j) * p.h_q + h * p.grp + (i0 + row) - j * p.grp) * D + d;
             const float f = L == 0.f ? 0.f : p.v_scale / L;
             if (L == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
             st_elem4(p.o, out, p.dtype, o.x * f, o.y * f, o.z * f, o.w * f);
@@ -1054,6 +1061,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                     for (int k = 0; k < D / 32; ++k)
                         *reinterpret_cast<float4*>(row + ((g3 * (D / 32) + k) ^ t3) * 4) =
                             make_float4(acc[a][2 * k][e], acc[a][2 * k][2 + e], acc[a][2 * k + 1][e], acc[a][2 * k + 1][2 + e]);
+                }
+                if (live <= 8 * (a + 1)) {     // the sums are written: their registers take the next part's queries
+                    have = step(get);
+                    if (have) load_q();
                 }
                 __syncthreads();
                 const int tid2 = tid_again(), ch = tid2 % CH;
@@ -1082,19 +1093,19 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         }
         if (!whole) {
             // CTAs that share this (request, head, tile): those between the cuts that stayed inside it
-            const int64_t seg0 = plan[9] - get.left - get.b1 - KV4_PART, share = plan[10];
+            const int64_t seg0 = cur.end - cur.left - cur.b1 - KV4_PART, share = cur.even;
             const int c0 = (int)((seg0 + SH::FIRST + share - 1) / share) - 1;
-            const int c1 = (int)((seg0 + get.q.units + KV4_PART - SH::LAST) / share);
+            const int c1 = (int)((seg0 + cur.q.units + KV4_PART - SH::LAST) / share);
             __syncthreads();
             if (tid == 0) {
                 __threadfence();        // the CTA's stores, ordered before by the barrier
                 const int old = atomicAdd(p.counters + c0, 1);
                 if (old == c1 - c0) p.counters[c0] = 0;
-                plan_i[0] = old == c1 - c0;
+                *last_to_come = old == c1 - c0;
                 __threadfence();
             }
             __syncthreads();
-            if (plan_i[0]) {
+            if (*last_to_come) {
                 // Thread groups a row wide; where there are more groups than rows, several share a
                 // row's parts and their sums meet in shared memory.
                 constexpr int GROUPS = KV4_THREADS / CH;
