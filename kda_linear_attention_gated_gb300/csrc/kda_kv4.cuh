@@ -125,6 +125,12 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+// Both halves of a times the low or the high half of s.
+template <bool HIGH> __device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t s) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&s);
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), HIGH ? __high2half2(h) : __low2half2(h));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 // Transposes an 8 x 8 matrix of 16-bit elements held two a lane (row lane / 4,
 // columns 2 (lane % 4) ..).
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
@@ -416,7 +422,7 @@ struct Kv4AttendParams {
 constexpr int KV4_8 = 0, KV4_REST = 1, KV4_16 = 2;
 constexpr int KV4_ROWS = 16;             // most rows of a tile
 constexpr int KV4_KEYS = 32;             // keys of a unit of work: two blocks
-constexpr int KV4_PART = 16;             // what beginning and ending a part costs a CTA, in units
+constexpr int KV4_PART = 24;             // what beginning and ending a part costs a CTA, in units
 constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
 constexpr int KV4_AHEAD = 16;            // units whose pages a warp looks up at a time: lanes 2 i, 2 i + 1 a block each
 constexpr float KV4_SLACK = 8.f;         // the running maximum may lag by this many powers of two
@@ -819,10 +825,11 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             }
         }
         // this lane's rows: 8 n + 2 t and the next, index 2 n + e
-        float m[2 * NB], l[2 * NB];
+        float m[2 * NB], l[2 * NB], bar[2 * NB];   // running maximum, sum, and the score above which the maximum moves
 #pragma unroll
         for (int a = 0; a < 2 * NB; ++a) {
             m[a] = -FLT_MAX;    // finite: nothing below is infinity minus infinity
+            bar[a] = -FLT_MAX;
             l[a] = 0.f;
         }
         auto row_of = [&](int a) { return 8 * (a >> 1) + 2 * t + (a & 1); };
@@ -857,21 +864,18 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                     const uint8_t* K = B + blk * F::BLOCK;
 #pragma unroll
                     for (int n = 0; n < NB; ++n) s[blk][n][0] = s[blk][n][1] = s[blk][n][2] = s[blk][n][3] = 0.f;
-                    uint32_t code[2][D / 32], sc[2][2];
+                    uint32_t code[2][D / 32], sc[2];   // sc: scales of the lane's two groups (D = 64: of its one)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         const int key = hf * 8 + g;
                         if constexpr (D == 128) {
                             const uint4 w = *reinterpret_cast<const uint4*>(K + F::KC + key * 64 + t * 16);
                             code[hf][0] = w.x; code[hf][1] = w.y; code[hf][2] = w.z; code[hf][3] = w.w;
-                            const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(K + F::KS + key * 8 + 2 * t));
-                            sc[hf][0] = __byte_perm(two, two, 0x1010);
-                            sc[hf][1] = __byte_perm(two, two, 0x3232);
+                            sc[hf] = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(K + F::KS + key * 8 + 2 * t));
                         } else {
                             const uint2 w = *reinterpret_cast<const uint2*>(K + F::KC + key * 32 + t * 8);
                             code[hf][0] = w.x; code[hf][1] = w.y;
-                            const uint32_t two = cvt_e4m3x2_f16x2(K[F::KS + key * 4 + t]);
-                            sc[hf][0] = sc[hf][1] = __byte_perm(two, two, 0x1010);
+                            sc[hf] = cvt_e4m3x2_f16x2(K[F::KS + key * 4 + t]);
                         }
                     }
 #pragma unroll
@@ -881,8 +885,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                         cvt_e2m1x8_f16(code[1][w], k1);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            k0[e] = hmul2_u32(k0[e], sc[0][w / 2]);
-                            k1[e] = hmul2_u32(k1[e], sc[1][w / 2]);
+                            k0[e] = w < 2 ? hmul2_half<false>(k0[e], sc[0]) : hmul2_half<true>(k0[e], sc[0]);
+                            k1[e] = w < 2 ? hmul2_half<false>(k1[e], sc[1]) : hmul2_half<true>(k1[e], sc[1]);
                         }
                         kv4_mma(s[blk][0], k0[0], k1[0], k0[1], k1[1], qa[w].x, qa[w].y);
                         if constexpr (MODE != KV4_8) kv4_mma(s[blk][NB - 1], k0[0], k1[0], k0[1], k1[1], qb[w].x, qb[w].y);
@@ -910,8 +914,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 #pragma unroll
                 for (int a = 0; a < 2 * NB; ++a) {
                     const int n = a >> 1, e = a & 1;
-                    top[a] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e])) * rowf[row_of(a)];
-                    grow |= top[a] > m[a] + KV4_SLACK;
+                    top[a] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+                    grow |= top[a] > bar[a];
                 }
                 // rarely: a score above the running maximum by more than its slack
                 if (__any_sync(0xffffffffu, grow)) {
@@ -919,7 +923,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                     for (int a = 0; a < 2 * NB; ++a) {
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], o));
+                        const float c = rowf[row_of(a)];
+                        top[a] *= c;
                         if (top[a] > m[a]) {
+                            bar[a] = (top[a] + KV4_SLACK) / c;
                             const float f = ex2f(m[a] - top[a]);
                             m[a] = top[a];
                             l[a] *= f;
