@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from ._build import LIB_DIR, SOURCES, build, lib_path  # noqa: F401  (re-exported)
@@ -165,12 +166,16 @@ class CkptPlaneDesc(ctypes.Structure):
                 ("num_entries", ctypes.c_int64), ("entry_stride", ctypes.c_int64)]
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(dt) -> int:
-    import torch
-    table = {torch.float32: KDA_F32, torch.float16: KDA_F16, torch.bfloat16: KDA_BF16}
-    if dt not in table:
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: KDA_F32, torch.float16: KDA_F16, torch.bfloat16: KDA_BF16})
+    if dt not in _dtype_codes:
         raise ValueError(f"dtype {dt} has no kda_dtype code")
-    return table[dt]
+    return _dtype_codes[dt]
 
 
 def pool_desc(pool) -> PoolDesc:
@@ -183,17 +188,30 @@ def pool_desc(pool) -> PoolDesc:
     return PoolDesc(pool.data_ptr(), _dtype_code(pool.dtype), hv, k, v, ns, pool.stride(0))
 
 
-def kv4_cache_desc(pages, k_scale=1.0, v_scale=1.0) -> Kv4CacheDesc:
-    """Descriptor of a uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor whose pages are dense."""
-    if pages.dim() != 4 or pages.element_size() != 1 or pages.is_floating_point() or not pages.is_cuda:
+# The same argument structs as native-layout packers: one pack() call makes the
+# bytes that the C side reads, at a fraction of a ctypes Structure's cost per
+# field (these calls serve decode steps of a few microseconds).  tests/test_layer_binding.py
+# holds them against the Structures above.
+_PACK_KV4_CACHE = struct.Struct("@P4i2q2f")
+_PACK_KV4_APPEND = struct.Struct("@10i2q9P")
+_PACK_KV4_ATTEND = struct.Struct("@10ifiq8Pq")
+_PACK_HEAD_NORM = struct.Struct("@6ifiq4P")
+_PACK_BLOCK_NORM = struct.Struct("@5i3f2q8P")
+
+
+def _kv4_cache(pages, k_scale, v_scale) -> tuple:
+    """Fields of a struct kda_kv4_cache over a uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor whose pages are dense."""
+    shape = pages.shape
+    if len(shape) != 4 or pages.dtype != _torch().uint8 or not pages.is_cuda:
         raise ValueError("a 4-bit cache is a CUDA uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor")
-    num, heads, blocks, size = pages.shape
-    if pages.stride(3) != 1 or pages.stride(2) != size or pages.stride(1) != blocks * size:
+    num, heads, blocks, size = shape
+    stride = pages.stride()
+    if stride[1:] != (blocks * size, size, 1):
         raise ValueError("the [heads, page_tokens / 16, 18 * dim] part of a 4-bit cache must be dense")
     dim, rest = divmod(size, 18)
     if rest:
         raise ValueError(f"the last dimension of a 4-bit cache is 18 * dim bytes, not {size}")
-    return Kv4CacheDesc(pages.data_ptr(), 16 * blocks, heads, dim, 0, num, pages.stride(0), k_scale, v_scale)
+    return pages.data_ptr(), 16 * blocks, heads, dim, 0, num, stride[0], k_scale, v_scale
 
 
 def _ptr(t) -> int | None:
@@ -214,50 +232,63 @@ def _expect(name, t, shape, dtypes) -> None:
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
-def _expect_rows(name, t, shape, dtype) -> int:
-    """As _expect for a tensor whose rows (its inner dimensions) are dense but may lie apart: the stride between them."""
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {tuple(shape)} {dtype} on CUDA")
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _is(name, t, shape, dtype) -> None:
+    """_expect for one dtype, with a short way through when all is well."""
+    if t is None or t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        _expect(name, t, shape, (dtype,))
+
+
+def _rows(name, t, shape, width, dtype) -> int:
+    """As _is for a tensor whose rows (its inner dimensions, `width` elements) are dense but may lie apart: the stride between them."""
+    if t is None or t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        _expect(name, t, shape, (dtype,))
     if t.is_contiguous():
-        width = 1
-        for d in shape[1:]:
-            width *= d
         return width
-    inner = 1
+    stride, inner = t.stride(), 1
     for d in range(len(shape) - 1, 0, -1):
-        if t.stride(d) != inner:
+        if stride[d] != inner and shape[d] != 1:
             raise ValueError(f"{name}: the dimensions behind the first must be dense")
         inner *= shape[d]
-    return t.stride(0)
+    return stride[0]
 
 
 def _tokens(cu_seqlens, max_t, n, total) -> int:
     """The most tokens of a request of a packed batch (see kda_step)."""
     if cu_seqlens is None:
-        return (total // n if n else 0) if max_t is None else int(max_t)
-    _expect("cu_seqlens", cu_seqlens, (n + 1,), (_torch().int32,))
+        return (total // n if n else 0) if max_t is None else max_t
+    _is("cu_seqlens", cu_seqlens, (n + 1,), _torch().int32)
     if max_t is None:
         raise ValueError("max_t is required with cu_seqlens")
-    return int(max_t)
+    return max_t
 
 
-def _rotation(cos, sin) -> tuple[int, int]:
-    """(rot_dim, rows) of a pair of fp32 [rows, rot_dim / 2] tables."""
+def _rotation(cos, sin) -> tuple:
+    """(rot_dim, rows, address, address) of a pair of fp32 [rows, rot_dim / 2] tables."""
     if cos is None and sin is None:
-        return 0, 0
+        return 0, 0, 0, 0
     if cos is None or sin is None:
         raise ValueError("cos and sin are given together")
-    if cos.dim() != 2:
+    shape, f32 = cos.shape, _torch().float32
+    if len(shape) != 2:
         raise ValueError("cos and sin are [rows, rot_dim / 2] tensors")
-    f32 = (_torch().float32,)
-    _expect("cos", cos, cos.shape, f32)
-    _expect("sin", sin, cos.shape, f32)
-    return 2 * cos.shape[1], cos.shape[0]
+    _is("cos", cos, shape, f32)
+    _is("sin", sin, shape, f32)
+    return 2 * shape[1], shape[0], cos.data_ptr(), sin.data_ptr()
 
 
-def _torch():
-    import torch
-    return torch
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 _libs: dict[bool, ctypes.CDLL] = {}
@@ -322,6 +353,12 @@ def _load(state16: bool) -> ctypes.CDLL:
         for fn, args in ((lib.kda_head_norm, HeadNormArgs), (lib.kda_block_norm, BlockNormArgs)):
             fn.restype = ctypes.c_int
             fn.argtypes = [ctypes.POINTER(args), u32, vp]
+        # the same entry points taking packed arguments
+        for name, kind in (("kda_kv4_append", 2), ("kda_kv4_attend", 2), ("kda_head_norm", 1), ("kda_block_norm", 1)):
+            fn = lib[name]
+            fn.restype = ctypes.c_int
+            fn.argtypes = [ctypes.c_char_p] * kind + [vp] * (kind == 2) + [u32, vp]
+            setattr(lib, "packed_" + name, fn)
         lib.kda_strerror.restype = ctypes.c_char_p
         lib.kda_strerror.argtypes = [i32]
         _libs[state16] = lib
@@ -731,6 +768,13 @@ class KdaLibrary:
                         "kda_prefill_chunked")
 
     # -- the operators around the recurrence ---------------------------------
+    @staticmethod
+    def _stream_of(t, stream) -> int:
+        """The caller's stream, or PyTorch's current one on the tensor's device."""
+        if stream is None:
+            return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
     def kda_kv4_page_bytes(self, page_tokens, heads, dim) -> int:
         """Bytes of a page of the 4-bit cache: heads * page_tokens / 16 * 18 * dim."""
         out = ctypes.c_int64(0)
@@ -747,26 +791,30 @@ class KdaLibrary:
         rotated by cos, sin [rows, rot_dim / 2] (see kda_kv4_append_args in
         include/kda.h): page_table [N, cols], ctx_len [N] the tokens in the
         cache before the call; k_out, v_out receive the values as stored."""
-        torch = _torch()
-        cache = kv4_cache_desc(pages, k_scale, v_scale)
-        n, total = int(page_table.shape[0]), int(k.shape[0])
-        shape = (total, cache.heads, cache.dim)
+        int32 = _torch().int32
+        cache = _kv4_cache(pages, k_scale, v_scale)
+        heads, dim = cache[2], cache[3]
+        n, cols = page_table.shape
+        total = k.shape[0]
+        shape, dtype = (total, heads, dim), k.dtype
         max_t = _tokens(cu_seqlens, max_t, n, total)
-        rot, rows = _rotation(cos, sin)
-        i32 = (torch.int32,)
-        _expect("page_table", page_table, (n, page_table.shape[-1]), i32)
-        _expect("ctx_len", ctx_len, (n,), i32)
-        _expect("status", status, (1,), i32)
-        ks, vs = _expect_rows("k", k, shape, k.dtype), _expect_rows("v", v, shape, k.dtype)
+        rot, rows, cos_at, sin_at = _rotation(cos, sin)
+        _is("page_table", page_table, (n, cols), int32)
+        _is("ctx_len", ctx_len, (n,), int32)
+        _is("status", status, (1,), int32)
+        ks, vs = _rows("k", k, shape, heads * dim, dtype), _rows("v", v, shape, heads * dim, dtype)
         out = None
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is not None:
-                _expect(name, t, shape, (out or t.dtype,))
-                out = t.dtype
-        args = Kv4AppendArgs(n, total, max_t, _dtype_code(k.dtype), page_table.shape[1], rot, int(bool(interleaved)), rows,
-                             0 if out is None else _dtype_code(out), 0, ks, vs, _ptr(cu_seqlens), page_table.data_ptr(),
-                             ctx_len.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(cos), _ptr(sin), _ptr(k_out), _ptr(v_out))
-        self._check(self.kda_kv4_append_raw(cache, args, status.data_ptr(), self._stream(stream), flags), "kda_kv4_append")
+                out = out or t.dtype
+                _is(name, t, shape, out)
+        args = _PACK_KV4_APPEND.pack(n, total, max_t, _dtype_code(dtype), cols, rot, bool(interleaved), rows,
+                                     0 if out is None else _dtype_code(out), 0, ks, vs, _at(cu_seqlens),
+                                     page_table.data_ptr(), ctx_len.data_ptr(), k.data_ptr(), v.data_ptr(), cos_at, sin_at,
+                                     _at(k_out), _at(v_out))
+        rc = self.lib.packed_kda_kv4_append(_PACK_KV4_CACHE.pack(*cache), args, status.data_ptr(), flags,
+                                            self._stream_of(pages, stream))
+        self._check(rc, "kda_kv4_append")
 
     def kda_kv4_attend_raw(self, cache: Kv4CacheDesc, args: Kv4AttendArgs, status, stream, flags=0) -> int:
         return self.lib.kda_kv4_attend(ctypes.byref(cache), ctypes.byref(args), status, flags, stream)
@@ -779,42 +827,47 @@ class KdaLibrary:
         lie apart), o alike and dense, ctx_len [N] the tokens in the cache
         before the step's own; workspace: KDA_KV4_WORKSPACE_BYTES bytes,
         zeroed once."""
-        torch = _torch()
-        cache = kv4_cache_desc(pages, k_scale, v_scale)
-        n, total, h_q = int(page_table.shape[0]), int(q.shape[0]), int(q.shape[1])
-        shape = (total, h_q, cache.dim)
+        int32 = _torch().int32
+        cache = _kv4_cache(pages, k_scale, v_scale)
+        n, cols = page_table.shape
+        total, h_q = q.shape[0], q.shape[1]
+        dim, dtype = cache[3], q.dtype
+        shape = (total, h_q, dim)
         max_t = _tokens(cu_seqlens, max_t, n, total)
-        rot, rows = _rotation(cos, sin)
-        i32 = (torch.int32,)
-        _expect("page_table", page_table, (n, page_table.shape[-1]), i32)
-        _expect("ctx_len", ctx_len, (n,), i32)
-        _expect("status", status, (1,), i32)
-        qs = _expect_rows("q", q, shape, q.dtype)
-        _expect("o", o, shape, (q.dtype,))
+        rot, rows, cos_at, sin_at = _rotation(cos, sin)
+        _is("page_table", page_table, (n, cols), int32)
+        _is("ctx_len", ctx_len, (n,), int32)
+        _is("status", status, (1,), int32)
+        qs = _rows("q", q, shape, h_q * dim, dtype)
+        _is("o", o, shape, dtype)
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
-        if scale is not None and scale == 0:
+        if scale is None:
+            scale = 0.0
+        elif scale == 0:
             raise ValueError("scale must not be zero")
-        args = Kv4AttendArgs(n, total, max_t, _dtype_code(q.dtype), page_table.shape[1], rot, int(bool(interleaved)), rows, h_q,
-                             int(window), 0.0 if scale is None else float(scale), 0, qs, _ptr(cu_seqlens),
-                             page_table.data_ptr(), ctx_len.data_ptr(), q.data_ptr(), _ptr(cos), _ptr(sin), o.data_ptr(),
-                             workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        self._check(self.kda_kv4_attend_raw(cache, args, status.data_ptr(), self._stream(stream), flags), "kda_kv4_attend")
+        args = _PACK_KV4_ATTEND.pack(n, total, max_t, _dtype_code(dtype), cols, rot, bool(interleaved), rows, h_q, window,
+                                     scale, 0, qs, _at(cu_seqlens), page_table.data_ptr(), ctx_len.data_ptr(), q.data_ptr(),
+                                     cos_at, sin_at, o.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size())
+        rc = self.lib.packed_kda_kv4_attend(_PACK_KV4_CACHE.pack(*cache), args, status.data_ptr(), flags,
+                                            self._stream_of(pages, stream))
+        self._check(rc, "kda_kv4_attend")
 
     def kda_head_norm(self, o, weight, y, gate=None, activation=1, eps=1e-6, stream=None, flags=0) -> None:
         """y = weight * o / rms(o) * act(gate) over the heads of o [total,
         heads, dim] (see kda_head_norm_args in include/kda.h): gate
         [total, heads, dim] of y's dtype (rows may lie apart), weight fp32
         [dim]; activation 0 none, 1 sigmoid, 2 SiLU."""
-        torch = _torch()
-        total, heads, dim = o.shape
-        _expect("o", o, (total, heads, dim), (o.dtype,))
-        _expect("y", y, (total, heads, dim), (y.dtype,))
-        _expect("weight", weight, (dim,), (torch.float32,))
-        gs = heads * dim if gate is None else _expect_rows("gate", gate, (total, heads, dim), y.dtype)
-        args = HeadNormArgs(total, heads, dim, _dtype_code(o.dtype), _dtype_code(y.dtype), int(activation), eps, 0, gs,
-                            o.data_ptr(), _ptr(gate), weight.data_ptr(), y.data_ptr())
-        self._check(self.lib.kda_head_norm(ctypes.byref(args), flags, self._stream(stream)), "kda_head_norm")
+        shape = o.shape
+        total, heads, dim = shape
+        _is("o", o, shape, o.dtype)
+        _is("y", y, shape, y.dtype)
+        _is("weight", weight, (dim,), _torch().float32)
+        gs = heads * dim if gate is None else _rows("gate", gate, shape, heads * dim, y.dtype)
+        args = _PACK_HEAD_NORM.pack(total, heads, dim, _dtype_code(o.dtype), _dtype_code(y.dtype), activation, eps, 0, gs,
+                                    o.data_ptr(), _at(gate), weight.data_ptr(), y.data_ptr())
+        self._check(self.lib.packed_kda_head_norm(args, flags, self._stream_of(o, stream)), "kda_head_norm")
 
     def kda_block_norm(self, residual, y, residual_out, w_post=None, gate=None, activation=1, scale=None, w_pre=None, x=None,
                        residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None, flags=0) -> None:
@@ -823,24 +876,27 @@ class KdaLibrary:
         [total, hidden] (fp32 or y's dtype; may be one tensor), y, gate
         [total, hidden] (rows may lie apart), x [total, hidden]; w_post,
         scale, w_pre fp32 [hidden].  y None: x is the norm of the residual."""
-        torch = _torch()
-        total, hidden = residual.shape
+        f32 = _torch().float32
+        shape = residual.shape
+        total, hidden = shape
         typed = x if y is None else y
         if typed is None:
             raise ValueError("y or x is required")
-        _expect("residual", residual, (total, hidden), (residual.dtype,))
+        dtype, rdtype = typed.dtype, residual.dtype
+        _is("residual", residual, shape, rdtype)
         ys = gs = hidden
         if y is not None:
-            ys = _expect_rows("y", y, (total, hidden), y.dtype)
-            _expect("residual_out", residual_out, (total, hidden), (residual.dtype,))
+            ys = _rows("y", y, shape, hidden, dtype)
+            _is("residual_out", residual_out, shape, rdtype)
         if gate is not None:
-            gs = _expect_rows("gate", gate, (total, hidden), typed.dtype)
+            gs = _rows("gate", gate, shape, hidden, dtype)
         if x is not None:
-            _expect("x", x, (total, hidden), (typed.dtype,))
+            _is("x", x, shape, dtype)
+        wide = (hidden,)
         for name, w in (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)):
             if w is not None:
-                _expect(name, w, (hidden,), (torch.float32,))
-        args = BlockNormArgs(total, hidden, _dtype_code(typed.dtype), _dtype_code(residual.dtype), int(activation), eps,
-                             residual_scale, branch_scale, ys, gs, residual.data_ptr(), _ptr(y), _ptr(gate), _ptr(w_post),
-                             _ptr(scale), _ptr(w_pre), _ptr(residual_out), _ptr(x))
-        self._check(self.lib.kda_block_norm(ctypes.byref(args), flags, self._stream(stream)), "kda_block_norm")
+                _is(name, w, wide, f32)
+        args = _PACK_BLOCK_NORM.pack(total, hidden, _dtype_code(dtype), _dtype_code(rdtype), activation, eps, residual_scale,
+                                     branch_scale, ys, gs, residual.data_ptr(), _at(y), _at(gate), _at(w_post), _at(scale),
+                                     _at(w_pre), _at(residual_out), _at(x))
+        self._check(self.lib.packed_kda_block_norm(args, flags, self._stream_of(residual, stream)), "kda_block_norm")

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <map>
 #include <mutex>
@@ -28,6 +29,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // kernel's dynamic shared-memory limit); cached per (kernel, device, threads).
 int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, int* sms) {
     static std::mutex mu;
+    static std::map<std::pair<const void*, int>, size_t> limit;
     static std::map<std::tuple<const void*, int, int>, std::pair<int, int>> cache;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_LAUNCH;
@@ -35,12 +37,14 @@ int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, 
     auto it = cache.find({kernel, dev, threads});
     if (it == cache.end()) {
         int occ = 0, count = 0;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-                cudaSuccess ||
+        size_t& most = limit[{kernel, dev}];
+        if ((smem > most && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+                                cudaSuccess) ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) != cudaSuccess ||
             cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             occ < 1)
             return KDA_ERR_LAUNCH;
+        most = std::max(most, smem);   // only ever raised: the same kernel runs with fewer threads and bytes too
         it = cache.emplace(std::make_tuple(kernel, dev, threads), std::make_pair(occ, count)).first;
     }
     *blocks_per_sm = it->second.first;
