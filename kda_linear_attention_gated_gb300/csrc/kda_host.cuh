@@ -27,7 +27,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 // Resident CTAs per SM of `kernel` with `smem` dynamic bytes (also raises the
 // kernel's dynamic shared-memory limit); cached per (kernel, device, threads).
-int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, int* sms) {
+int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, int* sms) try {
     static std::mutex mu;
     static std::map<std::pair<const void*, int>, size_t> limit;
     static std::map<std::tuple<const void*, int, int>, std::pair<int, int>> cache;
@@ -50,6 +50,8 @@ int occupancy(const void* kernel, int threads, size_t smem, int* blocks_per_sm, 
     *blocks_per_sm = it->second.first;
     *sms = it->second.second;
     return KDA_OK;
+} catch (...) {  // no memory for the cache: nothing leaves a C entry point as an exception
+    return KDA_ERR_LAUNCH;
 }
 
 // Programmatic dependent launch attribute when the caller asked for it.

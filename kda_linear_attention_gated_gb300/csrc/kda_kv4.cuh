@@ -175,32 +175,32 @@ struct Kv4AppendParams {
     int32_t* status;
 };
 
-constexpr int KV4_APPEND_THREADS = 256;
+constexpr int KV4_APPEND_THREADS = 128, KV4_APPEND_WARPS = KV4_APPEND_THREADS / 32;
 
-// Sixteen elements at element index i, 16-byte loads (the host checks the
-// alignment of base and stride).
-__device__ __forceinline__ void ld_elem16(const void* p, int64_t i, int dtype, float (&x)[16]) {
-    if (dtype == 0) {
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+// Sixteen elements of 2 or 4 bytes as loaded (the host checks the alignment of
+// base and stride), and widened to fp32.
+template <int ES> struct Raw16 { uint4 v[ES]; };
+template <int ES> __device__ __forceinline__ Raw16<ES> raw16(const void* p, int64_t i) {
+    Raw16<ES> r;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * ES);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 v = __ldg(q + j);
-            x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
-        }
-        return;
-    }
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    for (int j = 0; j < ES; ++j) r.v[j] = __ldg(q + j);
+    return r;
+}
+template <int ES> __device__ __forceinline__ void widen16(const Raw16<ES>& r, int dtype, float (&x)[16]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint4 v = __ldg(q + j);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int j = 0; j < ES; ++j) {
+        const uint32_t w[4] = {r.v[j].x, r.v[j].y, r.v[j].z, r.v[j].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float2 f;
-            if (dtype == 1) f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
-            x[8 * j + 2 * e] = f.x;
-            x[8 * j + 2 * e + 1] = f.y;
+            if constexpr (ES == 4) {
+                x[4 * j + e] = __uint_as_float(w[e]);
+            } else {
+                const float2 f = dtype == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&w[e]))
+                                            : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
+                x[8 * j + 2 * e] = f.x;
+                x[8 * j + 2 * e + 1] = f.y;
+            }
         }
     }
 }
@@ -209,28 +209,37 @@ __device__ __forceinline__ void ld_elem16(const void* p, int64_t i, int dtype, f
 //   t = x / scale of the cache (as a product with the reciprocal, 1 by default),
 //   s = e4m3(max|t| / 6), code = e2m1(t / s), each rounded to nearest even.
 // The quotients are those of IEEE division, so that a value half way between
-// two codes stays half way: max / 6 is one, and t / s is the product with the
-// rounded reciprocal, corrected once by its exact remainder (Markstein, IBM
-// Journal of Research and Development 34, 1990; s has four bits and lies in
-// 2^-9 .. 448; below 1/4 of a code, where the remainder may underflow, the code
-// is 0 either way).  A group that holds a NaN or an infinity gets a NaN scale:
-// it reads back as NaN.
+// two codes stays half way: the product with a reciprocal, corrected once by
+// its exact remainder (Markstein, IBM Journal of Research and Development 34,
+// 1990).  A reciprocal right to 2^-22 leaves the corrected quotient within 2^-44
+// of the true one, and a quotient by 6 or by a scale (four bits) that is no
+// float lies 2^-28 or more from the middle of two floats, so it rounds alike;
+// where the remainder may underflow the code is 0 either way.  A group that
+// holds a NaN or an infinity gets a NaN scale: it reads back as NaN.
 __device__ __forceinline__ uint32_t kv4_round(float* x, float inv, uint2& code) {
-    uint32_t amax = 0;  // bit patterns of |t| order like the values, NaN above infinity
+    if (inv != 1.f) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = __fmul_rn(x[j], inv);
+    }
+    float amax = 0.f, odd = 0.f;    // odd: NaN if a value is not finite (the maximum passes NaN over)
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-        x[j] = __fmul_rn(x[j], inv);
-        amax = max(amax, __float_as_uint(x[j]) & 0x7fffffffu);
+        amax = fmaxf(amax, fabsf(x[j]));
+        odd = fmaf(x[j], 0.f, odd);
     }
-    const bool fine = amax < 0x7f800000u;
-    const uint32_t s8 = fine ? cvt_f32_e4m3(__fdiv_rn(__uint_as_float(amax), 6.0f)) : 0x7fu;
+    constexpr float sixth = 1.f / 6.f;
+    const bool fine = odd == 0.f;
+    const uint32_t s8 = fine ? cvt_f32_e4m3(fmaf(-fmaf(amax * sixth, 6.f, -amax), sixth, amax * sixth)) : 0x7fu;
     const uint32_t sh = cvt_e4m3x2_f16x2(s8);
     const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-    const float rs = s > 0.f ? __frcp_rn(s) : 0.f;
+    float rs;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
+    if (!(s > 0.f)) rs = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
+        // as fma(q, s, -x) and minus its product, so that the sign of a zero stays
         const float q = x[j] * rs;
-        x[j] = copysignf(fmaf(fmaf(-q, s, x[j]), rs, q), x[j]);
+        x[j] = fmaf(-fmaf(q, s, -x[j]), rs, q);
     }
     code = fine ? make_uint2(cvt_f32x8_e2m1(x), cvt_f32x8_e2m1(x + 8)) : make_uint2(0u, 0u);
     return s8;
@@ -255,8 +264,12 @@ __device__ __forceinline__ void kv4_values(void* out, int64_t i, int dtype, uint
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q[j]));
-        x[2 * j] = f.x * g;
-        x[2 * j + 1] = f.y * g;
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+    }
+    if (g != 1.f) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= g;
     }
     if (dtype == 2) {
         uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + i);
@@ -285,15 +298,31 @@ __device__ __forceinline__ void kv4_turn(float& a, float& b, float c, float s) {
 // rotation pairs, so that every key and every table entry is loaded once.  A
 // warp's loads are whole 128-byte lines of a token (16-bit inputs), its key
 // codes whole 32-byte sectors, and its value codes 64 contiguous bytes when
-// the eight tokens fill half a block.  Rotation in fp32, products and sums
-// rounded one by one (no fused multiply-add).
-template <int D>
-__global__ void __launch_bounds__(KV4_APPEND_THREADS) kda_kv4_append_kernel(const Kv4AppendParams p) {
+// the eight tokens fill half a block.  The loads of a head do not wait for the
+// token's place: they are on their way while that is looked up.  Rotation in fp32, products and sums rounded one by
+// one (no fused multiply-add).
+template <int D, int ES>
+__global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_append_kernel(const Kv4AppendParams p) {
     constexpr int NG = Kv4<D>::NG, NP = NG / 2, HW = 4 / NP;     // groups and pairs of a head, heads of a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
     const int tok = (int)blockIdx.x * 8 + (lane >> 2);
+    // this lane's two groups: those of a rotated pair of halves, else neighbours
+    const int i = (lane & 3) % NP, half = p.rot >> 1, rg = p.rot >> 4;
+    const bool halves = !p.inter && 2 * i < rg;
+    const int grp[2] = {halves ? i : 2 * i, halves ? i + (rg >> 1) : 2 * i + 1};
+    const int items = (p.heads + HW - 1) / HW * 2, step = KV4_APPEND_WARPS * (int)gridDim.y;   // heads of k and of v in turn
+    int it = (int)blockIdx.y * KV4_APPEND_WARPS + warp;
+    Raw16<ES> raw[2];
+    auto load = [&](int at) {
+        const int h = (at >> 1) * HW + (lane & 3) / NP;
+        if (at >= items || h >= p.heads || tok >= p.total) return;
+        const int64_t base = (int64_t)tok * (at & 1 ? p.v_stride : p.k_stride) + h * D;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) raw[k] = raw16<ES>(at & 1 ? p.v : p.k, base + grp[k] * 16);
+    };
+    load(it);
     // the request that owns the token: the number of requests that end at or before it
     int r;
     if (p.cu == nullptr) {
@@ -309,11 +338,12 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS) kda_kv4_append_kernel(cons
             }
         }
     }
-    if (tok >= p.total) return;
     int pos = -1;
     uint8_t* blk = nullptr;   // the token's block of head 0
     int where = 0;
-    if (r < p.n) {
+    if (tok >= p.total) {
+        return;
+    } else if (r < p.n) {
         const int tok0 = p.cu ? __ldg(p.cu + r) : r * p.max_t;
         const int t = (p.cu ? __ldg(p.cu + r + 1) : tok0 + p.max_t) - tok0;
         const int64_t at = (int64_t)__ldg(p.ctx + r) + (tok - tok0);
@@ -335,14 +365,15 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS) kda_kv4_append_kernel(cons
         atomicCAS(p.status, 0, STATUS_ARG);
     }
     const int64_t head_bytes = (int64_t)(p.page_tokens >> 4) * Kv4<D>::BLOCK;
-    // this lane's two groups: those of a rotated pair of halves, else neighbours
-    const int i = (lane & 3) % NP, half = p.rot >> 1, rg = p.rot >> 4;
-    const bool halves = !p.inter && 2 * i < rg;
-    const int grp[2] = {halves ? i : 2 * i, halves ? i + (rg >> 1) : 2 * i + 1};
-    const int items = (p.heads + HW - 1) / HW * 2;
-    for (int it = (int)blockIdx.y * 8 + warp; it < items; it += 8 * (int)gridDim.y) {
+    bool late = false;
+    for (; it < items; it += step) {
+        if (late) load(it);
+        late = true;
         const bool is_v = (it & 1) != 0;
         const int h = (it >> 1) * HW + (lane & 3) / NP;
+        float x[2][16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) widen16<ES>(raw[k], p.dtype, x[k]);
         if (h >= p.heads) continue;
         void* out = is_v ? p.v_out : p.k_out;
         const int64_t row = ((int64_t)tok * p.heads + h) * D;
@@ -354,11 +385,6 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS) kda_kv4_append_kernel(cons
                     for (int j = 0; j < 16; j += 4) st_elem4(out, row + grp[k] * 16 + j, p.out_dtype, 0.f, 0.f, 0.f, 0.f);
             continue;
         }
-        float x[2][16];
-        const void* src = is_v ? p.v : p.k;
-        const int64_t base = (int64_t)tok * (is_v ? p.v_stride : p.k_stride) + h * D;
-        ld_elem16(src, base + grp[0] * 16, p.dtype, x[0]);
-        ld_elem16(src, base + grp[1] * 16, p.dtype, x[1]);
         if (!is_v && 2 * i < rg) {
             const float* cs = p.cos + (int64_t)pos * half;
             const float* sn = p.sin + (int64_t)pos * half;

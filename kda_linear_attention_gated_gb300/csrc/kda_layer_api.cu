@@ -178,15 +178,19 @@ int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, 
     prm.status = dev_status;
     // eight tokens a CTA; few tokens share their heads out over more CTAs
     const int tokens = (int)(((int64_t)g.total + 7) / 8), items = cache->dim == 128 ? cache->heads * 2 : (cache->heads + 1) / 2 * 2;
-    const int parts = std::max(1, std::min((items + 7) / 8, 608 / tokens));
+    const int parts = std::max(1, std::min((items + kda::KV4_APPEND_WARPS - 1) / kda::KV4_APPEND_WARPS, 2432 / tokens));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tokens, (unsigned)parts, 1);
     cfg.blockDim = dim3(kda::KV4_APPEND_THREADS, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr;
     set_pdl(cfg, &attr, flags);
-    const cudaError_t err = cache->dim == 128 ? cudaLaunchKernelEx(&cfg, kda::kda_kv4_append_kernel<128>, prm)
-                                              : cudaLaunchKernelEx(&cfg, kda::kda_kv4_append_kernel<64>, prm);
+    using namespace kda;
+    const cudaError_t err =
+        cache->dim == 128 ? (es == 2 ? cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<128, 2>, prm)
+                                     : cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<128, 4>, prm))
+                          : (es == 2 ? cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<64, 2>, prm)
+                                     : cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<64, 4>, prm));
     return err == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
