@@ -295,8 +295,8 @@ int kda_head_norm(const kda_head_norm_args* args, uint32_t flags, void* stream) 
     prm.eps = g.eps;
     int lpr_log2 = 0;
     while ((8 << lpr_log2) < g.dim) ++lpr_log2;
-    const int64_t per = (kda::HEAD_NORM_THREADS >> lpr_log2) * kda::HEAD_NORM_ROWS, ctas = (prm.rows + per - 1) / per;
-    if (ctas > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    const int64_t per = kda::HEAD_NORM_THREADS >> lpr_log2, ctas = (prm.rows + per - 1) / per;
+    if (prm.rows > 0x7fffffffLL) return KDA_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(kda::HEAD_NORM_THREADS, 1, 1);
