@@ -151,6 +151,12 @@ __device__ __forceinline__ void kv4_mma(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float ex2f(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -221,14 +227,11 @@ __device__ __forceinline__ uint32_t kv4_round(float* x, float inv, uint2& code) 
 #pragma unroll
         for (int j = 0; j < 16; ++j) x[j] = __fmul_rn(x[j], inv);
     }
-    float amax = 0.f, odd = 0.f;    // odd: NaN if a value is not finite (the maximum passes NaN over)
+    float amax = 0.f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        amax = fmaxf(amax, fabsf(x[j]));
-        odd = fmaf(x[j], 0.f, odd);
-    }
+    for (int j = 0; j < 16; j += 2) amax = max3_nan(amax, fabsf(x[j]), fabsf(x[j + 1]));
     constexpr float sixth = 1.f / 6.f;
-    const bool fine = odd == 0.f;
+    const bool fine = amax <= FLT_MAX;
     const uint32_t s8 = fine ? cvt_f32_e4m3(fmaf(-fmaf(amax * sixth, 6.f, -amax), sixth, amax * sixth)) : 0x7fu;
     const uint32_t sh = cvt_e4m3x2_f16x2(s8);
     const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
@@ -323,20 +326,18 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_a
         for (int k = 0; k < 2; ++k) raw[k] = raw16<ES>(at & 1 ? p.v : p.k, base + grp[k] * 16);
     };
     load(it);
-    // the request that owns the token: the number of requests that end at or before it
-    int r;
+    // the request that owns the token: the number of requests that end at or before it, counted
+    // for the CTA's first token and from there on
+    int r = 0;
     if (p.cu == nullptr) {
         r = tok / p.max_t;
     } else {
-        r = 0;
+        const int tok8 = (int)blockIdx.x * 8;
         for (int b = 0; b < p.n; b += 32) {
             const int32_t end = b + lane < p.n ? __ldg(p.cu + b + lane + 1) : 0x7fffffff;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = __popc(__ballot_sync(0xffffffffu, end <= (int)blockIdx.x * 8 + j));
-                if (j == (lane >> 2)) r += c;
-            }
+            r += __popc(__ballot_sync(0xffffffffu, end <= tok8));
         }
+        while (r < p.n && tok < p.total && __ldg(p.cu + r + 1) <= tok) ++r;
     }
     int pos = -1;
     uint8_t* blk = nullptr;   // the token's block of head 0
@@ -525,7 +526,7 @@ struct Kv4Walk {
     int64_t end, even;   // where the share ends in the list; an even share
     int r, off;          // request, and what is taken of it
     Kv4Req q;
-    int seg, b0, b1;     // the current step: head * tiles + tile, units [b0, b1)
+    int h, i0, b0, b1;   // the current step: head, first row of the tile, units [b0, b1)
     int b;               // (fetching) this warp's next unit not looked up
     __device__ __forceinline__ bool next(const Kv4AttendParams& p, int rows) {
         do {
@@ -536,8 +537,9 @@ struct Kv4Walk {
                 off = 0;
             }
             const int each = q.units + KV4_PART;
-            seg = off / each;
-            const int u = off - seg * each;
+            const int seg = off / each, u = off - seg * each;
+            h = seg / q.tiles;
+            i0 = (seg - h * q.tiles) * rows;
             const int take = (int)min((int64_t)(each - u), left);
             b0 = max(0, u - KV4_PART);
             b1 = max(0, u + take - KV4_PART);
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     constexpr int E = D / 32, R = (ROWS + KV4_WARPS - 1) / KV4_WARPS;
     float x[R][E], y[R][E], cs[R][E], sn[R][E];
     auto load_q = [&]() {
-        const int d = lane * E, half = p.rot >> 1, h = get.seg / get.q.tiles, i0 = (get.seg - h * get.q.tiles) * ROWS;
+        const int d = lane * E, half = p.rot >> 1, h = get.h, i0 = get.i0;
         const bool first = d < half;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -788,7 +790,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             const int pg = b / bpp, page = __ldg(p.table + (int64_t)put.r * p.cols + pg);
             ok = page >= 0 && page < p.num_pages;
             if (!ok) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
-            from = p.pages + (int64_t)page * p.page_stride + ((int64_t)(put.seg / put.q.tiles) * bpp + (b - pg * bpp)) * F::BLOCK;
+            from = p.pages + (int64_t)page * p.page_stride + ((int64_t)put.h * bpp + (b - pg * bpp)) * F::BLOCK;
         }
         there = __ballot_sync(0xffffffffu, ok);
         looked = min(KV4_AHEAD, (put.b1 - first + KV4_WARPS - 1) / KV4_WARPS);
@@ -824,11 +826,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     for (int s = 0; s < KV4_STAGES; ++s) fetch(s);
     uint32_t slot = 0;                  // the slot to work on, and then to fetch into
 
-    // the current tile's first row, a row's position and the tile's last one: worked out where
-    // they are needed, not kept in registers
-    auto first_row = [&]() { return cur.seg % cur.q.tiles * ROWS; };
-    auto row_pos = [&](int i) { return cur.q.ctx + (first_row() + i) / p.grp; };
-    auto last_row_pos = [&]() { return cur.q.ctx + min(cur.q.t - 1, (first_row() + ROWS - 1) / p.grp); };
+    // a row's position and the tile's last one: worked out where they are needed, not kept in
+    // registers
+    auto row_pos = [&](int i) { return cur.q.ctx + (cur.i0 + i) / p.grp; };
+    auto last_row_pos = [&]() { return cur.q.ctx + min(cur.q.t - 1, (cur.i0 + ROWS - 1) / p.grp); };
 
     while (have) {
         store_q();
@@ -851,11 +852,12 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             }
         }
         // this lane's rows: 8 n + 2 t and the next, index 2 n + e
-        float m[2 * NB], l[2 * NB], bar[2 * NB];   // running maximum, sum, and the score above which the maximum moves
+        float m[2 * NB], l[2 * NB];     // running maximum and sum
+        float bar[2];                   // the score above which the maximum moves (with two sets of rows worked out each time)
 #pragma unroll
         for (int a = 0; a < 2 * NB; ++a) {
             m[a] = -FLT_MAX;    // finite: nothing below is infinity minus infinity
-            bar[a] = -FLT_MAX;
+            if constexpr (NB == 1) bar[a] = -FLT_MAX;
             l[a] = 0.f;
         }
         auto row_of = [&](int a) { return 8 * (a >> 1) + 2 * t + (a & 1); };
@@ -941,7 +943,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 for (int a = 0; a < 2 * NB; ++a) {
                     const int n = a >> 1, e = a & 1;
                     top[a] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
-                    grow |= top[a] > bar[a];
+                    if constexpr (NB == 1) grow |= top[a] > bar[a];
+                    else grow |= top[a] * rowf[row_of(a)] > m[a] + KV4_SLACK;
                 }
                 // rarely: a score above the running maximum by more than its slack
                 if (__any_sync(0xffffffffu, grow)) {
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                         const float c = rowf[row_of(a)];
                         top[a] *= c;
                         if (top[a] > m[a]) {
-                            bar[a] = (top[a] + KV4_SLACK) / c;
+                            if constexpr (NB == 1) bar[a] = (top[a] + KV4_SLACK) / c;
                             const float f = ex2f(m[a] - top[a]);
                             m[a] = top[a];
                             l[a] *= f;
@@ -1060,7 +1063,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 
         // ---- the warps' sums of this part, joined in warp order ----
         __syncwarp();
-        const int h = cur.seg / cur.q.tiles, i0 = first_row(), live = min(ROWS, cur.q.t * p.grp - i0);
+        const int live = min(ROWS, cur.q.t * p.grp - cur.i0);
         const bool whole = cur.b0 == 0 && cur.b1 == cur.q.units;
         float* part = p.partials + (2 * blockIdx.x + (cur.b0 == 0 ? 1 : 0)) * (KV4_ROWS * (D + 2));
 #pragma unroll
@@ -1072,9 +1075,9 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 ml[(warp * KV4_ROWS + row_of(a)) * 2 + 1] = l[a];
             }
         }
-        auto join = [&](int row, int d, float4 o, float M, float L) {
-            const int j = (i0 + row) / p.grp;
-            const int64_t out = ((int64_t)(cur.q.tok0 + j) * p.h_q + h * p.grp + (i0 + row) - j * p.grp) * D + d;
+        auto join = [&](int row, int d, float4 o, float L) {
+            const int j = (cur.i0 + row) / p.grp;
+            const int64_t out = ((int64_t)(cur.q.tok0 + j) * p.h_q + cur.h * p.grp + (cur.i0 + row) - j * p.grp) * D + d;
             const float f = L == 0.f ? 0.f : p.v_scale / L;
             if (L == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
             st_elem4(p.o, out, p.dtype, o.x * f, o.y * f, o.z * f, o.w * f);
@@ -1116,7 +1119,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                         o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
                     }
                     if (whole) {
-                        join(row + 8 * a, ch * 4, o, M, L);
+                        join(row + 8 * a, ch * 4, o, L);
                     } else {
                         __stcg(reinterpret_cast<float4*>(part + (row + 8 * a) * D + ch * 4), o);
                         if (ch == 0) __stcg(reinterpret_cast<float2*>(part + KV4_ROWS * D) + row + 8 * a, make_float2(M, L));
@@ -1179,7 +1182,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                             L += ml[grp + k];
                         }
                     }
-                    if (on && kk == 0) join(row, ch * 4, o, M, L);
+                    if (on && kk == 0) join(row, ch * 4, o, L);
                 }
             }
         }
