@@ -84,25 +84,28 @@ cudaError_t launch_head_norm_t(const cudaLaunchConfig_t& cfg, const kda::HeadNor
     }
 }
 
-// Rows in turn over CTAs that all fit the card at once.
-template <typename T, typename R, int NV>
+// Rows in turn over CTAs that all fit the card at once, eight channels a thread.
+template <typename T, typename R, bool SHIFT>
 cudaError_t launch_block_norm_rows(cudaLaunchConfig_t& cfg, const kda::BlockNormParams& prm, int units) {
-    auto kernel = kda::kda_block_norm_kernel<T, R, NV>;
-    const int threads = ((units + NV - 1) / NV + 31) / 32 * 32;
+    auto kernel = kda::kda_block_norm_kernel<T, R, SHIFT>;
+    const int threads = (units + 31) / 32 * 32;
     int occ = 0, sms = 0;
-    const size_t smem = kda::block_norm_smem<T, R, NV>(threads);
+    const size_t smem = kda::block_norm_smem<T, R>(threads);
     if (occupancy(reinterpret_cast<const void*>(kernel), threads, smem, &occ, &sms) != KDA_OK) return cudaErrorUnknown;
     cfg.dynamicSmemBytes = smem;
-    cfg.gridDim = dim3((unsigned)std::min(prm.total, occ * sms));
+    const int most = SHIFT ? occ * sms & ~7 : occ * sms;   // see the kernel
+    cfg.gridDim = dim3((unsigned)std::min(prm.total, most));
     cfg.blockDim = dim3(threads);
     return cudaLaunchKernelEx(&cfg, kernel, prm);
 }
 
+// vec: buffers start on 16 bytes and every stride is the width apart from a multiple of eight
 template <typename T, typename R>
 cudaError_t launch_block_norm(cudaLaunchConfig_t& cfg, const kda::BlockNormParams& prm, bool vec) {
-    const int units = prm.hidden / 8;
-    if (vec && units <= 512) return launch_block_norm_rows<T, R, 1>(cfg, prm, units);
-    if (vec && units <= 1024) return launch_block_norm_rows<T, R, 2>(cfg, prm, units);
+    const bool shift = prm.hidden % 8 != 0;
+    const int units = shift ? (prm.hidden + 14) / 8 : prm.hidden / 8;   // vectors that a row can touch
+    if (vec && units <= 1024)
+        return shift ? launch_block_norm_rows<T, R, true>(cfg, prm, units) : launch_block_norm_rows<T, R, false>(cfg, prm, units);
     const int nv = prm.hidden <= 4096 ? 4 : 16;
     cfg.gridDim = dim3((unsigned)prm.total);
     cfg.blockDim = dim3(((prm.hidden + nv - 1) / nv + 31) / 32 * 32);
@@ -329,8 +332,8 @@ int kda_block_norm(const kda_block_norm_args* args, uint32_t flags, void* stream
     const void* typed[4] = {g.y, g.gate, g.x, nullptr};
     const void* res[2] = {g.residual, g.residual_out};
     const void* w[3] = {g.w_post, g.scale, g.w_pre};
-    // eight channels a thread when every address and stride is a multiple of 16 bytes, else one
-    bool vec = g.hidden % 8 == 0 && (!g.y || g.y_stride * es % 16 == 0) && (!g.gate || g.gate_stride * es % 16 == 0);
+    // eight channels an access when buffers start on 16 bytes and rows keep in step (launch_block_norm), else one
+    bool vec = (!g.y || (g.y_stride - g.hidden) % 8 == 0) && (!g.gate || (g.gate_stride - g.hidden) % 8 == 0);
     for (const void* t : typed) {
         if (!aligned(t, es)) return KDA_ERR_ALIGN;
         vec = vec && aligned(t, 16);
@@ -341,7 +344,7 @@ int kda_block_norm(const kda_block_norm_args* args, uint32_t flags, void* stream
     }
     for (const void* t : w) {
         if (!aligned(t, 4)) return KDA_ERR_ALIGN;
-        vec = vec && aligned(t, 16);
+        vec = vec && (g.hidden % 8 != 0 || aligned(t, 16));
     }
     kda::BlockNormParams prm;
     prm.residual = g.residual;

@@ -4,6 +4,8 @@
 // and products are fp32, each output is rounded once, to nearest even.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_common.cuh"
 
 namespace kda {
@@ -173,113 +175,145 @@ __device__ __forceinline__ float block_sum(float x, float* part, int warps) {
     return warp_sum(lane < warps ? part[lane] : 0.f);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes to shared memory; with `bytes` below 16 only so many are read, the rest is zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows in shared memory at a time, each its residual, y and gate: three, or two
-// of the widest (8192 channels of fp32 are 96 KB).
-template <typename T, int NV> struct BlockNormStages { static constexpr int N = NV == 2 && sizeof(T) == 4 ? 2 : 3; };
-template <typename T, typename R, int NV> constexpr size_t block_norm_smem(int threads) {
-    return (size_t)BlockNormStages<T, NV>::N * NV * (8 * sizeof(R) + 16 * sizeof(T)) * threads;
+// Rows in shared memory at a time, each its residual, y and gate.  Two: with three
+// fewer CTAs fit an SM (8192 x 4096: 86.5 us against 83; 1021 x 2049 of fp32:
+// 11.2 against 10.7).
+constexpr int BLOCK_NORM_STAGES = 2;
+template <typename T, typename R> constexpr size_t block_norm_smem(int threads) {
+    return (size_t)BLOCK_NORM_STAGES * (8 * sizeof(R) + 16 * sizeof(T)) * threads;
 }
 
 // h = a residual + b scale act(gate) [w_post y / rms(y)]; x = w_pre h / rms(h).
 // Bound by memory: every element of a row is read and written once, the row
-// stays in registers across both sums.  A CTA takes rows in turn, its threads
-// NV vectors of eight channels each; the weights stay in registers for all its
-// rows (reading them again for every row is half as many bytes again, from
-// L2).  The next rows are on their way to shared memory meanwhile: a thread
-// copies and reads only its own places, so the copies need no barrier.
-template <typename T, typename R, int NV>
-__global__ void __launch_bounds__(512) kda_block_norm_kernel(const BlockNormParams p) {
+// stays in registers across both sums.  A CTA takes rows in turn, eight channels
+// a thread (with two vectors a thread the registers leave half as many warps:
+// 2000 x 5001 33 against 30 us); the weights stay in registers for all its rows
+// (reading them again for every row is half as many bytes again, from L2).  The
+// next row is on its way to shared memory meanwhile: a thread copies and reads
+// only its own places, so the copies need no barrier.  8192 x 4096, bf16 with an
+// fp32 residual: 83 us, 0.84 of the measured copy bandwidth.
+//
+// SHIFT: a width that is no multiple of eight.  Vectors then lie on multiples
+// of eight in the buffer, not in the row: a row's first one begins up to seven
+// channels before it.  The grid is a multiple of eight (or holds every row), so
+// a CTA's rows all begin at the same place in a vector and the weights still
+// stay in registers; a row's two end vectors are masked, their stores are
+// single.  4096 x 1537: 21.5 us, 1536 wide 17.4.
+template <typename T, typename R, bool SHIFT>
+__global__ void __launch_bounds__(1024) kda_block_norm_kernel(const BlockNormParams p) {
     constexpr int CR = (int)sizeof(R) / 2, CT = (int)sizeof(T) / 2, CH = CR + 2 * CT;   // 16-byte chunks of a vector
-    constexpr int STAGES = BlockNormStages<T, NV>::N;
+    constexpr int STAGES = BLOCK_NORM_STAGES;
     extern __shared__ __align__(16) uint4 norm_ring[];
     __shared__ float part[2][32];
     const int nt = blockDim.x, warps = nt >> 5;
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
     const float inv = 1.f / (float)p.hidden;
-    auto at = [&](int stage, int i, int k) { return norm_ring + ((stage * NV + i) * CH + k) * nt + threadIdx.x; };
-    auto fetch = [&](int row, int stage) {
-        if (row < p.total) {
+    const int shift = SHIFT ? (int)((int64_t)blockIdx.x * p.hidden & 7) : 0;
+    const int c = (int)threadIdx.x * 8 - shift;      // this thread's channels
+    const bool on = c < p.hidden, whole = !SHIFT || (c >= 0 && c + 8 <= p.hidden);
+    auto at = [&](int stage, int k) { return norm_ring + (stage * CH + k) * nt + threadIdx.x; };
+    // one vector of a buffer whose rows are `stride` apart; nothing behind its last row's end is read
+    auto copy = [&](auto* base, int64_t stride, int row, int stage, int k0) {
+        using E = std::remove_const_t<std::remove_pointer_t<decltype(base)>>;
+        const int64_t from = (int64_t)row * stride + c;
+        constexpr int W = 16 / (int)sizeof(E);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * nt + (int)threadIdx.x) * 8;
-                if (c >= p.hidden) continue;
-                const R* res = static_cast<const R*>(p.residual) + (int64_t)row * p.hidden + c;
-#pragma unroll
-                for (int k = 0; k < CR; ++k) cp_async16(smem_u32(at(stage, i, k)), res + k * (16 / sizeof(R)));
-                if (p.y != nullptr) {
-                    const T* y = static_cast<const T*>(p.y) + (int64_t)row * p.y_stride + c;
-#pragma unroll
-                    for (int k = 0; k < CT; ++k) cp_async16(smem_u32(at(stage, i, CR + k)), y + k * (16 / sizeof(T)));
-                }
-                if (p.gate != nullptr) {
-                    const T* g = static_cast<const T*>(p.gate) + (int64_t)row * p.gate_stride + c;
-#pragma unroll
-                    for (int k = 0; k < CT; ++k) cp_async16(smem_u32(at(stage, i, CR + CT + k)), g + k * (16 / sizeof(T)));
-                }
+        for (int k = 0; k < (int)sizeof(E) / 2; ++k) {
+            int bytes = 16;
+            if constexpr (SHIFT) {
+                const int64_t left = ((int64_t)(p.total - 1) * stride + p.hidden - from - k * W) * (int)sizeof(E);
+                bytes = left < 0 ? 0 : left < 16 ? (int)left : 16;
             }
+            cp_async16(smem_u32(at(stage, k0 + k)), bytes > 0 ? base + from + k * W : base, bytes);
+        }
+    };
+    auto fetch = [&](int row, int stage) {
+        if (row < p.total && on) {
+            copy(static_cast<const R*>(p.residual), p.hidden, row, stage, 0);
+            if (p.y != nullptr) copy(static_cast<const T*>(p.y), p.y_stride, row, stage, CR);
+            if (p.gate != nullptr) copy(static_cast<const T*>(p.gate), p.gate_stride, row, stage, CR + CT);
         }
         cp_async_commit();
+    };
+    auto store = [&](auto* row, const float (&v)[8]) {
+        using E = std::remove_pointer_t<decltype(row)>;
+        if (whole) {
+            st8(row + c, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e >= 0 && c + e < p.hidden) row[c + e] = from_f32<E>(v[e]);
+        }
     };
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) fetch(blockIdx.x + k * gridDim.x, k);
 
-    float wb[NV][8], wq[NV][8];      // weights of the branch, of the next block's input
+    float wb[8], wq[8];      // weights of the branch, of the next block's input
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * nt + (int)threadIdx.x) * 8;
+    for (int e = 0; e < 8; ++e) {
+        wb[e] = p.branch_scale;
+        wq[e] = 1.f;
+    }
+    if (on) {
+        auto weights = [&](const float* w, float (&f)[8]) {
+            if constexpr (SHIFT) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = c + e >= 0 && c + e < p.hidden ? __ldg(w + c + e) : 0.f;
+            } else {
+                widen8(raw8(w + c), f);
+            }
+        };
         float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            wb[i][e] = p.branch_scale;
-            wq[i][e] = 1.f;
-        }
-        if (c >= p.hidden) continue;
         if (p.w_post != nullptr) {
-            widen8(raw8(p.w_post + c), f);
+            weights(p.w_post, f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wb[i][e] *= f[e];
+            for (int e = 0; e < 8; ++e) wb[e] *= f[e];
         }
         if (p.scale != nullptr) {
-            widen8(raw8(p.scale + c), f);
+            weights(p.scale, f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wb[i][e] *= f[e];
+            for (int e = 0; e < 8; ++e) wb[e] *= f[e];
         }
-        if (p.w_pre != nullptr) widen8(raw8(p.w_pre + c), wq[i]);
+        if (p.w_pre != nullptr) weights(p.w_pre, wq);
     }
     int stage = 0;
     for (int row = blockIdx.x; row < p.total; row += gridDim.x) {
         cp_async_wait<STAGES - 2>();
-        float h[NV][8], z[NV][8], s = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[i][e] = h[i][e] = 0.f;
-            if ((i * nt + (int)threadIdx.x) * 8 >= p.hidden) continue;
+        float h[8] = {}, z[8] = {}, s = 0.f;
+        if (on) {
             Raw8<R> res;
 #pragma unroll
-            for (int k = 0; k < CR; ++k) res.v[k] = *at(stage, i, k);
-            widen8(res, h[i]);
+            for (int k = 0; k < CR; ++k) res.v[k] = *at(stage, k);
+            widen8(res, h);
+            float f[8];
             if (p.y != nullptr) {
                 Raw8<T> raw;
 #pragma unroll
-                for (int k = 0; k < CT; ++k) raw.v[k] = *at(stage, i, CR + k);
-                widen8(raw, z[i]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(z[i][e], z[i][e], s);
+                for (int k = 0; k < CT; ++k) raw.v[k] = *at(stage, CR + k);
+                widen8(raw, z);
                 if (p.gate != nullptr) {
-                    float f[8];
 #pragma unroll
-                    for (int k = 0; k < CT; ++k) raw.v[k] = *at(stage, i, CR + CT + k);
+                    for (int k = 0; k < CT; ++k) raw.v[k] = *at(stage, CR + CT + k);
                     widen8(raw, f);
-                    apply_gate<T>(z[i], f, p.act);
                 }
+            }
+            if (SHIFT && !whole) {       // neighbours' channels
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < 0 || c + e >= p.hidden) h[e] = z[e] = f[e] = 0.f;
+            }
+            if (p.y != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(z[e], z[e], s);
+                if (p.gate != nullptr) apply_gate<T>(z, f, p.act);
             }
         }
         // the stage before this one is free: this thread read it in the last turn
@@ -289,33 +323,19 @@ __global__ void __launch_bounds__(512) kda_block_norm_kernel(const BlockNormPara
         float r = 1.f;
         if (p.w_post != nullptr) r = rsqrtf(block_sum(s, part[0], warps) * inv + p.eps);
         s = 0.f;
-        if (p.y != nullptr) {
+        if (p.y != nullptr && on) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * nt + (int)threadIdx.x) * 8;
-                if (c >= p.hidden) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    h[i][e] = fmaf(p.residual_scale, h[i][e], z[i][e] * r * wb[i][e]);
-                    s = fmaf(h[i][e], h[i][e], s);
-                }
-                st8(static_cast<R*>(p.residual_out) + (int64_t)row * p.hidden + c, h[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(h[i][e], h[i][e], s);
+            for (int e = 0; e < 8; ++e) h[e] = fmaf(p.residual_scale, h[e], z[e] * r * wb[e]);
+            store(static_cast<R*>(p.residual_out) + (int64_t)row * p.hidden, h);
         }
         if (p.x != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(h[e], h[e], s);
             r = rsqrtf(block_sum(s, part[1], warps) * inv + p.eps);
+            if (on) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * nt + (int)threadIdx.x) * 8;
-                if (c >= p.hidden) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] *= r * wq[i][e];
-                st8(static_cast<T*>(p.x) + (int64_t)row * p.hidden + c, h[i]);
+                for (int e = 0; e < 8; ++e) h[e] *= r * wq[e];
+                store(static_cast<T*>(p.x) + (int64_t)row * p.hidden, h);
             }
         }
         if ((p.w_post == nullptr) != (p.x == nullptr)) __syncthreads();  // one buffer only: the next row writes it again
@@ -323,8 +343,8 @@ __global__ void __launch_bounds__(512) kda_block_norm_kernel(const BlockNormPara
     cp_async_wait<0>();
 }
 
-// The same for rows that do not start on 16 bytes, are no multiple of eight
-// channels wide, or wider than 8192: one channel an access, NV of them a thread; the weights come
+// The same for buffers that do not start on 16 bytes, strides that are no
+// multiple of eight apart from the width, and rows wider than 8192 (8178): one channel an access, NV of them a thread; the weights come
 // from L1.  Row after row of an odd width is still contiguous, so a warp's
 // loads are whole lines.
 template <typename T, typename R, int NV>

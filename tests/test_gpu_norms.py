@@ -163,6 +163,28 @@ def test_block_norm_options(lib, kw, dtype, res):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("total,hidden,dtype,res,kw", [
+    (1700, 9, BF16, BF16, {}), (1300, 77, F16, F32, {}), (2500, 130, F32, F32, dict(in_place=True)), (700, 1001, BF16, F32, dict(in_place=True)),
+    (320, 4101, F16, F16, dict(kind=2)), (310, 8191, F32, F32, dict(kind=None)), (5, 3, BF16, F32, {}), (8, 8190, BF16, BF16, dict(post=False, out=False)),
+    (33, 101, BF16, BF16, dict(strided=True)), (9, 5, F32, F32, dict(strided=True, out=False)), (2000, 15, F16, F32, dict(kind=0, scale=False, pre=False)),
+])
+def test_block_norm_of_widths_that_are_no_multiple_of_eight(lib, total, hidden, dtype, res, kw):
+    """Rows that begin anywhere in a 16-byte vector, several to a CTA: neighbours' channels are neither summed nor written."""
+    run_block(lib, total, hidden, dtype, res, **kw)
+
+
+@pytest.mark.gpu
+def test_block_norm_odd_width_keeps_not_finite_rows_apart(lib):
+    y, r = torch.randn(40, 37), torch.randn(40, 37)
+    y[7, 36], y[9, 0], r[20, 5] = float("nan"), float("inf"), float("nan")
+    ro, x = torch.empty(40, 37, device="cuda"), torch.empty(40, 37, device="cuda")
+    w = torch.ones(37, device="cuda")
+    lib.kda_block_norm(r.cuda(), y.cuda(), ro, w_post=w, w_pre=w, x=x)
+    bad = sorted(set((~x.cpu().isfinite()).any(1).nonzero().flatten().tolist()))
+    assert bad == [7, 9, 20]
+
+
+@pytest.mark.gpu
 def test_block_norm_of_the_residual_alone(lib):
     r = torch.randn(5, 264)
     x = torch.empty(5, 264, dtype=BF16, device="cuda")
