@@ -1154,33 +1154,37 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 for (int row0 = 0; row0 < live; row0 += rows) {
                     const int row = row0 + grp / share, kk = grp % share;
                     const bool on = grp < rows * share && row < live;
+                    // one pass with a running maximum: the loads of several parts are on their way together
                     float M = -FLT_MAX, L = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = ch; k < np; k += CH)
-                        if (on) M = fmaxf(M, __ldcg(slot(k) + KV4_ROWS * D + 2 * row));
-#pragma unroll
-                    for (int o2 = CH / 2; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
+                    auto add = [&](float m, float l, const float4& v) {
+                        const float top = fmaxf(M, m), f = ex2f(M - top), w = ex2f(m - top);
+                        M = top;
+                        L = L * f + l * w;
+                        o.x = o.x * f + v.x * w;
+                        o.y = o.y * f + v.y * w;
+                        o.z = o.z * f + v.z * w;
+                        o.w = o.w * f + v.w * w;
+                    };
                     if (on) {
 #pragma unroll 4
                         for (int k = kk; k < np; k += share) {
                             const float* s = slot(k);
                             const float2 x = __ldcg(reinterpret_cast<const float2*>(s + KV4_ROWS * D) + row);
                             const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D + ch * 4));
-                            const float f = ex2f(x.x - M);
-                            L += f * x.y;
-                            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+                            add(x.x, x.y, v);
                         }
                     }
                     if (share > 1) {
                         __syncthreads();
                         reinterpret_cast<float4*>(merge)[tid2] = o;
-                        if (ch == 0) ml[grp] = L;
-                        __syncthreads();
-                        for (int k = 1; k < share && kk == 0; ++k) {
-                            const float4 v = reinterpret_cast<const float4*>(merge)[tid2 + k * CH];
-                            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-                            L += ml[grp + k];
+                        if (ch == 0) {
+                            ml[2 * grp] = M;
+                            ml[2 * grp + 1] = L;
                         }
+                        __syncthreads();
+                        for (int k = 1; k < share && kk == 0; ++k)
+                            add(ml[2 * (grp + k)], ml[2 * (grp + k) + 1], reinterpret_cast<const float4*>(merge)[tid2 + k * CH]);
                     }
                     if (on && kk == 0) join(row, ch * 4, o, L);
                 }
