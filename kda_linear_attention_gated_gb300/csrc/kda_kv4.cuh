@@ -1134,11 +1134,11 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             const int c1 = (int)((seg0 + cur.q.units + KV4_PART - SH::LAST) / share);
             __syncthreads();
             if (tid == 0) {
-                __threadfence();        // the CTA's stores, ordered before by the barrier
-                const int old = atomicAdd(p.counters + c0, 1);
+                // releases the CTA's stores (ordered before by the barrier), acquires the other CTAs'
+                int old;
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.counters + c0) : "memory");
                 if (old == c1 - c0) p.counters[c0] = 0;
                 *last_to_come = old == c1 - c0;
-                __threadfence();
             }
             __syncthreads();
             if (*last_to_come) {
@@ -1167,7 +1167,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                         o.w = o.w * f + v.w * w;
                     };
                     if (on) {
-#pragma unroll 4
+#pragma unroll 8
                         for (int k = kk; k < np; k += share) {
                             const float* s = slot(k);
                             const float2 x = __ldcg(reinterpret_cast<const float2*>(s + KV4_ROWS * D) + row);
