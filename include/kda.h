@@ -72,7 +72,7 @@ typedef enum kda_status {
     KDA_ERR_SHAPE = 5,             /* K or V outside 16..128 or not a multiple of 16; bad counts or strides */
     KDA_ERR_ALIGN = 6,             /* pool base, slot stride, q, k, v or a not 16-byte aligned; b, o, ids not 4-byte */
     KDA_ERR_LAUNCH = 7,            /* the CUDA launch itself failed */
-    KDA_ERR_SLOT_RANGE = 8,        /* device: a slot id outside [0, num_slots); its tiles were skipped */
+    KDA_ERR_SLOT_RANGE = 8,        /* device: a slot (page) id outside its pool; its tiles (tokens) were skipped */
     KDA_ERR_ARG = 9,               /* any other bad argument (negative counts, n_layers < 1) */
     KDA_ERR_TIMEOUT = 10,          /* device: a pipeline wait gave up after 1 s; results incomplete */
     KDA_ERR_LAYOUT = 11            /* a checkpoint plane written under another state layout (dtype or shape) */
@@ -101,13 +101,17 @@ typedef enum kda_status {
 
 /*
  * KDA_LAUNCH_TEST_WITHHOLD_STATE: a test hook of kda_decode_step,
- *   kda_spec_verify and kda_step, for the timeout path only; never for
- *   production calls, and refused by every other entry point.  Each tile arms
+ *   kda_spec_verify, kda_step and kda_kv4_attend, for the timeout path only;
+ *   never for production calls, and refused by every other entry point.  Each
+ *   tile arms
  *   its state tile's barrier but withholds the copy, so every wait on it gives
  *   up at its 1 s bound: the call then reports KDA_ERR_TIMEOUT through
  *   dev_status (after about 2 s: the wait, then a bounded drain), writes
  *   neither those tiles' states nor their outputs, and the context stays
  *   usable.  Requests that reset (no state read) are not affected.
+ *   kda_kv4_attend withholds its block copies: it reports KDA_ERR_TIMEOUT
+ *   after about 4 s, its output rows are zero or those of the keys worked on
+ *   before, and the workspace is ready for the next call.
  */
 #define KDA_LAUNCH_TEST_WITHHOLD_STATE (1u << 30)
 
@@ -671,7 +675,7 @@ typedef struct kda_kv4_append_args {
  * Appends a step's keys and values (see kda_kv4_append_args); cache and args
  * are host pointers.  Host checks: KDA_ERR_NULL, _DTYPE_UNSUPPORTED, _SHAPE
  * (the cache, strides, rot_dim, total inconsistent with n and max_t, a table
- * of 2^31 tokens or more), _ALIGN, _ARG (negative counts, reserved fields,
+ * of about 2^31 tokens or more), _ALIGN, _ARG (negative counts, reserved fields,
  * scales that are not positive numbers, flags other than KDA_LAUNCH_PDL).
  * Device checks (in *dev_status, that token skipped): KDA_ERR_ARG for token
  * offsets outside 0 .. max_t and for a position past the page table or the

@@ -943,11 +943,11 @@ const char* kda_strerror(int32_t code) {
         case KDA_ERR_DTYPE_MISMATCH: return "state pool dtype differs from the library's build dtype";
         case KDA_ERR_DTYPE_UNSUPPORTED: return "unsupported dtype (state pools are fp32 or fp16 only; q/k/v fp32, fp16 or bf16)";
         case KDA_ERR_LAYERS_DISAGREE: return "layers disagree on the state dtype or head shape";
-        case KDA_ERR_SHAPE: return "bad shape (K and V must be multiples of 16 in 16..128; slot stride >= hv*k*v)";
+        case KDA_ERR_SHAPE: return "bad shape (a state pool: K and V multiples of 16 in 16..128, slot stride >= hv*k*v; other calls: see kda.h)";
         case KDA_ERR_ALIGN: return "misaligned pointer or stride (pool, q, k, v, a 16-byte aligned; b, o, ids 4-byte)";
         case KDA_ERR_LAUNCH: return "CUDA kernel launch failed";
-        case KDA_ERR_SLOT_RANGE: return "a slot id lies outside [0, num_slots); its tiles were skipped";
-        case KDA_ERR_ARG: return "bad argument (on the device: an accepted column or token offsets out of range)";
+        case KDA_ERR_SLOT_RANGE: return "a slot or page id lies outside its pool; its tiles were skipped";
+        case KDA_ERR_ARG: return "bad argument (on the device: an accepted column, token offsets or a position out of range)";
         case KDA_ERR_TIMEOUT: return "a device-side pipeline wait ran out (1 s); the call's results are incomplete";
         case KDA_ERR_LAYOUT: return "the checkpoint plane was written under another state layout (dtype or shape)";
         default: return "unknown kda status code";

@@ -443,6 +443,7 @@ struct Kv4AttendParams {
     int32_t* counters;                   // [gridDim.x], zero between calls
     float* partials;                     // [2 gridDim.x][KV4_ROWS][D + 2]
     int32_t* status;
+    int withhold;                        // the test hook: copies are expected and not issued
 };
 
 // What the columns of a query tile hold, see kda_kv4_attend_kernel.
@@ -816,7 +817,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         const int mine = lane - turn;
         if ((mine & ~1) == 0) {         // the copies may complete before they are expected: the phase waits for the arrival
             if (mine == 0 && two != 0) mbar_arrive_expect_tx(bars + slot, two == 3u ? 2 * F::BLOCK : F::BLOCK);
-            if (two >> mine & 1u) bulk_load(ring + (2 * slot + mine) * F::BLOCK, from, F::BLOCK, bars + slot);
+            if ((two >> mine & 1u) && !p.withhold) bulk_load(ring + (2 * slot + mine) * F::BLOCK, from, F::BLOCK, bars + slot);
         }
         there >>= 2;
         turn += 2;

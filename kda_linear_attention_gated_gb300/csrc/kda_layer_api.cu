@@ -34,10 +34,10 @@ struct Common {
     const void *cu, *table, *ctx, *cos, *sin;
 };
 
-int check_common(const kda_kv4_cache* c, const Common& g, uint32_t flags) {
+int check_common(const kda_kv4_cache* c, const Common& g) {
     if (g.n < 0 || g.total < 0 || g.max_t < 0 || (g.inter != 0 && g.inter != 1)) return KDA_ERR_ARG;
-    if (flags & ~(uint32_t)KDA_LAUNCH_PDL) return KDA_ERR_ARG;
-    if (g.cols < 1 || (int64_t)g.cols * c->page_tokens > 0x7fffffffLL || g.rot < 0 || g.rot > c->dim || g.rot % 32 != 0 ||
+    // positions, rounded up to a unit of keys, stay below 2^31
+    if (g.cols < 1 || (int64_t)g.cols * c->page_tokens > 0x7fffffffLL - kda::KV4_KEYS || g.rot < 0 || g.rot > c->dim || g.rot % 32 != 0 ||
         (g.rot > 0 && g.rope_rows < 1))
         return KDA_ERR_SHAPE;
     if (g.cu == nullptr && (int64_t)g.total != (int64_t)g.n * g.max_t) return KDA_ERR_SHAPE;
@@ -136,7 +136,8 @@ int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, 
     if (es == 0 || ((g.k_out || g.v_out) && elem_size(g.out_dtype) == 0)) return KDA_ERR_DTYPE_UNSUPPORTED;
     const Common c = {g.n, g.total, g.max_t, g.table_cols, g.rot_dim, g.interleaved, g.rope_rows,
                       g.cu_seqlens, g.page_table, g.ctx_len, g.cos, g.sin};
-    rc = check_common(cache, c, flags);
+    if (flags & ~(uint32_t)KDA_LAUNCH_PDL) return KDA_ERR_ARG;
+    rc = check_common(cache, c);
     if (rc != KDA_OK) return rc;
     if (g.reserved != 0) return KDA_ERR_ARG;
     const int64_t row = (int64_t)cache->heads * cache->dim;
@@ -207,7 +208,8 @@ int kda_kv4_attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, 
     if (es == 0) return KDA_ERR_DTYPE_UNSUPPORTED;
     const Common c = {g.n, g.total, g.max_t, g.table_cols, g.rot_dim, g.interleaved, g.rope_rows,
                       g.cu_seqlens, g.page_table, g.ctx_len, g.cos, g.sin};
-    rc = check_common(cache, c, flags);
+    if (flags & ~(uint32_t)(KDA_LAUNCH_PDL | KDA_LAUNCH_TEST_WITHHOLD_STATE)) return KDA_ERR_ARG;
+    rc = check_common(cache, c);
     if (rc != KDA_OK) return rc;
     if (g.reserved != 0 || g.window < 0 || !std::isfinite(g.scale)) return KDA_ERR_ARG;
     if (g.h_q < 1 || g.h_q % cache->heads != 0 || g.max_t > KDA_KV4_MAX_TOKENS || g.q_stride < (int64_t)g.h_q * cache->dim)
@@ -256,6 +258,7 @@ int kda_kv4_attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, 
     prm.counters = static_cast<int32_t*>(g.workspace);
     prm.partials = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + kda::KV4_MAX_CTAS * sizeof(int32_t));
     prm.status = dev_status;
+    prm.withhold = (flags & KDA_LAUNCH_TEST_WITHHOLD_STATE) != 0;
     static_assert(kda::KV4_MAX_CTAS * (4 + 2 * kda::KV4_ROWS * (128 + 2) * 4) <= KDA_KV4_WORKSPACE_BYTES, "workspace");
     const int64_t list = units * std::min<int64_t>(tiles * cache->heads * g.n, 1 << 20);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

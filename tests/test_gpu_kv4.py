@@ -1,6 +1,7 @@
 """The 4-bit paged cache: kda_kv4_append (bytes, bit for bit) and
 kda_kv4_attend (against fp64, tolerance derived in _layer_ref)."""
 import ctypes
+import time
 
 import pytest
 import torch
@@ -72,6 +73,8 @@ def test_refusals_before_any_launch(lib, which):
                (dict(q=None), kda.KDA_ERR_NULL)]
     for kw, code in own:
         assert call(cache_desc(), make(**kw), P, None) == code, kw
+    hook = kda.KDA_OK if which == "attend" else kda.KDA_ERR_ARG       # the test hook is an option of the one that waits
+    assert call(cache_desc(), make(n=0, total=0), P, None, flags=kda.KDA_LAUNCH_TEST_WITHHOLD_STATE) == hook
     # nothing to do: accepted without a launch
     assert call(cache_desc(), make(n=0, total=0), P, None) == kda.KDA_OK
 
@@ -383,6 +386,27 @@ def test_attend_is_deterministic_and_leaves_the_workspace_ready(lib):
     b, _ = run_attend(lib, **kw)
     c, _ = run_attend(lib_for(torch.float16), **kw)
     assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ctx", [[63, 20], [5000, 20]])     # whole in their CTAs; in parts that meet in the workspace
+def test_withheld_copies_time_out_and_leave_the_call_usable(lib, ctx):
+    """Every wait for a block is bounded: with the copies withheld the call reports the timeout, and the next one is right."""
+    ws = torch.zeros(kda.KDA_KV4_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    kw = dict(heads=1, grp=2, dim=128, page=16, ctx=ctx, lens=[1, 1], dtype=BF16, rot=0, inter=False, ws=ws)
+    want, _ = run_attend(lib, **kw)
+    g = torch.Generator().manual_seed(0)
+    cache = ref.Cache([c + 1 for c in ctx], 1, 128, 16, g)
+    q, st = torch.randn(2, 2, 128, dtype=BF16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = torch.full_like(q, float("nan"))
+    t0 = time.monotonic()
+    lib.kda_kv4_attend(cache.pages.cuda(), cache.table.cuda(), torch.tensor(ctx, dtype=torch.int32, device="cuda"), q, o, ws, st,
+                       flags=kda.KDA_LAUNCH_TEST_WITHHOLD_STATE)
+    torch.cuda.synchronize()
+    assert st.item() == kda.KDA_ERR_TIMEOUT and 0.9 <= time.monotonic() - t0 < 30
+    assert not ws[:2048].any() and (o == 0).all()
+    again, _ = run_attend(lib, **kw)
+    assert torch.equal(want, again)
 
 
 @pytest.mark.gpu
