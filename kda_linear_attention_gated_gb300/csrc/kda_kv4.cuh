@@ -303,7 +303,8 @@ __device__ __forceinline__ void kv4_turn(float& a, float& b, float c, float s) {
 // codes whole 32-byte sectors, and its value codes 64 contiguous bytes when
 // the eight tokens fill half a block.  The loads of a head do not wait for the
 // token's place: they are on their way while that is looked up.  Rotation in fp32, products and sums rounded one by
-// one (no fused multiply-add).
+// one (no fused multiply-add).  8192 tokens of 8 heads of 128, bf16: 20.4 us, 3.8 TB/s, bound
+// by issue (about 20 instructions an element) and the look-up's latency.
 template <int D, int ES>
 __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_append_kernel(const Kv4AppendParams p) {
     constexpr int NG = Kv4<D>::NG, NP = NG / 2, HW = 4 / NP;     // groups and pairs of a head, heads of a warp
@@ -450,7 +451,9 @@ struct Kv4AttendParams {
 constexpr int KV4_8 = 0, KV4_REST = 1, KV4_16 = 2;
 constexpr int KV4_ROWS = 16;             // most rows of a tile
 constexpr int KV4_KEYS = 32;             // keys of a unit of work: two blocks
-constexpr int KV4_PART = 24;             // what beginning and ending a part costs a CTA, in units
+// What beginning and ending a part costs a CTA, in units: 32 x 8 ragged tokens took 90 us with 12,
+// 66 with 16, 62 with 20, 60 with 24, 61 with 28.
+constexpr int KV4_PART = 24;
 constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
 constexpr int KV4_AHEAD = 16;            // units whose pages a warp looks up at a time: lanes 2 i, 2 i + 1 a block each
 constexpr float KV4_SLACK = 8.f;         // the running maximum may lag by this many powers of two
@@ -578,6 +581,13 @@ struct Kv4Walk {
 // its own ring of bulk copies, and join at the end of a part.  Parts of one
 // (request, head, tile) in several CTAs go to the workspace, and the CTA that
 // arrives last joins them in order (results do not depend on who that is).
+//
+// Bound by issue: decoding fills half of the ALU pipe, and 16 warps an SM (the
+// registers of the sums, the rings) leave 0.4 of the issue slots empty.  A loop
+// of decode and mma alone takes 290 cycles a block and scheduler, this kernel
+// about 430.  64 requests x 8192 tokens, 32/8 heads of 128: 116 us, 5.2 TB/s of
+// cache, 0.77 of the measured copy bandwidth.  Keys and values as the B operand
+// (query rows on the 16-row side, half of it idle): 168 us.
 template <int D, int MODE>
 __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_kernel(const Kv4AttendParams p) {
     using F = Kv4<D>;
@@ -971,13 +981,15 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 uint32_t pf[2][NB][2], pr[SPLIT ? 2 : 1][2];   // B fragments of the probabilities, of their remainders
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const float c0 = rowf[row_of(2 * n)], c1 = rowf[row_of(2 * n + 1)];
+                    // both rows at once (packed fp32)
+                    const float2 c = *reinterpret_cast<const float2*>(rowf + row_of(2 * n));
+                    const float2 neg = make_float2(-m[2 * n], -m[2 * n + 1]);
+                    float2 sum = make_float2(l[2 * n], l[2 * n + 1]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x0 = ex2f(fmaf(s[i >> 1][n][2 * (i & 1)], c0, -m[2 * n]));
-                        const float x1 = ex2f(fmaf(s[i >> 1][n][2 * (i & 1) + 1], c1, -m[2 * n + 1]));
-                        l[2 * n] += x0;
-                        l[2 * n + 1] += x1;
+                        const float2 e = __ffma2_rn(make_float2(s[i >> 1][n][2 * (i & 1)], s[i >> 1][n][2 * (i & 1) + 1]), c, neg);
+                        const float x0 = ex2f(e.x), x1 = ex2f(e.y);
+                        sum = __fadd2_rn(sum, make_float2(x0, x1));
                         const __half2 hi = __floats2half2_rn(x0, x1);
                         pf[i >> 1][n][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&hi));
                         if constexpr (SPLIT) {
@@ -986,6 +998,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                             pr[i >> 1][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&rest));
                         }
                     }
+                    l[2 * n] = sum.x;
+                    l[2 * n + 1] = sum.y;
                 }
                 // ---- values ----
 #pragma unroll
