@@ -302,9 +302,10 @@ __device__ __forceinline__ void kv4_turn(float& a, float& b, float c, float s) {
 // warp's loads are whole 128-byte lines of a token (16-bit inputs), its key
 // codes whole 32-byte sectors, and its value codes 64 contiguous bytes when
 // the eight tokens fill half a block.  The loads of a head do not wait for the
-// token's place: they are on their way while that is looked up.  Rotation in fp32, products and sums rounded one by
-// one (no fused multiply-add).  8192 tokens of 8 heads of 128, bf16: 20.4 us, 3.8 TB/s, bound
-// by issue (about 20 instructions an element) and the look-up's latency.
+// token's place: they are on their way while that is looked up.  Rotation in
+// fp32, products and sums rounded one by one (no fused multiply-add).  8192
+// tokens of 8 heads of 128, bf16: 20.4 us, 3.8 TB/s, bound by issue (about 20
+// instructions an element) and the look-up's latency.
 template <int D, int ES>
 __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_append_kernel(const Kv4AppendParams p) {
     constexpr int NG = Kv4<D>::NG, NP = NG / 2, HW = 4 / NP;     // groups and pairs of a head, heads of a warp
