@@ -345,9 +345,10 @@ __global__ void __launch_bounds__(1024) kda_block_norm_kernel(const BlockNormPar
 }
 
 // The same for buffers that do not start on 16 bytes, strides that are no
-// multiple of eight apart from the width, and rows wider than 8192 (8178): one channel an access, NV of them a thread; the weights come
-// from L1.  Row after row of an odd width is still contiguous, so a warp's
-// loads are whole lines.
+// multiple of eight apart from the width, and rows wider than 8192 (odd widths:
+// 8178): one channel an access, NV of them a thread; the weights come from L1.
+// Row after row of an odd width is still contiguous, so a warp's loads are
+// whole lines.
 template <typename T, typename R, int NV>
 __global__ void __launch_bounds__(1024, NV > 8 ? 0 : 1) kda_block_norm_any_kernel(const BlockNormParams p) {
     __shared__ float part[2][32];
