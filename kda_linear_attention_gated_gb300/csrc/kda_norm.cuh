@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(1024) kda_block_norm_kernel(const BlockNormPar
     const bool on = c < p.hidden, whole = !SHIFT || (c >= 0 && c + 8 <= p.hidden);
     auto at = [&](int stage, int k) { return norm_ring + (stage * CH + k) * nt + threadIdx.x; };
     // one vector of a buffer whose rows are `stride` apart; nothing behind its last row's end is read
-    auto copy = [&](auto* base, int64_t stride, int row, int stage, int k0) {
+    auto copy = [&](auto* base, int64_t stride, unsigned row, int stage, int k0) {
         using E = std::remove_const_t<std::remove_pointer_t<decltype(base)>>;
         const int64_t from = (int64_t)row * stride + c;
         constexpr int W = 16 / (int)sizeof(E);
@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(1024) kda_block_norm_kernel(const BlockNormPar
             cp_async16(smem_u32(at(stage, k0 + k)), bytes > 0 ? base + from + k * W : base, bytes);
         }
     };
-    auto fetch = [&](int row, int stage) {
-        if (row < p.total && on) {
+    auto fetch = [&](unsigned row, int stage) {
+        if (row < (unsigned)p.total && on) {
             copy(static_cast<const R*>(p.residual), p.hidden, row, stage, 0);
             if (p.y != nullptr) copy(static_cast<const T*>(p.y), p.y_stride, row, stage, CR);
             if (p.gate != nullptr) copy(static_cast<const T*>(p.gate), p.gate_stride, row, stage, CR + CT);
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(1024) kda_block_norm_kernel(const BlockNormPar
         if (p.w_pre != nullptr) weights(p.w_pre, wq);
     }
     int stage = 0;
-    for (int row = blockIdx.x; row < p.total; row += gridDim.x) {
+    // unsigned: behind the last of up to 2^31 - 1 rows a grid more must not wrap
+    for (unsigned row = blockIdx.x; row < (unsigned)p.total; row += gridDim.x) {
         cp_async_wait<STAGES - 2>();
         float h[8] = {}, z[8] = {}, s = 0.f;
         if (on) {
