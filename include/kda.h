@@ -629,6 +629,9 @@ typedef struct kda_kv4_cache {
 /* Bytes of one page.  KDA_ERR_SHAPE for a shape that a cache cannot have. */
 int kda_kv4_page_bytes(int32_t page_tokens, int32_t heads, int32_t dim, int64_t* bytes);
 
+/* Most requests, and most packed tokens, of one call on the cache. */
+#define KDA_KV4_MAX_COUNT 0x7fffff00
+
 /*
  * Arguments of kda_kv4_append (device pointers; optional ones may be NULL).
  * Request r owns tokens cu_seqlens[r] .. cu_seqlens[r+1] - 1 of k and v (or
@@ -674,8 +677,8 @@ typedef struct kda_kv4_append_args {
 /*
  * Appends a step's keys and values (see kda_kv4_append_args); cache and args
  * are host pointers.  Host checks: KDA_ERR_NULL, _DTYPE_UNSUPPORTED, _SHAPE
- * (the cache, strides, rot_dim, total inconsistent with n and max_t, a table
- * of about 2^31 tokens or more), _ALIGN, _ARG (negative counts, reserved fields,
+ * (the cache, strides, rot_dim, total inconsistent with n and max_t, n or total
+ * past KDA_KV4_MAX_COUNT, a table of about 2^31 tokens or more), _ALIGN, _ARG (negative counts, reserved fields,
  * scales that are not positive numbers, flags other than KDA_LAUNCH_PDL).
  * Device checks (in *dev_status, that token skipped): KDA_ERR_ARG for token
  * offsets outside 0 .. max_t and for a position past the page table or the

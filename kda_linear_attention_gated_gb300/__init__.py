@@ -27,13 +27,13 @@ __all__ = ["KdaError", "KdaLibrary", "PoolDesc", "build", "lib_path",
            "KDA_ERR_DTYPE_MISMATCH", "KDA_ERR_DTYPE_UNSUPPORTED", "KDA_ERR_LAYERS_DISAGREE",
            "KDA_ERR_SHAPE", "KDA_ERR_ALIGN", "KDA_ERR_LAUNCH", "KDA_ERR_SLOT_RANGE",
            "KDA_ERR_ARG", "KDA_ERR_TIMEOUT", "KDA_ERR_LAYOUT", "KDA_LAUNCH_PDL", "KDA_LAUNCH_PDL_EARLY_STATE",
-           "KDA_LAUNCH_TEST_WITHHOLD_STATE", "KDA_KV4_WORKSPACE_BYTES", "KDA_KV4_MAX_TOKENS", "KDA_BLOCK_NORM_MAX",
+           "KDA_LAUNCH_TEST_WITHHOLD_STATE", "KDA_KV4_WORKSPACE_BYTES", "KDA_KV4_MAX_TOKENS", "KDA_KV4_MAX_COUNT", "KDA_BLOCK_NORM_MAX",
            "EXPORTED_SYMBOLS"]
 
 KDA_F32, KDA_F16, KDA_BF16 = 0, 1, 2
 KDA_LAUNCH_PDL, KDA_LAUNCH_PDL_EARLY_STATE = 1, 2
 KDA_LAUNCH_TEST_WITHHOLD_STATE = 1 << 30  # test hook of the timeout path (include/kda.h)
-KDA_KV4_WORKSPACE_BYTES, KDA_KV4_MAX_TOKENS, KDA_BLOCK_NORM_MAX = 20 << 20, 16, 16384
+KDA_KV4_WORKSPACE_BYTES, KDA_KV4_MAX_TOKENS, KDA_KV4_MAX_COUNT, KDA_BLOCK_NORM_MAX = 20 << 20, 16, 0x7FFFFF00, 16384
 (KDA_OK, KDA_ERR_NULL, KDA_ERR_DTYPE_MISMATCH, KDA_ERR_DTYPE_UNSUPPORTED,
  KDA_ERR_LAYERS_DISAGREE, KDA_ERR_SHAPE, KDA_ERR_ALIGN, KDA_ERR_LAUNCH,
  KDA_ERR_SLOT_RANGE, KDA_ERR_ARG, KDA_ERR_TIMEOUT, KDA_ERR_LAYOUT) = range(12)

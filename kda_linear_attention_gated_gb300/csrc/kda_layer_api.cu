@@ -36,6 +36,8 @@ struct Common {
 
 int check_common(const kda_kv4_cache* c, const Common& g) {
     if (g.n < 0 || g.total < 0 || g.max_t < 0 || (g.inter != 0 && g.inter != 1)) return KDA_ERR_ARG;
+    // the kernels round requests up to 32 and tokens up to 8 in 32 bits
+    if (g.n > KDA_KV4_MAX_COUNT || g.total > KDA_KV4_MAX_COUNT) return KDA_ERR_SHAPE;
     // positions, rounded up to a unit of keys, stay below 2^31
     if (g.cols < 1 || (int64_t)g.cols * c->page_tokens > 0x7fffffffLL - kda::KV4_KEYS || g.rot < 0 || g.rot > c->dim || g.rot % 32 != 0 ||
         (g.rot > 0 && g.rope_rows < 1))
