@@ -693,6 +693,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         int ok = 0;
         __syncwarp();
         if (lane == 0) ok = w.next(p, ROWS);
+        __syncwarp();               // the walk is in shared memory, and a shuffle orders no memory
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
 
