@@ -888,7 +888,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         for (int unit = cur.q.first + cur.b0 + warp, end = cur.q.first + cur.b1; unit < end; unit += KV4_WARPS) {
             bool use = (flags & ALIVE) && (flags >> (8 + 2 * slot) & 3u) != 3u;
             if (use) {
-                use = mbar_wait(bars + slot, flags >> slot & 1u);
+                // the warp's verdict, not a lane's: a copy may land while some lanes give up
+                use = __all_sync(0xffffffffu, mbar_wait(bars + slot, flags >> slot & 1u));
                 if (use) {
                     flags ^= 1u << slot;
                 } else {

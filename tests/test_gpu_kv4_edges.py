@@ -5,7 +5,8 @@ import torch
 
 import kda_linear_attention_gated_gb300 as kda
 
-from test_gpu_kv4 import P, append_args, attend_args, cache_desc, run_attend
+import _layer_ref as ref
+from test_gpu_kv4 import P, append_args, attend_args, cache_desc, ragged, run_attend
 
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
 
@@ -51,3 +52,22 @@ def test_attend_of_more_requests_than_lanes(lib, n, heads, grp, dim, dtype, wind
     """Many parts a CTA, each with its own request, head and queries; shares that begin inside a lane's second or later request."""
     ctx, lens = many(n, seed=n + dim)
     run_attend(lib, heads, grp, dim, 32, ctx, lens, dtype, dim // 2, False, window, seed=n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,grp,dim,lens,dtype", [(2, 4, 64, [8, 1, 3], BF16), (1, 3, 128, [2, 1, 1], F32), (3, 2, 64, [1, 1, 1], F16)])
+def test_withheld_copies_of_every_build_time_out(lib, heads, grp, dim, lens, dtype):
+    """Copies that never land, in parts that lie whole in a CTA and in ones that meet: zero rows, the timeout, a usable workspace."""
+    ws = torch.zeros(kda.KDA_KV4_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    ctx = [3000, 40, 700]
+    kw = dict(heads=heads, grp=grp, dim=dim, page=16, ctx=ctx, lens=lens, dtype=dtype, rot=0, inter=False, ws=ws)
+    want, _ = run_attend(lib, **kw)
+    cache = ref.Cache([c + t for c, t in zip(ctx, lens)], heads, dim, 16, torch.Generator().manual_seed(0))
+    q = torch.randn(sum(lens), heads * grp, dim, device="cuda").to(dtype)
+    o, st = torch.full_like(q, float("nan")), torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib.kda_kv4_attend(cache.pages.cuda(), cache.table.cuda(), torch.tensor(ctx, dtype=torch.int32, device="cuda"), q, o, ws, st,
+                       cu_seqlens=ragged(lens), max_t=max(lens), flags=kda.KDA_LAUNCH_TEST_WITHHOLD_STATE)
+    torch.cuda.synchronize()
+    assert st.item() == kda.KDA_ERR_TIMEOUT and not ws[:2048].any() and (o == 0).all()
+    again, _ = run_attend(lib, **kw)
+    assert torch.equal(want, again)
