@@ -205,13 +205,15 @@ def _kv4_cache(pages, k_scale, v_scale) -> tuple:
     if len(shape) != 4 or pages.dtype != _torch().uint8 or not pages.is_cuda:
         raise ValueError("a 4-bit cache is a CUDA uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor")
     num, heads, blocks, size = shape
-    stride = pages.stride()
-    if stride[1:] != (blocks * size, size, 1):
-        raise ValueError("the [heads, page_tokens / 16, 18 * dim] part of a 4-bit cache must be dense")
+    page = heads * blocks * size
+    if not pages.is_contiguous():
+        page, *inner = pages.stride()
+        if inner[2] != 1 or (blocks != 1 and inner[1] != size) or (heads != 1 and inner[0] != blocks * size):
+            raise ValueError("the [heads, page_tokens / 16, 18 * dim] part of a 4-bit cache must be dense")
     dim, rest = divmod(size, 18)
     if rest:
         raise ValueError(f"the last dimension of a 4-bit cache is 18 * dim bytes, not {size}")
-    return pages.data_ptr(), 16 * blocks, heads, dim, 0, num, stride[0], k_scale, v_scale
+    return pages.data_ptr(), 16 * blocks, heads, dim, 0, num, page, k_scale, v_scale
 
 
 def _ptr(t) -> int | None:

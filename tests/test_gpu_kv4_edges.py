@@ -71,3 +71,35 @@ def test_withheld_copies_of_every_build_time_out(lib, heads, grp, dim, lens, dty
     assert st.item() == kda.KDA_ERR_TIMEOUT and not ws[:2048].any() and (o == 0).all()
     again, _ = run_attend(lib, **kw)
     assert torch.equal(want, again)
+
+
+@pytest.mark.gpu
+def test_a_cache_with_dimensions_of_one_and_odd_strides(lib):
+    """A dimension of size 1 says nothing about the layout, whatever its stride; real gaps between heads or blocks are refused."""
+    size, st = 18 * 64, torch.zeros(1, dtype=torch.int32, device="cuda")
+    ctx, table = torch.full((1,), 5, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+
+    def append(pages, heads):
+        x = torch.randn(1, heads, 64, generator=torch.Generator().manual_seed(2)).cuda()
+        lib.kda_kv4_append(pages, table, ctx, x, x, st)
+        torch.cuda.synchronize()
+        return pages
+
+    for num, heads, blocks in ((3, 1, 4), (3, 4, 1), (3, 1, 1), (1, 2, 2), (1, 1, 1)):
+        want = append(torch.zeros(num, heads, blocks, size, dtype=torch.uint8, device="cuda"), heads)
+        assert want.any()
+        for odd in (7, size + 16):
+            strides = list(want.stride())
+            for d, n in enumerate(want.shape):
+                if n == 1:
+                    strides[d] = odd
+            assert torch.equal(append(torch.zeros_like(want).as_strided(want.shape, strides), heads), want)
+    # pages apart from each other are fine, as before
+    wide = torch.zeros(3, 2 * 4 * size, dtype=torch.uint8, device="cuda")
+    append(wide[:, :4 * size].view(3, 1, 4, size), 1)
+    assert wide[0, :size].any() and not wide[:, size:].any() and not wide[1:].any()
+    for bad in (torch.zeros(3, 2, 4, size, dtype=torch.uint8, device="cuda").transpose(1, 2), wide.view(3, 2, 4, size)[:, :, :2],
+                torch.zeros(3, 2, 4, 2 * size, dtype=torch.uint8, device="cuda")[..., ::2]):
+        with pytest.raises(ValueError):
+            append(bad, bad.shape[1])
+    assert st.item() == 0
