@@ -457,7 +457,11 @@ constexpr int KV4_KEYS = 32;             // keys of a unit of work: two blocks
 constexpr int KV4_PART = 24;
 constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
 constexpr int KV4_AHEAD = 16;            // units whose pages a warp looks up at a time: lanes 2 i, 2 i + 1 a block each
-constexpr float KV4_SLACK = 8.f;         // the running maximum may lag by this many powers of two
+// The running maximum may lag by SLACK powers of two, and probabilities are held times 2^LIFT: at most
+// 2^15 in fp16, whose last step then stands for 2^-35 of the maximum's (unlifted, what many keys add behind
+// a dominant one was lost).  A smaller slack moves the maximum more often: 32 x 8 ragged tokens 57.9 us
+// with 8 and with 5, 58.5 with 3, 59.9 with 2.
+constexpr float KV4_SLACK = 5.f, KV4_LIFT = 10.f;
 
 // Warps of a CTA (two CTAs an SM) and units that each has in flight: as many
 // warps as the registers of a mode allow.
@@ -570,6 +574,8 @@ struct Kv4Walk {
 //             probabilities into the same sums, so that products carry 22
 //             bits: fp16 and fp32 queries
 //   KV4_16    two times 8 rows as KV4_8: bf16 queries with more
+// In every mode a probability is also off by up to 2^-35 of the row's largest
+// (fp16's smallest steps, see KV4_LIFT).
 // P leaves the first product with keys along the lane's rows and enters the
 // second with keys along its columns: two 8 x 8 transposes a block.
 //
@@ -986,7 +992,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 for (int n = 0; n < NB; ++n) {
                     // both rows at once (packed fp32)
                     const float2 c = *reinterpret_cast<const float2*>(rowf + row_of(2 * n));
-                    const float2 neg = make_float2(-m[2 * n], -m[2 * n + 1]);
+                    const float2 neg = make_float2(KV4_LIFT - m[2 * n], KV4_LIFT - m[2 * n + 1]);
                     float2 sum = make_float2(l[2 * n], l[2 * n + 1]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

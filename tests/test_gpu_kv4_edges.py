@@ -103,3 +103,58 @@ def test_a_cache_with_dimensions_of_one_and_odd_strides(lib):
         with pytest.raises(ValueError):
             append(bad, bad.shape[1])
     assert st.item() == 0
+
+
+def pages_of(k, v, page):
+    """Pages [n, heads, page / 16, 18 dim] that hold fp32 k, v [tokens, heads, dim] from position 0 on, and the values they stand for."""
+    t, heads, dim = k.shape
+    pad = -t % page
+    z = torch.zeros(pad, heads, dim)
+    (ck, sk), (cv, sv) = ref.encode(torch.cat((k, z))), ref.encode(torch.cat((v, z)))
+    blocks = ref.pack(ck, sk, cv, sv)
+    pages = blocks.view(heads, -1, page // 16, 18 * dim).transpose(0, 1).contiguous()
+    return pages, ref.decode(ck, sk)[:t], ref.decode(cv, sv)[:t]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [19, 24, 26])
+@pytest.mark.parametrize("dim,grp,dtype", [(128, 2, F32), (64, 2, F16), (64, 2, F32), (128, 2, BF16), (64, 12, BF16)])
+def test_attend_behind_a_few_dominant_keys(lib, dim, grp, dtype, bits):
+    """Sinks: keys that outweigh each of the others by about 2^bits, with values of zero in most channels, so that what the many
+    others add stands alone.  Enough requests (on the same pages) that a warp works on thousands of keys behind a sink.
+
+    Bound.  A probability is rounded to 2^-12 of it (with remainders 2^-22), or, where it is small, by an absolute 2^-35 (half of
+    fp16's smallest step, 2^-25, with the maximum held at 2^10 or more).  Its exponent carries the score's errors.  The sums of a
+    warp run over at most N / 16 mma (twice with remainders) of 17 addends, each off by 2^-24 of the sum of magnitudes; the sum of
+    probabilities over N.  Then the output's rounding."""
+    n, N, page, split = 400, 16384, 64, dtype != BF16
+    g = torch.Generator().manual_seed(bits)
+    k, v = torch.randn(N, 1, dim, generator=g), 1 + 0.3 * torch.randn(N, 1, dim, generator=g)
+    k[:, 0, 0] = torch.tensor([-0.5, 0.0, 0.5])[torch.randint(0, 3, (N,), generator=g)]
+    k[:, 0, 1] = 6.0                  # the group's scale is 1: channel 0 holds its values as they are
+    sinks = torch.arange(8) * 32      # one in the first unit of each warp
+    k[sinks, 0, 0] = 6.0
+    v[sinks, 0, 16:] = 0.0
+    pages, kv, vv = pages_of(k, v, page)
+    q = torch.zeros(n, grp, dim)
+    q[:, :, 0] = torch.tensor([1.0, 0.5, 0.75, 0.25]).repeat(3)[:grp]
+    q = q.to(dtype)
+    scale = bits * 0.6931471805599453 / 6
+    o, st = torch.full((n, grp, dim), float("nan"), dtype=dtype, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(kda.KDA_KV4_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    lib.kda_kv4_attend(pages.cuda(), torch.arange(N // page, dtype=torch.int32, device="cuda").repeat(n, 1),
+                       torch.full((n,), N - 1, dtype=torch.int32, device="cuda"), q.cuda(), o, ws, st, scale=scale)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    s = torch.tensor(scale, dtype=F32).double() * q[0].double() @ kv[:, 0].T
+    p = torch.exp(s - s.amax(-1, keepdim=True))
+    p /= p.sum(-1, keepdim=True)
+    want, mag = p @ vv[:, 0], p @ vv[:, 0].abs()
+    score = 2 * s.abs().amax() * 20 * 2.0 ** -24
+    sums = (N / 16 * (2 if split else 1) * 17 + N) * 2.0 ** -24
+    rel = 2 * torch.expm1(score) + (2.0 ** -21 if split else 2.0 ** -11) + sums
+    lim = ref.half_step(dtype) * want.abs() + mag * rel + N * 2.0 ** -35 * vv.abs().max() * p.amax(-1, keepdim=True)
+    if dtype == F16:
+        lim = lim + 2.0 ** -25        # the output's own smallest step
+    bad = (o.cpu().double() - want).abs() > lim
+    assert not bad.any(), f"worst {((o.cpu().double() - want).abs() / lim).max():.3g} of the bound"
