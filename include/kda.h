@@ -693,7 +693,8 @@ int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, 
  * over the cache, after the step's own keys and values were appended.  Token j
  * of request r (packed as for kda_kv4_append, at most KDA_KV4_MAX_TOKENS a
  * request) stands at position ctx_len[r] + j and sees the keys at positions
- * up to its own, with window > 0 the last `window` of them:
+ * up to its own, with window > 0 the last `window` of them (pages that end
+ * left of every token's window are not looked up and may be released):
  *   o = sum_p softmax_p(scale * rot(q) . K_p) V_p;
  * query head h reads key/value head h / (h_q / heads).  Queries are rotated
  * like the keys (rot_dim 0: not at all).  A row that sees no key (a negative

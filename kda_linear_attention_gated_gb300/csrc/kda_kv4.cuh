@@ -805,7 +805,9 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         const int first = put.b, mine = first + KV4_WARPS * (lane >> 1);
         bool ok = false;
         const int b = (put.q.first + mine) * 2 + (lane & 1);
-        if (mine < put.b1 && b * 16 < put.q.ctx + put.q.t) {     // a request's last unit may be one block
+        // a request's last unit may be one block, and so may its first: the page left of a window may be released
+        if (mine < put.b1 && b * 16 < put.q.ctx + put.q.t &&
+            (p.window <= 0 || max(put.q.ctx, 0) - p.window + 1 < (b + 1) * 16)) {
             const int pg = b / bpp, page = __ldg(p.table + (int64_t)put.r * p.cols + pg);
             ok = page >= 0 && page < p.num_pages;
             if (!ok) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);

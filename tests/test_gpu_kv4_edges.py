@@ -158,3 +158,30 @@ def test_attend_behind_a_few_dominant_keys(lib, dim, grp, dtype, bits):
         lim = lim + 2.0 ** -25        # the output's own smallest step
     bad = (o.cpu().double() - want).abs() > lim
     assert not bad.any(), f"worst {((o.cpu().double() - want).abs() / lim).max():.3g} of the bound"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("grp,lens,dtype,window,page", [(2, [1, 1], BF16, 100, 16), (4, [4, 1], F32, 100, 16), (3, [8, 2], BF16, 33, 48), (1, [2, 2], F16, 1, 32)])
+def test_attend_window_with_released_pages(lib, grp, lens, dtype, window, page):
+    """Pages whose keys lie left of every window were released (no page there): not an error, and not read."""
+    heads, dim, ctx = 2, 64, [700, 300]
+    g = torch.Generator().manual_seed(window)
+    cache = ref.Cache([c + t for c, t in zip(ctx, lens)], heads, dim, page, g)
+    for r, c in enumerate(ctx):
+        gone = (c - window + 1) // page       # pages that end at or before the first query's first key
+        assert gone > 0
+        cache.table[r, :gone] = torch.tensor([-1, 2 ** 31 - 1], dtype=torch.int32).repeat(gone)[:gone]
+    q = torch.randn(sum(lens), heads * grp, dim, generator=g).to(dtype)
+    o, st = torch.full(q.shape, float("nan"), dtype=dtype, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(kda.KDA_KV4_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    args = (cache.pages.cuda(), cache.table.cuda(), torch.tensor(ctx, dtype=torch.int32, device="cuda"), q.cuda(), o, ws, st)
+    lib.kda_kv4_attend(*args, cu_seqlens=ragged(lens), max_t=max(lens), window=window)
+    torch.cuda.synchronize()
+    assert st.item() == kda.KDA_OK
+    want, err, big, top = ref.attend(cache, ctx, lens, q, None, None, False, window)
+    assert ((o.cpu().double() - want).abs() <= ref.attend_tolerance(want, err, big, top, dtype, dtype != BF16)).all()
+    # one page more is a page that the first query needs
+    args[1][0, (ctx[0] - window + 1) // page] = -1
+    lib.kda_kv4_attend(*args, cu_seqlens=ragged(lens), max_t=max(lens), window=window)
+    torch.cuda.synchronize()
+    assert st.item() == kda.KDA_ERR_SLOT_RANGE
