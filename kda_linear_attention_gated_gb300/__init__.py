@@ -202,7 +202,7 @@ _PACK_BLOCK_NORM = struct.Struct("@5i3f2q8P")
 def _kv4_cache(pages, k_scale, v_scale) -> tuple:
     """Fields of a struct kda_kv4_cache over a uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor whose pages are dense."""
     shape = pages.shape
-    if len(shape) != 4 or pages.dtype != _torch().uint8 or not pages.is_cuda:
+    if len(shape) != 4 or pages.dtype != _torch_module.uint8:
         raise ValueError("a 4-bit cache is a CUDA uint8 [num_pages, heads, page_tokens / 16, 18 * dim] tensor")
     num, heads, blocks, size = shape
     page = heads * blocks * size
@@ -245,16 +245,31 @@ def _torch():
     return _torch_module
 
 
-def _is(name, t, shape, dtype) -> None:
-    """_expect for one dtype, with a short way through when all is well."""
-    if t is None or t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+def _device(name, t) -> int:
+    """The GPU of a call's first tensor, which has to be the current one: that is where the library launches."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    now = _torch()._C._cuda_getDevice()     # _torch_module is set from here on
+    if at != now:
+        raise ValueError(f"{name} is on cuda:{at}, but the current device is cuda:{now}")
+    return at
+
+
+def _is(name, t, shape, dtype, at) -> None:
+    """_expect for one dtype and the GPU `at`, with a short way through when all is well."""
+    if t is None or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         _expect(name, t, shape, (dtype,))
+    if t.get_device() != at:
+        raise ValueError(f"{name} must be on cuda:{at}, as the call's first tensor is")
 
 
-def _rows(name, t, shape, width, dtype) -> int:
+def _rows(name, t, shape, width, dtype, at) -> int:
     """As _is for a tensor whose rows (its inner dimensions, `width` elements) are dense but may lie apart: the stride between them."""
-    if t is None or t.shape != shape or t.dtype != dtype or not t.is_cuda:
+    if t is None or t.shape != shape or t.dtype != dtype:
         _expect(name, t, shape, (dtype,))
+    if t.get_device() != at:
+        raise ValueError(f"{name} must be on cuda:{at}, as the call's first tensor is")
     if t.is_contiguous():
         return width
     stride, inner = t.stride(), 1
@@ -265,27 +280,27 @@ def _rows(name, t, shape, width, dtype) -> int:
     return stride[0]
 
 
-def _tokens(cu_seqlens, max_t, n, total) -> int:
+def _tokens(cu_seqlens, max_t, n, total, at) -> int:
     """The most tokens of a request of a packed batch (see kda_step)."""
     if cu_seqlens is None:
         return (total // n if n else 0) if max_t is None else max_t
-    _is("cu_seqlens", cu_seqlens, (n + 1,), _torch().int32)
+    _is("cu_seqlens", cu_seqlens, (n + 1,), _torch_module.int32, at)
     if max_t is None:
         raise ValueError("max_t is required with cu_seqlens")
     return max_t
 
 
-def _rotation(cos, sin) -> tuple:
+def _rotation(cos, sin, at) -> tuple:
     """(rot_dim, rows, address, address) of a pair of fp32 [rows, rot_dim / 2] tables."""
     if cos is None and sin is None:
         return 0, 0, 0, 0
     if cos is None or sin is None:
         raise ValueError("cos and sin are given together")
-    shape, f32 = cos.shape, _torch().float32
+    shape, f32 = cos.shape, _torch_module.float32
     if len(shape) != 2:
         raise ValueError("cos and sin are [rows, rot_dim / 2] tensors")
-    _is("cos", cos, shape, f32)
-    _is("sin", sin, shape, f32)
+    _is("cos", cos, shape, f32, at)
+    _is("sin", sin, shape, f32, at)
     return 2 * shape[1], shape[0], cos.data_ptr(), sin.data_ptr()
 
 
@@ -771,10 +786,10 @@ class KdaLibrary:
 
     # -- the operators around the recurrence ---------------------------------
     @staticmethod
-    def _stream_of(t, stream) -> int:
-        """The caller's stream, or PyTorch's current one on the tensor's device."""
+    def _stream_of(at, stream) -> int:
+        """The caller's stream, or PyTorch's current one on the GPU `at`."""
         if stream is None:
-            return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+            return _torch_module._C._cuda_getCurrentRawStream(at)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     def kda_kv4_page_bytes(self, page_tokens, heads, dim) -> int:
@@ -793,29 +808,30 @@ class KdaLibrary:
         rotated by cos, sin [rows, rot_dim / 2] (see kda_kv4_append_args in
         include/kda.h): page_table [N, cols], ctx_len [N] the tokens in the
         cache before the call; k_out, v_out receive the values as stored."""
-        int32 = _torch().int32
+        at = _device("pages", pages)
+        int32 = _torch_module.int32
         cache = _kv4_cache(pages, k_scale, v_scale)
         heads, dim = cache[2], cache[3]
         n, cols = page_table.shape
         total = k.shape[0]
         shape, dtype = (total, heads, dim), k.dtype
-        max_t = _tokens(cu_seqlens, max_t, n, total)
-        rot, rows, cos_at, sin_at = _rotation(cos, sin)
-        _is("page_table", page_table, (n, cols), int32)
-        _is("ctx_len", ctx_len, (n,), int32)
-        _is("status", status, (1,), int32)
-        ks, vs = _rows("k", k, shape, heads * dim, dtype), _rows("v", v, shape, heads * dim, dtype)
+        max_t = _tokens(cu_seqlens, max_t, n, total, at)
+        rot, rows, cos_at, sin_at = _rotation(cos, sin, at)
+        _is("page_table", page_table, (n, cols), int32, at)
+        _is("ctx_len", ctx_len, (n,), int32, at)
+        _is("status", status, (1,), int32, at)
+        ks, vs = _rows("k", k, shape, heads * dim, dtype, at), _rows("v", v, shape, heads * dim, dtype, at)
         out = None
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is not None:
                 out = out or t.dtype
-                _is(name, t, shape, out)
+                _is(name, t, shape, out, at)
         args = _PACK_KV4_APPEND.pack(n, total, max_t, _dtype_code(dtype), cols, rot, bool(interleaved), rows,
                                      0 if out is None else _dtype_code(out), 0, ks, vs, _at(cu_seqlens),
                                      page_table.data_ptr(), ctx_len.data_ptr(), k.data_ptr(), v.data_ptr(), cos_at, sin_at,
                                      _at(k_out), _at(v_out))
         rc = self.lib.packed_kda_kv4_append(_PACK_KV4_CACHE.pack(*cache), args, status.data_ptr(), flags,
-                                            self._stream_of(pages, stream))
+                                            self._stream_of(at, stream))
         self._check(rc, "kda_kv4_append")
 
     def kda_kv4_attend_raw(self, cache: Kv4CacheDesc, args: Kv4AttendArgs, status, stream, flags=0) -> int:
@@ -829,21 +845,22 @@ class KdaLibrary:
         lie apart), o alike and dense, ctx_len [N] the tokens in the cache
         before the step's own; workspace: KDA_KV4_WORKSPACE_BYTES bytes,
         zeroed once."""
-        int32 = _torch().int32
+        at = _device("pages", pages)
+        int32 = _torch_module.int32
         cache = _kv4_cache(pages, k_scale, v_scale)
         n, cols = page_table.shape
         total, h_q = q.shape[0], q.shape[1]
         dim, dtype = cache[3], q.dtype
         shape = (total, h_q, dim)
-        max_t = _tokens(cu_seqlens, max_t, n, total)
-        rot, rows, cos_at, sin_at = _rotation(cos, sin)
-        _is("page_table", page_table, (n, cols), int32)
-        _is("ctx_len", ctx_len, (n,), int32)
-        _is("status", status, (1,), int32)
-        qs = _rows("q", q, shape, h_q * dim, dtype)
-        _is("o", o, shape, dtype)
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
+        max_t = _tokens(cu_seqlens, max_t, n, total, at)
+        rot, rows, cos_at, sin_at = _rotation(cos, sin, at)
+        _is("page_table", page_table, (n, cols), int32, at)
+        _is("ctx_len", ctx_len, (n,), int32, at)
+        _is("status", status, (1,), int32, at)
+        qs = _rows("q", q, shape, h_q * dim, dtype, at)
+        _is("o", o, shape, dtype, at)
+        if workspace.get_device() != at or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{at}")
         if scale is None:
             scale = 0.0
         elif scale == 0:
@@ -853,7 +870,7 @@ class KdaLibrary:
                                      cos_at, sin_at, o.data_ptr(), workspace.data_ptr(),
                                      workspace.numel() * workspace.element_size())
         rc = self.lib.packed_kda_kv4_attend(_PACK_KV4_CACHE.pack(*cache), args, status.data_ptr(), flags,
-                                            self._stream_of(pages, stream))
+                                            self._stream_of(at, stream))
         self._check(rc, "kda_kv4_attend")
 
     def kda_head_norm(self, o, weight, y, gate=None, activation=1, eps=1e-6, stream=None, flags=0) -> None:
@@ -863,13 +880,14 @@ class KdaLibrary:
         [dim]; activation 0 none, 1 sigmoid, 2 SiLU."""
         shape = o.shape
         total, heads, dim = shape
-        _is("o", o, shape, o.dtype)
-        _is("y", y, shape, y.dtype)
-        _is("weight", weight, (dim,), _torch().float32)
-        gs = heads * dim if gate is None else _rows("gate", gate, shape, heads * dim, y.dtype)
+        at = _device("o", o)
+        _is("o", o, shape, o.dtype, at)
+        _is("y", y, shape, y.dtype, at)
+        _is("weight", weight, (dim,), _torch_module.float32, at)
+        gs = heads * dim if gate is None else _rows("gate", gate, shape, heads * dim, y.dtype, at)
         args = _PACK_HEAD_NORM.pack(total, heads, dim, _dtype_code(o.dtype), _dtype_code(y.dtype), activation, eps, 0, gs,
                                     o.data_ptr(), _at(gate), weight.data_ptr(), y.data_ptr())
-        self._check(self.lib.packed_kda_head_norm(args, flags, self._stream_of(o, stream)), "kda_head_norm")
+        self._check(self.lib.packed_kda_head_norm(args, flags, self._stream_of(at, stream)), "kda_head_norm")
 
     def kda_block_norm(self, residual, y, residual_out, w_post=None, gate=None, activation=1, scale=None, w_pre=None, x=None,
                        residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None, flags=0) -> None:
@@ -878,27 +896,28 @@ class KdaLibrary:
         [total, hidden] (fp32 or y's dtype; may be one tensor), y, gate
         [total, hidden] (rows may lie apart), x [total, hidden]; w_post,
         scale, w_pre fp32 [hidden].  y None: x is the norm of the residual."""
-        f32 = _torch().float32
         shape = residual.shape
         total, hidden = shape
+        at = _device("residual", residual)
+        f32 = _torch_module.float32
         typed = x if y is None else y
         if typed is None:
             raise ValueError("y or x is required")
         dtype, rdtype = typed.dtype, residual.dtype
-        _is("residual", residual, shape, rdtype)
+        _is("residual", residual, shape, rdtype, at)
         ys = gs = hidden
         if y is not None:
-            ys = _rows("y", y, shape, hidden, dtype)
-            _is("residual_out", residual_out, shape, rdtype)
+            ys = _rows("y", y, shape, hidden, dtype, at)
+            _is("residual_out", residual_out, shape, rdtype, at)
         if gate is not None:
-            gs = _rows("gate", gate, shape, hidden, dtype)
+            gs = _rows("gate", gate, shape, hidden, dtype, at)
         if x is not None:
-            _is("x", x, shape, dtype)
+            _is("x", x, shape, dtype, at)
         wide = (hidden,)
         for name, w in (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)):
             if w is not None:
-                _is(name, w, wide, f32)
+                _is(name, w, wide, f32, at)
         args = _PACK_BLOCK_NORM.pack(total, hidden, _dtype_code(dtype), _dtype_code(rdtype), activation, eps, residual_scale,
                                      branch_scale, ys, gs, residual.data_ptr(), _at(y), _at(gate), _at(w_post), _at(scale),
                                      _at(w_pre), _at(residual_out), _at(x))
-        self._check(self.lib.packed_kda_block_norm(args, flags, self._stream_of(residual, stream)), "kda_block_norm")
+        self._check(self.lib.packed_kda_block_norm(args, flags, self._stream_of(at, stream)), "kda_block_norm")
