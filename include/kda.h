@@ -698,7 +698,8 @@ int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, 
  *   o = sum_p softmax_p(scale * rot(q) . K_p) V_p;
  * query head h reads key/value head h / (h_q / heads).  Queries are rotated
  * like the keys (rot_dim 0: not at all).  A row that sees no key (a negative
- * position) is zero.  o has q's dtype.
+ * position) is zero, one whose query holds a NaN, an infinity or a value of
+ * 1e37 or more is NaN.  o has q's dtype.
  */
 #define KDA_KV4_MAX_TOKENS 16
 #define KDA_KV4_WORKSPACE_BYTES (20 << 20)

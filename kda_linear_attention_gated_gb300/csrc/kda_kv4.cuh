@@ -757,10 +757,12 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // 2^-z with amax 2^-z in [1/2, 1); rows of nothing, below 1e-30 or past 1e37 stay as they are
+            // 2^-z with amax 2^-z in [1/2, 1); rows of nothing or below 1e-30 stay as they are; rows of an
+            // infinity or past 1e37 become NaN (scores of minus infinity alone would read as keys not seen)
             const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
             // the factor is positive (not 0: a masked score times it stays -infinity), queries take the sign
-            const float down = __uint_as_float((uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u));
+            const float down =
+                __uint_as_float(amax < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
             if (i < ROWS) {
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {

@@ -185,3 +185,35 @@ def test_attend_window_with_released_pages(lib, grp, lens, dtype, window, page):
     lib.kda_kv4_attend(*args, cu_seqlens=ragged(lens), max_t=max(lens), window=window)
     torch.cuda.synchronize()
     assert st.item() == kda.KDA_ERR_SLOT_RANGE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,grp,dtype,rot", [(64, 2, F32, 0), (128, 2, BF16, 0), (64, 12, BF16, 0), (64, 2, F16, 32), (128, 2, F32, 128)])
+def test_attend_queries_that_are_not_finite(lib, dim, grp, dtype, rot):
+    """A query with an infinity (or of 1e37 and more) scores infinities or NaN with every key: its row is NaN by the softmax's
+    definition, also where every score is minus infinity; other rows and requests stay right."""
+    n, page = 6, 16
+    for sign in (1.0, -1.0):
+        k, v = sign * torch.ones(48, 1, dim), torch.randn(48, 1, dim, generator=torch.Generator().manual_seed(4))
+        pages, kv, vv = pages_of(k, v, page)
+        cos, sin = ref.tables(64, rot) if rot else (None, None)
+        q = torch.randn(n, grp, dim, generator=torch.Generator().manual_seed(5))
+        q[0, 0, 3], q[1, 1, dim - 1], q[2, 0, 5], q[3, 1, 0] = float("inf"), float("-inf"), float("nan"), float("-inf")
+        if dtype != F16:
+            q[4, 0, 1] = -2e38
+        q = q.to(dtype)
+        ctx = [0, 0, 40, 40, 9, 47]
+        o, st = torch.zeros(n, grp, dim, dtype=dtype, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = torch.zeros(kda.KDA_KV4_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+        lib.kda_kv4_attend(pages.cuda(), torch.arange(3, dtype=torch.int32, device="cuda").repeat(n, 1), torch.tensor(ctx, dtype=torch.int32, device="cuda"),
+                           q.cuda(), o, ws, st, cos=None if cos is None else cos.cuda(), sin=None if sin is None else sin.cuda())
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        got = o.cpu().double()
+        lost = ~(q.abs() < 1e37).all(-1)
+        assert torch.equal(got.isnan(), lost.unsqueeze(-1).expand_as(got))
+        cache = ref.Cache([0], 1, dim, page, torch.Generator())
+        cache.k, cache.v = [kv] * n, [vv] * n
+        want, err, big, top = ref.attend(cache, ctx, [1] * n, torch.where(lost.unsqueeze(-1), torch.zeros((), dtype=dtype), q), cos, sin, False)
+        lim = ref.attend_tolerance(want, err, big, top, dtype, dtype != BF16)
+        assert ((got - want).abs() <= lim)[~lost].all()
