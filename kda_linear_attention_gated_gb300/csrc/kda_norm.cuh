@@ -61,10 +61,10 @@ template <typename T> __device__ __forceinline__ T from_f32(float x) {
     else return __float2bfloat16_rn(x);
 }
 
-// sigmoid(x) = 1 / (1 + e^-x).  FINE (an fp32 gate): expf and the hardware's
-// approximate reciprocal refined by one Newton step as in sigmoid_neg; below
-// -87 it stays at e^-87 (1.6e-38), where the infinite sum would make the step
-// NaN.  Otherwise (a 16-bit gate, whose own rounding is 2^-12 or more of it) four
+// sigmoid(x) = 1 / (1 + e^-x).  FINE (an fp32 gate): with t = e^-|x| it is
+// 1 / (1 + t) or t / (1 + t), so that nothing overflows and a far negative gate
+// goes to 0 through the subnormal numbers; expf and the hardware's approximate
+// reciprocal refined by one Newton step as in sigmoid_neg.  Otherwise (a 16-bit gate, whose own rounding is 2^-12 or more of it) four
 // instructions: the exponent's product with log2(e) is rounded once, so the
 // result is within (|x| + 6) 2^-24 of the true one, relatively.  Instructions
 // bound the head norm: with FINE everywhere 8192 x 12 x 128 took 20.2 us.
@@ -72,9 +72,10 @@ template <typename T> __device__ __forceinline__ T from_f32(float x) {
 template <bool FINE> __device__ __forceinline__ float sigmoid_f(float x) {
     float r;
     if constexpr (FINE) {
-        const float y = 1.f + expf(x < -87.f ? 87.f : -x);
+        const float t = expf(-fabsf(x)), y = 1.f + t;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-        return fmaf(r, fmaf(-y, r, 1.f), r);
+        r = fmaf(r, fmaf(-y, r, 1.f), r);
+        return x < 0.f ? t * r : r;
     } else {
         float e;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));

@@ -29,3 +29,31 @@ def test_block_norm_of_the_most_rows_there_can_be(lib):
         # one rounding to bf16 behind fp32 work of a few half steps
         bad = (x[a:a + (1 << 27)].double() - want).abs() > (ref.half_step(BF16) + 2.0 ** -19) * want.abs()
         assert not bad.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [1, 2])
+def test_gates_far_from_zero_in_fp32(lib, kind):
+    """sigmoid and SiLU to the ends of fp32: e^x below -87 down to subnormal numbers and zero, one above.
+
+    Bound: the fp32 work behind a gate's factor is 24 half steps (exponential, reciprocal, products), and a subnormal sigmoid is
+    off by a last step, 2^-149, once for its exponential and once for the product; the gate and the row multiply that."""
+    g = torch.tensor([0.0, -0.0, 1e-20, 20.0, 87.0, 200.0, 1e30, float("inf"), -20.0, -86.9, -87.1, -88.5, -95.0, -100.0, -103.5, -104.5, -150.0,
+                      -1e4, -1e30, -3e38, float("-inf"), float("nan"), 5.0, -5.0])
+    dim = g.numel()
+    gate = g.view(1, 1, dim).repeat(2, 1, 1)
+    o = torch.ones(2, 1, dim)
+    o[1] = -3.0
+    y = torch.empty(2, 1, dim, device="cuda")
+    lib.kda_head_norm(o.cuda(), torch.ones(dim, device="cuda"), y, gate=gate.cuda(), activation=kind, eps=0.0)
+    ro, x = torch.empty(2, dim, device="cuda"), torch.empty(2, dim, device="cuda")
+    lib.kda_block_norm(torch.zeros(2, dim, device="cuda"), o[:, 0].cuda(), ro, w_post=torch.ones(dim, device="cuda"), gate=gate[:, 0].cuda(),
+                       activation=kind, eps=0.0)
+    want = ref.head_norm(o, torch.ones(dim), gate, kind, 0.0)
+    lim = 25 * 2.0 ** -24 * want.abs() + 2.0 ** -148 * ((1 + gate.double().abs()) if kind == 2 else 1.0)
+    for got in (y, ro.view(2, 1, dim)):
+        got = got.cpu().double()
+        assert torch.equal(got.isnan(), want.isnan())
+        fine = want.isfinite()
+        assert torch.equal(got[~fine & ~want.isnan()], want[~fine & ~want.isnan()])
+        assert ((got - want).abs() <= lim)[fine].all(), ((got - want).abs() / lim).nan_to_num(0).view(2, -1)
