@@ -64,11 +64,13 @@ template <typename T> __device__ __forceinline__ T from_f32(float x) {
 // sigmoid(x) = 1 / (1 + e^-x).  FINE (an fp32 gate): with t = e^-|x| it is
 // 1 / (1 + t) or t / (1 + t), so that nothing overflows and a far negative gate
 // goes to 0 through the subnormal numbers; expf and the hardware's approximate
-// reciprocal refined by one Newton step as in sigmoid_neg.  Otherwise (a 16-bit gate, whose own rounding is 2^-12 or more of it) four
-// instructions: the exponent's product with log2(e) is rounded once, so the
-// result is within (|x| + 6) 2^-24 of the true one, relatively.  Instructions
-// bound the head norm: with FINE everywhere 8192 x 12 x 128 took 20.2 us.
-// A NaN passes through both.
+// reciprocal refined by one Newton step as in sigmoid_neg.  Otherwise (a 16-bit
+// gate, whose own rounding is 2^-12 or more of it) four instructions.  Their
+// relative error is within (1.25 |x| + 7) 2^-24 while the result is a normal
+// fp32 number, x >= -87: the rounding of the exponent's product with log2(e) and
+// of that constant (1.23 |x| together), the exponential (4), its sum with 1 (1)
+// and the reciprocal (2); below it is 0.  Instructions bound the head norm: with
+// FINE everywhere 8192 x 12 x 128 took 20.2 us.  A NaN passes through both.
 template <bool FINE> __device__ __forceinline__ float sigmoid_f(float x) {
     float r;
     if constexpr (FINE) {

@@ -57,3 +57,21 @@ def test_gates_far_from_zero_in_fp32(lib, kind):
         fine = want.isfinite()
         assert torch.equal(got[~fine & ~want.isnan()], want[~fine & ~want.isnan()])
         assert ((got - want).abs() <= lim)[fine].all(), ((got - want).abs() / lim).nan_to_num(0).view(2, -1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_sigmoid_of_every_16_bit_gate(lib, dtype):
+    """The factor of a 16-bit gate, seen whole through an fp32 residual: within (1.25 |x| + 7) 2^-24 of the sigmoid where that is
+    a normal fp32 number, nothing (less than 2^-125) below."""
+    g = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16).view(dtype)
+    g = g[~g.isnan()].cuda()
+    n = g.numel() // 8 * 8
+    g = torch.cat((g[:n], g[-8:])).view(-1, 8)
+    h, zero = torch.empty(g.shape, device="cuda"), torch.zeros(g.shape, device="cuda")
+    lib.kda_block_norm(zero, torch.ones_like(g), h, gate=g, activation=1)
+    x, h = g.cpu().double().flatten(), h.cpu().double().flatten()
+    want = torch.sigmoid(x)
+    normal = x >= -87.0
+    assert ((h - want).abs() <= (1.25 * x.abs().clamp(max=90) + 7) * 2.0 ** -24 * want)[normal].all()
+    assert (h[~normal].abs() <= 2.0 ** -125).all() and normal.sum() > 40000
