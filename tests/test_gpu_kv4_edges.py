@@ -6,7 +6,7 @@ import torch
 import kda_linear_attention_gated_gb300 as kda
 
 import _layer_ref as ref
-from test_gpu_kv4 import P, append_args, attend_args, cache_desc, ragged, run_attend
+from test_gpu_kv4 import P, append_args, attend_args, cache_desc, ragged, run_append, run_attend
 
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
 
@@ -217,3 +217,21 @@ def test_attend_queries_that_are_not_finite(lib, dim, grp, dtype, rot):
         want, err, big, top = ref.attend(cache, ctx, [1] * n, torch.where(lost.unsqueeze(-1), torch.zeros((), dtype=dtype), q), cos, sin, False)
         lim = ref.attend_tolerance(want, err, big, top, dtype, dtype != BF16)
         assert ((got - want).abs() <= lim)[~lost].all()
+
+
+# -- append -------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,heads,dim,dtype,rot,inter,out", [(33, 2, 64, BF16, 64, False, True), (70, 3, 128, F16, 64, True, True), (131, 1, 64, F32, 0, False, False)])
+def test_append_of_more_requests_than_lanes(lib, n, heads, dim, dtype, rot, inter, out):
+    """The request of a token is found among more than 32, with empty and padding ones on both sides of every 32nd."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 4, (n,), generator=g).tolist()
+    ctx = torch.randint(0, 50, (n,), generator=g).tolist()
+    for r in (0, 30, 31, 32, 33, 62, 63, 64, 65, 95, 96, 127, 128):
+        if r < n:
+            lens[r] = 0
+    for r in range(4, n, 13):
+        lens[r], ctx[r] = 3, -3
+    run_append(lib, heads, dim, 16, ctx, lens, dtype, rot, inter, seed=n, out=out)
+    lens = [0] * 32 + [9] + [0] * (n - 33)     # every token behind the first 32 requests
+    run_append(lib, heads, dim, 16, ctx, lens, dtype, rot, inter, seed=n, out=out)
