@@ -611,8 +611,10 @@ int kda_ckpt_load(const kda_pool* pool, const kda_ckpt_plane* plane, const int32
  *   [17 dim, 18 dim)  value scales: group i of token w at (i * 4 + w % 8 / 2) * 4 + w / 8 * 2 + w % 2
  * (the order in which the attention kernel's tensor-core fragments take
  * them).  Pages need no initial value: what was never appended is never read
- * as a value.  (The pages of pull request 2945, Performance, count a key/value
- * pool in blocks of 128 tokens; its format is this library's own.)
+ * as a value.  (The format is this library's own, for layers with plain key
+ * and value heads.  Pull request 2945, Performance, counts a pool in blocks of
+ * 128 tokens: its model's attention layers cache a latent instead (MLA), which
+ * these calls do not serve.)
  */
 typedef struct kda_kv4_cache {
     void* base;           /* device, 16-byte aligned */
@@ -643,12 +645,16 @@ int kda_kv4_page_bytes(int32_t page_tokens, int32_t heads, int32_t dim, int64_t*
  * sin at the token's position, in fp32:
  *   interleaved 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1);
  *   x_a <- x_a cos_i - x_b sin_i,  x_b <- x_b cos_i + x_a sin_i.
- * A group of 16 values t (x / k_scale or x / v_scale) is rounded as
+ * A group of 16 values t (x times the fp32 reciprocal of k_scale or v_scale)
+ * is rounded as
  *   scale = e4m3(max |t| / 6), code = e2m1(t / scale), to nearest even, at
  *   most 448 and 6; a group that holds a NaN or an infinity reads back as NaN.
  * k_out and v_out receive the values that the cache then stands for, rounded
  * to out_dtype: attention over a prompt's own tokens can run on the values
  * that later steps will see.
+ * Rows behind the last request's tokens (cu_seqlens[n] < total) belong to no
+ * one: KDA_ERR_ARG, and zero rows of k_out and v_out; kda_kv4_attend leaves its
+ * rows there as they are.
  */
 typedef struct kda_kv4_append_args {
     int32_t n;                  /* requests */

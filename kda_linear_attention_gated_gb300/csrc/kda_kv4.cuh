@@ -182,6 +182,10 @@ struct Kv4AppendParams {
 };
 
 constexpr int KV4_APPEND_THREADS = 128, KV4_APPEND_WARPS = KV4_APPEND_THREADS / 32;
+// The heads of eight tokens are shared out over several CTAs while the grid stays below 16 CTAs for each of
+// 152 SMs.  8 x 1024 tokens of 8 heads of 128: 22.8 us with half as many, 20.5 with these, 20.9 with twice;
+// the same of fp32 26.5, 26.6, 27.5; 64 x 8 tokens and fewer 4 us with any.
+constexpr int KV4_APPEND_CTAS = 16 * 152;
 
 // Sixteen elements of 2 or 4 bytes as loaded (the host checks the alignment of
 // base and stride), and widened to fp32.
@@ -304,8 +308,10 @@ __device__ __forceinline__ void kv4_turn(float& a, float& b, float c, float s) {
 // the eight tokens fill half a block.  The loads of a head do not wait for the
 // token's place: they are on their way while that is looked up.  Rotation in
 // fp32, products and sums rounded one by one (no fused multiply-add).  8192
-// tokens of 8 heads of 128, bf16: 20.4 us, 3.8 TB/s, bound by issue (about 20
-// instructions an element) and the look-up's latency.
+// tokens of 8 heads of 128, bf16: 20.4 us, 3.8 TB/s.  Bound by latency: 16 warps
+// an SM (registers) wait for the look-up and for every head after a warp's
+// first, whose loads are not ahead; half of the issue slots go to the about 20
+// instructions an element.
 template <int D, int ES>
 __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_append_kernel(const Kv4AppendParams p) {
     constexpr int NG = Kv4<D>::NG, NP = NG / 2, HW = 4 / NP;     // groups and pairs of a head, heads of a warp
@@ -452,8 +458,11 @@ struct Kv4AttendParams {
 constexpr int KV4_8 = 0, KV4_REST = 1, KV4_16 = 2;
 constexpr int KV4_ROWS = 16;             // most rows of a tile
 constexpr int KV4_KEYS = 32;             // keys of a unit of work: two blocks
-// What beginning and ending a part costs a CTA, in units: 32 x 8 ragged tokens took 90 us with 12,
-// 66 with 16, 62 with 20, 60 with 24, 61 with 28.
+// What beginning and ending a part costs a CTA, in units.  With 12, 16, 20, 24, 28, 32, us:
+//   ragged 32 x 8 tokens, bf16, grp 6, D = 128 (KV4_16)  87.7, 71.9, 63.6, 61.2, 61.2, 63.0;  D = 64  58.5, 47.7, 44.9, 41.3, 40.2, 41.6
+//   ragged 64 x 1, bf16, grp 4 (KV4_8)  D = 128  41.3, 38.1, 36.1, 35.8, 36.1, 37.7;  D = 64  36.1, 32.4, 30.7, 29.4, 28.6, 28.9
+//   ragged 32 x 2, grp 4 (KV4_REST)  fp16, D = 128  25.5, 25.9, 26.8, 26.9, 28.1, 27.9;  fp32, D = 64  19.2, 18.9, 19.2, 19.5, 19.3, 19.2
+// One value for all builds: the fp16 and fp32 ones, whose units take longer, would gain 5 % and 3 % with 12 and 16.
 constexpr int KV4_PART = 24;
 constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
 constexpr int KV4_AHEAD = 16;            // units whose pages a warp looks up at a time: lanes 2 i, 2 i + 1 a block each
@@ -592,8 +601,8 @@ struct Kv4Walk {
 // Bound by issue: decoding fills half of the ALU pipe, and 16 warps an SM (the
 // registers of the sums, the rings) leave 0.4 of the issue slots empty.  A loop
 // of decode and mma alone takes 290 cycles a block and scheduler, this kernel
-// about 430.  64 requests x 8192 tokens, 32/8 heads of 128: 116 us, 5.2 TB/s of
-// cache, 0.77 of the measured copy bandwidth.  Keys and values as the B operand
+// about 430.  64 requests x 8192 tokens, 32/8 heads of 128: 118 us, 5.1 TB/s of
+// cache, 0.75 of the measured copy bandwidth.  Keys and values as the B operand
 // (query rows on the 16-row side, half of it idle): 168 us.
 template <int D, int MODE>
 __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_kernel(const Kv4AttendParams p) {

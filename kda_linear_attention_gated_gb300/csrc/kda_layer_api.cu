@@ -184,7 +184,7 @@ int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, 
     prm.status = dev_status;
     // eight tokens a CTA; few tokens share their heads out over more CTAs
     const int tokens = (int)(((int64_t)g.total + 7) / 8), items = cache->dim == 128 ? cache->heads * 2 : (cache->heads + 1) / 2 * 2;
-    const int parts = std::max(1, std::min((items + kda::KV4_APPEND_WARPS - 1) / kda::KV4_APPEND_WARPS, 2432 / tokens));
+    const int parts = std::max(1, std::min((items + kda::KV4_APPEND_WARPS - 1) / kda::KV4_APPEND_WARPS, kda::KV4_APPEND_CTAS / tokens));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tokens, (unsigned)parts, 1);
     cfg.blockDim = dim3(kda::KV4_APPEND_THREADS, 1, 1);

@@ -116,7 +116,7 @@ constexpr int HEAD_NORM_THREADS = 256;
 // y = w o / sqrt(mean o^2 + eps) * act(gate), a row a head.  A row is LPR lanes (a
 // power of two) of eight channels each, so a warp takes 32 / LPR rows and the
 // sum takes log2 LPR shuffles.  8192 x 12 x 128, fp32 in, bf16 gate and out: 17.0
-// us, 0.88 of the measured copy bandwidth.  Two rows a thread (more loads on
+// us, 0.87 of the measured copy bandwidth.  Two rows a thread (more loads on
 // their way) were no faster: 19.2 against 18.7 us at the time.
 template <typename OT, typename T>
 __global__ void __launch_bounds__(HEAD_NORM_THREADS) kda_head_norm_kernel(const HeadNormParams p, int lpr_log2) {
@@ -186,9 +186,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows in shared memory at a time, each its residual, y and gate.  Two: with three
-// fewer CTAs fit an SM (8192 x 4096: 86.5 us against 83; 1021 x 2049 of fp32:
-// 11.2 against 10.7).
+// Rows in shared memory at a time, each its residual, y and gate.  Two: three took
+// 86.5 us against 83 for 8192 x 4096 (two CTAs an SM by registers either way) and
+// 11.2 against 10.7 for 1021 x 2049 of fp32 (two CTAs an SM instead of three).
 constexpr int BLOCK_NORM_STAGES = 2;
 template <typename T, typename R> constexpr size_t block_norm_smem(int threads) {
     return (size_t)BLOCK_NORM_STAGES * (8 * sizeof(R) + 16 * sizeof(T)) * threads;
@@ -202,7 +202,7 @@ template <typename T, typename R> constexpr size_t block_norm_smem(int threads) 
 // (reading them again for every row is half as many bytes again, from L2).  The
 // next row is on its way to shared memory meanwhile: a thread copies and reads
 // only its own places, so the copies need no barrier.  8192 x 4096, bf16 with an
-// fp32 residual: 84 us, 0.83 of the measured copy bandwidth.
+// fp32 residual: 83 us, 0.83 of the measured copy bandwidth.
 //
 // SHIFT: a width that is no multiple of eight.  Vectors then lie on multiples
 // of eight in the buffer, not in the row: a row's first one begins up to seven
