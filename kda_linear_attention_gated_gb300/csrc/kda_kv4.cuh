@@ -601,8 +601,8 @@ struct Kv4Walk {
 // Bound by issue: decoding fills half of the ALU pipe, and 16 warps an SM (the
 // registers of the sums, the rings) leave 0.4 of the issue slots empty.  A loop
 // of decode and mma alone takes 290 cycles a block and scheduler, this kernel
-// about 430.  64 requests x 8192 tokens, 32/8 heads of 128: 118 us, 5.1 TB/s of
-// cache, 0.75 of the measured copy bandwidth.  Keys and values as the B operand
+// about 430.  64 requests x 8192 tokens, 32/8 heads of 128: 117 us, 5.2 TB/s of
+// cache, 0.76 of the measured copy bandwidth.  Keys and values as the B operand
 // (query rows on the 16-row side, half of it idle): 168 us.
 template <int D, int MODE>
 __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_kernel(const Kv4AttendParams p) {
