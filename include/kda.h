@@ -813,6 +813,135 @@ typedef struct kda_block_norm_args {
  */
 int kda_block_norm(const kda_block_norm_args* args, uint32_t flags, void* stream);
 
+/*
+ * A speculative step over a tree of drafted tokens.
+ *
+ * A request's tokens (packed as everywhere: cu_seqlens, or max_t each; at most
+ * KDA_TREE_MAX_TOKENS a request) form a tree behind its context: token 0 is
+ * the last token that was accepted, the others are drafts of what may follow
+ * it.  `tree` is a device array [total] of masks: bit i of token j's mask says
+ * that the request's token i is an ancestor of j; parents come before their
+ * children.  Bit j counts as set and the bits above it as not set, whatever the
+ * mask holds.  A token's parent is the highest of its ancestors, its depth their
+ * number; a token without ancestors stands directly behind the context.  The
+ * ancestors of an ancestor have to be a token's ancestors too (a precondition;
+ * no mask makes a kernel leave its buffers).
+ *
+ * A step of a hybrid model: kda_conv_step_tree and kda_step_tree in its KDA
+ * layers, kda_kv4_append_tree and kda_kv4_attend_tree in its attention
+ * layers, kda_accept on the target's probabilities.  Then the accepted path is
+ * kept: the recurrence goes on from the path's last token (kda_accept's `node` is
+ * the next step's `accepted`), and the path's inputs, gathered by kda_accept's
+ * `path`, go through kda_conv_step and kda_kv4_append, which write the window
+ * and the cache as a chain of those tokens does.  The window's history then
+ * ends with the window, so its accepted index is state_len - kernel_width + 2
+ * in every call (1, or NULL, in a window of kernel_width - 1 entries).
+ * (Pull request 2894, deployment flags, and pull request 2945, Performance:
+ * drafts verified by the target in one step, there as one chain.)
+ */
+#define KDA_TREE_MAX_TOKENS 64
+
+/*
+ * kda_step over a tree: token j's state follows from its parent's (from the
+ * initial state for a token without ancestors), o and the snapshot in column
+ * j of the slot table as in kda_step.  States are carried in fp32 along every
+ * path, not rounded between tokens, and do not depend on their siblings.
+ * args as for kda_step with in_place 0 and max_t <= KDA_TREE_MAX_TOKENS
+ * (KDA_ERR_SHAPE); flags other than KDA_LAUNCH_PDL: KDA_ERR_ARG.  A request
+ * with an id outside the pool is skipped whole.
+ */
+int kda_step_tree(const kda_pool* pool, const kda_step_args* args, const uint64_t* tree, int32_t* dev_status, uint32_t flags,
+                  void* stream);
+
+/*
+ * kda_conv_step over a tree: y_j from the last kernel_width inputs on token
+ * j's path, before its first token the history of the window (at the accepted
+ * index, as in kda_conv_step; bit for bit its y for a chain).  The window is
+ * not written.  args and checks as for kda_conv_step, and max_t <=
+ * KDA_TREE_MAX_TOKENS (KDA_ERR_SHAPE); flags other than KDA_LAUNCH_PDL:
+ * KDA_ERR_ARG; device checks 0 <= acc and acc + kernel_width - 1 <= state_len.
+ */
+int kda_conv_step_tree(const kda_conv_window* win, const kda_conv_args* args, const uint64_t* tree, int32_t* dev_status,
+                       uint32_t flags, void* stream);
+
+/*
+ * kda_kv4_append and kda_kv4_attend over a tree.  Token j is stored at position
+ * ctx_len[r] + j and rotated, key and query, by the row of cos and sin at
+ * ctx_len[r] + its depth; cos and sin need a row for every position up to
+ * ctx_len[r] + T_r - 1.  It sees the ctx_len[r] keys before the tree, its
+ * ancestors and itself; with window > 0 those of them less than `window`
+ * positions before its own, ctx_len[r] + depth.  ctx_len[r] >= 0, or
+ * ctx_len[r] <= -T_r for padding (KDA_ERR_ARG on the device else, that
+ * request's rows zero).  Otherwise args and checks as for the calls without a
+ * tree, max_t <= KDA_TREE_MAX_TOKENS.
+ */
+int kda_kv4_append_tree(const kda_kv4_cache* cache, const kda_kv4_append_args* args, const uint64_t* tree, int32_t* dev_status,
+                        uint32_t flags, void* stream);
+int kda_kv4_attend_tree(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, const uint64_t* tree, int32_t* dev_status,
+                        uint32_t flags, void* stream);
+
+/*
+ * Arguments of kda_accept: drafts verified against the target's probabilities
+ * with given random numbers, and the next token drawn.  Row j of p is the
+ * target's distribution of the token behind token j (and its ancestors), row j
+ * of q the one that token j's children were drawn from, independently of each
+ * other; q NULL: drafts that were given, not drawn.  Rows are taken as
+ * distributions; an entry that is negative or NaN counts as zero.
+ *
+ * The walk begins at token 0 with W = p(. | token 0), Z = 1.  The children x
+ * of the last accepted token, in order:
+ *   with q:  accepted if u q(x) Z < W(x), else W <- max(W - Z q, 0), Z <- sum W
+ *   q NULL:  accepted if u Z < W(x),      else Z <- Z - W(x), W(x) <- 0
+ * with the child's own u.  An accepted child goes on with W its row of p, Z =
+ * 1.  Where no child is left, the next token is the lowest i with W(i) > 0 and
+ * sum_{l <= i} W(l) > u_last sum W, or, if rounding leaves none, the last with
+ * W(i) > 0; if W is zero throughout, W is the row of p again.  Accepted tokens
+ * and the next one are distributed as the target's own.  Sums are held in 48
+ * bits or more, tests in 53.
+ *   accepted  [n]         tokens accepted, token 0 among them; 0 without tokens
+ *   node      [n]         1 + the last one's place in its request (kda_step_tree's
+ *                         `accepted` in the next step, where its columns are); 0 without tokens
+ *   path      [n][max_t]  their rows, in order; -1 behind the last
+ *   token     [n]         the next token; -1 without tokens
+ * Device checks (in *dev_status): KDA_ERR_ARG for token offsets outside
+ * 0 .. max_t or past total (outputs as without tokens), for a draft's id outside
+ * the vocabulary (not tested, its subtree not accepted), and for a row of p
+ * whose sum is zero or not finite when the next token is drawn from it (token
+ * -1, the other outputs as they are).
+ */
+#define KDA_ACCEPT_MAX_VOCAB (1 << 30)
+typedef struct kda_accept_args {
+    int32_t n;                  /* requests */
+    int32_t total;              /* packed tokens */
+    int32_t max_t;              /* most tokens of any request, <= KDA_TREE_MAX_TOKENS */
+    int32_t vocab;              /* 1 .. KDA_ACCEPT_MAX_VOCAB */
+    int32_t dtype;              /* of p and q: KDA_F32, KDA_F16 or KDA_BF16 */
+    int32_t reserved;           /* 0 */
+    int64_t p_stride;           /* elements from one row to the next, >= vocab; any alignment (16-byte aligned */
+    int64_t q_stride;           /* rows of q, or rows of q and p that lie alike, run faster) */
+    const int32_t* cu_seqlens;  /* [n + 1] or NULL */
+    const uint64_t* tree;       /* [total] or NULL: a chain */
+    const void* p;              /* [total] rows of [vocab] */
+    const void* q;              /* [total] rows of [vocab] or NULL */
+    const int32_t* tokens;      /* [total] */
+    const float* u;             /* [total], in [0, 1); token 0's is not used */
+    const float* u_last;        /* [n], in [0, 1) */
+    int32_t* accepted;
+    int32_t* node;
+    int32_t* path;
+    int32_t* token;
+} kda_accept_args;
+
+/*
+ * Verification (see kda_accept_args); args is a host pointer.  Host checks:
+ * KDA_ERR_NULL, _DTYPE_UNSUPPORTED, _SHAPE (vocab, strides, max_t, total
+ * inconsistent with n and max_t, n above 2^28 - 1), _ALIGN (every array to its
+ * element size), _ARG (negative counts, reserved, flags other than
+ * KDA_LAUNCH_PDL).  n == 0 or max_t == 0 is a no-op; total == 0 writes the
+ * outputs of requests without tokens.
+ */
+int kda_accept(const kda_accept_args* args, int32_t* dev_status, uint32_t flags, void* stream);
+
 /* A static, human-readable string for a kda_status code. */
 const char* kda_strerror(int32_t code);
 

@@ -28,12 +28,13 @@ __all__ = ["KdaError", "KdaLibrary", "PoolDesc", "build", "lib_path",
            "KDA_ERR_SHAPE", "KDA_ERR_ALIGN", "KDA_ERR_LAUNCH", "KDA_ERR_SLOT_RANGE",
            "KDA_ERR_ARG", "KDA_ERR_TIMEOUT", "KDA_ERR_LAYOUT", "KDA_LAUNCH_PDL", "KDA_LAUNCH_PDL_EARLY_STATE",
            "KDA_LAUNCH_TEST_WITHHOLD_STATE", "KDA_KV4_WORKSPACE_BYTES", "KDA_KV4_MAX_TOKENS", "KDA_KV4_MAX_COUNT", "KDA_BLOCK_NORM_MAX",
-           "EXPORTED_SYMBOLS"]
+           "KDA_TREE_MAX_TOKENS", "KDA_ACCEPT_MAX_VOCAB", "EXPORTED_SYMBOLS"]
 
 KDA_F32, KDA_F16, KDA_BF16 = 0, 1, 2
 KDA_LAUNCH_PDL, KDA_LAUNCH_PDL_EARLY_STATE = 1, 2
 KDA_LAUNCH_TEST_WITHHOLD_STATE = 1 << 30  # test hook of the timeout path (include/kda.h)
 KDA_KV4_WORKSPACE_BYTES, KDA_KV4_MAX_TOKENS, KDA_KV4_MAX_COUNT, KDA_BLOCK_NORM_MAX = 20 << 20, 16, 0x7FFFFF00, 16384
+KDA_TREE_MAX_TOKENS, KDA_ACCEPT_MAX_VOCAB = 64, 1 << 30
 (KDA_OK, KDA_ERR_NULL, KDA_ERR_DTYPE_MISMATCH, KDA_ERR_DTYPE_UNSUPPORTED,
  KDA_ERR_LAYERS_DISAGREE, KDA_ERR_SHAPE, KDA_ERR_ALIGN, KDA_ERR_LAUNCH,
  KDA_ERR_SLOT_RANGE, KDA_ERR_ARG, KDA_ERR_TIMEOUT, KDA_ERR_LAYOUT) = range(12)
@@ -44,6 +45,7 @@ EXPORTED_SYMBOLS = ("kda_build_state_dtype", "kda_pool_check", "kda_state_bytes"
                     "kda_step_conv",
                     "kda_layout_id", "kda_ckpt_flush", "kda_ckpt_load", "kda_stage_host",
                     "kda_kv4_page_bytes", "kda_kv4_append", "kda_kv4_attend", "kda_head_norm", "kda_block_norm",
+                    "kda_step_tree", "kda_conv_step_tree", "kda_kv4_append_tree", "kda_kv4_attend_tree", "kda_accept",
                     "kda_strerror")
 
 
@@ -160,6 +162,14 @@ class BlockNormArgs(ctypes.Structure):
                [(f, ctypes.c_void_p) for f in ("residual", "y", "gate", "w_post", "scale", "w_pre", "residual_out", "x")]
 
 
+class AcceptArgs(ctypes.Structure):
+    """Mirror of ``struct kda_accept_args`` (include/kda.h)."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("n", "total", "max_t", "vocab", "dtype", "reserved")] + \
+               [("p_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64)] + \
+               [(f, ctypes.c_void_p) for f in ("cu_seqlens", "tree", "p", "q", "tokens", "u", "u_last", "accepted", "node",
+                                               "path", "token")]
+
+
 class CkptPlaneDesc(ctypes.Structure):
     """Mirror of ``struct kda_ckpt_plane`` (include/kda.h)."""
     _fields_ = [("base", ctypes.c_void_p), ("layout_id", ctypes.c_uint32), ("reserved", ctypes.c_int32),
@@ -197,6 +207,11 @@ _PACK_KV4_APPEND = struct.Struct("@10i2q9P")
 _PACK_KV4_ATTEND = struct.Struct("@10ifiq8Pq")
 _PACK_HEAD_NORM = struct.Struct("@6ifiq4P")
 _PACK_BLOCK_NORM = struct.Struct("@5i3f2q8P")
+_PACK_POOL = struct.Struct("@P4i2q")
+_PACK_STEP = struct.Struct("@8i12P")
+_PACK_CONV_WINDOW = struct.Struct("@P4i2q")
+_PACK_CONV = struct.Struct("@6i8P")
+_PACK_ACCEPT = struct.Struct("@6i2q11P")
 
 
 def _kv4_cache(pages, k_scale, v_scale) -> tuple:
@@ -304,6 +319,12 @@ def _rotation(cos, sin, at) -> tuple:
     return 2 * shape[1], shape[0], cos.data_ptr(), sin.data_ptr()
 
 
+def _masks(tree, total, at) -> int:
+    """The address of a tree's masks."""
+    _is("tree", tree, (total,), _torch_module.int64, at)
+    return tree.data_ptr()
+
+
 def _at(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -370,11 +391,21 @@ def _load(state16: bool) -> ctypes.CDLL:
         for fn, args in ((lib.kda_head_norm, HeadNormArgs), (lib.kda_block_norm, BlockNormArgs)):
             fn.restype = ctypes.c_int
             fn.argtypes = [ctypes.POINTER(args), u32, vp]
-        # the same entry points taking packed arguments
-        for name, kind in (("kda_kv4_append", 2), ("kda_kv4_attend", 2), ("kda_head_norm", 1), ("kda_block_norm", 1)):
+        W = ctypes.POINTER(ConvWindowDesc)
+        for fn, args in ((lib.kda_step_tree, [P, ctypes.POINTER(StepArgs), vp]),
+                         (lib.kda_conv_step_tree, [W, ctypes.POINTER(ConvArgs), vp]),
+                         (lib.kda_kv4_append_tree, [C, ctypes.POINTER(Kv4AppendArgs), vp]),
+                         (lib.kda_kv4_attend_tree, [C, ctypes.POINTER(Kv4AttendArgs), vp]),
+                         (lib.kda_accept, [ctypes.POINTER(AcceptArgs)])):
+            fn.restype = ctypes.c_int
+            fn.argtypes = args + [vp, u32, vp]
+        # the same entry points taking packed arguments: structs, then addresses
+        for name, kind, more in (("kda_kv4_append", 2, 1), ("kda_kv4_attend", 2, 1), ("kda_head_norm", 1, 0),
+                                 ("kda_block_norm", 1, 0), ("kda_step_tree", 2, 2), ("kda_conv_step_tree", 2, 2),
+                                 ("kda_kv4_append_tree", 2, 2), ("kda_kv4_attend_tree", 2, 2), ("kda_accept", 1, 1)):
             fn = lib[name]
             fn.restype = ctypes.c_int
-            fn.argtypes = [ctypes.c_char_p] * kind + [vp] * (kind == 2) + [u32, vp]
+            fn.argtypes = [ctypes.c_char_p] * kind + [vp] * more + [u32, vp]
             setattr(lib, "packed_" + name, fn)
         lib.kda_strerror.restype = ctypes.c_char_p
         lib.kda_strerror.argtypes = [i32]
@@ -808,6 +839,22 @@ class KdaLibrary:
         rotated by cos, sin [rows, rot_dim / 2] (see kda_kv4_append_args in
         include/kda.h): page_table [N, cols], ctx_len [N] the tokens in the
         cache before the call; k_out, v_out receive the values as stored."""
+        self._kv4_append(pages, page_table, ctx_len, k, v, None, status, cu_seqlens, max_t, cos, sin, interleaved, k_scale,
+                         v_scale, k_out, v_out, stream, flags)
+
+    def kda_kv4_append_tree(self, pages, page_table, ctx_len, k, v, tree, status, cu_seqlens=None, max_t=None, cos=None,
+                            sin=None, interleaved=False, k_scale=1.0, v_scale=1.0, k_out=None, v_out=None, stream=None,
+                            flags=0) -> None:
+        """kda_kv4_append for a tree of drafted tokens: keys rotated by their
+        depth in it.  tree: int64 [total] masks (see KDA_TREE_MAX_TOKENS in
+        include/kda.h)."""
+        if tree is None:
+            raise ValueError("tree is required")
+        self._kv4_append(pages, page_table, ctx_len, k, v, tree, status, cu_seqlens, max_t, cos, sin, interleaved, k_scale,
+                         v_scale, k_out, v_out, stream, flags)
+
+    def _kv4_append(self, pages, page_table, ctx_len, k, v, tree, status, cu_seqlens, max_t, cos, sin, interleaved, k_scale,
+                    v_scale, k_out, v_out, stream, flags) -> None:
         at = _device("pages", pages)
         int32 = _torch_module.int32
         cache = _kv4_cache(pages, k_scale, v_scale)
@@ -830,9 +877,13 @@ class KdaLibrary:
                                      0 if out is None else _dtype_code(out), 0, ks, vs, _at(cu_seqlens),
                                      page_table.data_ptr(), ctx_len.data_ptr(), k.data_ptr(), v.data_ptr(), cos_at, sin_at,
                                      _at(k_out), _at(v_out))
-        rc = self.lib.packed_kda_kv4_append(_PACK_KV4_CACHE.pack(*cache), args, status.data_ptr(), flags,
-                                            self._stream_of(at, stream))
-        self._check(rc, "kda_kv4_append")
+        cache = _PACK_KV4_CACHE.pack(*cache)
+        if tree is None:
+            rc = self.lib.packed_kda_kv4_append(cache, args, status.data_ptr(), flags, self._stream_of(at, stream))
+        else:
+            rc = self.lib.packed_kda_kv4_append_tree(cache, args, _masks(tree, total, at), status.data_ptr(), flags,
+                                                     self._stream_of(at, stream))
+        self._check(rc, "kda_kv4_append" if tree is None else "kda_kv4_append_tree")
 
     def kda_kv4_attend_raw(self, cache: Kv4CacheDesc, args: Kv4AttendArgs, status, stream, flags=0) -> int:
         return self.lib.kda_kv4_attend(ctypes.byref(cache), ctypes.byref(args), status, flags, stream)
@@ -845,6 +896,23 @@ class KdaLibrary:
         lie apart), o alike and dense, ctx_len [N] the tokens in the cache
         before the step's own; workspace: KDA_KV4_WORKSPACE_BYTES bytes,
         zeroed once."""
+        self._kv4_attend(pages, page_table, ctx_len, q, None, o, workspace, status, cu_seqlens, max_t, cos, sin, interleaved,
+                         window, scale, k_scale, v_scale, stream, flags)
+
+    def kda_kv4_attend_tree(self, pages, page_table, ctx_len, q, tree, o, workspace, status, cu_seqlens=None, max_t=None,
+                            cos=None, sin=None, interleaved=False, window=0, scale=None, k_scale=1.0, v_scale=1.0,
+                            stream=None, flags=0) -> None:
+        """kda_kv4_attend for a tree of drafted tokens, whose keys and values
+        kda_kv4_append_tree stored: each sees the ctx_len keys before the tree,
+        its ancestors and itself.  tree: int64 [total] masks (see
+        KDA_TREE_MAX_TOKENS in include/kda.h)."""
+        if tree is None:
+            raise ValueError("tree is required")
+        self._kv4_attend(pages, page_table, ctx_len, q, tree, o, workspace, status, cu_seqlens, max_t, cos, sin, interleaved,
+                         window, scale, k_scale, v_scale, stream, flags)
+
+    def _kv4_attend(self, pages, page_table, ctx_len, q, tree, o, workspace, status, cu_seqlens, max_t, cos, sin, interleaved,
+                    window, scale, k_scale, v_scale, stream, flags) -> None:
         at = _device("pages", pages)
         int32 = _torch_module.int32
         cache = _kv4_cache(pages, k_scale, v_scale)
@@ -869,9 +937,13 @@ class KdaLibrary:
                                      scale, 0, qs, _at(cu_seqlens), page_table.data_ptr(), ctx_len.data_ptr(), q.data_ptr(),
                                      cos_at, sin_at, o.data_ptr(), workspace.data_ptr(),
                                      workspace.numel() * workspace.element_size())
-        rc = self.lib.packed_kda_kv4_attend(_PACK_KV4_CACHE.pack(*cache), args, status.data_ptr(), flags,
-                                            self._stream_of(at, stream))
-        self._check(rc, "kda_kv4_attend")
+        cache = _PACK_KV4_CACHE.pack(*cache)
+        if tree is None:
+            rc = self.lib.packed_kda_kv4_attend(cache, args, status.data_ptr(), flags, self._stream_of(at, stream))
+        else:
+            rc = self.lib.packed_kda_kv4_attend_tree(cache, args, _masks(tree, total, at), status.data_ptr(), flags,
+                                                     self._stream_of(at, stream))
+        self._check(rc, "kda_kv4_attend" if tree is None else "kda_kv4_attend_tree")
 
     def kda_head_norm(self, o, weight, y, gate=None, activation=1, eps=1e-6, stream=None, flags=0) -> None:
         """y = weight * o / rms(o) * act(gate) over the heads of o [total,
@@ -921,3 +993,108 @@ class KdaLibrary:
                                      branch_scale, ys, gs, residual.data_ptr(), _at(y), _at(gate), _at(w_post), _at(scale),
                                      _at(w_pre), _at(residual_out), _at(x))
         self._check(self.lib.packed_kda_block_norm(args, flags, self._stream_of(at, stream)), "kda_block_norm")
+
+    # -- a speculative step over a tree of drafted tokens ----------------------
+    def kda_step_tree_raw(self, desc: PoolDesc, args: StepArgs, tree, status, stream, flags=0) -> int:
+        return self.lib.kda_step_tree(ctypes.byref(desc), ctypes.byref(args), tree, status, flags, stream)
+
+    def kda_step_tree(self, pool, slot_table, q, k, v, a, b, tree, o, status, cu_seqlens=None, max_t=None, accepted=None,
+                      reset=None, a_log=None, dt_bias=None, stream=None, flags=0) -> None:
+        """kda_step over a tree of drafted tokens (see kda_step_tree in
+        include/kda.h): tokens packed and stored as for kda_step, tree int64
+        [total] masks."""
+        at = _device("pool", pool)
+        int32, f32 = _torch_module.int32, _torch_module.float32
+        if pool.dim() != 4:
+            raise ValueError("a state pool is a [num_slots, hv, k, v] tensor")
+        (num, hv, kd, vd), strides = pool.shape, pool.stride()
+        if strides[1:] != (kd * vd, vd, 1):
+            raise ValueError("the [hv, k, v] part of a state pool must be dense (v innermost)")
+        n, cols = slot_table.shape
+        total, h_qk = q.shape[0], q.shape[1]
+        dtype = q.dtype
+        max_t = _tokens(cu_seqlens, max_t, n, total, at)
+        _is("slot_table", slot_table, (n, cols), int32, at)
+        _is("q", q, (total, h_qk, kd), dtype, at)
+        _is("k", k, (total, h_qk, kd), dtype, at)
+        _is("v", v, (total, hv, vd), dtype, at)
+        _is("a", a, (total, hv, kd), f32, at)
+        _is("b", b, (total, hv), f32, at)
+        _is("o", o, (total, hv, vd), f32, at)
+        _is("status", status, (1,), int32, at)
+        for name, t, shape, dt in (("accepted", accepted, (n,), int32), ("reset", reset, (n,), _torch_module.uint8),
+                                   ("a_log", a_log, (hv,), f32), ("dt_bias", dt_bias, (hv, kd), f32)):
+            if t is not None:
+                _is(name, t, shape, dt, at)
+        args = _PACK_STEP.pack(n, total, max_t, h_qk, cols, 0, _dtype_code(dtype), 0, _at(cu_seqlens), slot_table.data_ptr(),
+                               _at(accepted), _at(reset), q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
+                               _at(a_log), _at(dt_bias), o.data_ptr())
+        desc = _PACK_POOL.pack(pool.data_ptr(), _dtype_code(pool.dtype), hv, kd, vd, num, strides[0])
+        rc = self.lib.packed_kda_step_tree(desc, args, _masks(tree, total, at), status.data_ptr(), flags,
+                                           self._stream_of(at, stream))
+        self._check(rc, "kda_step_tree")
+
+    def kda_conv_step_tree_raw(self, win: ConvWindowDesc, args: ConvArgs, tree, status, stream, flags=0) -> int:
+        return self.lib.kda_conv_step_tree(ctypes.byref(win), ctypes.byref(args), tree, status, flags, stream)
+
+    def kda_conv_step_tree(self, window, conv_slot, x, weight, tree, y, status, bias=None, cu_seqlens=None, max_t=None,
+                           accepted=None, reset=None, silu=True, stream=None, flags=0) -> None:
+        """kda_conv_step over a tree of drafted tokens (see kda_conv_step_tree
+        in include/kda.h): the window is read, not written; tree int64 [total]
+        masks."""
+        at = _device("window", window)
+        int32, f32 = _torch_module.int32, _torch_module.float32
+        if window.dim() != 3 or window.stride(2) != 1 or window.stride(1) != window.shape[2]:
+            raise ValueError("a conv window pool is a [num_slots, L, C] tensor, dense in [L, C]")
+        num, length, channels = window.shape
+        n, total, width = conv_slot.shape[0], x.shape[0], weight.shape[1]
+        dtype = window.dtype
+        max_t = _tokens(cu_seqlens, max_t, n, total, at)
+        _is("conv_slot", conv_slot, (n,), int32, at)
+        _is("x", x, (total, channels), dtype, at)
+        _is("y", y, (total, channels), dtype, at)
+        _is("weight", weight, (channels, width), f32, at)
+        _is("status", status, (1,), int32, at)
+        for name, t, shape, dt in (("bias", bias, (channels,), f32), ("accepted", accepted, (n,), int32),
+                                   ("reset", reset, (n,), _torch_module.uint8)):
+            if t is not None:
+                _is(name, t, shape, dt, at)
+        win = _PACK_CONV_WINDOW.pack(window.data_ptr(), _dtype_code(dtype), channels, length, 0, num, window.stride(0))
+        args = _PACK_CONV.pack(n, total, max_t, width, bool(silu), 0, _at(cu_seqlens), conv_slot.data_ptr(), _at(accepted),
+                               _at(reset), x.data_ptr(), weight.data_ptr(), _at(bias), y.data_ptr())
+        rc = self.lib.packed_kda_conv_step_tree(win, args, _masks(tree, total, at), status.data_ptr(), flags,
+                                                self._stream_of(at, stream))
+        self._check(rc, "kda_conv_step_tree")
+
+    def kda_accept_raw(self, args: AcceptArgs, status, stream, flags=0) -> int:
+        return self.lib.kda_accept(ctypes.byref(args), status, flags, stream)
+
+    def kda_accept(self, p, tokens, u, u_last, accepted, node, path, token, status, q=None, tree=None, cu_seqlens=None,
+                   max_t=None, stream=None, flags=0) -> None:
+        """Drafts verified against the target's probabilities p [total, vocab]
+        with the given random numbers, and the next token drawn (see
+        kda_accept_args in include/kda.h): tokens int32 [total], u fp32
+        [total], u_last fp32 [N]; q [total, vocab] the drafts' distributions
+        (None: drafts that were given), rows of p and q may lie apart; tree
+        int64 [total] masks (None: chains).  Out: accepted, node, token int32
+        [N], path int32 [N, max_t]."""
+        at = _device("p", p)
+        int32, f32 = _torch_module.int32, _torch_module.float32
+        total, vocab = p.shape
+        n, dtype, shape = accepted.shape[0], p.dtype, p.shape
+        max_t = _tokens(cu_seqlens, max_t, n, total, at)
+        ps = _rows("p", p, shape, vocab, dtype, at)
+        qs = 0 if q is None else _rows("q", q, shape, vocab, dtype, at)
+        _is("tokens", tokens, (total,), int32, at)
+        _is("u", u, (total,), f32, at)
+        _is("u_last", u_last, (n,), f32, at)
+        _is("accepted", accepted, (n,), int32, at)
+        _is("node", node, (n,), int32, at)
+        _is("path", path, (n, max_t), int32, at)
+        _is("token", token, (n,), int32, at)
+        _is("status", status, (1,), int32, at)
+        args = _PACK_ACCEPT.pack(n, total, max_t, vocab, _dtype_code(dtype), 0, ps, qs, _at(cu_seqlens),
+                                 0 if tree is None else _masks(tree, total, at), p.data_ptr(), _at(q), tokens.data_ptr(),
+                                 u.data_ptr(), u_last.data_ptr(), accepted.data_ptr(), node.data_ptr(), path.data_ptr(),
+                                 token.data_ptr())
+        self._check(self.lib.packed_kda_accept(args, status.data_ptr(), flags, self._stream_of(at, stream)), "kda_accept")

@@ -27,10 +27,6 @@
 #include "kda_prefill_chunk.cuh"
 #include "kda_stage.cuh"
 
-#ifndef KDA_STATE16
-#error "build with -DKDA_STATE16=0 (fp32 pool) or -DKDA_STATE16=1 (fp16 pool)"
-#endif
-
 // Tile shapes.  A tile is BV state columns x all K rows; BV * element size is
 // 128 bytes, one TMA box row and one swizzle span, so a 2-byte state takes
 // twice the columns of a 4-byte one and a tile moves the same bytes (the
@@ -42,7 +38,6 @@
 // rows for fp16), for registers and for parallelism.
 #if KDA_STATE16
 using state_t = __half;
-static constexpr int kBuildDtype = KDA_F16;
 #ifndef KDA_DEC_BV
 #define KDA_DEC_BV 64
 #endif
@@ -51,7 +46,6 @@ static constexpr int kBuildDtype = KDA_F16;
 #endif
 #else
 using state_t = float;
-static constexpr int kBuildDtype = KDA_F32;
 #ifndef KDA_DEC_BV
 #define KDA_DEC_BV 32
 #endif
@@ -106,29 +100,6 @@ static constexpr int kBuildDtype = KDA_F32;
 #endif
 
 namespace {
-
-// Shape, alignment and dtype of one pool, without the build-dtype rule.
-int check_pool_self(const kda_pool* p) {
-    if (p == nullptr) return KDA_ERR_NULL;
-    if (p->dtype != KDA_F32 && p->dtype != KDA_F16) return KDA_ERR_DTYPE_UNSUPPORTED;
-    if (p->base == nullptr) return KDA_ERR_NULL;
-    if (p->hv < 1 || p->num_slots < 1) return KDA_ERR_SHAPE;
-    if (p->k < 16 || p->k > kda::KMAX || p->k % 16 != 0) return KDA_ERR_SHAPE;
-    if (p->v < 16 || p->v > kda::KMAX || p->v % 16 != 0) return KDA_ERR_SHAPE;
-    const int64_t per_slot = (int64_t)p->hv * p->k * p->v;
-    if (p->slot_stride < per_slot) return KDA_ERR_SHAPE;
-    if (p->num_slots > 0x7fffffffLL) return KDA_ERR_SHAPE;  // slot ids are int32
-    const int es = elem_size(p->dtype);
-    if (!aligned(p->base, 16) || (p->slot_stride * es) % 16 != 0) return KDA_ERR_ALIGN;
-    return KDA_OK;
-}
-
-int check_pool_for_build(const kda_pool* p) {
-    const int rc = check_pool_self(p);
-    if (rc != KDA_OK) return rc;
-    if (p->dtype != kBuildDtype) return KDA_ERR_DTYPE_MISMATCH;
-    return KDA_OK;
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -352,49 +323,6 @@ int check_step_args(const kda_pool* pool, const int32_t* init_slot, int32_t n, i
         !aligned(a, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
         return KDA_ERR_ALIGN;
     return KDA_OK;
-}
-
-kda::StepParams make_params(const kda_pool* pool, const int32_t* init_slot,
-                            const int32_t* snap_slot, const uint8_t* reset, int32_t n,
-                            int32_t t, const void* q, const void* k, const void* v,
-                            const float* a, const float* b, float* o, int32_t* dev_status,
-                            uint32_t flags) {
-    kda::StepParams prm;
-    prm.pool = pool->base;
-    prm.num_slots = pool->num_slots;
-    prm.slot_stride = pool->slot_stride;
-    prm.hv = pool->hv;
-    prm.k = pool->k;
-    prm.v = pool->v;
-    prm.n = n;
-    prm.t = t;
-    prm.init_slot = init_slot;
-    prm.snap_slot = snap_slot;
-    prm.reset = reset;
-    prm.q = q;
-    prm.kk = k;
-    prm.vv = v;
-    prm.a = a;
-    prm.b = b;
-    prm.o = o;
-    prm.status = dev_status;
-    prm.inv_sqrt_k = 1.0f / sqrtf((float)pool->k);
-    prm.flags = flags;
-    // plain decode / verify: one q/k head per value head, one slot per request
-    // row (init), t snapshot columns, no accepted column, no offsets, plain gate
-    prm.hqk = pool->hv;
-    prm.init_stride = 1;
-    prm.snap_stride = t;
-    prm.num_cols = 1;
-    prm.accepted = nullptr;
-    prm.cu = nullptr;
-    prm.a_log = nullptr;
-    prm.dt_bias = nullptr;
-    prm.mode = 0;
-    prm.total = n * t;
-    prm.final_slot = nullptr;
-    prm.conv = kda::StepParams::Conv{};
-    return prm;
 }
 
 }  // namespace

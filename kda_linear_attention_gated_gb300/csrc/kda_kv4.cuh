@@ -20,6 +20,7 @@
 #include <cfloat>
 
 #include "kda_common.cuh"
+#include "kda_tree.cuh"
 
 namespace kda {
 
@@ -179,6 +180,7 @@ struct Kv4AppendParams {
     int out_dtype;
     float inv_k, inv_v, k_scale, v_scale;
     int32_t* status;
+    const uint64_t* tree;                // [total] masks (TREE)
 };
 
 constexpr int KV4_APPEND_THREADS = 128, KV4_APPEND_WARPS = KV4_APPEND_THREADS / 32;
@@ -311,8 +313,9 @@ __device__ __forceinline__ void kv4_turn(float& a, float& b, float c, float s) {
 // tokens of 8 heads of 128, bf16: 20.4 us, 3.8 TB/s.  Bound by latency: 16 warps
 // an SM (registers) wait for the look-up and for every head after a warp's
 // first, whose loads are not ahead; half of the issue slots go to the about 20
-// instructions an element.
-template <int D, int ES>
+// instructions an element.  TREE: a token's key is rotated as at its depth in
+// the request's tree of drafted tokens, and stored at its place in the request.
+template <int D, int ES, bool TREE = false>
 __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_append_kernel(const Kv4AppendParams p) {
     constexpr int NG = Kv4<D>::NG, NP = NG / 2, HW = 4 / NP;     // groups and pairs of a head, heads of a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_a
         }
         while (r < p.n && tok < p.total && __ldg(p.cu + r + 1) <= tok) ++r;
     }
-    int pos = -1;
+    int pos = -1, turn = 0;   // the token's position, and the one that its key is rotated by
     uint8_t* blk = nullptr;   // the token's block of head 0
     int where = 0;
     if (tok >= p.total) {
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_a
         const int tok0 = p.cu ? __ldg(p.cu + r) : r * p.max_t;
         const int t = (p.cu ? __ldg(p.cu + r + 1) : tok0 + p.max_t) - tok0;
         const int64_t at = (int64_t)__ldg(p.ctx + r) + (tok - tok0);
-        if (tok0 < 0 || tok < tok0 || t > p.max_t ||
+        if (tok0 < 0 || tok < tok0 || t > p.max_t || (TREE && at - (tok - tok0) < 0 && at - (tok - tok0) + t > 0) ||
             (at >= 0 && (at >= (int64_t)p.cols * p.page_tokens || (p.rot && at >= p.rope_rows)))) {
             atomicCAS(p.status, 0, STATUS_ARG);
         } else if (at >= 0) {
@@ -365,7 +368,8 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_a
             if (id < 0 || id >= p.num_pages) {
                 atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
             } else {
-                pos = (int)at;
+                pos = turn = (int)at;
+                if constexpr (TREE) turn = pos - (tok - tok0) + __popcll(tree_mask(p.tree, tok, tok - tok0)) - 1;
                 where = in & 15;
                 blk = p.pages + (int64_t)id * p.page_stride + (int64_t)(in >> 4) * Kv4<D>::BLOCK;
             }
@@ -395,8 +399,8 @@ __global__ void __launch_bounds__(KV4_APPEND_THREADS, ES == 2 ? 5 : 4) kda_kv4_a
             continue;
         }
         if (!is_v && 2 * i < rg) {
-            const float* cs = p.cos + (int64_t)pos * half;
-            const float* sn = p.sin + (int64_t)pos * half;
+            const float* cs = p.cos + (int64_t)turn * half;
+            const float* sn = p.sin + (int64_t)turn * half;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float c[4], s[4];
@@ -452,6 +456,7 @@ struct Kv4AttendParams {
     float* partials;                     // [2 gridDim.x][KV4_ROWS][D + 2]
     int32_t* status;
     int withhold;                        // the test hook: copies are expected and not issued
+    const uint64_t* tree;                // [total] masks (TREE)
 };
 
 // What the columns of a query tile hold, see kda_kv4_attend_kernel.
@@ -507,7 +512,7 @@ struct Kv4Req {
     int tok0, t, ctx, first, units, tiles, err;
 };
 
-__device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, int rows) {
+template <bool TREE> __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, int rows) {
     Kv4Req q;
     q.err = 0;
     q.tok0 = p.cu ? __ldg(p.cu + r) : r * p.max_t;
@@ -521,7 +526,7 @@ __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int r, i
     q.tiles = (q.t * p.grp + rows - 1) / rows;
     const int64_t end = (int64_t)q.ctx + q.t;
     if (q.t > 0 && end > 0) {
-        if (end > (int64_t)p.cols * p.page_tokens || (p.rot && end > p.rope_rows)) {
+        if (end > (int64_t)p.cols * p.page_tokens || (p.rot && end > p.rope_rows) || (TREE && q.ctx < 0)) {
             q.err = STATUS_ARG;
         } else {
             if (p.window > 0) q.first = max(0, max(q.ctx, 0) - p.window + 1) / KV4_KEYS;
@@ -546,12 +551,12 @@ struct Kv4Walk {
     Kv4Req q;
     int h, i0, b0, b1;   // the current step: head, first row of the tile, units [b0, b1)
     int b;               // (fetching) this warp's next unit not looked up
-    __device__ __forceinline__ bool next(const Kv4AttendParams& p, int rows) {
+    template <bool TREE> __device__ __forceinline__ bool next(const Kv4AttendParams& p, int rows) {
         do {
             if (left <= 0) return false;
             while (off >= kv4_cost(q, p.heads)) {
                 if (++r >= p.n) return false;
-                q = kv4_request(p, r, rows);
+                q = kv4_request<TREE>(p, r, rows);
                 off = 0;
             }
             const int each = q.units + KV4_PART;
@@ -604,7 +609,11 @@ struct Kv4Walk {
 // about 430.  64 requests x 8192 tokens, 32/8 heads of 128: 117 us, 5.2 TB/s of
 // cache, 0.76 of the measured copy bandwidth.  Keys and values as the B operand
 // (query rows on the 16-row side, half of it idle): 168 us.
-template <int D, int MODE>
+//
+// TREE: the request's tokens are a tree of drafted tokens behind its ctx keys.
+// Token j is rotated as at position ctx + its depth, and of the keys from ctx on
+// sees those in its mask: only the units there are masked key by key.
+template <int D, int MODE, bool TREE = false>
 __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_kernel(const Kv4AttendParams p) {
     using F = Kv4<D>;
     using SM = Kv4Smem<D, MODE>;
@@ -645,7 +654,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     Kv4Req own;      // of a lane with one request
 #pragma unroll 2
     for (int r = lane * cnt; r < min(p.n, (lane + 1) * cnt); ++r) {
-        own = kv4_request(p, r, ROWS);
+        own = kv4_request<TREE>(p, r, ROWS);
         mine += kv4_cost(own, p.heads);
         empty |= own.t > 0 && own.units == 0;
         if (own.err && blockIdx.x == 0 && warp == 0) atomicCAS(p.status, 0, own.err);
@@ -671,7 +680,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
             Kv4Req q = own;
             int r = lane * cnt;
             for (;; ++r) {
-                if (cnt > 1) q = kv4_request(p, r, ROWS);
+                if (cnt > 1) q = kv4_request<TREE>(p, r, ROWS);
                 const int c = kv4_cost(q, p.heads);
                 if (at < c) break;
                 at -= c;
@@ -690,7 +699,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     }
     if (__any_sync(0xffffffffu, empty)) {  // requests without a visible key: zero rows
         for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
-            const Kv4Req q = kv4_request(p, r, ROWS);
+            const Kv4Req q = kv4_request<TREE>(p, r, ROWS);
             if (q.units > 0) continue;
             const int64_t base = (int64_t)q.tok0 * p.h_q * D;
             for (int64_t i = tid * 4; i < (int64_t)q.t * p.h_q * D; i += KV4_THREADS * 4)
@@ -707,7 +716,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     auto step = [&](Kv4Walk& w) {   // lane 0 walks, all lanes see it
         int ok = 0;
         __syncwarp();
-        if (lane == 0) ok = w.next(p, ROWS);
+        if (lane == 0) ok = w.template next<TREE>(p, ROWS);
         __syncwarp();               // the walk is in shared memory, and a shuffle orders no memory
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
@@ -720,7 +729,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         const bool first = d < half;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int i = i0 + warp + k * KV4_WARPS, j = i / p.grp, pos = get.q.ctx + j;
+            const int i = i0 + warp + k * KV4_WARPS, j = i / p.grp;
+            int pos = get.q.ctx + j;
+            if constexpr (TREE)
+                if (j < get.q.t) pos = get.q.ctx + __popcll(tree_mask(p.tree, get.q.tok0 + j, j)) - 1;
             const int64_t base = (int64_t)(get.q.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + i - j * p.grp) * D;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -861,7 +873,25 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     // a row's position and the tile's last one: worked out where they are needed, not kept in
     // registers
     auto row_pos = [&](int i) { return cur.q.ctx + (cur.i0 + i) / p.grp; };
-    auto last_row_pos = [&]() { return cur.q.ctx + min(cur.q.t - 1, (cur.i0 + ROWS - 1) / p.grp); };
+    // (a tree's row may see any token of the request: the last one)
+    auto last_row_pos = [&]() { return cur.q.ctx + (TREE ? cur.q.t - 1 : min(cur.q.t - 1, (cur.i0 + ROWS - 1) / p.grp)); };
+    // whether a row sees a key: a chain's by their positions
+    auto sees_chain = [&](int pos, int key) { return key <= pos && (p.window <= 0 || key > pos - p.window); };
+    // a tree's by row i's mask, of which a window leaves the last ones, and the first key of the context that it sees
+    auto tree_row = [&](int i, uint64_t& own, int& low) {
+        const int j = (cur.i0 + i) / p.grp;
+        own = 0;
+        low = 0x7fffffff;
+        if (j >= cur.q.t) return;
+        own = tree_mask(p.tree, cur.q.tok0 + j, j);
+        low = p.window > 0 ? cur.q.ctx + __popcll(own) - p.window : 0;
+        if (p.window > 0)
+            for (int more = __popcll(own) - p.window; more > 0; --more) own &= own - 1;
+    };
+    auto sees_tree = [&](uint64_t own, int low, int key) {
+        const int at = key - cur.q.ctx;
+        return at < 0 ? key >= low : at < TREE_MAX && (own >> at & 1u) != 0;
+    };
 
     while (have) {
         store_q();
@@ -894,7 +924,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         }
         auto row_of = [&](int a) { return 8 * (a >> 1) + 2 * t + (a & 1); };
         // units that every row of the tile sees whole: [see0, see1)
-        const int see1 = (row_pos(0) + 1) / KV4_KEYS;
+        const int see1 = (TREE ? cur.q.ctx : row_pos(0) + 1) / KV4_KEYS;
         const int see0 = p.window > 0 ? (max(0, last_row_pos() - p.window + 1) + KV4_KEYS - 1) / KV4_KEYS : 0;
         // sums of channels g D / 8 + 2 i (elements 0, 1: the lane's rows) and the next (2, 3)
         float acc[NB][MT][4];
@@ -962,10 +992,13 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 #pragma unroll
                     for (int a = 0; a < 2 * NB; ++a) {
                         const int pos = row_pos(row_of(a));
+                        uint64_t own = 0;
+                        int low = 0;
+                        if constexpr (TREE) tree_row(row_of(a), own, low);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int key = unit * KV4_KEYS + i * 8 + g;
-                            if (key > pos || (p.window > 0 && key <= pos - p.window) || (miss >> (i >> 1) & 1u))
+                            if (!(TREE ? sees_tree(own, low, key) : sees_chain(pos, key)) || (miss >> (i >> 1) & 1u))
                                 s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
                         }
                     }
@@ -1050,7 +1083,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 #pragma unroll
                                 for (int a = 0; a < 2 * NB; ++a) {
                                     const int pos = row_pos(row_of(a));
-                                    if (key0 + w <= pos && (p.window <= 0 || key0 + w > pos - p.window)) hit |= 1u << a;
+                                    uint64_t own = 0;
+                                    int low = 0;
+                                    if constexpr (TREE) tree_row(row_of(a), own, low);
+                                    if (TREE ? sees_tree(own, low, key0 + w) : sees_chain(pos, key0 + w)) hit |= 1u << a;
                                 }
                             }
 #pragma unroll

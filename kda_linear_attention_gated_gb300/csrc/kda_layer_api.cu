@@ -54,9 +54,9 @@ int check_common_pointers(const kda_kv4_cache* c, const Common& g, const int32_t
     return KDA_OK;
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool TREE>
 int launch_attend(kda::Kv4AttendParams& prm, int64_t list, uint32_t flags, cudaStream_t stream) {
-    auto kernel = kda::kda_kv4_attend_kernel<D, MODE>;
+    auto kernel = kda::kda_kv4_attend_kernel<D, MODE, TREE>;
     int occ = 0, sms = 0;
     const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::Kv4Shape<D, MODE>::THREADS, kda::Kv4Smem<D, MODE>::BYTES, &occ, &sms);
     if (rc != KDA_OK) return rc;
@@ -71,6 +71,156 @@ int launch_attend(kda::Kv4AttendParams& prm, int64_t list, uint32_t flags, cudaS
     cudaLaunchAttribute attr;
     set_pdl(cfg, &attr, flags);
     return cudaLaunchKernelEx(&cfg, kernel, prm) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+template <bool TREE>
+int append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, const uint64_t* tree, int32_t* dev_status, uint32_t flags,
+           void* stream) {
+    if (args == nullptr) return KDA_ERR_NULL;
+    int rc = check_cache(cache);
+    if (rc != KDA_OK) return rc;
+    const kda_kv4_append_args& g = *args;
+    const int es = elem_size(g.dtype);
+    if (es == 0 || ((g.k_out || g.v_out) && elem_size(g.out_dtype) == 0)) return KDA_ERR_DTYPE_UNSUPPORTED;
+    const Common c = {g.n, g.total, g.max_t, g.table_cols, g.rot_dim, g.interleaved, g.rope_rows,
+                      g.cu_seqlens, g.page_table, g.ctx_len, g.cos, g.sin};
+    if (flags & ~(uint32_t)KDA_LAUNCH_PDL) return KDA_ERR_ARG;
+    rc = check_common(cache, c);
+    if (rc != KDA_OK) return rc;
+    if (g.reserved != 0) return KDA_ERR_ARG;
+    const int64_t row = (int64_t)cache->heads * cache->dim;
+    if (g.k_stride < row || g.v_stride < row || (TREE && g.max_t > kda::TREE_MAX)) return KDA_ERR_SHAPE;
+    if (g.n == 0 || g.total == 0 || g.max_t == 0) return KDA_OK;
+    rc = check_common_pointers(cache, c, dev_status);
+    if (rc != KDA_OK) return rc;
+    if (!g.k || !g.v || (TREE && !tree)) return KDA_ERR_NULL;
+    if (!aligned(tree, 8) || !aligned(g.k, 16) || !aligned(g.v, 16) || g.k_stride * es % 16 != 0 || g.v_stride * es % 16 != 0 ||
+        !aligned(g.k_out, 16) || !aligned(g.v_out, 16))
+        return KDA_ERR_ALIGN;
+    kda::Kv4AppendParams prm;
+    prm.pages = static_cast<uint8_t*>(cache->base);
+    prm.num_pages = cache->num_pages;
+    prm.page_stride = cache->page_stride;
+    prm.page_tokens = cache->page_tokens;
+    prm.heads = cache->heads;
+    prm.n = g.n;
+    prm.total = g.total;
+    prm.max_t = g.max_t;
+    prm.dtype = g.dtype;
+    prm.cols = g.table_cols;
+    prm.rot = g.rot_dim;
+    prm.inter = g.interleaved;
+    prm.rope_rows = g.rope_rows;
+    prm.k_stride = g.k_stride;
+    prm.v_stride = g.v_stride;
+    prm.cu = g.cu_seqlens;
+    prm.table = g.page_table;
+    prm.ctx = g.ctx_len;
+    prm.k = g.k;
+    prm.v = g.v;
+    prm.cos = g.cos;
+    prm.sin = g.sin;
+    prm.k_out = g.k_out;
+    prm.v_out = g.v_out;
+    prm.out_dtype = g.out_dtype;
+    prm.k_scale = cache->k_scale;
+    prm.v_scale = cache->v_scale;
+    prm.inv_k = 1.0f / cache->k_scale;
+    prm.inv_v = 1.0f / cache->v_scale;
+    prm.status = dev_status;
+    prm.tree = tree;
+    // eight tokens a CTA; few tokens share their heads out over more CTAs
+    const int tokens = (int)(((int64_t)g.total + 7) / 8), items = cache->dim == 128 ? cache->heads * 2 : (cache->heads + 1) / 2 * 2;
+    const int parts = std::max(1, std::min((items + kda::KV4_APPEND_WARPS - 1) / kda::KV4_APPEND_WARPS, kda::KV4_APPEND_CTAS / tokens));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tokens, (unsigned)parts, 1);
+    cfg.blockDim = dim3(kda::KV4_APPEND_THREADS, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    set_pdl(cfg, &attr, flags);
+    using namespace kda;
+    const cudaError_t err =
+        cache->dim == 128 ? (es == 2 ? cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<128, 2, TREE>, prm)
+                                     : cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<128, 4, TREE>, prm))
+                          : (es == 2 ? cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<64, 2, TREE>, prm)
+                                     : cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<64, 4, TREE>, prm));
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+template <bool TREE>
+int attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, const uint64_t* tree, int32_t* dev_status, uint32_t flags,
+           void* stream) {
+    if (args == nullptr) return KDA_ERR_NULL;
+    int rc = check_cache(cache);
+    if (rc != KDA_OK) return rc;
+    const kda_kv4_attend_args& g = *args;
+    const int es = elem_size(g.dtype);
+    if (es == 0) return KDA_ERR_DTYPE_UNSUPPORTED;
+    const Common c = {g.n, g.total, g.max_t, g.table_cols, g.rot_dim, g.interleaved, g.rope_rows,
+                      g.cu_seqlens, g.page_table, g.ctx_len, g.cos, g.sin};
+    if (flags & ~(uint32_t)(KDA_LAUNCH_PDL | KDA_LAUNCH_TEST_WITHHOLD_STATE)) return KDA_ERR_ARG;
+    rc = check_common(cache, c);
+    if (rc != KDA_OK) return rc;
+    if (g.reserved != 0 || g.window < 0 || !std::isfinite(g.scale)) return KDA_ERR_ARG;
+    if (g.h_q < 1 || g.h_q % cache->heads != 0 || g.max_t > (TREE ? kda::TREE_MAX : KDA_KV4_MAX_TOKENS) || g.q_stride < (int64_t)g.h_q * cache->dim)
+        return KDA_ERR_SHAPE;
+    const int grp = g.h_q / cache->heads;
+    // rows of a tile and their rounding (kda_kv4.cuh)
+    const int mode = g.dtype != KDA_BF16 ? kda::KV4_REST : (int64_t)g.max_t * grp <= 8 ? kda::KV4_8 : kda::KV4_16;
+    const int rows = mode == kda::KV4_16 ? 16 : 8;
+    const int64_t units = ((int64_t)g.table_cols * cache->page_tokens + kda::KV4_KEYS - 1) / kda::KV4_KEYS;
+    const int64_t tiles = ((int64_t)g.max_t * grp + rows - 1) / rows;
+    if ((units + kda::KV4_PART) * tiles * cache->heads > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if (g.n == 0 || g.total == 0 || g.max_t == 0) return KDA_OK;
+    rc = check_common_pointers(cache, c, dev_status);
+    if (rc != KDA_OK) return rc;
+    if (!g.q || !g.o || !g.workspace || (TREE && !tree)) return KDA_ERR_NULL;
+    if (!aligned(tree, 8) || !aligned(g.q, 16) || g.q_stride * es % 16 != 0 || !aligned(g.o, 16) || !aligned(g.workspace, 16)) return KDA_ERR_ALIGN;
+    if (g.workspace_bytes < KDA_KV4_WORKSPACE_BYTES) return KDA_ERR_SHAPE;
+    kda::Kv4AttendParams prm;
+    prm.pages = static_cast<const uint8_t*>(cache->base);
+    prm.num_pages = cache->num_pages;
+    prm.page_stride = cache->page_stride;
+    prm.page_tokens = cache->page_tokens;
+    prm.heads = cache->heads;
+    prm.n = g.n;
+    prm.total = g.total;
+    prm.max_t = g.max_t;
+    prm.dtype = g.dtype;
+    prm.cols = g.table_cols;
+    prm.rot = g.rot_dim;
+    prm.inter = g.interleaved;
+    prm.rope_rows = g.rope_rows;
+    prm.h_q = g.h_q;
+    prm.grp = grp;
+    prm.window = g.window;
+    prm.q_stride = g.q_stride;
+    prm.cu = g.cu_seqlens;
+    prm.table = g.page_table;
+    prm.ctx = g.ctx_len;
+    prm.q = g.q;
+    prm.cos = g.cos;
+    prm.sin = g.sin;
+    prm.o = g.o;
+    const float scale = g.scale == 0.f ? 1.0f / std::sqrt((float)cache->dim) : g.scale;
+    prm.scale_log2 = (float)((double)scale * cache->k_scale * 1.4426950408889634);
+    prm.v_scale = cache->v_scale;
+    prm.counters = static_cast<int32_t*>(g.workspace);
+    prm.partials = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + kda::KV4_MAX_CTAS * sizeof(int32_t));
+    prm.status = dev_status;
+    prm.tree = tree;
+    prm.withhold = (flags & KDA_LAUNCH_TEST_WITHHOLD_STATE) != 0;
+    static_assert(kda::KV4_MAX_CTAS * (4 + 2 * kda::KV4_ROWS * (128 + 2) * 4) <= KDA_KV4_WORKSPACE_BYTES, "workspace");
+    const int64_t list = units * std::min<int64_t>(tiles * cache->heads * g.n, 1 << 20);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    using namespace kda;
+    if (cache->dim == 128)
+        return mode == KV4_8 ? launch_attend<128, KV4_8, TREE>(prm, list, flags, st)
+               : mode == KV4_16 ? launch_attend<128, KV4_16, TREE>(prm, list, flags, st)
+                                : launch_attend<128, KV4_REST, TREE>(prm, list, flags, st);
+    return mode == KV4_8 ? launch_attend<64, KV4_8, TREE>(prm, list, flags, st)
+           : mode == KV4_16 ? launch_attend<64, KV4_16, TREE>(prm, list, flags, st)
+                            : launch_attend<64, KV4_REST, TREE>(prm, list, flags, st);
 }
 
 template <typename OT, typename T>
@@ -130,148 +280,22 @@ int kda_kv4_page_bytes(int32_t page_tokens, int32_t heads, int32_t dim, int64_t*
 
 int kda_kv4_append(const kda_kv4_cache* cache, const kda_kv4_append_args* args, int32_t* dev_status, uint32_t flags,
                    void* stream) {
-    if (args == nullptr) return KDA_ERR_NULL;
-    int rc = check_cache(cache);
-    if (rc != KDA_OK) return rc;
-    const kda_kv4_append_args& g = *args;
-    const int es = elem_size(g.dtype);
-    if (es == 0 || ((g.k_out || g.v_out) && elem_size(g.out_dtype) == 0)) return KDA_ERR_DTYPE_UNSUPPORTED;
-    const Common c = {g.n, g.total, g.max_t, g.table_cols, g.rot_dim, g.interleaved, g.rope_rows,
-                      g.cu_seqlens, g.page_table, g.ctx_len, g.cos, g.sin};
-    if (flags & ~(uint32_t)KDA_LAUNCH_PDL) return KDA_ERR_ARG;
-    rc = check_common(cache, c);
-    if (rc != KDA_OK) return rc;
-    if (g.reserved != 0) return KDA_ERR_ARG;
-    const int64_t row = (int64_t)cache->heads * cache->dim;
-    if (g.k_stride < row || g.v_stride < row) return KDA_ERR_SHAPE;
-    if (g.n == 0 || g.total == 0 || g.max_t == 0) return KDA_OK;
-    rc = check_common_pointers(cache, c, dev_status);
-    if (rc != KDA_OK) return rc;
-    if (!g.k || !g.v) return KDA_ERR_NULL;
-    if (!aligned(g.k, 16) || !aligned(g.v, 16) || g.k_stride * es % 16 != 0 || g.v_stride * es % 16 != 0 ||
-        !aligned(g.k_out, 16) || !aligned(g.v_out, 16))
-        return KDA_ERR_ALIGN;
-    kda::Kv4AppendParams prm;
-    prm.pages = static_cast<uint8_t*>(cache->base);
-    prm.num_pages = cache->num_pages;
-    prm.page_stride = cache->page_stride;
-    prm.page_tokens = cache->page_tokens;
-    prm.heads = cache->heads;
-    prm.n = g.n;
-    prm.total = g.total;
-    prm.max_t = g.max_t;
-    prm.dtype = g.dtype;
-    prm.cols = g.table_cols;
-    prm.rot = g.rot_dim;
-    prm.inter = g.interleaved;
-    prm.rope_rows = g.rope_rows;
-    prm.k_stride = g.k_stride;
-    prm.v_stride = g.v_stride;
-    prm.cu = g.cu_seqlens;
-    prm.table = g.page_table;
-    prm.ctx = g.ctx_len;
-    prm.k = g.k;
-    prm.v = g.v;
-    prm.cos = g.cos;
-    prm.sin = g.sin;
-    prm.k_out = g.k_out;
-    prm.v_out = g.v_out;
-    prm.out_dtype = g.out_dtype;
-    prm.k_scale = cache->k_scale;
-    prm.v_scale = cache->v_scale;
-    prm.inv_k = 1.0f / cache->k_scale;
-    prm.inv_v = 1.0f / cache->v_scale;
-    prm.status = dev_status;
-    // eight tokens a CTA; few tokens share their heads out over more CTAs
-    const int tokens = (int)(((int64_t)g.total + 7) / 8), items = cache->dim == 128 ? cache->heads * 2 : (cache->heads + 1) / 2 * 2;
-    const int parts = std::max(1, std::min((items + kda::KV4_APPEND_WARPS - 1) / kda::KV4_APPEND_WARPS, kda::KV4_APPEND_CTAS / tokens));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tokens, (unsigned)parts, 1);
-    cfg.blockDim = dim3(kda::KV4_APPEND_THREADS, 1, 1);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr;
-    set_pdl(cfg, &attr, flags);
-    using namespace kda;
-    const cudaError_t err =
-        cache->dim == 128 ? (es == 2 ? cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<128, 2>, prm)
-                                     : cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<128, 4>, prm))
-                          : (es == 2 ? cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<64, 2>, prm)
-                                     : cudaLaunchKernelEx(&cfg, kda_kv4_append_kernel<64, 4>, prm));
-    return err == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+    return append<false>(cache, args, nullptr, dev_status, flags, stream);
+}
+
+int kda_kv4_append_tree(const kda_kv4_cache* cache, const kda_kv4_append_args* args, const uint64_t* tree, int32_t* dev_status,
+                        uint32_t flags, void* stream) {
+    return append<true>(cache, args, tree, dev_status, flags, stream);
 }
 
 int kda_kv4_attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, int32_t* dev_status, uint32_t flags,
                    void* stream) {
-    if (args == nullptr) return KDA_ERR_NULL;
-    int rc = check_cache(cache);
-    if (rc != KDA_OK) return rc;
-    const kda_kv4_attend_args& g = *args;
-    const int es = elem_size(g.dtype);
-    if (es == 0) return KDA_ERR_DTYPE_UNSUPPORTED;
-    const Common c = {g.n, g.total, g.max_t, g.table_cols, g.rot_dim, g.interleaved, g.rope_rows,
-                      g.cu_seqlens, g.page_table, g.ctx_len, g.cos, g.sin};
-    if (flags & ~(uint32_t)(KDA_LAUNCH_PDL | KDA_LAUNCH_TEST_WITHHOLD_STATE)) return KDA_ERR_ARG;
-    rc = check_common(cache, c);
-    if (rc != KDA_OK) return rc;
-    if (g.reserved != 0 || g.window < 0 || !std::isfinite(g.scale)) return KDA_ERR_ARG;
-    if (g.h_q < 1 || g.h_q % cache->heads != 0 || g.max_t > KDA_KV4_MAX_TOKENS || g.q_stride < (int64_t)g.h_q * cache->dim)
-        return KDA_ERR_SHAPE;
-    const int grp = g.h_q / cache->heads;
-    // rows of a tile and their rounding (kda_kv4.cuh)
-    const int mode = g.dtype != KDA_BF16 ? kda::KV4_REST : (int64_t)g.max_t * grp <= 8 ? kda::KV4_8 : kda::KV4_16;
-    const int rows = mode == kda::KV4_16 ? 16 : 8;
-    const int64_t units = ((int64_t)g.table_cols * cache->page_tokens + kda::KV4_KEYS - 1) / kda::KV4_KEYS;
-    const int64_t tiles = ((int64_t)g.max_t * grp + rows - 1) / rows;
-    if ((units + kda::KV4_PART) * tiles * cache->heads > 0x7fffffffLL) return KDA_ERR_SHAPE;
-    if (g.n == 0 || g.total == 0 || g.max_t == 0) return KDA_OK;
-    rc = check_common_pointers(cache, c, dev_status);
-    if (rc != KDA_OK) return rc;
-    if (!g.q || !g.o || !g.workspace) return KDA_ERR_NULL;
-    if (!aligned(g.q, 16) || g.q_stride * es % 16 != 0 || !aligned(g.o, 16) || !aligned(g.workspace, 16)) return KDA_ERR_ALIGN;
-    if (g.workspace_bytes < KDA_KV4_WORKSPACE_BYTES) return KDA_ERR_SHAPE;
-    kda::Kv4AttendParams prm;
-    prm.pages = static_cast<const uint8_t*>(cache->base);
-    prm.num_pages = cache->num_pages;
-    prm.page_stride = cache->page_stride;
-    prm.page_tokens = cache->page_tokens;
-    prm.heads = cache->heads;
-    prm.n = g.n;
-    prm.total = g.total;
-    prm.max_t = g.max_t;
-    prm.dtype = g.dtype;
-    prm.cols = g.table_cols;
-    prm.rot = g.rot_dim;
-    prm.inter = g.interleaved;
-    prm.rope_rows = g.rope_rows;
-    prm.h_q = g.h_q;
-    prm.grp = grp;
-    prm.window = g.window;
-    prm.q_stride = g.q_stride;
-    prm.cu = g.cu_seqlens;
-    prm.table = g.page_table;
-    prm.ctx = g.ctx_len;
-    prm.q = g.q;
-    prm.cos = g.cos;
-    prm.sin = g.sin;
-    prm.o = g.o;
-    const float scale = g.scale == 0.f ? 1.0f / std::sqrt((float)cache->dim) : g.scale;
-    prm.scale_log2 = (float)((double)scale * cache->k_scale * 1.4426950408889634);
-    prm.v_scale = cache->v_scale;
-    prm.counters = static_cast<int32_t*>(g.workspace);
-    prm.partials = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + kda::KV4_MAX_CTAS * sizeof(int32_t));
-    prm.status = dev_status;
-    prm.withhold = (flags & KDA_LAUNCH_TEST_WITHHOLD_STATE) != 0;
-    static_assert(kda::KV4_MAX_CTAS * (4 + 2 * kda::KV4_ROWS * (128 + 2) * 4) <= KDA_KV4_WORKSPACE_BYTES, "workspace");
-    const int64_t list = units * std::min<int64_t>(tiles * cache->heads * g.n, 1 << 20);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    using namespace kda;
-    if (cache->dim == 128)
-        return mode == KV4_8 ? launch_attend<128, KV4_8>(prm, list, flags, st)
-               : mode == KV4_16 ? launch_attend<128, KV4_16>(prm, list, flags, st)
-                                : launch_attend<128, KV4_REST>(prm, list, flags, st);
-    return mode == KV4_8 ? launch_attend<64, KV4_8>(prm, list, flags, st)
-           : mode == KV4_16 ? launch_attend<64, KV4_16>(prm, list, flags, st)
-                            : launch_attend<64, KV4_REST>(prm, list, flags, st);
+    return attend<false>(cache, args, nullptr, dev_status, flags, stream);
+}
+
+int kda_kv4_attend_tree(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, const uint64_t* tree, int32_t* dev_status,
+                        uint32_t flags, void* stream) {
+    return attend<true>(cache, args, tree, dev_status, flags, stream);
 }
 
 int kda_head_norm(const kda_head_norm_args* args, uint32_t flags, void* stream) {
