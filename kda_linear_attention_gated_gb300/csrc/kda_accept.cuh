@@ -28,7 +28,8 @@ constexpr int ACC_SEGS = ACC_CTAS * ACC_WARPS;      // 64 pieces of the vocabula
 static_assert(ACC_SEGS == 64, "two pieces a lane");
 
 // A sum of two floats, hi + lo with |lo| at most half a step of hi: 48 bits.
-// fp64 runs at a 64th of the fp32 rate here, and 32 bits lose the places next
+// fp64 runs at a 64th of the fp32 rate here (a version with the tests and the
+// scans in fp64: 70 us where this takes ...), and 32 bits lose the places next
 // to a border between two tokens.
 struct Pair { float hi, lo; };
 // s += x (Knuth's exact sum of two floats; the errors add up in lo)
@@ -37,10 +38,34 @@ __device__ __forceinline__ void pair_add(Pair& s, float x, float x_lo) {
     s.lo += ((s.hi - (t - b)) + (x - b)) + x_lo;
     s.hi = t;
 }
-__device__ __forceinline__ double pair_f64(const Pair& s) { return (double)s.hi + (double)s.lo; }
-__device__ __forceinline__ Pair f64_pair(double x) {
-    const float hi = (float)x;
-    return {hi, isfinite(hi) ? (float)(x - (double)hi) : 0.f};
+__device__ __forceinline__ Pair pair_norm(Pair s) {
+    const float t = s.hi + s.lo;
+    return {t, s.lo - (t - s.hi)};
+}
+__device__ __forceinline__ Pair operator+(Pair a, const Pair& b) {
+    pair_add(a, b.hi, b.lo);
+    return pair_norm(a);
+}
+__device__ __forceinline__ Pair operator-(Pair a, const Pair& b) {
+    pair_add(a, -b.hi, -b.lo);
+    return pair_norm(a);
+}
+__device__ __forceinline__ Pair operator*(const Pair& a, float f) {
+    const float h = a.hi * f;
+    return pair_norm({h, fmaf(a.hi, f, -h) + a.lo * f});
+}
+__device__ __forceinline__ bool operator<(const Pair& a, const Pair& b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ Pair pair_shfl(const Pair& a, int lane) {
+    return {__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+// Running sums over the lanes of a warp.
+__device__ __forceinline__ Pair pair_scan(Pair a, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair up = {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+        if (lane >= o) a = up + a;
+    }
+    return a;
 }
 
 // What every CTA of a request walks by, written by the cluster's first CTA.
@@ -49,9 +74,9 @@ struct AcceptInfo {
     int tok[TREE_MAX];
     float p[TREE_MAX], q[TREE_MAX], u[TREE_MAX];    // of the token in its parent's rows; p < 0: not a token
     unsigned long long child[TREE_MAX];
-    double sum[2][ACC_WARPS];       // a pass's sums, in turn
-    Pair z[TREE_MAX];               // Z_k of the current node
-    int found;
+    Pair sum[2][ACC_WARPS];         // a pass's sums, in turn
+    Pair part[ACC_WARPS];
+    int vote[2][ACC_WARPS];
 };
 
 __device__ __forceinline__ float acc_weight(float x) { return x > 0.f ? x : 0.f; }   // NaN: 0
@@ -62,7 +87,8 @@ template <typename T, bool DRAWN> struct AcceptRow {
     const T *p, *q;
     int vocab, shift, vecs;         // elements before the row in its first 16-byte vector; vectors
     bool together;                  // q's row lies on its vectors as p's does
-    int k;                          // rejections
+    int k;                          // rejections with q
+    Pair c;                         // and the sum of their Z: W = max(p - c q, 0)
     unsigned long long gone;        // rejected siblings (without q)
     const AcceptInfo* info;
 
@@ -97,42 +123,37 @@ template <typename T, bool DRAWN> struct AcceptRow {
         if (DRAWN && k > 0) r.q = whole && together ? __ldg(reinterpret_cast<const uint4*>(q + i0)) : edge(q, i0);
         return r;
     }
-    // The weights of a vector, as exact sums of two floats.
-    __device__ __forceinline__ void weights(const Raw& r, int vec, Pair (&w)[VE]) const {
+    // A vector's weights, as exact sums of two floats, in order.
+    template <typename F> __device__ __forceinline__ void weights(const Raw& r, int vec, F&& use) const {
         T pe[VE], qe[VE];
         memcpy(pe, &r.p, 16);
         memcpy(qe, &r.q, 16);
-#pragma unroll
-        for (int x = 0; x < VE; ++x) w[x] = {acc_weight(conv_f32(pe[x])), 0.f};
-        if constexpr (DRAWN) {
-            if (k > 0) {
-#pragma unroll
-                for (int x = 0; x < VE; ++x) {      // Z_0 = 1: p - q and its error, exact for p > q
-                    const float pf = w[x].hi, qf = acc_weight(conv_f32(qe[x])), d = pf - qf;
-                    w[x] = pf > qf ? Pair{d, (pf - d) - qf} : Pair{0.f, 0.f};
-                }
-                for (int j = 1; j < k; ++j) {
-                    const Pair z = info->z[j];
-#pragma unroll
-                    for (int x = 0; x < VE; ++x) {
-                        const float qf = acc_weight(conv_f32(qe[x]));
-                        const float h = z.hi * qf, e = fmaf(z.hi, qf, -h) + z.lo * qf;
-                        Pair s = w[x];
-                        pair_add(s, -h, -e);
-                        const float hi = s.hi + s.lo;
-                        w[x] = hi > 0.f && w[x].hi > 0.f ? Pair{hi, s.lo - (hi - s.hi)} : Pair{0.f, 0.f};
-                    }
-                }
-            }
-        } else {
+        uint32_t out = 0;           // given drafts: the vector's rejected tokens
+        if constexpr (!DRAWN) {
             const int i0 = vec * VE - shift;
             for (unsigned long long g = gone; g != 0; g &= g - 1) {
                 const int at = info->tok[__ffsll((long long)g) - 1] - i0;
-                if (at >= 0 && at < VE)
-#pragma unroll
-                    for (int x = 0; x < VE; ++x)
-                        if (x == at) w[x] = {0.f, 0.f};
+                if (at >= 0 && at < VE) out |= 1u << at;
             }
+        }
+#pragma unroll
+        for (int x = 0; x < VE; ++x) {
+            Pair w = {acc_weight(conv_f32(pe[x])), 0.f};
+            if constexpr (DRAWN) {
+                const float qf = acc_weight(conv_f32(qe[x]));
+                if (k == 1) {       // c = 1: p - q and its error, exact for p > q
+                    const float d = w.hi - qf;
+                    w = w.hi > qf ? Pair{d, (w.hi - d) - qf} : Pair{0.f, 0.f};
+                } else if (k > 1) {
+                    const float h = c.hi * qf;
+                    pair_add(w, -h, -(fmaf(c.hi, qf, -h) + c.lo * qf));
+                    w = pair_norm(w);
+                    if (!(w.hi > 0.f)) w = {0.f, 0.f};
+                }
+            } else {
+                if (out >> x & 1u) w = {0.f, 0.f};
+            }
+            use(w, x);
         }
     }
 };
@@ -141,7 +162,8 @@ template <typename T, bool DRAWN> struct AcceptRow {
 // Z_0 = 1.  Its children x in order, with W, Z of the rejections so far:
 //   drafts drawn from q:  accepted if u q(x) Z < W(x), else W <- max(W - Z q, 0), Z <- sum W
 //   drafts given:         accepted if u Z < W(x),      else W(x) <- 0,            Z <- Z - W(x)
-// (W / Z is the distribution that is left; nothing is divided).  An accepted
+// (W / Z is the distribution that is left; nothing is divided, and W = max(p - c q,
+// 0) with c the sum of the Z so far, as W only falls).  An accepted
 // child becomes cur.  Where no child is left the next token is drawn from W by
 // its inverse distribution function: the first i with W(i) > 0 whose running
 // sum passes u_last sum W.
@@ -149,10 +171,10 @@ template <typename T, bool DRAWN> struct AcceptRow {
 // A cluster of eight CTAs shares a request's row, 64 warps a piece each.  The
 // first CTA gathers what the tests need and gives it to the others, so all
 // walk alike; a rejection with q and the draw take one pass over the row's
-// pieces and a sum over the cluster, the draw then one warp's second look at its
-// piece.  Bound by memory: a row of p and one of q.
+// pieces and a sum over the cluster, the draw then a second look at one piece
+// by its whole CTA.  Bound by memory: a row of p and one of q.
 template <typename T, bool DRAWN>
-__global__ void __cluster_dims__(ACC_CTAS, 1, 1) __launch_bounds__(ACC_THREADS) kda_accept_kernel(const AcceptParams a) {
+__global__ void __cluster_dims__(ACC_CTAS, 1, 1) __launch_bounds__(ACC_THREADS, 4) kda_accept_kernel(const AcceptParams a) {
     namespace cg = cooperative_groups;
     using Row = AcceptRow<T, DRAWN>;
     constexpr int VE = Row::VE;
@@ -226,55 +248,46 @@ __global__ void __cluster_dims__(ACC_CTAS, 1, 1) __launch_bounds__(ACC_THREADS) 
     Row row;
     row.info = &info;
     int cur = 0, count = 1, turn = 0;
-    double z = 1.0, s0 = 0.0, s1 = 0.0, upto = 0.0, total = 0.0;
-    int v0 = 0, v1 = 0;         // this warp's vectors
+    Pair z = {1.f, 0.f}, s0, s1, upto, total;
+    int v0 = 0, v1 = 0, each = 0;       // this warp's vectors
     auto use = [&](int node) {
         row.set(P + (int64_t)(tb + node) * a.p_stride, DRAWN ? Q + (int64_t)(tb + node) * a.q_stride : nullptr, a.vocab);
         row.k = 0;
+        row.c = {0.f, 0.f};
         row.gone = 0;
-        const int each = (row.vecs + ACC_SEGS - 1) / ACC_SEGS, seg = rank * ACC_WARPS + warp;
-        v0 = min(row.vecs, seg * each);
+        each = (row.vecs + ACC_SEGS - 1) / ACC_SEGS;
+        v0 = min(row.vecs, (rank * ACC_WARPS + warp) * each);
         v1 = min(row.vecs, v0 + each);
     };
-    // sum W over the cluster; lane l then holds the sums s0, s1 of pieces 2 l and 2 l + 1
+    // sum W over the cluster; lane l then holds the sums s0, s1 of pieces 2 l and 2 l + 1 and the running sum `upto`
     auto sum = [&]() {
         Pair s[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        auto add = [&](const Pair& w, int x) { pair_add(s[x & 1], w.hi, w.lo); };
         constexpr int U = 4;
         int v = v0 + lane;
-        for (; v + 32 * (U - 1) < v1; v += 32 * U) {
+        for (; v < v1; v += 32 * U) {
             typename Row::Raw raw[U];
 #pragma unroll
-            for (int x = 0; x < U; ++x) raw[x] = row.load(v + 32 * x);
+            for (int x = 0; x < U; ++x)
+                if (v + 32 * x < v1) raw[x] = row.load(v + 32 * x);
 #pragma unroll
-            for (int x = 0; x < U; ++x) {
-                Pair w[VE];
-                row.weights(raw[x], v + 32 * x, w);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) pair_add(s[e & 1], w[e].hi, w[e].lo);
-            }
+            for (int x = 0; x < U; ++x)
+                if (v + 32 * x < v1) row.weights(raw[x], v + 32 * x, add);
         }
-        for (; v < v1; v += 32) {
-            const typename Row::Raw raw = row.load(v);
-            Pair w[VE];
-            row.weights(raw, v, w);
+        Pair d = pair_norm(s[0]) + pair_norm(s[1]);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) pair_add(s[e & 1], w[e].hi, w[e].lo);
+        for (int o = 16; o > 0; o >>= 1) {
+            // the lower lane's first: both get the same sum
+            const Pair to = {__shfl_xor_sync(0xffffffffu, d.hi, o), __shfl_xor_sync(0xffffffffu, d.lo, o)};
+            d = lane & o ? to + d : d + to;
         }
-        double d = pair_f64(s[0]) + pair_f64(s[1]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         if (lane == 0) info.sum[turn][warp] = d;
         cluster.sync();
-        const double* of = &cluster.map_shared_rank(&info, (2 * lane) / ACC_WARPS)->sum[turn][(2 * lane) % ACC_WARPS];
+        const Pair* of = &cluster.map_shared_rank(&info, (2 * lane) / ACC_WARPS)->sum[turn][(2 * lane) % ACC_WARPS];
         s0 = of[0];
         s1 = of[1];
-        upto = s0 + s1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += up;
-        }
-        total = __shfl_sync(0xffffffffu, upto, 31);
+        upto = pair_scan(s0 + s1, lane);
+        total = pair_shfl(upto, 31);
         turn ^= 1;      // the other half: a CTA may still read this one
     };
     use(0);
@@ -284,105 +297,102 @@ __global__ void __cluster_dims__(ACC_CTAS, 1, 1) __launch_bounds__(ACC_THREADS) 
         const int i = __ffsll((long long)rest) - 1;
         rest &= rest - 1;
         if (info.p[i] < 0.f) continue;
-        double w = info.p[i];
-        const double qx = DRAWN ? info.q[i] : 1.0;
+        Pair w = {info.p[i], 0.f};
+        const float qx = DRAWN ? info.q[i] : 1.f;
         if constexpr (DRAWN) {
-            for (int j = 0; j < row.k; ++j) {
-                w -= (j == 0 ? 1.0 : pair_f64(info.z[j])) * qx;
-                if (!(w > 0.0)) w = 0.0;
-            }
+            if (row.k > 0) w = w - row.c * qx;      // not above zero: not accepted
         } else {
             for (unsigned long long g = row.gone; g != 0; g &= g - 1)
-                if (info.tok[__ffsll((long long)g) - 1] == info.tok[i]) w = 0.0;
+                if (info.tok[__ffsll((long long)g) - 1] == info.tok[i]) w = {0.f, 0.f};
         }
-        if ((double)info.u[i] * qx * z < w) {
+        // u q is exact as a pair, and so the first child's test
+        const float u = info.u[i], uq = u * qx;
+        const Pair bar = row.k == 0 && row.gone == 0 ? Pair{uq, fmaf(u, qx, -uq)} : (z * qx) * u;
+        if (bar < w) {
             cur = i;
             if (writer) path[count] = tb + i;
             ++count;
             use(i);
-            z = 1.0;
+            z = {1.f, 0.f};
             summed = false;
             rest = info.child[i];
         } else if constexpr (DRAWN) {
             ++row.k;
+            row.c = row.c + z;
             sum();
             z = total;
             summed = true;
-            __syncthreads();
-            if (tid == 0 && row.k < TREE_MAX) info.z[row.k] = f64_pair(total);
-            __syncthreads();
         } else {
             row.gone |= 1ull << i;
-            z -= w;
+            z = z - w;
         }
     }
     if (!summed) sum();
-    if (!(total > 0.0) && (row.k > 0 || row.gone != 0)) {    // nothing left: from the target's own
+    if (!(total.hi > 0.f) && (row.k > 0 || row.gone != 0)) {    // nothing left: from the target's own
         row.k = 0;
         row.gone = 0;
         sum();
     }
+    const bool draw = total.hi > 0.f && total.hi <= FLT_MAX;
     if (writer) {
         a.accepted[r] = count;
         a.node[r] = cur + 1;
-        if (!(total > 0.0) || !(total <= DBL_MAX)) {
+        if (!draw) {
             a.token[r] = -1;
             atomicCAS(a.status, 0, STATUS_ARG);
         }
     }
     if (rank == 0)
         for (int j = count + tid; j < a.max_t; j += ACC_THREADS) path[j] = -1;
-    if (total > 0.0 && total <= DBL_MAX) {
+    if (draw) {
         // the piece where the running sum passes u_last of the whole, else the last that has weight
-        const double target = (double)__ldg(a.u_last + r) * total, before = upto - (s0 + s1);
-        const bool in0 = s0 > 0.0 && before + s0 > target, in1 = s1 > 0.0 && before + s0 + s1 > target;
-        const uint32_t hit = __ballot_sync(0xffffffffu, in0 || in1), some = __ballot_sync(0xffffffffu, s0 > 0.0 || s1 > 0.0);
+        const Pair target = total * __ldg(a.u_last + r), before = {__shfl_up_sync(0xffffffffu, upto.hi, 1), __shfl_up_sync(0xffffffffu, upto.lo, 1)};
+        const Pair base0 = lane == 0 ? Pair{0.f, 0.f} : before, base1 = base0 + s0;
+        const bool in0 = s0.hi > 0.f && target < base1, in1 = s1.hi > 0.f && target < upto;
+        const uint32_t hit = __ballot_sync(0xffffffffu, in0 || in1), some = __ballot_sync(0xffffffffu, s0.hi > 0.f || s1.hi > 0.f);
         const int who = hit != 0 ? __ffs(hit) - 1 : 31 - __clz(some);
-        const bool odd = hit != 0 ? !in0 : s1 > 0.0;
-        const int seg = 2 * who + (int)__shfl_sync(0xffffffffu, (int)odd, who);
-        if (seg == rank * ACC_WARPS + warp) {
-            double base = __shfl_sync(0xffffffffu, before, who);
-            if (seg & 1) base += __shfl_sync(0xffffffffu, s0, who);
-            int last = -1;
-            bool done = false;
-            for (int v = v0; v < v1 && !done; v += 32) {
-                Pair w[VE];
-                double mine = 0.0;
-                const int vec = v + lane;
-                if (vec < v1) {
-                    const typename Row::Raw raw = row.load(vec);
-                    row.weights(raw, vec, w);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) mine += pair_f64(w[e]);
-                }
-                double run = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double up = __shfl_up_sync(0xffffffffu, run, o);
-                    if (lane >= o) run += up;
-                }
-                const uint32_t over = __ballot_sync(0xffffffffu, mine > 0.0 && base + run > target);
-                const uint32_t has = __ballot_sync(0xffffffffu, mine > 0.0);
-                if (has != 0) {
-                    const int l = over != 0 ? __ffs(over) - 1 : 31 - __clz(has);
-                    int at = -1;
-                    if (lane == l) {
-                        double cum = base + (run - mine);
-                        bool stop = false;
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            if (stop || !(w[e].hi > 0.f)) continue;
-                            cum += pair_f64(w[e]);
-                            at = vec * VE - row.shift + e;
-                            stop = over != 0 && cum > target;
-                        }
-                    }
-                    last = __shfl_sync(0xffffffffu, at, l);
-                }
-                done = over != 0;
-                base += __shfl_sync(0xffffffffu, run, 31);
+        const int odd = __shfl_sync(0xffffffffu, (int)(hit != 0 ? !in0 : s1.hi > 0.f), who), seg = 2 * who + odd;
+        if (seg / ACC_WARPS == rank) {
+            // a thread takes neighbouring vectors of the piece
+            const Pair base = pair_shfl(odd ? base1 : base0, who);
+            const int g0 = min(row.vecs, seg * each), g1 = min(row.vecs, g0 + each), per = (each + ACC_THREADS - 1) / ACC_THREADS;
+            const int a0 = min(g1, g0 + tid * per), a1 = min(g1, a0 + per);
+            Pair mine = {0.f, 0.f};
+            for (int v = a0; v < a1; ++v) row.weights(row.load(v), v, [&](const Pair& w, int) { pair_add(mine, w.hi, w.lo); });
+            mine = pair_norm(mine);
+            const Pair run = pair_scan(mine, lane);
+            if (lane == 31) info.part[warp] = run;
+            __syncthreads();
+            Pair left = base;
+            for (int x = 0; x < warp; ++x) left = left + info.part[x];
+            const Pair end = left + run;
+            // the first thread that passes the target, else the last with weight; a vote over the CTA
+            const bool over = mine.hi > 0.f && target < end;
+            const uint32_t o = __ballot_sync(0xffffffffu, over), h = __ballot_sync(0xffffffffu, mine.hi > 0.f);
+            if (lane == 0) {
+                info.vote[0][warp] = o != 0 ? 32 * warp + __ffs(o) - 1 : 0x7fffffff;
+                info.vote[1][warp] = h != 0 ? 32 * warp + 31 - __clz(h) : -1;
             }
-            if (lane == 0) a.token[r] = last;
+            __syncthreads();
+            int first = 0x7fffffff, last = -1;
+#pragma unroll
+            for (int x = 0; x < ACC_WARPS; ++x) {
+                first = min(first, info.vote[0][x]);
+                last = max(last, info.vote[1][x]);
+            }
+            if (tid == (first != 0x7fffffff ? first : last)) {
+                Pair cum = left + (run - mine);
+                int at = -1;
+                bool stop = false;
+                for (int v = a0; v < a1 && !stop; ++v)
+                    row.weights(row.load(v), v, [&](const Pair& w, int x) {
+                        if (stop || !(w.hi > 0.f)) return;
+                        cum = cum + w;
+                        at = v * VE - row.shift + x;
+                        stop = first != 0x7fffffff && target < cum;
+                    });
+                a.token[r] = at;
+            }
         }
     }
     cluster.sync();     // a CTA's sums are read by the others until here

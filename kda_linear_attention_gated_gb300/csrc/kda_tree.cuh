@@ -24,7 +24,25 @@ __device__ __forceinline__ int tree_top(uint64_t m) { return 63 - __clzll((long 
 // ---------------------------------------------------------------------------
 // Convolution
 // ---------------------------------------------------------------------------
-constexpr int CONV_TREE_THREADS = 64;
+constexpr int CONV_TREE_CH = 64;        // channel vectors of a CTA
+constexpr int CONV_TREE_GROUPS = 4;     // threads of a channel vector, which share the tokens
+
+// Shared memory of a CTA: a row for each history entry and token, and the rows
+// of each token's taps.
+template <typename ET, int VC> struct ConvTreeSmem {
+    static constexpr int ROW = CONV_TREE_CH * VC * (int)sizeof(ET);
+    static __host__ __device__ constexpr int bytes(int t) { return (CONV_KW_MAX - 1 + t) * ROW + t * 8; }
+};
+
+// silu_fast in five instructions: the exponential and the reciprocal without
+// their steps for subnormal numbers, which come to the same (e^-s below 2^-126
+// vanishes beside 1, and above 2^126 both divide to -0).
+__device__ __forceinline__ float silu_short(float s) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return s * r;
+}
 
 // y_j = act(bias + sum_i weight[i] z_i) over the last KW inputs z on token j's
 // path: its ancestors', and before the first of them the window's history.
@@ -32,83 +50,109 @@ constexpr int CONV_TREE_THREADS = 64;
 // last), so that a chain gives its bits.  The window is not written: what is
 // kept are the accepted tokens, which the caller passes to kda_conv_step.
 //
-// VC channels a thread (16 bytes, or 1), `chunk` tokens of a request a CTA, the
-// weights and the history loaded once for them; an ancestor's row comes out of
-// L1 or L2.
+// A CTA takes a request and 64 vectors of channels (16 bytes, or one channel)
+// and loads the history and all inputs to shared memory at once, where a token
+// finds its ancestors' wherever they stand; four threads a vector share the
+// tokens.  A token's taps are row numbers, a byte each, worked out by one thread.
 template <typename ET, int VC, int KWM>
-__global__ void __launch_bounds__(CONV_TREE_THREADS) kda_conv_tree_kernel(const ConvParams p, const uint64_t* tree, int chunk) {
+__global__ void __launch_bounds__(CONV_TREE_CH * CONV_TREE_GROUPS) kda_conv_tree_kernel(const ConvParams p, const uint64_t* tree) {
     using IO = ConvIO<ET, VC>;
     using R = typename IO::R;
-    const int cblocks = (p.C / VC + CONV_TREE_THREADS - 1) / CONV_TREE_THREADS, chunks = (p.t + chunk - 1) / chunk;
-    const int cb = (int)blockIdx.x % cblocks, rc = (int)blockIdx.x / cblocks, r = rc / chunks, j0 = (rc - r * chunks) * chunk;
-    const int c = (cb * CONV_TREE_THREADS + (int)threadIdx.x) * VC;
+    extern __shared__ __align__(16) uint8_t smem[];
+    R* rows = reinterpret_cast<R*>(smem);       // [KW - 1 + T][64]
+    const int cblocks = (p.C / VC + CONV_TREE_CH - 1) / CONV_TREE_CH;
+    const int cb = (int)blockIdx.x % cblocks, r = (int)blockIdx.x / cblocks;
+    const int ch = threadIdx.x % CONV_TREE_CH, grp = threadIdx.x / CONV_TREE_CH, tid = threadIdx.x;
+    const int c = (cb * CONV_TREE_CH + ch) * VC, KW = p.KW;
+    uint64_t* taps = reinterpret_cast<uint64_t*>(rows + (KW - 1 + p.t) * CONV_TREE_CH);   // rows are multiples of 128 bytes
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
-    if (c >= p.C) return;
     int tb = r * p.t, T = p.t;
     if (p.cu != nullptr) {
         tb = __ldg(p.cu + r);
         T = __ldg(p.cu + r + 1) - tb;
     }
     const int32_t slot = __ldg(p.conv_slot + r);
-    const int acc = p.accepted != nullptr ? __ldg(p.accepted + r) - 1 : 0, KW = p.KW;
-    const bool rst = p.reset != nullptr && __ldg(p.reset + r) != 0;
+    const int acc = p.accepted != nullptr ? __ldg(p.accepted + r) - 1 : 0;
+    const bool rst = p.reset != nullptr && __ldg(p.reset + r) != 0, on = c < p.C;
     if (tb < 0 || T < 0 || T > p.t || tb > p.total - T) {
-        if (threadIdx.x == 0) atomicCAS(p.status, 0, STATUS_ARG);
+        if (tid == 0) atomicCAS(p.status, 0, STATUS_ARG);
         return;
     }
-    const int j1 = min(T, j0 + chunk);
-    if (j0 >= j1) return;
+    if (T == 0) return;
     ET* y = static_cast<ET*>(p.y) + (int64_t)tb * p.C + c;
+    float zero[VC] = {};
     if (slot < 0) {
-        float zero[VC] = {};
-        for (int j = j0; j < j1; ++j) IO::st(y + (int64_t)j * p.C, IO::narrow(zero));
+        for (int j = grp; on && j < T; j += CONV_TREE_GROUPS) IO::st(y + (int64_t)j * p.C, IO::narrow(zero));
         return;
     }
     if (slot >= p.num_slots || acc < 0 || acc > p.L - (KW - 1)) {
-        if (threadIdx.x == 0) atomicCAS(p.status, 0, slot >= p.num_slots ? STATUS_SLOT_RANGE : STATUS_ARG);
+        if (tid == 0) atomicCAS(p.status, 0, slot >= p.num_slots ? STATUS_SLOT_RANGE : STATUS_ARG);
         return;
     }
-    const ET* x = static_cast<const ET*>(p.x) + (int64_t)tb * p.C + c;
-    const ET* W = static_cast<const ET*>(p.window) + (int64_t)slot * p.slot_stride + (int64_t)acc * p.C + c;
-    // taps right-aligned: place i of KWM holds tap i - (KWM - KW)
-    const int pad = KWM - KW;
-    float w[KWM][VC], bias[VC];
-    R hist[KWM - 1], none;
-    {
-        float zero[VC] = {};
-        none = IO::narrow(zero);
+    if (on) {
+        const ET* x = static_cast<const ET*>(p.x) + (int64_t)tb * p.C + c;
+        const ET* W = static_cast<const ET*>(p.window) + (int64_t)slot * p.slot_stride + (int64_t)acc * p.C + c;
+        for (int i = grp; i < KW - 1; i += CONV_TREE_GROUPS) rows[i * CONV_TREE_CH + ch] = rst ? IO::narrow(zero) : IO::ld(W + (int64_t)i * p.C);
+        constexpr int U = 8;
+        int j = grp;
+        for (; j + (U - 1) * CONV_TREE_GROUPS < T; j += U * CONV_TREE_GROUPS) {
+            R v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) v[i] = IO::ld(x + (int64_t)(j + i * CONV_TREE_GROUPS) * p.C);
+#pragma unroll
+            for (int i = 0; i < U; ++i) rows[(KW - 1 + j + i * CONV_TREE_GROUPS) * CONV_TREE_CH + ch] = v[i];
+        }
+        for (; j < T; j += CONV_TREE_GROUPS) rows[(KW - 1 + j) * CONV_TREE_CH + ch] = IO::ld(x + (int64_t)j * p.C);
     }
-#pragma unroll
-    for (int i = 0; i < KWM - 1; ++i) hist[i] = i >= pad && !rst ? IO::ld(W + (int64_t)(i - pad) * p.C) : none;
-#pragma unroll
-    for (int v = 0; v < VC; ++v) {
-        bias[v] = p.bias != nullptr ? __ldg(p.bias + c + v) : 0.f;
-#pragma unroll
-        for (int i = 0; i < KWM; ++i) w[i][v] = i >= pad ? __ldg(p.w + (int64_t)(c + v) * KW + i - pad) : 0.f;
-    }
-    for (int j = j0; j < j1; ++j) {
-        uint64_t m = tree_mask(tree, tb + j, j);
-        R z[KWM];
-#pragma unroll
-        for (int i = KWM - 1; i >= 0; --i) {
-            // m == 0: the place KWM - 1 - d lies d - (tokens on the path) before the history's end; both
-            // the path's length and the place are the CTA's, and the select has constant indexes
+    if (tid < T) {
+        // byte i: the row of tap i
+        uint64_t m = tree_mask(tree, tb + tid, tid), packed = 0;
+        int hist = KW - 2;
+        for (int i = KW - 1; i >= 0; --i) {
+            int row = hist;
             if (m != 0) {
                 const int at = tree_top(m);
                 m ^= 1ull << at;
-                z[i] = i >= pad ? IO::ld(x + (int64_t)at * p.C) : none;
+                row = KW - 1 + at;
             } else {
-                z[i] = none;
+                --hist;
             }
+            packed |= (uint64_t)row << (8 * i);
         }
-        const int depth = min(KWM, __popcll(tree_mask(tree, tb + j, j)));   // places that the path fills
-        // place i < KWM - depth: history entry i + depth - 1 of the right-aligned KWM - 1
+        taps[tid] = packed;
+    }
+    // taps right-aligned: place i of KWM holds tap i - (KWM - KW)
+    const int pad = KWM - KW;
+    float w[KWM][VC], bias[VC];
+    if (on) {
+        const float* wp = p.w + (int64_t)c * KW;
+        if (VC % 4 == 0 && KWM == 4 && KW == 4 && (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0) {
 #pragma unroll
-        for (int i = 0; i < KWM - 1; ++i)
+            for (int v = 0; v < VC; ++v) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(wp) + v);
+                w[0][v] = f.x;
+                w[1 % KWM][v] = f.y;
+                w[2 % KWM][v] = f.z;
+                w[3 % KWM][v] = f.w;
+            }
+        } else {
 #pragma unroll
-            for (int d = 1; d < KWM - i; ++d)
-                if (depth == d) z[i] = hist[i + d - 1];
+            for (int v = 0; v < VC; ++v)
+#pragma unroll
+                for (int i = 0; i < KWM; ++i) w[i][v] = i >= pad ? __ldg(wp + v * KW + i - pad) : 0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < VC; ++v) bias[v] = p.bias != nullptr ? __ldg(p.bias + c + v) : 0.f;
+    }
+    __syncthreads();
+    if (!on) return;
+    for (int j = grp; j < T; j += CONV_TREE_GROUPS) {
+        const uint64_t packed = taps[j] << (8 * pad);
+        R z[KWM];
+#pragma unroll
+        for (int i = 0; i < KWM; ++i)
+            if (i >= pad) z[i] = rows[(int)(packed >> (8 * i) & 0xffu) * CONV_TREE_CH + ch];
         float s[VC];
 #pragma unroll
         for (int v = 0; v < VC; ++v) s[v] = bias[v];
@@ -117,12 +161,21 @@ __global__ void __launch_bounds__(CONV_TREE_THREADS) kda_conv_tree_kernel(const 
             if (i < pad) continue;
             float f[VC];
             IO::widen(z[i], f);
+            if constexpr (VC % 2 == 0) {    // two at a time, each as fmaf rounds
 #pragma unroll
-            for (int v = 0; v < VC; ++v) s[v] = fmaf(w[i][v], f[v], s[v]);
+                for (int v = 0; v < VC; v += 2) {
+                    const float2 t = __ffma2_rn(make_float2(w[i][v], w[i][v + 1]), make_float2(f[v], f[v + 1]), make_float2(s[v], s[v + 1]));
+                    s[v] = t.x;
+                    s[v + 1] = t.y;
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < VC; ++v) s[v] = fmaf(w[i][v], f[v], s[v]);
+            }
         }
         if (p.silu) {
 #pragma unroll
-            for (int v = 0; v < VC; ++v) s[v] = silu_fast(s[v]);
+            for (int v = 0; v < VC; ++v) s[v] = silu_short(s[v]);
         }
         IO::st(y + (int64_t)j * p.C, IO::narrow(s));
     }
@@ -139,23 +192,27 @@ template <typename ST> struct TreeSmem {
     static __host__ __device__ constexpr int vecs(int t) { return 3 * t * KMAX * 4; }              // k, alpha, q of each token
     static __host__ __device__ constexpr int delta(int t, int warps) { return t * warps * CW * 4; }
     static __host__ __device__ constexpr int bytes(int t, int warps) {
-        return vecs(t) + delta(t, warps) + warps * 32 * 8 * 16 + t * (8 + 8 + 4) + 16;
+        return vecs(t) + delta(t, warps) + warps * 32 * 8 * 16 + t * (8 + 8 + 8 + 4);
     }
 };
 
 // One CTA: one request, one value head, `warps` times 32 bytes' worth of state
-// columns.  A warp owns its columns whole: lane l holds rows 8 (l / 2) .. + 7
-// of VEC columns, so the sums over K are shuffles within the warp and nothing
-// waits for another warp once the tokens' vectors are in shared memory.
+// columns.  A warp owns its columns whole: lane l holds VEC columns of the rows
+// 4 (l / 2) .. + 3 and 64 more, so the sums over K are shuffles within the
+// warp and nothing waits for another warp once the tokens' vectors are in
+// shared memory.
 //
 // A token's state is S_j = diag(alpha_j) S_parent + khat_j delta_j^T with
-// delta_j = beta_j (v_j - S_parent^T diag(alpha_j) khat_j).  Token j - 1's
-// state is in registers; where that is j's parent, j goes on from it.  Else the
-// parent's is built again from the initial state (kept on chip as it was
-// loaded: its slot may be one of the snapshots') with the ancestors' deltas,
-// which are kept: two operations an element and ancestor, no sums, the same
-// bits as on the way there.  So states carry fp32 along every path whatever
-// the pool's type, and siblings do not depend on their order.
+// delta_j = beta_j (v_j - S_parent^T diag(alpha_j) khat_j), and both of its sums
+// are over the parent's state, which is in registers.  Tokens are taken depth
+// first: of a token's children first the leaves, whose states only pass
+// through on their way out, then the first of the others, in place.  Where
+// another branch begins its parent's state is built again from the initial
+// state (kept on chip as it was loaded: its slot may be one of the
+// snapshots') with the ancestors' deltas, which are kept: two operations an
+// element and ancestor, no sums, the same bits as on the way there.  So states
+// carry fp32 along every path whatever the pool's type, and do not depend on
+// the order of siblings.
 template <typename ST, typename QT>
 __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const StepParams p, const uint64_t* tree) {
     using SV = StateVec<ST>;
@@ -165,15 +222,17 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
     float* kh = reinterpret_cast<float*>(smem);
     float* al = kh + p.t * KMAX;
     float* qh = al + p.t * KMAX;
-    float* du = qh + p.t * KMAX;                                            // [t][BV]
+    float* du = qh + p.t * KMAX;                                            // [t][BV]: v, then delta
     uint4* stash = reinterpret_cast<uint4*>(du + p.t * BV);                 // [8][threads]
-    uint64_t* masks = reinterpret_cast<uint64_t*>(stash + 8 * blockDim.x);
-    float2* sc = reinterpret_cast<float2*>(masks + p.t);                    // beta, khat . qhat
+    unsigned long long* masks = reinterpret_cast<unsigned long long*>(stash + 8 * blockDim.x);
+    unsigned long long* child = masks + p.t;
+    float2* sc = reinterpret_cast<float2*>(child + p.t);                    // beta, khat . qhat
     int32_t* snaps = reinterpret_cast<int32_t*>(sc + p.t);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cblocks = (p.v + BV - 1) / BV;
     const int cb = (int)blockIdx.x % cblocks, nh = (int)blockIdx.x / cblocks, n = nh / p.hv, h = nh - n * p.hv;
+    for (int j = tid; j < p.t; j += blockDim.x) child[j] = 0;
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
     int tb = n * p.t, T = p.t;
@@ -202,7 +261,7 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
         return;
     }
     const int c0 = cb * BV + warp * CW + (lane & 1) * VEC;                  // the lane's first column
-    const int r0 = (lane >> 1) * 8;                                         // and row
+    const int r0 = (lane >> 1) * 4;                                         // and row; its i-th is r0 + i % 4 + 64 (i / 4)
     const bool mine = c0 < p.v;
     if (slot < 0) {     // a padding request
         for (int i = tid; i < T * BV; i += blockDim.x) {
@@ -212,56 +271,82 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
         return;
     }
     const bool rst = p.reset != nullptr && __ldg(p.reset + n) != 0;
+    // half 0 and half 1 of the lane's rows are in the state
+    const bool live[2] = {mine && r0 < p.k, mine && r0 + 64 < p.k};
     ST* pool = static_cast<ST*>(p.pool);
     const int64_t tile = (int64_t)r0 * p.v + c0;
+    auto at_row = [&](int i) { return (int64_t)((i & 3) + 64 * (i >> 2)) * p.v; };
     uint4 raw[8];
     {
         const ST* from = pool + state_at(p, slot, h) + tile;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            raw[i] = mine && !rst && r0 + i < p.k ? *reinterpret_cast<const uint4*>(from + (int64_t)i * p.v) : make_uint4(0, 0, 0, 0);
+            raw[i] = live[i >> 2] && !rst ? *reinterpret_cast<const uint4*>(from + at_row(i)) : make_uint4(0, 0, 0, 0);
     }
+    __syncthreads();    // child is zero
     // ---- the tokens' vectors, a token a warp at a time ----
     const int hq = h / (p.hv / p.hqk);
     const bool scaled = p.a_log != nullptr;
     const float gate = scaled ? expf(__ldg(p.a_log + h)) : 1.f;
-    for (int j = warp; j < T; j += warps) {
-        const int d = 4 * lane;
-        const bool on = d < p.k;
-        const int64_t at = ((int64_t)(tb + j) * p.hqk + hq) * p.k + d;
-        float k4[4] = {}, q4[4] = {};
-        float4 a4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-            ConvIO<QT, 4>::widen(ConvIO<QT, 4>::ld(static_cast<const QT*>(p.kk) + at), k4);
-            ConvIO<QT, 4>::widen(ConvIO<QT, 4>::ld(static_cast<const QT*>(p.q) + at), q4);
-            a4 = __ldg(reinterpret_cast<const float4*>(p.a + ((int64_t)(tb + j) * p.hv + h) * p.k + d));
-        }
-        float kk = 0.f, qq = 0.f, kq = 0.f;
+    constexpr int AHEAD = 4;        // tokens whose loads a warp has on their way
+    const int d = 4 * lane;
+    const bool on = d < p.k;
+    float bias[4] = {};
+    if (on && scaled && p.dt_bias != nullptr) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            kk = fmaf(k4[e], k4[e], kk);
-            qq = fmaf(q4[e], q4[e], qq);
-            kq = fmaf(k4[e], q4[e], kq);
-        }
-        kk = warp_sum(kk);
-        qq = warp_sum(qq);
-        kq = warp_sum(kq);
-        const float rk = __frsqrt_rn(kk + L2_EPS), rq = __frsqrt_rn(qq + L2_EPS);
-        float bias[4] = {};
-        if (on && scaled && p.dt_bias != nullptr) {
+        for (int e = 0; e < 4; ++e) bias[e] = __ldg(p.dt_bias + h * p.k + d + e);
+    }
+    using QIO = ConvIO<QT, 4>;
+    for (int j0 = warp; j0 < T; j0 += AHEAD * warps) {
+        typename QIO::R kr[AHEAD], qr[AHEAD];
+        float4 ar[AHEAD];
+        float br[AHEAD], vr[AHEAD];
+        unsigned long long mr[AHEAD];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bias[e] = __ldg(p.dt_bias + h * p.k + d + e);
+        for (int x = 0; x < AHEAD; ++x) {
+            const int j = min(j0 + x * warps, T - 1);
+            const int64_t tok = tb + j, at = (tok * p.hqk + hq) * p.k + (on ? d : 0);
+            kr[x] = QIO::ld(static_cast<const QT*>(p.kk) + at);
+            qr[x] = QIO::ld(static_cast<const QT*>(p.q) + at);
+            ar[x] = __ldg(reinterpret_cast<const float4*>(p.a + (tok * p.hv + h) * p.k + (on ? d : 0)));
+            br[x] = __ldg(p.b + tok * p.hv + h);
+            mr[x] = tree_mask(tree, tok, j) ^ (1ull << j);
+            vr[x] = lane < BV && cb * BV + lane < p.v ? to_f32(static_cast<const QT*>(p.vv)[(tok * p.hv + h) * p.v + cb * BV + lane]) : 0.f;
         }
-        const float a[4] = {a4.x, a4.y, a4.z, a4.w};
-        float g[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = gate_alpha(a[e], scaled, gate, bias[e]);
-        *reinterpret_cast<float4*>(kh + j * KMAX + d) = make_float4(k4[0] * rk, k4[1] * rk, k4[2] * rk, k4[3] * rk);
-        *reinterpret_cast<float4*>(qh + j * KMAX + d) = make_float4(q4[0] * rq, q4[1] * rq, q4[2] * rq, q4[3] * rq);
-        *reinterpret_cast<float4*>(al + j * KMAX + d) = make_float4(g[0], g[1], g[2], g[3]);
-        if (lane == 0) {
-            sc[j] = make_float2(sigmoid_neg(-__ldg(p.b + (int64_t)(tb + j) * p.hv + h)), kq * rk * rq);
-            masks[j] = tree_mask(tree, tb + j, j);
+        for (int x = 0; x < AHEAD; ++x) {
+            const int j = j0 + x * warps;
+            if (j >= T) break;
+            float k4[4], q4[4];
+            QIO::widen(kr[x], k4);
+            QIO::widen(qr[x], q4);
+            float kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!on) k4[e] = q4[e] = 0.f;
+                kk = fmaf(k4[e], k4[e], kk);
+                qq = fmaf(q4[e], q4[e], qq);
+                kq = fmaf(k4[e], q4[e], kq);
+            }
+            kk = warp_sum(kk);
+            qq = warp_sum(qq);
+            kq = warp_sum(kq);
+            const float rk = __frsqrt_rn(kk + L2_EPS), rq = __frsqrt_rn(qq + L2_EPS);
+            const float a[4] = {ar[x].x, ar[x].y, ar[x].z, ar[x].w};
+            float g[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = on ? gate_alpha(a[e], scaled, gate, bias[e]) : 0.f;
+            *reinterpret_cast<float4*>(kh + j * KMAX + d) = make_float4(k4[0] * rk, k4[1] * rk, k4[2] * rk, k4[3] * rk);
+            *reinterpret_cast<float4*>(qh + j * KMAX + d) = make_float4(q4[0] * rq, q4[1] * rq, q4[2] * rq, q4[3] * rq);
+            *reinterpret_cast<float4*>(al + j * KMAX + d) = make_float4(g[0], g[1], g[2], g[3]);
+            if (lane < BV) du[j * BV + lane] = vr[x];
+            for (int c = lane + 32; c < BV; c += 32)
+                du[j * BV + c] = cb * BV + c < p.v ? to_f32(static_cast<const QT*>(p.vv)[((int64_t)(tb + j) * p.hv + h) * p.v + cb * BV + c]) : 0.f;
+            if (lane == 0) {
+                sc[j] = make_float2(sigmoid_neg(-br[x]), kq * rk * rq);
+                masks[j] = mr[x];
+                if (mr[x] != 0) atomicOr(child + tree_top(mr[x]), 1ull << j);
+            }
         }
     }
     float2 S[8][P2];
@@ -273,54 +358,59 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
     __syncthreads();
 
     // which of the warp's sums this lane ends up with: lane bits 4.. down to SB count columns, bit SB is
-    // 0 for S^T khat and 1 for S^T qhat, bit 0 the column half
+    // 0 for the sum with khat and 1 for the one with qhat, bit 0 the column half
     constexpr int SB = VEC == 4 ? 2 : 1;
     const int vc = lane >> (SB + 1), second = lane >> SB & 1;
-    const int my_col = cb * BV + warp * CW + (lane & 1) * VEC + vc;
-    const bool live_col = my_col < p.v;
-    const QT* vv = static_cast<const QT*>(p.vv) + ((int64_t)tb * p.hv + h) * p.v + my_col;
-    const int64_t v_step = (int64_t)p.hv * p.v;
-    float v_next = live_col ? to_f32(vv[0]) : 0.f;
+    const int my_col = warp * CW + (lane & 1) * VEC + vc;
+    const bool first_of = VEC == 8 || (lane & 2) == 0, live_col = cb * BV + my_col < p.v && first_of;
+    auto vec8 = [&](const float* v, int j, float (&x)[8]) {
+        const float4 lo = *reinterpret_cast<const float4*>(v + j * KMAX + r0), hi = *reinterpret_cast<const float4*>(v + j * KMAX + 64 + r0);
+        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+    };
+    auto deltas = [&](int j, float2 (&d)[P2]) {
+#pragma unroll
+        for (int x = 0; x < P2; x += 2) {
+            const float4 f = *reinterpret_cast<const float4*>(du + j * BV + warp * CW + (lane & 1) * VEC + 2 * x);
+            d[x] = make_float2(f.x, f.y);
+            d[x + 1] = make_float2(f.z, f.w);
+        }
+    };
     // S <- diag(alpha_i) S + khat_i delta_i^T of an earlier token
     auto again = [&](int i) {
-        const float4 a0 = *reinterpret_cast<const float4*>(al + i * KMAX + r0), a1 = *reinterpret_cast<const float4*>(al + i * KMAX + r0 + 4);
-        const float4 k0 = *reinterpret_cast<const float4*>(kh + i * KMAX + r0), k1 = *reinterpret_cast<const float4*>(kh + i * KMAX + r0 + 4);
-        const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-        const float k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+        float a[8], k[8];
         float2 d[P2];
-#pragma unroll
-        for (int x = 0; x < P2; ++x) d[x] = *reinterpret_cast<const float2*>(du + i * BV + warp * CW + (lane & 1) * VEC + 2 * x);
+        vec8(al, i, a);
+        vec8(kh, i, k);
+        deltas(i, d);
 #pragma unroll
         for (int r = 0; r < 8; ++r)
 #pragma unroll
             for (int x = 0; x < P2; ++x) S[r][x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], __fmul2_rn(S[r][x], make_float2(a[r], a[r])));
     };
-    for (int j = 0; j < T; ++j) {
-        uint64_t above = masks[j] ^ (1ull << j);
-        if (j > 0 && above != masks[j - 1]) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) SV::widen2(stash[i * blockDim.x + tid], S[i]);
-            for (; above != 0; above &= above - 1) again(__ffsll((long long)above) - 1);
-        }
-        const float v_now = v_next;
-        if (j + 1 < T && live_col) v_next = to_f32(vv[(j + 1) * v_step]);
-        const float4 a0 = *reinterpret_cast<const float4*>(al + j * KMAX + r0), a1 = *reinterpret_cast<const float4*>(al + j * KMAX + r0 + 4);
-        const float4 k0 = *reinterpret_cast<const float4*>(kh + j * KMAX + r0), k1 = *reinterpret_cast<const float4*>(kh + j * KMAX + r0 + 4);
-        const float4 q0 = *reinterpret_cast<const float4*>(qh + j * KMAX + r0), q1 = *reinterpret_cast<const float4*>(qh + j * KMAX + r0 + 4);
-        const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-        const float k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-        const float q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    // Token j, a child of the token whose state S is: outputs, and the state to its snapshot; keep: and to S.
+    auto step = [&](int j, bool keep) {
+        float a[8], k[8];
+        vec8(al, j, a);
+        vec8(kh, j, k);
         float2 su[P2], sq[P2];
 #pragma unroll
         for (int x = 0; x < P2; ++x) su[x] = sq[x] = make_float2(0.f, 0.f);
+        {
+            float q[8];
+            vec8(qh, j, q);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
+            for (int r = 0; r < 8; ++r) {
+                const float ak = a[r] * k[r], aq = a[r] * q[r];
 #pragma unroll
-            for (int x = 0; x < P2; ++x) {
-                S[r][x] = __fmul2_rn(S[r][x], make_float2(a[r], a[r]));
-                su[x] = __ffma2_rn(S[r][x], make_float2(k[r], k[r]), su[x]);
-                sq[x] = __ffma2_rn(S[r][x], make_float2(q[r], q[r]), sq[x]);
+                for (int x = 0; x < P2; ++x) {
+                    su[x] = __ffma2_rn(S[r][x], make_float2(ak, ak), su[x]);
+                    sq[x] = __ffma2_rn(S[r][x], make_float2(aq, aq), sq[x]);
+                }
             }
+        }
+        const float v = du[j * BV + my_col];
+        const float2 bs = sc[j];
         // sums over the 16 row groups (lane bits 4 .. 1), scattered: value 2 c + s of column c
         float f[NV];
 #pragma unroll
@@ -336,30 +426,66 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
             const bool upper = (lane & m) != 0;
 #pragma unroll
             for (int x = 0; x < cnt / 2; ++x) {
-                const float send = upper ? f[x] : f[x + cnt / 2], keep = upper ? f[x + cnt / 2] : f[x];
-                f[x] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                const float send = upper ? f[x] : f[x + cnt / 2], keep_f = upper ? f[x + cnt / 2] : f[x];
+                f[x] = keep_f + __shfl_xor_sync(0xffffffffu, send, m);
             }
         }
         if constexpr (VEC == 4) f[0] += __shfl_xor_sync(0xffffffffu, f[0], 2);
         const float other = __shfl_xor_sync(0xffffffffu, f[0], 1 << SB);
         const float u = second ? other : f[0], pq = second ? f[0] : other;
-        const float2 bs = sc[j];
-        const float delta = bs.x * (v_now - u);
-        if (!second && (VEC == 8 || (lane & 2) == 0)) du[j * BV + warp * CW + (lane & 1) * VEC + vc] = delta;
-        if (second && live_col && (VEC == 8 || (lane & 2) == 0))
-            p.o[((int64_t)(tb + j) * p.hv + h) * p.v + my_col] = fmaf(bs.y, delta, pq) * p.inv_sqrt_k;
+        const float delta = bs.x * (v - u);
+        __syncwarp();       // v is read
+        if (!second && first_of) du[j * BV + my_col] = delta;
+        if (second && live_col) p.o[((int64_t)(tb + j) * p.hv + h) * p.v + cb * BV + my_col] = fmaf(bs.y, delta, pq) * p.inv_sqrt_k;
         __syncwarp();
         float2 d[P2];
-#pragma unroll
-        for (int x = 0; x < P2; ++x) d[x] = *reinterpret_cast<const float2*>(du + j * BV + warp * CW + (lane & 1) * VEC + 2 * x);
+        deltas(j, d);
         const int32_t snap = snaps[j];
         ST* to = pool + state_at(p, snap, h) + tile;
+        if (keep) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < 8; ++r) {
 #pragma unroll
-            for (int x = 0; x < P2; ++x) S[r][x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], S[r][x]);
-            if (snap >= 0 && mine && r0 + r < p.k) *reinterpret_cast<uint4*>(to + (int64_t)r * p.v) = SV::narrow2(S[r]);
+                for (int x = 0; x < P2; ++x) S[r][x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], __fmul2_rn(S[r][x], make_float2(a[r], a[r])));
+                if (snap >= 0 && live[r >> 2]) *reinterpret_cast<uint4*>(to + at_row(r)) = SV::narrow2(S[r]);
+            }
+        } else if (snap >= 0) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float2 out[P2];
+#pragma unroll
+                for (int x = 0; x < P2; ++x) out[x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], __fmul2_rn(S[r][x], make_float2(a[r], a[r])));
+                if (live[r >> 2]) *reinterpret_cast<uint4*>(to + at_row(r)) = SV::narrow2(out);
+            }
         }
+    };
+    // ---- depth first ----
+    unsigned long long todo, leaves, kids;      // kids: of the token whose state S is (at first the context)
+    {
+        const bool in0 = lane < T, in1 = lane + 32 < T;
+        auto both = [&](bool b0, bool b1) {
+            return __ballot_sync(0xffffffffu, b0) | (unsigned long long)__ballot_sync(0xffffffffu, b1) << 32;
+        };
+        todo = both(in0, in1);
+        leaves = both(in0 && child[lane] == 0, in1 && child[lane + 32] == 0);
+        kids = both(in0 && masks[lane] == 0, in1 && masks[lane + 32] == 0);
+    }
+    while (todo != 0) {
+        kids &= todo;
+        if (kids == 0) {
+            // another branch: the lowest token left, whose parent is done
+            const int j = __ffsll((long long)todo) - 1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) SV::widen2(stash[i * blockDim.x + tid], S[i]);
+            const unsigned long long above = masks[j];
+            for (unsigned long long m = above; m != 0; m &= m - 1) again(__ffsll((long long)m) - 1);
+            kids = above != 0 ? child[tree_top(above)] & todo : 1ull << j;
+        }
+        const unsigned long long ends = kids & leaves;
+        const int j = __ffsll((long long)(ends != 0 ? ends : kids)) - 1;
+        step(j, ends == 0);
+        todo &= ~(1ull << j);
+        if (ends == 0) kids = child[j];
     }
 }
 

@@ -50,10 +50,28 @@ int launch_tree(const kda::StepParams& prm, const uint64_t* tree, uint32_t flags
     return cudaLaunchKernelEx(&cfg, kernel, prm, tree) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
+template <typename ET, int VC, int KWM>
+int launch_conv_width(cudaLaunchConfig_t& cfg, const kda::ConvParams& prm, const uint64_t* tree) {
+    auto kernel = kda::kda_conv_tree_kernel<ET, VC, KWM>;
+    using SM = kda::ConvTreeSmem<ET, VC>;
+    int occ = 0, sms = 0;   // raises the kernel's limit to the most that any call takes
+    const int rc = occupancy(reinterpret_cast<const void*>(kernel), (int)cfg.blockDim.x, SM::bytes(kda::TREE_MAX), &occ, &sms);
+    if (rc != KDA_OK) return rc;
+    cfg.dynamicSmemBytes = SM::bytes(prm.t);
+    return cudaLaunchKernelEx(&cfg, kernel, prm, tree) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
 template <typename ET, int VC>
-cudaError_t launch_conv(const cudaLaunchConfig_t& cfg, const kda::ConvParams& prm, const uint64_t* tree, int chunk) {
-    return prm.KW <= 4 ? cudaLaunchKernelEx(&cfg, kda::kda_conv_tree_kernel<ET, VC, 4>, prm, tree, chunk)
-                       : cudaLaunchKernelEx(&cfg, kda::kda_conv_tree_kernel<ET, VC, 8>, prm, tree, chunk);
+int launch_conv(const kda::ConvParams& prm, const uint64_t* tree, uint32_t flags, cudaStream_t stream) {
+    const int64_t grid = (int64_t)((prm.C / VC + kda::CONV_TREE_CH - 1) / kda::CONV_TREE_CH) * prm.n;
+    if (grid > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(kda::CONV_TREE_CH * kda::CONV_TREE_GROUPS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    set_pdl(cfg, &attr, flags);
+    return prm.KW <= 4 ? launch_conv_width<ET, VC, 4>(cfg, prm, tree) : launch_conv_width<ET, VC, 8>(cfg, prm, tree);
 }
 
 template <typename T>
@@ -148,28 +166,12 @@ int kda_conv_step_tree(const kda_conv_window* win, const kda_conv_args* args, co
     const int ve = 16 / es;
     const bool vec = win->channels % ve == 0 && win->slot_stride % ve == 0 && aligned(win->base, 16) && aligned(g.x, 16) &&
                      aligned(g.y, 16);
-    const int units = vec ? win->channels / ve : win->channels;
-    const int64_t cblocks = (units + kda::CONV_TREE_THREADS - 1) / kda::CONV_TREE_THREADS;
-    // the tokens of a request are shared out over CTAs until there are eight for each SM
-    int chunk = g.max_t;
-    while (chunk > 1 && cblocks * g.n * ((g.max_t + chunk - 1) / chunk) < 8 * kSms) chunk = (chunk + 1) / 2;
-    const int64_t grid = cblocks * g.n * ((g.max_t + chunk - 1) / chunk);
-    if (grid > 0x7fffffffLL) return KDA_ERR_SHAPE;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3(kda::CONV_TREE_THREADS, 1, 1);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr;
-    set_pdl(cfg, &attr, flags);
-    cudaError_t err;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (win->dtype) {
-        case KDA_F32: err = vec ? launch_conv<float, 4>(cfg, prm, tree, chunk) : launch_conv<float, 1>(cfg, prm, tree, chunk); break;
-        case KDA_F16: err = vec ? launch_conv<__half, 8>(cfg, prm, tree, chunk) : launch_conv<__half, 1>(cfg, prm, tree, chunk); break;
-        default:
-            err = vec ? launch_conv<__nv_bfloat16, 8>(cfg, prm, tree, chunk) : launch_conv<__nv_bfloat16, 1>(cfg, prm, tree, chunk);
-            break;
+        case KDA_F32: return vec ? launch_conv<float, 4>(prm, tree, flags, st) : launch_conv<float, 1>(prm, tree, flags, st);
+        case KDA_F16: return vec ? launch_conv<__half, 8>(prm, tree, flags, st) : launch_conv<__half, 1>(prm, tree, flags, st);
+        default: return vec ? launch_conv<__nv_bfloat16, 8>(prm, tree, flags, st) : launch_conv<__nv_bfloat16, 1>(prm, tree, flags, st);
     }
-    return err == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 int kda_accept(const kda_accept_args* args, int32_t* dev_status, uint32_t flags, void* stream) {

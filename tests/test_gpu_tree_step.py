@@ -283,3 +283,15 @@ def test_conv_step_tree_chain_has_the_bits_of_kda_conv_step(libs, width, channel
     libs[F32].kda_conv_step_tree(window, slots, x, w, tree, y, st, bias=b, cu_seqlens=offsets(lens), max_t=7, accepted=acc)
     libs[F32].kda_conv_step(window.clone(), slots, x, w, y2, st, bias=b, cu_seqlens=offsets(lens), max_t=7, accepted=acc)
     assert st.item() == 0 and torch.equal(y, y2)
+
+
+def test_conv_step_tree_far_preactivations(libs):
+    """SiLU from -200 to 200, infinities and NaN: the values of kda_conv_step."""
+    x = torch.cat((torch.linspace(-200, 200, 4001), torch.tensor([-88.8, -87.4, 88.0, 1e-40, -1e-40, 0.0, float("inf"), float("-inf"), float("nan")])))
+    x = x[: len(x) // 2 * 2].view(2, -1).repeat(2, 4)[:, :8016].contiguous().cuda()
+    w, y, y2, st = torch.ones(x.shape[1], 1, device="cuda"), torch.zeros_like(x), torch.zeros_like(x), ints([0])
+    window = torch.zeros(4, 1, x.shape[1], device="cuda")
+    slots = ints([0, 1, 2, 3])
+    libs[F32].kda_conv_step_tree(window, slots, x, w, torch.ones(4, dtype=torch.int64, device="cuda"), y, st)
+    libs[F32].kda_conv_step(window, slots, x, w, y2, st)
+    assert st.item() == 0 and torch.equal(y.view(torch.int32)[~y.isnan()], y2.view(torch.int32)[~y2.isnan()]) and torch.equal(y.isnan(), y2.isnan())
