@@ -873,8 +873,11 @@ int kda_conv_step_tree(const kda_conv_window* win, const kda_conv_args* args, co
  * positions before its own, ctx_len[r] + depth.  ctx_len[r] >= 0, or
  * ctx_len[r] <= -T_r for padding (KDA_ERR_ARG on the device else, that
  * request's rows zero).  Otherwise args and checks as for the calls without a
- * tree, max_t <= KDA_TREE_MAX_TOKENS.
+ * tree, max_t <= KDA_TREE_MAX_TOKENS, workspace_bytes >=
+ * KDA_KV4_TREE_WORKSPACE_BYTES (zeroed once; it may serve kda_kv4_attend too).
+ * kda_kv4_attend_tree enqueues one kernel, or two in a row.
  */
+#define KDA_KV4_TREE_WORKSPACE_BYTES (64 << 20)
 int kda_kv4_append_tree(const kda_kv4_cache* cache, const kda_kv4_append_args* args, const uint64_t* tree, int32_t* dev_status,
                         uint32_t flags, void* stream);
 int kda_kv4_attend_tree(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, const uint64_t* tree, int32_t* dev_status,

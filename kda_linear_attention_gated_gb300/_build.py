@@ -24,7 +24,7 @@ LIB_DIR = os.path.join(PKG_DIR, "lib")
 SOURCES = [os.path.join(CSRC, f) for f in ("kda_api.cu", "kda_common.cuh", "kda_decode_tma.cuh",
                                           "kda_verify_tma.cuh", "kda_conv.cuh", "kda_ckpt.cuh",
                                           "kda_prefill_chunk.cuh", "kda_stage.cuh", "kda_host.cuh",
-                                          "kda_layer_api.cu", "kda_kv4.cuh", "kda_norm.cuh",
+                                          "kda_layer_api.cu", "kda_kv4.cuh", "kda_kv4_tree.cuh", "kda_norm.cuh",
                                           "kda_tree_api.cu", "kda_tree.cuh", "kda_accept.cuh")] + [os.path.join(INCLUDE, "kda.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

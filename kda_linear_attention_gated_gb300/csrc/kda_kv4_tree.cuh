@@ -1,0 +1,781 @@
+// Attention of wide trees of drafted tokens over the 4-bit cache: many query
+// rows of a key/value head, on the 5th-generation tensor cores.  The format, the
+// scores' units and the softmax's constants are those of kda_kv4.cuh.
+#pragma once
+
+#include "kda_kv4.cuh"
+
+namespace kda {
+
+// ---------------------------------------------------------------------------
+// tcgen05
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Everything issued so far, done: one arrival on `bar`.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// d (fp32 in tensor memory) = a b, or += with `more`; fp16 operands in shared memory, 16 deep.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool more) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)more) : "memory");
+}
+// 32 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&x)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+}
+// 16 columns, out and back.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&x)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&x)[16]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n\t"
+        "tcgen05.wait::st.sync.aligned;"
+        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+          "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr) : "memory");
+}
+// Descriptor of a tile of 128-byte rows in shared memory, 16-byte pieces at
+// their place xor (row % 8) (the 128-byte swizzle), groups of eight rows 1024
+// bytes apart.  `lead`: bytes between 64-element stretches of the other
+// dimension, for operands whose rows run along it.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+// fp16 operands, fp32 sums; B_ROWS: b's rows run along N (else along K).
+__host__ __device__ constexpr uint32_t tc_idesc(int m, int n, bool b_rows) {
+    return 1u << 4 | (b_rows ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (uint32_t)(m / 16) << 24;
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+constexpr int KVT_ROWS = 128;            // query rows of a tile: the tensor cores' M
+constexpr int KVT_KEYS = 64;             // keys of a unit of work: four blocks
+constexpr int KVT_THREADS = 256, KVT_WARPS = KVT_THREADS / 32;
+constexpr int KVT_STAGES = 2;            // units of codes in flight
+constexpr int KVT_PART = 6;              // what beginning and ending a part costs a CTA, in units
+constexpr int KVT_FIRST = KVT_PART + 2, KVT_LAST = 2;   // what a cut leaves before and after it in a tile (see Kv4Shape)
+constexpr int KVT_MAX_CTAS = 304;        // two for each of 152 SMs
+constexpr int KVT_MIN_ROWS = 32;         // narrower trees go to kda_kv4_attend_kernel
+constexpr int KVT_JOIN_GROUPS = 16;      // CTAs that join a tile
+constexpr int KVT_COUNTERS = 4096;       // bytes at the head of the workspace that kda_kv4_attend_kernel's counters take
+constexpr int KVT_TMEM = 256;            // columns: scores and sums; two CTAs an SM share 512
+
+template <int D, bool SPLIT> struct KvtSmem {
+    static constexpr int SLABS = D / 64;                         // 64-channel stretches, 128 bytes a row
+    static constexpr int Q = SLABS * KVT_ROWS * 128, K = SLABS * KVT_KEYS * 128, P = KVT_ROWS * 128;
+    static constexpr int STAGE = 4 * Kv4<D>::BLOCK;
+    static constexpr int OFF_Q = 0, OFF_K = OFF_Q + Q * (SPLIT ? 2 : 1), OFF_V = OFF_K + K, OFF_P = OFF_V + K,
+                         OFF_RAW = OFF_P + P * (SPLIT ? 2 : 1), OFF_ROWF = OFF_RAW + KVT_STAGES * STAGE,
+                         OFF_MAX = OFF_ROWF + KVT_ROWS * 4,      // [2][128] halves' maxima, then sums
+                         OFF_NAN = OFF_MAX + 2 * KVT_ROWS * 4,   // [D / 16] tokens of the unit whose value group is NaN
+                         OFF_BAR = OFF_NAN + 8 * 8,              // raw [stages], scores, sums
+                         OFF_MISC = OFF_BAR + 8 * 8,             // tensor memory base, blocks not there [stages]
+                         OFF_WALK = OFF_MISC + 32, BYTES = OFF_WALK + 2 * 128 + 1024;   // and 1024 to align
+};
+
+// One request's part of the work (see Kv4Req), units of 64 keys.
+__device__ __forceinline__ Kv4Req kvt_request(const Kv4AttendParams& p, int r) {
+    Kv4Req q;
+    q.err = 0;
+    q.tok0 = p.cu ? __ldg(p.cu + r) : r * p.max_t;
+    q.t = (p.cu ? __ldg(p.cu + r + 1) : q.tok0 + p.max_t) - q.tok0;
+    q.ctx = __ldg(p.ctx + r);
+    q.first = q.units = 0;
+    if (q.tok0 < 0 || q.t < 0 || q.t > p.max_t || (int64_t)q.tok0 + q.t > p.total) {
+        q.err = STATUS_ARG;
+        q.tok0 = q.t = 0;
+    }
+    q.tiles = (q.t * p.grp + KVT_ROWS - 1) / KVT_ROWS;
+    const int64_t end = (int64_t)q.ctx + q.t;
+    if (q.t > 0 && end > 0) {
+        if (end > (int64_t)p.cols * p.page_tokens || (p.rot && end > p.rope_rows) || q.ctx < 0) {
+            q.err = STATUS_ARG;
+        } else {
+            if (p.window > 0) q.first = max(0, q.ctx - p.window + 1) / KVT_KEYS;
+            q.units = (int)((end + KVT_KEYS - 1) / KVT_KEYS) - q.first;
+        }
+    }
+    return q;
+}
+__device__ __forceinline__ int64_t kvt_cost(const Kv4Req& q, int heads) {
+    return q.units > 0 ? (int64_t)(q.units + KVT_PART) * q.tiles * heads : 0;
+}
+
+// The list of all (request, head, row tile, unit), cut evenly: CTA c's share
+// begins at cut c, moved to a tile's end where too little of the tile would be
+// left on one side (as in kda_kv4_attend_kernel).
+__device__ __forceinline__ int64_t kvt_even(int64_t total, int ctas) {
+    return max((int64_t)(KVT_FIRST + KVT_LAST), (total + ctas - 1) / ctas);
+}
+
+// A CTA's share: thread 0 walks it, from part to part.
+struct KvtWalk {
+    int64_t at, end;     // in the list: the next place, the share's end
+    int64_t r0;          // where request r begins
+    int64_t s0;          // and the current tile
+    int r, h, i0, b0, b1;
+    Kv4Req q;
+    __device__ __forceinline__ bool next(const Kv4AttendParams& p) {
+        for (;;) {
+            if (at >= end) return false;
+            while (at >= r0 + kvt_cost(q, p.heads)) {
+                r0 += kvt_cost(q, p.heads);
+                if (++r >= p.n) return false;
+                q = kvt_request(p, r);
+            }
+            const int each = q.units + KVT_PART;
+            const int64_t off = at - r0;
+            const int seg = (int)(off / each), u = (int)(off - (int64_t)seg * each);
+            h = seg / q.tiles;
+            i0 = (seg - h * q.tiles) * KVT_ROWS;
+            s0 = at - u;
+            const int take = (int)min((int64_t)(each - u), end - at);
+            b0 = max(0, u - KVT_PART);
+            b1 = max(0, u + take - KVT_PART);
+            at += take;
+            if (b0 < b1) return true;
+        }
+    }
+};
+
+// Where cut c falls (moved as above), by a warp: lanes share the requests.
+// `walk` (of the lane that finds it): the request there.
+__device__ __forceinline__ int64_t kvt_cut(const Kv4AttendParams& p, int64_t even, int64_t total, int c, int lane, KvtWalk* walk) {
+    const int64_t cut = even * c;
+    if (cut >= total) return total;
+    int64_t begin = 0;
+    for (int base = 0; base < p.n; base += 32) {
+        Kv4Req q = {};
+        if (base + lane < p.n) q = kvt_request(p, base + lane);
+        const int64_t mine = kvt_cost(q, p.heads);
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += up;
+        }
+        upto += begin;
+        const uint32_t who = __ballot_sync(0xffffffffu, cut < upto);
+        if (who != 0) {
+            const int l = __ffs(who) - 1;
+            int64_t moved = cut;
+            if (lane == l) {
+                const int each = q.units + KVT_PART, u = (int)((cut - (upto - mine)) % each);
+                moved += u < KVT_FIRST ? -u : each - u < KVT_LAST ? each - u : 0;
+                if (walk != nullptr) {
+                    walk->r = base + l;
+                    walk->r0 = upto - mine;
+                    walk->q = q;
+                }
+            }
+            return __shfl_sync(0xffffffffu, moved, l);
+        }
+        begin = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return total;
+}
+
+// What CTA c leaves for the join at the head of the workspace: the tile that its
+// share begins inside, if it is the second of the CTAs that share it.
+struct KvtJoin {
+    int32_t last;        // the last CTA of the tile; 0: nothing to join here
+    int32_t row0, rows;  // the tile's rows: query head h * grp + i % grp of token tok0 + i / grp, i from row0 on
+    int32_t tok0, h, pad[3];
+};
+static_assert(sizeof(KvtJoin) == 32, "workspace");
+constexpr int KVT_HEAD = 16384;          // bytes of the workspace before the partial sums
+static_assert(KVT_MAX_CTAS * sizeof(KvtJoin) <= KVT_HEAD, "workspace");
+
+// Partial sums of a part: [rows][D] sums, [rows] (maximum, sum).
+template <int D> struct KvtPart {
+    static constexpr int FLOATS = KVT_ROWS * (D + 2);
+};
+
+// S = Q K^T and O += P V on the tensor cores (M 128 query rows of a key/value
+// head, fp16 operands, fp32 sums in tensor memory), one pass with a running
+// maximum and sum.  Codes times scales are exact in fp16; queries are scaled by a
+// power of two a row and rounded as in kda_kv4_attend_kernel, SPLIT: with their
+// remainders, and probabilities with theirs, as second operands into the same
+// sums.
+//
+// A unit of 64 keys: all threads write K's values to shared memory in the
+// tensor cores' layout; while they take the scores, all write V's; two threads a
+// row then take its scores to probabilities, to shared memory again; while the
+// tensor cores add P V, the next unit's keys are on.  The other CTA of the SM
+// fills what one leaves idle.  V is used as it lies, keys by channels (its rows
+// run along N).
+//
+// Parts of a (request, head, tile) that several CTAs share go to the
+// workspace, and kda_kv4_tree_join_kernel adds them in order.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(KVT_THREADS, SPLIT && D == 128 ? 1 : 2) kda_kv4_tree_kernel(const Kv4AttendParams p) {
+    using F = Kv4<D>;
+    using SM = KvtSmem<D, SPLIT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t *Q = smem + SM::OFF_Q, *K = smem + SM::OFF_K, *V = smem + SM::OFF_V, *P = smem + SM::OFF_P, *raw = smem + SM::OFF_RAW;
+    float* rowf = reinterpret_cast<float*>(smem + SM::OFF_ROWF);
+    float* half_max = reinterpret_cast<float*>(smem + SM::OFF_MAX);
+    unsigned long long* nan_tok = reinterpret_cast<unsigned long long*>(smem + SM::OFF_NAN);
+    uint64_t *bar_raw = reinterpret_cast<uint64_t*>(smem + SM::OFF_BAR), *bar_s = bar_raw + KVT_STAGES, *bar_o = bar_s + 1;
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + SM::OFF_MISC);
+    volatile uint32_t* missing = misc + 1;      // [stages] blocks of a unit that are not there
+    KvtWalk& walk = *reinterpret_cast<KvtWalk*>(smem + SM::OFF_WALK);
+    volatile int *have_s = reinterpret_cast<int*>(misc + 4), *nan_any = have_s + 1;
+    static_assert(sizeof(KvtWalk) <= 128, "KvtSmem::OFF_WALK");
+
+    if (tid == 0) {
+        for (int i = 0; i < KVT_STAGES + 2; ++i) mbar_init(bar_raw + i, 1);
+        fence_mbar_init();
+    }
+    if (tid < 8) nan_tok[tid] = 0;
+    if (tid == 0) *nan_any = 0;
+    if (warp == 1) tmem_alloc(misc, KVT_TMEM);
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+
+    // ---- this CTA's share ----
+    if (warp == 0) {
+        int64_t total = 0;
+        bool empty = false;
+        for (int r = lane; r < p.n; r += 32) {
+            const Kv4Req q = kvt_request(p, r);
+            total += kvt_cost(q, p.heads);
+            if (q.err && blockIdx.x == 0) atomicCAS(p.status, 0, q.err);
+            empty |= q.t > 0 && q.units == 0;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        empty = __any_sync(0xffffffffu, empty);
+        const int64_t even = kvt_even(total, gridDim.x);
+        const int64_t c0 = kvt_cut(p, even, total, blockIdx.x, lane, &walk), c1 = kvt_cut(p, even, total, blockIdx.x + 1, lane, nullptr);
+        __syncwarp();
+        if (lane == 0) {
+            walk.at = c0;
+            walk.end = c1;
+            const bool ok = c0 < c1 && walk.next(p);
+            *have_s = (int)ok | (int)empty << 1;
+            KvtJoin j = {};
+            if (ok && walk.b0 > 0) {     // the CTAs of a tile: those between the cuts that stayed inside it
+                const int first = (int)((walk.s0 + KVT_FIRST + even - 1) / even) - 1;
+                if (first + 1 == (int)blockIdx.x) {
+                    j.last = (int)((walk.s0 + walk.q.units + KVT_PART - KVT_LAST) / even);
+                    j.row0 = walk.i0;
+                    j.rows = min(KVT_ROWS, walk.q.t * p.grp - walk.i0);
+                    j.tok0 = walk.q.tok0;
+                    j.h = walk.h;
+                }
+            }
+            reinterpret_cast<KvtJoin*>(p.counters)[blockIdx.x] = j;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0], tm_s = tmem, tm_o = tmem + KVT_KEYS;
+    bool have = *have_s & 1;
+    if (*have_s & 2) {   // requests without a visible key: zero rows
+        for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
+            const Kv4Req q = kvt_request(p, r);
+            if (q.units > 0) continue;
+            const int64_t base = (int64_t)q.tok0 * p.h_q * D;
+            for (int64_t i = tid * 4; i < (int64_t)q.t * p.h_q * D; i += KVT_THREADS * 4) st_elem4(p.o, base + i, p.dtype, 0.f, 0.f, 0.f, 0.f);
+        }
+    }
+
+    const int bpp = p.page_tokens >> 4;
+    uint32_t phases = 0;                // bits: raw stages, then scores, then sums
+    auto phase = [&](int i) { return phases >> i & 1u; };
+    bool alive = true;
+    // this thread's row of a tile (a lane of tensor memory) and half of a unit's keys
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t aQ = smem_u32(Q), aK = smem_u32(K), aV = smem_u32(V), aP = smem_u32(P);
+
+    while (have) {
+        const Kv4Req& req = walk.q;        // read from shared memory where it is needed
+        const int &r = walk.r, &h = walk.h, &i0 = walk.i0, &b0 = walk.b0, &b1 = walk.b1;
+        const int rows = min(KVT_ROWS, req.t * p.grp - i0);
+        // Fetches a unit's blocks: warp 0, lanes 0 .. 3 a block each.
+        auto fetch = [&](int b) {
+            const int st = (b - b0) % KVT_STAGES;
+            bool ok = false;
+            const uint8_t* from = nullptr;
+            const int blk = (req.first + b) * 4 + lane;
+            if (lane < 4 && blk * 16 < req.ctx + req.t && (p.window <= 0 || req.ctx - p.window + 1 < (blk + 1) * 16)) {
+                const int pg = blk / bpp, page = __ldg(p.table + (int64_t)r * p.cols + pg);
+                ok = page >= 0 && page < p.num_pages;
+                if (!ok) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
+                from = p.pages + (int64_t)page * p.page_stride + ((int64_t)h * bpp + (blk - pg * bpp)) * F::BLOCK;
+            }
+            const uint32_t there = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0) {
+                missing[st] = there ^ 15u;
+                if (there != 0) mbar_arrive_expect_tx(bar_raw + st, __popc(there) * F::BLOCK);
+                else mbar_arrive(bar_raw + st);
+            }
+            __syncwarp();
+            if (ok && !p.withhold) bulk_load(raw + st * SM::STAGE + lane * F::BLOCK, from, F::BLOCK, bar_raw + st);
+        };
+        if (warp == 0 && alive) {
+            for (int b = b0; b < min(b1, b0 + KVT_STAGES); ++b) fetch(b);
+        }
+        // ---- queries: rotated, scaled to below 1 by a power of two, rounded; a warp a row ----
+        {
+            constexpr int E = D / 32;
+            const int d = lane * E, hr = p.rot >> 1;
+            const bool first = d < hr;
+#pragma unroll 2
+            for (int k = 0; k < KVT_ROWS / KVT_WARPS; ++k) {
+                const int i = warp + k * KVT_WARPS;
+                float x[E] = {}, y[E] = {}, cs[E], sn[E] = {};
+#pragma unroll
+                for (int e = 0; e < E; ++e) cs[e] = 1.f;
+                if (i < rows) {
+                    const int j = (i0 + i) / p.grp;
+                    const int pos = req.ctx + __popcll(tree_mask(p.tree, req.tok0 + j, j)) - 1;
+                    const int64_t base = (int64_t)(req.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + i0 + i - j * p.grp) * D;
+                    ld_elems<E>(p.q, base + d, p.dtype, x);
+                    if (d < p.rot) {
+                        const int64_t at = (int64_t)pos * hr;
+                        if (p.inter) {
+                            ld_elems<E / 2>(p.cos, at + d / 2, 0, cs);
+                            ld_elems<E / 2>(p.sin, at + d / 2, 0, sn);
+#pragma unroll
+                            for (int e = E / 2 - 1; e >= 0; --e) {
+                                const float a = x[2 * e], b = x[2 * e + 1];
+                                x[2 * e] = a * cs[e] - b * sn[e];
+                                x[2 * e + 1] = b * cs[e] + a * sn[e];
+                            }
+                        } else {
+                            ld_elems<E>(p.q, base + (first ? d + hr : d - hr), p.dtype, y);
+                            ld_elems<E>(p.cos, at + (first ? d : d - hr), 0, cs);
+                            ld_elems<E>(p.sin, at + (first ? d : d - hr), 0, sn);
+#pragma unroll
+                            for (int e = 0; e < E; ++e) x[e] = x[e] * cs[e] + (first ? -y[e] : y[e]) * sn[e];
+                        }
+                    }
+                }
+                float amax = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                // as in kda_kv4_attend_kernel
+                const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
+                const float down =
+                    __uint_as_float(amax < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
+                uint8_t* to = Q + (d / 64) * (KVT_ROWS * 128) + i * 128 + (((d % 64 / 8) ^ (i & 7)) << 4) + d % 8 * 2;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float u = x[e] * down, v = x[e + 1] * down;
+                    const __half2 hi = __floats2half2_rn(u, v);
+                    *reinterpret_cast<__half2*>(to + e * 2) = hi;
+                    if constexpr (SPLIT) {
+                        const float2 f = __half22float2(hi);
+                        *reinterpret_cast<__half2*>(to + SM::Q + e * 2) = __floats2half2_rn(u - f.x, v - f.y);
+                    }
+                }
+                if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
+            }
+        }
+        // ---- what this thread's row sees of the tree and of the context ----
+        uint64_t own = 0;
+        int low = 0x7fffffff;
+        if (row < rows) {
+            const int j = (i0 + row) / p.grp;
+            own = tree_mask(p.tree, req.tok0 + j, j);
+            low = p.window > 0 ? req.ctx + __popcll(own) - p.window : 0;
+            if (p.window > 0)
+                for (int more = __popcll(own) - p.window; more > 0; --more) own &= own - 1;
+        }
+        auto sees = [&](int key) {
+            const int at = key - req.ctx;
+            return at < 0 ? key >= low : at < TREE_MAX && (own >> at & 1u) != 0;
+        };
+        // keys that every row sees: [see0, ctx)
+        const int see0 = p.window > 0 ? req.ctx + req.t - p.window : 0;
+        float m = -FLT_MAX, l = 0.f;
+        uint32_t nan_groups = 0;        // value groups in which this row has seen a NaN
+        bool pending = false;           // P V not waited for
+
+        for (int b = b0; b < b1; ++b) {
+            const int st = (b - b0) % KVT_STAGES, key0 = (req.first + b) * KVT_KEYS;
+            const uint8_t* R = raw + st * SM::STAGE;
+            bool ok = mbar_wait(bar_raw + st, phase(st));
+            if (ok) phases ^= 1u << st;
+            const uint32_t miss = missing[st];
+            const bool masked = key0 + KVT_KEYS > req.ctx || key0 < see0 || miss != 0;
+            // ---- keys: a token's quarter (half) a thread ----
+            if (ok) {
+                const int key = tid >> 2, q = tid & 3;
+                const uint8_t* B = R + (key >> 4) * F::BLOCK;
+                const bool gone = miss >> (key >> 4) & 1u;
+                if constexpr (D == 128) {
+                    uint4 c = *reinterpret_cast<const uint4*>(B + F::KC + (key & 15) * 64 + q * 16);
+                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::KS + (key & 15) * 8 + 2 * q);
+                    if (gone) s2 = 0;
+                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                    uint8_t* to = K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t v[4];
+                        cvt_e2m1x8_f16(w[i], v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
+                        *reinterpret_cast<uint4*>(to + ((((q & 1) * 4 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                } else {
+                    const uint2 c = *reinterpret_cast<const uint2*>(B + F::KC + (key & 15) * 32 + q * 8);
+                    uint32_t s2 = B[F::KS + (key & 15) * 4 + q];
+                    if (gone) s2 = 0;
+                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t v[4];
+                        cvt_e2m1x8_f16(w[i], v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = hmul2_half<false>(v[e], sc);
+                        *reinterpret_cast<uint4*>(K + key * 128 + (((q * 2 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            alive = __syncthreads_and(ok);      // also: every row's queries and factors are written
+            if (!alive) break;
+            if (tid == 0) {
+                tc_fence_after();
+                constexpr uint32_t idesc = tc_idesc(KVT_ROWS, KVT_KEYS, false);
+#pragma unroll
+                for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma(tm_s, tc_desc(aQ + part * SM::Q + k / 4 * (KVT_ROWS * 128) + k % 4 * 32, 16),
+                               tc_desc(aK + k / 4 * (KVT_KEYS * 128) + k % 4 * 32, 16), idesc, part + k > 0);
+                tc_commit(bar_s);
+            }
+            // ---- values, when the last unit's are done with: two tokens' groups of 16 a thread ----
+            if (pending) {
+                ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
+                if (ok) phases ^= 1u << (KVT_STAGES + 1);
+                pending = false;
+            }
+            if (ok) {
+                if constexpr (D == 128) {
+                    const int bk = tid >> 6, hf2 = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
+                    const uint8_t* B = R + bk * F::BLOCK;
+                    const uint4 c = *reinterpret_cast<const uint4*>(B + F::VC + hf2 * 512 + lane * 16);
+                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::VS + lane * 4 + hf2 * 2);
+                    const int key = bk * 16 + hf2 * 8 + 2 * tp;
+                    if (masked) {
+                        // tokens behind the end hold anything, and 0 * NaN is NaN: their scales become 0, and so do NaN
+                        // ones, whose groups of the rows that see them are then set by hand (a rare path)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const bool out = (miss >> bk & 1u) || key0 + key + e >= req.ctx + req.t, nan = (s2 >> (8 * e) & 0x7fu) == 0x7fu;
+                            if (nan && !out) {
+                                *nan_any = 1;
+                                atomicOr(nan_tok + g, 1ull << (key + e));
+                            }
+                            if (nan || out) s2 &= ~(0xffu << (8 * e));
+                        }
+                    }
+                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                    uint8_t* to = V + (g >> 2) * (KVT_KEYS * 128);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int ch = (g & 3) * 2 + (i & 1), kk = key + (i >> 1);
+                        uint32_t v[4];
+                        cvt_e2m1x8_f16(w[i], v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
+                        *reinterpret_cast<uint4*>(to + kk * 128 + ((ch ^ (kk & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                } else {
+                    // 16 tokens of 64 channels: (half, group eighth, pair) pieces of 8 bytes, a token's 8 channels 4 bytes
+                    const int bk = tid >> 6, hf2 = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
+                    const uint8_t* B = R + bk * F::BLOCK;
+                    const uint2 c = *reinterpret_cast<const uint2*>(B + F::VC + hf2 * 256 + lane * 8);
+                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::VS + ((g >> 1) * 4 + tp) * 4 + hf2 * 2);
+                    const int key = bk * 16 + hf2 * 8 + 2 * tp;
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const bool out = (miss >> bk & 1u) || key0 + key + e >= req.ctx + req.t, nan = (s2 >> (8 * e) & 0x7fu) == 0x7fu;
+                            if (nan && !out) {
+                                *nan_any = 1;
+                                atomicOr(nan_tok + (g >> 1), 1ull << (key + e));
+                            }
+                            if (nan || out) s2 &= ~(0xffu << (8 * e));
+                        }
+                    }
+                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int kk = key + i;
+                        uint32_t v[4];
+                        cvt_e2m1x8_f16(w[i], v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = i < 1 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
+                        *reinterpret_cast<uint4*>(V + kk * 128 + ((g ^ (kk & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            // ---- scores to probabilities ----
+            // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(bar_s, phase(KVT_STAGES)));
+            if (ok) phases ^= 1u << KVT_STAGES;
+            tc_fence_after();
+            float s[32], top = -INFINITY;
+            if (ok) {
+                tmem_ld32(tm_s + lane_base + 32 * half, s);
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int at = 32 * half + i;
+                        if (!sees(key0 + at) || (miss >> (at >> 4) & 1u)) s[i] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i]);
+            }
+            half_max[half * KVT_ROWS + row] = top;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+            if (ok) {
+                const float c = rowf[row];
+                top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]) * c;
+                const bool grow = top > m + KV4_SLACK;
+                if (__any_sync(0xffffffffu, grow)) {        // both warps alike: the same rows
+                    const float f = grow ? ex2f(m - top) : 1.f;
+                    if (grow) m = top;
+                    l *= f;
+                    if (b > b0) {
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            const uint32_t at = tm_o + lane_base + half * (D / 2) + 16 * k;
+                            float o[16];
+                            tmem_ld16(at, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= f;
+                            tmem_st16(at, o);
+                        }
+                    }
+                }
+                const float neg = KV4_LIFT - m;
+                uint8_t* to = P + row * 128;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = __ffma2_rn(make_float2(s[i + 2 * e], s[i + 2 * e + 1]), make_float2(c, c), make_float2(neg, neg));
+                        const float x0 = ex2f(x.x), x1 = ex2f(x.y);
+                        l += x0 + x1;
+                        const __half2 hh = __floats2half2_rn(x0, x1);
+                        hi[e] = *reinterpret_cast<const uint32_t*>(&hh);
+                        if constexpr (SPLIT) {
+                            const float2 f = __half22float2(hh);
+                            const __half2 rest = __floats2half2_rn(x0 - f.x, x1 - f.y);
+                            lo[e] = *reinterpret_cast<const uint32_t*>(&rest);
+                        }
+                    }
+                    uint4* at = reinterpret_cast<uint4*>(to + (((half * 4 + i / 8) ^ (row & 7)) << 4));
+                    *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (SPLIT) at[SM::P / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            alive = __syncthreads_and(ok);      // the unit's codes are read, its probabilities written
+            if (!alive) break;
+            if (tid == 0) {
+                tc_fence_after();
+                constexpr uint32_t idesc = tc_idesc(KVT_ROWS, D, true);
+#pragma unroll
+                for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+                    for (int k = 0; k < KVT_KEYS / 16; ++k)
+                        tc_mma(tm_o, tc_desc(aP + part * SM::P + k * 32, 16), tc_desc(aV + k * 2048, KVT_KEYS * 128), idesc,
+                               b > b0 || part + k > 0);
+                tc_commit(bar_o);
+            }
+            pending = true;
+            if (warp == 0 && b + KVT_STAGES < b1) fetch(b + KVT_STAGES);
+            if (*nan_any != 0) {        // a NaN among values that not all rows see
+#pragma unroll 1
+                for (int g = 0; g < D / 16; ++g)
+                    for (unsigned long long t = nan_tok[g]; t != 0; t &= t - 1)
+                        if (sees(key0 + __ffsll((long long)t) - 1)) nan_groups |= 1u << g;
+                __syncthreads();
+                if (tid < 8) nan_tok[tid] = 0;      // the next unit's are set behind the next barrier
+                if (tid == 0) *nan_any = 0;
+            }
+        }
+        // ---- the part's sums ----
+        if (alive && pending) {
+            const bool ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
+            if (ok) phases ^= 1u << (KVT_STAGES + 1);
+            alive = __syncthreads_and(ok);
+        }
+        tc_fence_after();
+        half_max[half * KVT_ROWS + row] = l;
+        __syncthreads();
+        if (alive) {
+            l += half_max[(half ^ 1) * KVT_ROWS + row];
+        } else {                        // a wait ran out: nothing of this part
+            m = -FLT_MAX;
+            l = 0.f;
+        }
+        {
+            const bool whole = b0 == 0 && b1 == req.units;
+            float* part = p.partials + (int64_t)(2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * KvtPart<D>::FLOATS;
+            const int j = (i0 + row) / p.grp;
+            const int64_t out = ((int64_t)(req.tok0 + j) * p.h_q + h * p.grp + (i0 + row) - j * p.grp) * D;
+            const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                float o[16];
+                const int d0 = half * (D / 2) + 16 * k;
+                tmem_ld16(tm_o + lane_base + d0, o);
+                if (row < rows) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        float4 v = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        if (l == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (nan_groups >> ((d0 + i) >> 4) & 1u) v = make_float4(NAN, NAN, NAN, NAN);
+                        if (whole) st_elem4(p.o, out + d0 + i, p.dtype, v.x * f, v.y * f, v.z * f, v.w * f);
+                        else __stcg(reinterpret_cast<float4*>(part + row * D + d0 + i), v);
+                    }
+                }
+            }
+            if (!whole && half == 0 && row < rows) __stcg(reinterpret_cast<float2*>(part + KVT_ROWS * D) + row, make_float2(m, l));
+        }
+        if (!alive && tid == 0) atomicCAS(p.status, 0, STATUS_TIMEOUT);
+        if (!alive) {
+            // copies and products in flight end (or time out) before their memory is used again; nothing more is begun
+            (void)mbar_wait(bar_raw, phase(0));
+            (void)mbar_wait(bar_raw + 1, phase(1));
+            (void)mbar_wait(bar_s, phase(KVT_STAGES));
+            (void)mbar_wait(bar_o, phase(KVT_STAGES + 1));
+        }
+        tc_fence_before();
+        __syncthreads();                // tensor memory, queries and the walk are free
+        tc_fence_after();
+        if (!alive) break;
+        if (tid == 0) *have_s = walk.next(p);
+        __syncthreads();
+        have = *have_s & 1;
+    }
+    if (!alive && have) {               // the share's other parts: as if they saw no key
+        for (;;) {
+            if (tid == 0) *have_s = walk.next(p);
+            __syncthreads();
+            const bool more = *have_s & 1;
+            if (!more) break;
+            const bool whole = walk.b0 == 0 && walk.b1 == walk.q.units;
+            const int rows = min(KVT_ROWS, walk.q.t * p.grp - walk.i0);
+            float* part = p.partials + (int64_t)(2 * blockIdx.x + (walk.b0 == 0 ? 1 : 0)) * KvtPart<D>::FLOATS;
+            for (int i = tid; i < rows * (D / 4); i += KVT_THREADS) {
+                const int x = walk.i0 + i / (D / 4), j = x / p.grp, d = i % (D / 4) * 4;
+                if (whole) st_elem4(p.o, ((int64_t)(walk.q.tok0 + j) * p.h_q + walk.h * p.grp + x - j * p.grp) * D + d, p.dtype, 0.f, 0.f, 0.f, 0.f);
+                else __stcg(reinterpret_cast<float4*>(part + i / (D / 4) * D + d), make_float4(0.f, 0.f, 0.f, 0.f));
+                if (!whole && d == 0) __stcg(reinterpret_cast<float2*>(part + KVT_ROWS * D) + i / (D / 4), make_float2(-FLT_MAX, 0.f));
+            }
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, KVT_TMEM);
+}
+
+// Joins the parts of the tiles that more than one CTA of kda_kv4_tree_kernel
+// worked on, in order; several CTAs a tile, found by its second CTA there.
+template <int D>
+__global__ void __launch_bounds__(256) kda_kv4_tree_join_kernel(const Kv4AttendParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+    constexpr int GROUPS = KVT_JOIN_GROUPS, each = KVT_ROWS / 8 / GROUPS;     // rows of a warp
+    const int c1 = (int)blockIdx.x / GROUPS + 1, g = (int)blockIdx.x % GROUPS;
+    const KvtJoin j = reinterpret_cast<const KvtJoin*>(p.counters)[c1];
+    if (j.last == 0) return;
+    constexpr int E = D / 32;
+    for (int row = (g * 8 + warp) * each, end = min(j.rows, row + each); row < end; ++row) {
+        float M = -FLT_MAX, L = 0.f, o[E] = {};
+#pragma unroll 4
+        for (int c = c1 - 1; c <= j.last; ++c) {
+            const float* part = p.partials + (int64_t)(2 * c + (c == c1 - 1 ? 1 : 0)) * KvtPart<D>::FLOATS;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + KVT_ROWS * D) + row);
+            float v[E];
+            if constexpr (E == 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(part + row * D) + lane);
+                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+            } else {
+                const float2 f = __ldcg(reinterpret_cast<const float2*>(part + row * D) + lane);
+                v[0] = f.x; v[1] = f.y;
+            }
+            const float top = fmaxf(M, ml.x), a = ex2f(M - top), b = ex2f(ml.x - top);
+            M = top;
+            L = L * a + ml.y * b;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * b;
+        }
+        const int i = j.row0 + row, t = i / p.grp;
+        const int64_t out = ((int64_t)(j.tok0 + t) * p.h_q + j.h * p.grp + i - t * p.grp) * D + lane * E;
+        const float f = L == 0.f ? 0.f : p.v_scale / L;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = L == 0.f ? 0.f : o[e] * f;
+        if constexpr (E == 4) {
+            st_elem4(p.o, out, p.dtype, o[0], o[1], o[2], o[3]);
+        } else if (p.dtype == 0) {
+            *reinterpret_cast<float2*>(static_cast<float*>(p.o) + out) = make_float2(o[0], o[1]);
+        } else if (p.dtype == 1) {
+            *reinterpret_cast<__half2*>(static_cast<__half*>(p.o) + out) = __floats2half2_rn(o[0], o[1]);
+        } else {
+            *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.o) + out) = __floats2bfloat162_rn(o[0], o[1]);
+        }
+    }
+}
+
+}  // namespace kda

@@ -13,6 +13,7 @@
 #include "kda.h"
 #include "kda_host.cuh"
 #include "kda_kv4.cuh"
+#include "kda_kv4_tree.cuh"
 #include "kda_norm.cuh"
 
 namespace {
@@ -71,6 +72,35 @@ int launch_attend(kda::Kv4AttendParams& prm, int64_t list, uint32_t flags, cudaS
     cudaLaunchAttribute attr;
     set_pdl(cfg, &attr, flags);
     return cudaLaunchKernelEx(&cfg, kernel, prm) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+// The wide tree's kernel and the join of its parts behind it.
+template <int D, bool SPLIT>
+int launch_tree(kda::Kv4AttendParams& prm, int64_t list, uint32_t flags, cudaStream_t stream) {
+    using SM = kda::KvtSmem<D, SPLIT>;
+    auto kernel = kda::kda_kv4_tree_kernel<D, SPLIT>;
+    int occ = 0, sms = 0;
+    const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::KVT_THREADS, SM::BYTES, &occ, &sms);
+    if (rc != KDA_OK) return rc;
+    // two CTAs' tensor memory fits an SM; none without four units
+    int64_t grid = std::min<int64_t>((int64_t)std::min(occ, 2) * sms, kda::KVT_MAX_CTAS);
+    grid = std::max<int64_t>(1, std::min(grid, list / 4));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(kda::KVT_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SM::BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    set_pdl(cfg, &attr, flags);
+    if (cudaLaunchKernelEx(&cfg, kernel, prm) != cudaSuccess) return KDA_ERR_LAUNCH;
+    if (grid == 1) return KDA_OK;
+    cudaLaunchConfig_t join = {};
+    join.gridDim = dim3((unsigned)(grid - 1) * kda::KVT_JOIN_GROUPS, 1, 1);
+    join.blockDim = dim3(256, 1, 1);
+    join.stream = stream;
+    cudaLaunchAttribute after;
+    set_pdl(join, &after, KDA_LAUNCH_PDL);      // its CTAs wait for the kernel's end themselves
+    return cudaLaunchKernelEx(&join, kda::kda_kv4_tree_join_kernel<D>, prm) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 template <bool TREE>
@@ -176,7 +206,7 @@ int attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, const ui
     if (rc != KDA_OK) return rc;
     if (!g.q || !g.o || !g.workspace || (TREE && !tree)) return KDA_ERR_NULL;
     if (!aligned(tree, 8) || !aligned(g.q, 16) || g.q_stride * es % 16 != 0 || !aligned(g.o, 16) || !aligned(g.workspace, 16)) return KDA_ERR_ALIGN;
-    if (g.workspace_bytes < KDA_KV4_WORKSPACE_BYTES) return KDA_ERR_SHAPE;
+    if (g.workspace_bytes < (TREE ? KDA_KV4_TREE_WORKSPACE_BYTES : KDA_KV4_WORKSPACE_BYTES)) return KDA_ERR_SHAPE;
     kda::Kv4AttendParams prm;
     prm.pages = static_cast<const uint8_t*>(cache->base);
     prm.num_pages = cache->num_pages;
@@ -214,6 +244,17 @@ int attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, const ui
     const int64_t list = units * std::min<int64_t>(tiles * cache->heads * g.n, 1 << 20);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     using namespace kda;
+    if (TREE && (int64_t)g.max_t * grp > KVT_MIN_ROWS) {
+        static_assert(KVT_COUNTERS + KVT_HEAD + 2LL * KVT_MAX_CTAS * KvtPart<128>::FLOATS * 4 <= KDA_KV4_TREE_WORKSPACE_BYTES, "workspace");
+        static_assert(KV4_MAX_CTAS * sizeof(int32_t) <= KVT_COUNTERS, "the other kernel's counters stay zero");
+        const int64_t wide = ((int64_t)g.table_cols * cache->page_tokens + KVT_KEYS - 1) / KVT_KEYS * cache->heads * g.n *
+                             (((int64_t)g.max_t * grp + KVT_ROWS - 1) / KVT_ROWS);
+        const bool split = g.dtype != KDA_BF16;
+        prm.counters = reinterpret_cast<int32_t*>(static_cast<char*>(g.workspace) + KVT_COUNTERS);
+        prm.partials = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + KVT_COUNTERS + KVT_HEAD);
+        if (cache->dim == 128) return split ? launch_tree<128, true>(prm, wide, flags, st) : launch_tree<128, false>(prm, wide, flags, st);
+        return split ? launch_tree<64, true>(prm, wide, flags, st) : launch_tree<64, false>(prm, wide, flags, st);
+    }
     if (cache->dim == 128)
         return mode == KV4_8 ? launch_attend<128, KV4_8, TREE>(prm, list, flags, st)
                : mode == KV4_16 ? launch_attend<128, KV4_16, TREE>(prm, list, flags, st)

@@ -58,7 +58,7 @@ template <typename ET, int VC, int KWM>
 __global__ void __launch_bounds__(CONV_TREE_CH * CONV_TREE_GROUPS) kda_conv_tree_kernel(const ConvParams p, const uint64_t* tree) {
     using IO = ConvIO<ET, VC>;
     using R = typename IO::R;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     R* rows = reinterpret_cast<R*>(smem);       // [KW - 1 + T][64]
     const int cblocks = (p.C / VC + CONV_TREE_CH - 1) / CONV_TREE_CH;
     const int cb = (int)blockIdx.x % cblocks, r = (int)blockIdx.x / cblocks;
@@ -217,7 +217,7 @@ template <typename ST, typename QT>
 __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const StepParams p, const uint64_t* tree) {
     using SV = StateVec<ST>;
     constexpr int VEC = SV::VEC, CW = 2 * VEC, NV = 2 * VEC, P2 = VEC / 2;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     const int warps = blockDim.x >> 5, BV = warps * CW;
     float* kh = reinterpret_cast<float*>(smem);
     float* al = kh + p.t * KMAX;

@@ -19,7 +19,7 @@ def lib(built_libs):
 
 @pytest.fixture(scope="module")
 def workspace():
-    return torch.zeros(kda.KDA_KV4_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    return torch.zeros(kda.KDA_KV4_TREE_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
 
 
 def i32(v):
