@@ -23,10 +23,18 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// A descriptor `bytes` further on.
+__device__ __forceinline__ uint64_t tc_step(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+// One lane of a converged warp.
+__device__ __forceinline__ bool tc_elect() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
 // d (fp32 in tensor memory) = a b, or += with `more`; fp16 operands in shared memory, 16 deep.
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool more) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)more) : "memory");
 }
@@ -85,8 +93,9 @@ __host__ __device__ constexpr uint32_t tc_idesc(int m, int n, bool b_rows) {
 // ---------------------------------------------------------------------------
 constexpr int KVT_ROWS = 128;            // query rows of a tile: the tensor cores' M
 constexpr int KVT_KEYS = 64;             // keys of a unit of work: four blocks
-constexpr int KVT_THREADS = 256, KVT_WARPS = KVT_THREADS / 32;
-constexpr int KVT_STAGES = 2;            // units of codes in flight
+constexpr int KVT_WARPS = 8;              // that compute; one more fetches the codes and starts the products
+constexpr int KVT_THREADS = 32 * (KVT_WARPS + 1);
+constexpr int KVT_STAGES = 3;            // units of codes in flight
 constexpr int KVT_PART = 6;              // what beginning and ending a part costs a CTA, in units
 constexpr int KVT_FIRST = KVT_PART + 2, KVT_LAST = 2;   // what a cut leaves before and after it in a tile (see Kv4Shape)
 constexpr int KVT_MAX_CTAS = 304;        // two for each of 152 SMs
@@ -102,11 +111,35 @@ template <int D, bool SPLIT> struct KvtSmem {
     static constexpr int OFF_Q = 0, OFF_K = OFF_Q + Q * (SPLIT ? 2 : 1), OFF_V = OFF_K + K, OFF_P = OFF_V + K,
                          OFF_RAW = OFF_P + P * (SPLIT ? 2 : 1), OFF_ROWF = OFF_RAW + KVT_STAGES * STAGE,
                          OFF_MAX = OFF_ROWF + KVT_ROWS * 4,      // [2][128] halves' maxima, then sums
-                         OFF_NAN = OFF_MAX + 2 * KVT_ROWS * 4,   // [D / 16] tokens of the unit whose value group is NaN
-                         OFF_BAR = OFF_NAN + 8 * 8,              // raw [stages], scores, sums
+                         OFF_ROWNAN = OFF_MAX + 2 * KVT_ROWS * 4,     // [128] value groups in which a row has seen a NaN
+                         OFF_NAN = OFF_ROWNAN + KVT_ROWS * 4,    // [2][8] tokens of an even or odd unit whose value group is NaN
+                         OFF_BAR = OFF_NAN + 2 * 8 * 8,              // raw [stages], scores, sums
                          OFF_MISC = OFF_BAR + 8 * 8,             // tensor memory base, blocks not there [stages]
-                         OFF_WALK = OFF_MISC + 32, BYTES = OFF_WALK + 2 * 128 + 1024;   // and 1024 to align
+                         OFF_WALK = OFF_MISC + 32, BYTES = OFF_WALK + 2 * 128 + 1024;       // and 1024 to align
+    static_assert(KVT_ROWS * D * (SPLIT ? 4 : 2) <= OFF_RAW - OFF_K, "a tile's queries as they come");
+    // CTAs an SM (228 KB of shared memory, 1 KB of it taken for each)
+    static constexpr int CTAS = 2 * (BYTES + 1024) <= 228 * 1024 ? 2 : 1;
 };
+
+// N (2 or 4) neighbouring elements of a typed array in shared memory, from a multiple of N.
+template <int N> __device__ __forceinline__ void ld_shared(const void* p, int i, int dtype, float (&x)[N]) {
+    if (dtype == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i + e);
+            x[e] = f.x;
+            x[e + 1] = f.y;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i + e);
+        const float2 f = dtype == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&w)) : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+        x[e] = f.x;
+        x[e + 1] = f.y;
+    }
+}
 
 // One request's part of the work (see Kv4Req), units of 64 keys.
 __device__ __forceinline__ Kv4Req kvt_request(const Kv4AttendParams& p, int r) {
@@ -149,6 +182,7 @@ struct KvtWalk {
     int64_t r0;          // where request r begins
     int64_t s0;          // and the current tile
     int r, h, i0, b0, b1;
+    int valid;           // there is a part
     Kv4Req q;
     __device__ __forceinline__ bool next(const Kv4AttendParams& p) {
         for (;;) {
@@ -159,8 +193,8 @@ struct KvtWalk {
                 q = kvt_request(p, r);
             }
             const int each = q.units + KVT_PART;
-            const int64_t off = at - r0;
-            const int seg = (int)(off / each), u = (int)(off - (int64_t)seg * each);
+            const uint32_t off = (uint32_t)(at - r0);       // the host bounds a request's cost
+            const int seg = (int)(off / (uint32_t)each), u = (int)(off - (uint32_t)seg * each);
             h = seg / q.tiles;
             i0 = (seg - h * q.tiles) * KVT_ROWS;
             s0 = at - u;
@@ -174,14 +208,20 @@ struct KvtWalk {
 };
 
 // Where cut c falls (moved as above), by a warp: lanes share the requests.
-// `walk` (of the lane that finds it): the request there.
-__device__ __forceinline__ int64_t kvt_cut(const Kv4AttendParams& p, int64_t even, int64_t total, int c, int lane, KvtWalk* walk) {
+// `own`: the lane's request where there are at most 32.  `walk` (of the lane
+// that finds it): the request there.
+__device__ __forceinline__ int64_t kvt_cut(const Kv4AttendParams& p, int64_t even, int64_t total, int c, int lane, const Kv4Req& own,
+                                           KvtWalk* walk) {
     const int64_t cut = even * c;
     if (cut >= total) return total;
     int64_t begin = 0;
+#pragma unroll 1
     for (int base = 0; base < p.n; base += 32) {
-        Kv4Req q = {};
-        if (base + lane < p.n) q = kvt_request(p, base + lane);
+        Kv4Req q = own;
+        if (p.n > 32) {
+            q = Kv4Req{};
+            if (base + lane < p.n) q = kvt_request(p, base + lane);
+        }
         const int64_t mine = kvt_cost(q, p.heads);
         int64_t upto = mine;
 #pragma unroll
@@ -195,7 +235,7 @@ __device__ __forceinline__ int64_t kvt_cut(const Kv4AttendParams& p, int64_t eve
             const int l = __ffs(who) - 1;
             int64_t moved = cut;
             if (lane == l) {
-                const int each = q.units + KVT_PART, u = (int)((cut - (upto - mine)) % each);
+                const int each = q.units + KVT_PART, u = (int)((uint32_t)(cut - (upto - mine)) % (uint32_t)each);
                 moved += u < KVT_FIRST ? -u : each - u < KVT_LAST ? each - u : 0;
                 if (walk != nullptr) {
                     walk->r = base + l;
@@ -243,7 +283,7 @@ template <int D> struct KvtPart {
 // Parts of a (request, head, tile) that several CTAs share go to the
 // workspace, and kda_kv4_tree_join_kernel adds them in order.
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(KVT_THREADS, SPLIT && D == 128 ? 1 : 2) kda_kv4_tree_kernel(const Kv4AttendParams p) {
+__global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_tree_kernel(const Kv4AttendParams p) {
     using F = Kv4<D>;
     using SM = KvtSmem<D, SPLIT>;
     extern __shared__ uint8_t smem_raw[];
@@ -251,21 +291,22 @@ __global__ void __launch_bounds__(KVT_THREADS, SPLIT && D == 128 ? 1 : 2) kda_kv
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t *Q = smem + SM::OFF_Q, *K = smem + SM::OFF_K, *V = smem + SM::OFF_V, *P = smem + SM::OFF_P, *raw = smem + SM::OFF_RAW;
     float* rowf = reinterpret_cast<float*>(smem + SM::OFF_ROWF);
+    uint32_t* row_nan = reinterpret_cast<uint32_t*>(smem + SM::OFF_ROWNAN);
     float* half_max = reinterpret_cast<float*>(smem + SM::OFF_MAX);
     unsigned long long* nan_tok = reinterpret_cast<unsigned long long*>(smem + SM::OFF_NAN);
     uint64_t *bar_raw = reinterpret_cast<uint64_t*>(smem + SM::OFF_BAR), *bar_s = bar_raw + KVT_STAGES, *bar_o = bar_s + 1;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + SM::OFF_MISC);
     volatile uint32_t* missing = misc + 1;      // [stages] blocks of a unit that are not there
-    KvtWalk& walk = *reinterpret_cast<KvtWalk*>(smem + SM::OFF_WALK);
-    volatile int *have_s = reinterpret_cast<int*>(misc + 4), *nan_any = have_s + 1;
-    static_assert(sizeof(KvtWalk) <= 128, "KvtSmem::OFF_WALK");
+    volatile int *any_empty = reinterpret_cast<int*>(misc + 4), *nan_any = any_empty + 1;     // nan_any: [2], as nan_tok
+    auto walk = [&](int i) -> KvtWalk& { return *reinterpret_cast<KvtWalk*>(smem + SM::OFF_WALK + 128 * i); };   // this part's, the next's
+    static_assert(sizeof(KvtWalk) <= 128 && KVT_STAGES == 3, "KvtSmem");
 
     if (tid == 0) {
         for (int i = 0; i < KVT_STAGES + 2; ++i) mbar_init(bar_raw + i, 1);
         fence_mbar_init();
+        nan_any[0] = nan_any[1] = 0;
     }
-    if (tid < 8) nan_tok[tid] = 0;
-    if (tid == 0) *nan_any = 0;
+    if (tid < 16) nan_tok[tid] = 0;
     if (warp == 1) tmem_alloc(misc, KVT_TMEM);
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
@@ -274,32 +315,35 @@ __global__ void __launch_bounds__(KVT_THREADS, SPLIT && D == 128 ? 1 : 2) kda_kv
     if (warp == 0) {
         int64_t total = 0;
         bool empty = false;
+        Kv4Req own = {};
+#pragma unroll 1
         for (int r = lane; r < p.n; r += 32) {
-            const Kv4Req q = kvt_request(p, r);
-            total += kvt_cost(q, p.heads);
-            if (q.err && blockIdx.x == 0) atomicCAS(p.status, 0, q.err);
-            empty |= q.t > 0 && q.units == 0;
+            own = kvt_request(p, r);
+            total += kvt_cost(own, p.heads);
+            if (own.err && blockIdx.x == 0) atomicCAS(p.status, 0, own.err);
+            empty |= own.t > 0 && own.units == 0;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         empty = __any_sync(0xffffffffu, empty);
         const int64_t even = kvt_even(total, gridDim.x);
-        const int64_t c0 = kvt_cut(p, even, total, blockIdx.x, lane, &walk), c1 = kvt_cut(p, even, total, blockIdx.x + 1, lane, nullptr);
+        KvtWalk& w = walk(0);
+        const int64_t c0 = kvt_cut(p, even, total, blockIdx.x, lane, own, &w), c1 = kvt_cut(p, even, total, blockIdx.x + 1, lane, own, nullptr);
         __syncwarp();
         if (lane == 0) {
-            walk.at = c0;
-            walk.end = c1;
-            const bool ok = c0 < c1 && walk.next(p);
-            *have_s = (int)ok | (int)empty << 1;
+            w.at = c0;
+            w.end = c1;
+            w.valid = c0 < c1 && w.next(p);
+            *any_empty = empty;
             KvtJoin j = {};
-            if (ok && walk.b0 > 0) {     // the CTAs of a tile: those between the cuts that stayed inside it
-                const int first = (int)((walk.s0 + KVT_FIRST + even - 1) / even) - 1;
+            if (w.valid && w.b0 > 0) {   // the CTAs of a tile: those between the cuts that stayed inside it
+                const int first = (int)((w.s0 + KVT_FIRST + even - 1) / even) - 1;
                 if (first + 1 == (int)blockIdx.x) {
-                    j.last = (int)((walk.s0 + walk.q.units + KVT_PART - KVT_LAST) / even);
-                    j.row0 = walk.i0;
-                    j.rows = min(KVT_ROWS, walk.q.t * p.grp - walk.i0);
-                    j.tok0 = walk.q.tok0;
-                    j.h = walk.h;
+                    j.last = (int)((w.s0 + w.q.units + KVT_PART - KVT_LAST) / even);
+                    j.row0 = w.i0;
+                    j.rows = min(KVT_ROWS, w.q.t * p.grp - w.i0);
+                    j.tok0 = w.q.tok0;
+                    j.h = w.h;
                 }
             }
             reinterpret_cast<KvtJoin*>(p.counters)[blockIdx.x] = j;
@@ -308,9 +352,10 @@ __global__ void __launch_bounds__(KVT_THREADS, SPLIT && D == 128 ? 1 : 2) kda_kv
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0], tm_s = tmem, tm_o = tmem + KVT_KEYS;
-    bool have = *have_s & 1;
-    if (*have_s & 2) {   // requests without a visible key: zero rows
+    // read again where it is needed: registers are short
+    auto tm_s = [&]() { return *static_cast<volatile uint32_t*>(misc); };
+    auto tm_o = [&]() { return tm_s() + KVT_KEYS; };
+    if (*any_empty) {   // requests without a visible key: zero rows
         for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
             const Kv4Req q = kvt_request(p, r);
             if (q.units > 0) continue;
@@ -326,186 +371,330 @@ __global__ void __launch_bounds__(KVT_THREADS, SPLIT && D == 128 ? 1 : 2) kda_kv
     // this thread's row of a tile (a lane of tensor memory) and half of a unit's keys
     const int row = 32 * (warp & 3) + lane, half = warp >> 2;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t aQ = smem_u32(Q), aK = smem_u32(K), aV = smem_u32(V), aP = smem_u32(P);
+    // a part's output or its place in the workspace
+    auto part_at = [&](const KvtWalk& w) { return p.partials + (int64_t)(2 * blockIdx.x + (w.b0 == 0 ? 1 : 0)) * KvtPart<D>::FLOATS; };
+    auto is_whole = [](const KvtWalk& w) { return w.b0 == 0 && w.b1 == w.q.units; };
+    auto out_at = [&](const KvtWalk& w, int i) {        // of row i of the tile
+        const int x = w.i0 + i, j = x / p.grp;
+        return ((int64_t)(w.q.tok0 + j) * p.h_q + w.h * p.grp + x - j * p.grp) * D;
+    };
+    int cur = 0;
 
-    while (have) {
-        const Kv4Req& req = walk.q;        // read from shared memory where it is needed
-        const int &r = walk.r, &h = walk.h, &i0 = walk.i0, &b0 = walk.b0, &b1 = walk.b1;
-        const int rows = min(KVT_ROWS, req.t * p.grp - i0);
-        // Fetches a unit's blocks: warp 0, lanes 0 .. 3 a block each.
-        auto fetch = [&](int b) {
-            const int st = (b - b0) % KVT_STAGES;
-            bool ok = false;
-            const uint8_t* from = nullptr;
-            const int blk = (req.first + b) * 4 + lane;
-            if (lane < 4 && blk * 16 < req.ctx + req.t && (p.window <= 0 || req.ctx - p.window + 1 < (blk + 1) * 16)) {
-                const int pg = blk / bpp, page = __ldg(p.table + (int64_t)r * p.cols + pg);
-                ok = page >= 0 && page < p.num_pages;
-                if (!ok) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
-                from = p.pages + (int64_t)page * p.page_stride + ((int64_t)h * bpp + (blk - pg * bpp)) * F::BLOCK;
-            }
-            const uint32_t there = __ballot_sync(0xffffffffu, ok);
-            if (lane == 0) {
-                missing[st] = there ^ 15u;
-                if (there != 0) mbar_arrive_expect_tx(bar_raw + st, __popc(there) * F::BLOCK);
-                else mbar_arrive(bar_raw + st);
+    for (; walk(cur).valid; cur ^= 1) {
+        const KvtWalk& w = walk(cur);
+        const Kv4Req& req = w.q;        // read from shared memory where it is needed
+        if (warp == KVT_WARPS) {
+            // ---- codes fetched and products started: a lane a block, its page looked up a unit ahead ----
+            const int b0 = w.b0, b1 = w.b1, last = req.ctx + req.t;
+            const int32_t* table = p.table + (int64_t)w.r * p.cols;
+            const uint8_t* base = p.pages + (int64_t)w.h * bpp * F::BLOCK;
+            // the lane's next block, by page and place in it
+            int blk = (req.first + b0) * 4 + lane, pg = blk / bpp, in = blk - pg * bpp, stage = 0, page = -1;
+            const int low_end = p.window > 0 ? req.ctx - p.window + 1 : -1;     // blocks that end there are in no window
+            auto look = [&](int b) {
+                page = b < b1 && lane < 4 && blk * 16 < last && low_end < (blk + 1) * 16 ? __ldg(table + pg) : -2;      // -2: not wanted
+            };
+            auto fetch = [&](int b) {
+                const bool ok = page >= 0 && page < p.num_pages;
+                if (!ok && page != -2) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
+                const uint32_t there = __ballot_sync(0xffffffffu, ok);
+                if (lane == 0) {
+                    missing[stage] = there ^ 15u;
+                    if (there != 0) mbar_arrive_expect_tx(bar_raw + stage, __popc(there) * F::BLOCK);
+                    else mbar_arrive(bar_raw + stage);
+                }
+                __syncwarp();
+                if (ok && !p.withhold)
+                    bulk_load(raw + stage * SM::STAGE + lane * F::BLOCK, base + (int64_t)page * p.page_stride + in * F::BLOCK, F::BLOCK, bar_raw + stage);
+                stage = stage + 1 == KVT_STAGES ? 0 : stage + 1;
+                blk += 4;
+                for (in += 4; in >= bpp; in -= bpp) ++pg;
+                look(b + 1);
+            };
+            look(b0);
+            for (int b = b0; b < min(b1, b0 + 2); ++b) fetch(b);
+            if (lane == 0) {            // what comes behind this part
+                KvtWalk& n = walk(cur ^ 1);
+                n = w;
+                n.valid = n.next(p);
             }
             __syncwarp();
-            if (ok && !p.withhold) bulk_load(raw + st * SM::STAGE + lane * F::BLOCK, from, F::BLOCK, bar_raw + st);
-        };
-        if (warp == 0 && alive) {
-            for (int b = b0; b < min(b1, b0 + KVT_STAGES); ++b) fetch(b);
-        }
-        // ---- queries: rotated, scaled to below 1 by a power of two, rounded; a warp a row ----
-        {
-            constexpr int E = D / 32;
-            const int d = lane * E, hr = p.rot >> 1;
-            const bool first = d < hr;
-#pragma unroll 2
-            for (int k = 0; k < KVT_ROWS / KVT_WARPS; ++k) {
-                const int i = warp + k * KVT_WARPS;
-                float x[E] = {}, y[E] = {}, cs[E], sn[E] = {};
-#pragma unroll
-                for (int e = 0; e < E; ++e) cs[e] = 1.f;
-                if (i < rows) {
-                    const int j = (i0 + i) / p.grp;
-                    const int pos = req.ctx + __popcll(tree_mask(p.tree, req.tok0 + j, j)) - 1;
-                    const int64_t base = (int64_t)(req.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + i0 + i - j * p.grp) * D;
-                    ld_elems<E>(p.q, base + d, p.dtype, x);
-                    if (d < p.rot) {
-                        const int64_t at = (int64_t)pos * hr;
-                        if (p.inter) {
-                            ld_elems<E / 2>(p.cos, at + d / 2, 0, cs);
-                            ld_elems<E / 2>(p.sin, at + d / 2, 0, sn);
-#pragma unroll
-                            for (int e = E / 2 - 1; e >= 0; --e) {
-                                const float a = x[2 * e], b = x[2 * e + 1];
-                                x[2 * e] = a * cs[e] - b * sn[e];
-                                x[2 * e + 1] = b * cs[e] + a * sn[e];
-                            }
-                        } else {
-                            ld_elems<E>(p.q, base + (first ? d + hr : d - hr), p.dtype, y);
-                            ld_elems<E>(p.cos, at + (first ? d : d - hr), 0, cs);
-                            ld_elems<E>(p.sin, at + (first ? d : d - hr), 0, sn);
-#pragma unroll
-                            for (int e = 0; e < E; ++e) x[e] = x[e] * cs[e] + (first ? -y[e] : y[e]) * sn[e];
-                        }
-                    }
-                }
-                float amax = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                // as in kda_kv4_attend_kernel
-                const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
-                const float down =
-                    __uint_as_float(amax < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
-                uint8_t* to = Q + (d / 64) * (KVT_ROWS * 128) + i * 128 + (((d % 64 / 8) ^ (i & 7)) << 4) + d % 8 * 2;
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float u = x[e] * down, v = x[e + 1] * down;
-                    const __half2 hi = __floats2half2_rn(u, v);
-                    *reinterpret_cast<__half2*>(to + e * 2) = hi;
-                    if constexpr (SPLIT) {
-                        const float2 f = __half22float2(hi);
-                        *reinterpret_cast<__half2*>(to + SM::Q + e * 2) = __floats2half2_rn(u - f.x, v - f.y);
-                    }
-                }
-                if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
-            }
-        }
-        // ---- what this thread's row sees of the tree and of the context ----
-        uint64_t own = 0;
-        int low = 0x7fffffff;
-        if (row < rows) {
-            const int j = (i0 + row) / p.grp;
-            own = tree_mask(p.tree, req.tok0 + j, j);
-            low = p.window > 0 ? req.ctx + __popcll(own) - p.window : 0;
-            if (p.window > 0)
-                for (int more = __popcll(own) - p.window; more > 0; --more) own &= own - 1;
-        }
-        auto sees = [&](int key) {
-            const int at = key - req.ctx;
-            return at < 0 ? key >= low : at < TREE_MAX && (own >> at & 1u) != 0;
-        };
-        // keys that every row sees: [see0, ctx)
-        const int see0 = p.window > 0 ? req.ctx + req.t - p.window : 0;
-        float m = -FLT_MAX, l = 0.f;
-        uint32_t nan_groups = 0;        // value groups in which this row has seen a NaN
-        bool pending = false;           // P V not waited for
-
-        for (int b = b0; b < b1; ++b) {
-            const int st = (b - b0) % KVT_STAGES, key0 = (req.first + b) * KVT_KEYS;
-            const uint8_t* R = raw + st * SM::STAGE;
-            bool ok = mbar_wait(bar_raw + st, phase(st));
-            if (ok) phases ^= 1u << st;
-            const uint32_t miss = missing[st];
-            const bool masked = key0 + KVT_KEYS > req.ctx || key0 < see0 || miss != 0;
-            // ---- keys: a token's quarter (half) a thread ----
-            if (ok) {
-                const int key = tid >> 2, q = tid & 3;
-                const uint8_t* B = R + (key >> 4) * F::BLOCK;
-                const bool gone = miss >> (key >> 4) & 1u;
-                if constexpr (D == 128) {
-                    uint4 c = *reinterpret_cast<const uint4*>(B + F::KC + (key & 15) * 64 + q * 16);
-                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::KS + (key & 15) * 8 + 2 * q);
-                    if (gone) s2 = 0;
-                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
-                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-                    uint8_t* to = K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t v[4];
-                        cvt_e2m1x8_f16(w[i], v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
-                        *reinterpret_cast<uint4*>(to + ((((q & 1) * 4 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                } else {
-                    const uint2 c = *reinterpret_cast<const uint2*>(B + F::KC + (key & 15) * 32 + q * 8);
-                    uint32_t s2 = B[F::KS + (key & 15) * 4 + q];
-                    if (gone) s2 = 0;
-                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
-                    const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t v[4];
-                        cvt_e2m1x8_f16(w[i], v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = hmul2_half<false>(v[e], sc);
-                        *reinterpret_cast<uint4*>(K + key * 128 + (((q * 2 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            alive = __syncthreads_and(ok);      // also: every row's queries and factors are written
-            if (!alive) break;
-            if (tid == 0) {
-                tc_fence_after();
-                constexpr uint32_t idesc = tc_idesc(KVT_ROWS, KVT_KEYS, false);
+            constexpr uint32_t id_s = tc_idesc(KVT_ROWS, KVT_KEYS, false), id_o = tc_idesc(KVT_ROWS, D, true);
+            const uint32_t s_at = tm_s(), o_at = tm_o();
+            const uint64_t dQ = tc_desc(smem_u32(Q), 16), dK = tc_desc(smem_u32(K), 16), dP = tc_desc(smem_u32(P), 16),
+                           dV = tc_desc(smem_u32(V), KVT_KEYS * 128);
+            auto add_values = [&](bool more) {
 #pragma unroll
                 for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma(tm_s, tc_desc(aQ + part * SM::Q + k / 4 * (KVT_ROWS * 128) + k % 4 * 32, 16),
-                               tc_desc(aK + k / 4 * (KVT_KEYS * 128) + k % 4 * 32, 16), idesc, part + k > 0);
-                tc_commit(bar_s);
+                    for (int k = 0; k < KVT_KEYS / 16; ++k)
+                        tc_mma(o_at, tc_step(dP, part * SM::P + k * 32), tc_step(dV, k * 2048), id_o, more || part + k > 0);
+                tc_commit(bar_o);
+            };
+            for (int b = b0; b <= b1; ++b) {
+                alive = __syncthreads_and(true);
+                if (!alive) break;
+                if (tc_elect()) {
+                    tc_fence_after();
+                    if (b < b1) {
+#pragma unroll
+                        for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k)
+                                tc_mma(s_at, tc_step(dQ, part * SM::Q + k / 4 * (KVT_ROWS * 128) + k % 4 * 32),
+                                       tc_step(dK, k / 4 * (KVT_KEYS * 128) + k % 4 * 32), id_s, part + k > 0);
+                        tc_commit(bar_s);
+                    }
+                    if (b > b0) add_values(b > b0 + 1);
+                }
+                __syncwarp();
+                const bool rare = nan_any[(b - 1) & 1] != 0;
+                if (b + 2 < b1) fetch(b + 2);           // into the stage of the unit before
+                if (rare) __syncthreads();              // the others look through that unit's tokens
             }
-            // ---- values, when the last unit's are done with: two tokens' groups of 16 a thread ----
-            if (pending) {
-                ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
-                if (ok) phases ^= 1u << (KVT_STAGES + 1);
-                pending = false;
+            alive = __syncthreads_and(alive);
+        } else {
+            const int &b0 = w.b0, &b1 = w.b1;
+            const int rows = min(KVT_ROWS, req.t * p.grp - w.i0);
+            // ---- queries: fetched together, where keys, values and probabilities will be; then rotated, scaled to
+            // below 1 by a power of two, rounded: 16 neighbouring rows a warp, a row at a time ----
+            {
+                const int es = p.dtype == 0 ? 4 : 2, chunks = D * es / 16;       // 16-byte pieces of a row
+                const uint32_t hold = smem_u32(K);
+#pragma unroll 4
+                for (int i = tid; i < rows * chunks; i += 32 * KVT_WARPS) {
+                    const int x = i / chunks, c = i - x * chunks, j = (w.i0 + x) / p.grp;
+                    const int64_t at = (int64_t)(req.tok0 + j) * p.q_stride + (int64_t)(w.h * p.grp + w.i0 + x - j * p.grp) * D;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                 ::"r"(hold + i * 16), "l"(static_cast<const char*>(p.q) + at * es + c * 16) : "memory");
+                }
+                const int hr = p.rot >> 1, w0 = warp * (KVT_ROWS / KVT_WARPS);
+                int pos = 0;            // of the lane's row of the warp's
+                if (lane < KVT_ROWS / KVT_WARPS && w0 + lane < rows) {
+                    const int j = (w.i0 + w0 + lane) / p.grp;
+                    pos = req.ctx + __popcll(tree_mask(p.tree, req.tok0 + j, j)) - 1;
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                asm volatile("bar.sync 5, 256;" ::: "memory");
+                constexpr int E = D / 32;
+                const int d = lane * E;
+                const bool first = d < hr;
+#pragma unroll 4
+                for (int k = 0; k < KVT_ROWS / KVT_WARPS; ++k) {
+                    const int i = w0 + k;
+                    float x[E] = {}, y[E] = {}, cs[E], sn[E] = {};
+#pragma unroll
+                    for (int e = 0; e < E; ++e) cs[e] = 1.f;
+                    const int64_t at = (int64_t)__shfl_sync(0xffffffffu, pos, k) * hr;
+                    if (i < rows) {
+                        ld_shared<E>(K, i * D + d, p.dtype, x);
+                        if (d < p.rot) {
+                            if (p.inter) {
+                                ld_elems<E / 2>(p.cos, at + d / 2, 0, cs);
+                                ld_elems<E / 2>(p.sin, at + d / 2, 0, sn);
+#pragma unroll
+                                for (int e = E / 2 - 1; e >= 0; --e) {
+                                    const float a = x[2 * e], b = x[2 * e + 1];
+                                    x[2 * e] = a * cs[e] - b * sn[e];
+                                    x[2 * e + 1] = b * cs[e] + a * sn[e];
+                                }
+                            } else {
+                                ld_shared<E>(K, i * D + (first ? d + hr : d - hr), p.dtype, y);
+                                ld_elems<E>(p.cos, at + (first ? d : d - hr), 0, cs);
+                                ld_elems<E>(p.sin, at + (first ? d : d - hr), 0, sn);
+#pragma unroll
+                                for (int e = 0; e < E; ++e) x[e] = x[e] * cs[e] + (first ? -y[e] : y[e]) * sn[e];
+                            }
+                        }
+                    }
+                    float amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    // as in kda_kv4_attend_kernel
+                    const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
+                    const float down =
+                        __uint_as_float(amax < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
+                    uint8_t* to = Q + (d / 64) * (KVT_ROWS * 128) + i * 128 + (((d % 64 / 8) ^ (i & 7)) << 4) + d % 8 * 2;
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float u = x[e] * down, v = x[e + 1] * down;
+                        const __half2 hi = __floats2half2_rn(u, v);
+                        *reinterpret_cast<__half2*>(to + e * 2) = hi;
+                        if constexpr (SPLIT) {
+                            const float2 f = __half22float2(hi);
+                            *reinterpret_cast<__half2*>(to + SM::Q + e * 2) = __floats2half2_rn(u - f.x, v - f.y);
+                        }
+                    }
+                    if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
+                }
+                asm volatile("bar.sync 5, 256;" ::: "memory");      // the keys go where the queries were
             }
-            if (ok) {
-                if constexpr (D == 128) {
-                    const int bk = tid >> 6, hf2 = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
-                    const uint8_t* B = R + bk * F::BLOCK;
-                    const uint4 c = *reinterpret_cast<const uint4*>(B + F::VC + hf2 * 512 + lane * 16);
-                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::VS + lane * 4 + hf2 * 2);
-                    const int key = bk * 16 + hf2 * 8 + 2 * tp;
+            // ---- what this thread's row sees of the tree and of the context ----
+            uint64_t own = 0;
+            int low = 0x7fffffff;
+            if (row < rows) {
+                const int j = (w.i0 + row) / p.grp;
+                own = tree_mask(p.tree, req.tok0 + j, j);
+                low = p.window > 0 ? req.ctx + __popcll(own) - p.window : 0;
+                if (p.window > 0)
+                    for (int more = __popcll(own) - p.window; more > 0; --more) own &= own - 1;
+            }
+            auto sees = [&](int key) {
+                const int at = key - req.ctx;
+                return at < 0 ? key >= low : at < TREE_MAX && (own >> at & 1u) != 0;
+            };
+            float m = -FLT_MAX, l = 0.f;
+            if (half == 0) row_nan[row] = 0;
+            bool ok = true;
+            int st = 0;                 // the stage of unit b + 1, whose keys are next
+
+            // NaN among unit b's values that not all rows see, behind the barrier that ends it: the flags of even and odd
+            // units lie apart, and are set again two barriers on.
+            auto find_nan = [&](int b) {
+                if (nan_any[b & 1] == 0) return;
+#pragma unroll 1
+                for (int g = 0; g < D / 16; ++g)
+                    for (unsigned long long t = nan_tok[(b & 1) * 8 + g]; t != 0; t &= t - 1)
+                        if (half == 0 && sees((req.first + b) * KVT_KEYS + __ffsll((long long)t) - 1)) row_nan[row] |= 1u << g;
+                __syncthreads();
+                if (tid < 8) nan_tok[(b & 1) * 8 + tid] = 0;
+                if (tid == 0) nan_any[b & 1] = 0;
+            };
+
+            // Unit b's scores and values, and unit b + 1's keys while the tensor cores are on the scores.
+#pragma unroll 1
+            for (int b = b0 - 1; b < b1; ++b) {
+                if (b >= b0) {
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    alive = __syncthreads_and(ok);      // keys b, probabilities and values b - 1 are written, codes b - 1 read
+                    if (!alive) break;
+                    find_nan(b - 1);
+                    ok = mbar_wait(bar_s, phase(KVT_STAGES));
+                    if (ok) phases ^= 1u << KVT_STAGES;
+                    tc_fence_after();
+                }
+                // ---- keys: a token's quarter a thread ----
+                if (b + 1 < b1) {
+                    if (ok) ok = mbar_wait(bar_raw + st, phase(st));
+                    if (ok) {
+                        phases ^= 1u << st;
+                        const int key = tid >> 2, q = tid & 3;
+                        const uint8_t* B = raw + st * SM::STAGE + (key >> 4) * F::BLOCK;
+                        const bool gone = missing[st] >> (key >> 4) & 1u;
+                        if constexpr (D == 128) {
+                            const uint4 c = *reinterpret_cast<const uint4*>(B + F::KC + (key & 15) * 64 + q * 16);
+                            uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::KS + (key & 15) * 8 + 2 * q);
+                            if (gone) s2 = 0;
+                            const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                            const uint32_t code[4] = {c.x, c.y, c.z, c.w};
+                            uint8_t* to = K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t v[4];
+                                cvt_e2m1x8_f16(code[i], v);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
+                                *reinterpret_cast<uint4*>(to + ((((q & 1) * 4 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                            }
+                        } else {
+                            const uint2 c = *reinterpret_cast<const uint2*>(B + F::KC + (key & 15) * 32 + q * 8);
+                            uint32_t s2 = B[F::KS + (key & 15) * 4 + q];
+                            if (gone) s2 = 0;
+                            const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                            const uint32_t code[2] = {c.x, c.y};
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t v[4];
+                                cvt_e2m1x8_f16(code[i], v);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) v[e] = hmul2_half<false>(v[e], sc);
+                                *reinterpret_cast<uint4*>(K + key * 128 + (((q * 2 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                            }
+                        }
+                    }
+                }
+                st = st + 1 == KVT_STAGES ? 0 : st + 1;
+                if (b < b0) continue;
+                const int sv = st >= 2 ? st - 2 : st + 1;               // the stage of unit b
+                const int key0 = (req.first + b) * KVT_KEYS;
+                const uint32_t miss = missing[sv];
+                // keys that every row sees: [ctx + t - window, ctx)
+                const bool masked = key0 + KVT_KEYS > req.ctx || (p.window > 0 && key0 < req.ctx + req.t - p.window) || miss != 0;
+                // ---- scores to probabilities, when the last unit's are done with ----
+                if (ok && b > b0) {
+                    ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
+                    if (ok) phases ^= 1u << (KVT_STAGES + 1);
+                }
+                // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                float s[32], top = -INFINITY;
+                if (ok) {
+                    tmem_ld32(tm_s() + lane_base + 32 * half, s);
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int at = 32 * half + i;
+                            if (!sees(key0 + at) || (miss >> (at >> 4) & 1u)) s[i] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(s[i], s[i + 1]), top);
+                }
+                half_max[half * KVT_ROWS + row] = top;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+                if (ok) {
+                    const float c = rowf[row];
+                    top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]) * c;
+                    const bool grow = top > m + KV4_SLACK;
+                    if (__any_sync(0xffffffffu, grow)) {        // both warps alike: the same rows
+                        const float f = grow ? ex2f(m - top) : 1.f;
+                        if (grow) m = top;
+                        l *= f;
+                        if (b > b0) {
+#pragma unroll 1
+                            for (int k = 0; k < D / 32; ++k) {
+                                const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
+                                float o[16];
+                                tmem_ld16(at, o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] *= f;
+                                tmem_st16(at, o);
+                            }
+                        }
+                    }
+                    const float neg = KV4_LIFT - m;
+                    float2 sum = make_float2(l, 0.f);
+                    uint8_t* to = P + row * 128;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 x = __ffma2_rn(make_float2(s[i + 2 * e], s[i + 2 * e + 1]), make_float2(c, c), make_float2(neg, neg));
+                            const float x0 = ex2f(x.x), x1 = ex2f(x.y);
+                            sum = __fadd2_rn(sum, make_float2(x0, x1));
+                            const __half2 hh = __floats2half2_rn(x0, x1);
+                            hi[e] = *reinterpret_cast<const uint32_t*>(&hh);
+                            if constexpr (SPLIT) {
+                                const float2 f = __half22float2(hh);
+                                const __half2 rest = __floats2half2_rn(x0 - f.x, x1 - f.y);
+                                lo[e] = *reinterpret_cast<const uint32_t*>(&rest);
+                            }
+                        }
+                        uint4* at = reinterpret_cast<uint4*>(to + (((half * 4 + i / 8) ^ (row & 7)) << 4));
+                        *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if constexpr (SPLIT) at[SM::P / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    l = sum.x + sum.y;
+                    // ---- values: 16 channels (64: 8) of two tokens a thread ----
+                    const int bk = tid >> 6, hf = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
+                    const uint8_t* B = raw + sv * SM::STAGE + bk * F::BLOCK;
+                    const int key = bk * 16 + hf * 8 + 2 * tp, grp = D == 128 ? g : g >> 1;     // its first token, its scale group
+                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::VS + (grp * 4 + tp) * 4 + hf * 2);
                     if (masked) {
                         // tokens behind the end hold anything, and 0 * NaN is NaN: their scales become 0, and so do NaN
                         // ones, whose groups of the rows that see them are then set by hand (a rare path)
@@ -513,220 +702,118 @@ __global__ void __launch_bounds__(KVT_THREADS, SPLIT && D == 128 ? 1 : 2) kda_kv
                         for (int e = 0; e < 2; ++e) {
                             const bool out = (miss >> bk & 1u) || key0 + key + e >= req.ctx + req.t, nan = (s2 >> (8 * e) & 0x7fu) == 0x7fu;
                             if (nan && !out) {
-                                *nan_any = 1;
-                                atomicOr(nan_tok + g, 1ull << (key + e));
+                                nan_any[b & 1] = 1;
+                                atomicOr(nan_tok + (b & 1) * 8 + grp, 1ull << (key + e));
                             }
                             if (nan || out) s2 &= ~(0xffu << (8 * e));
                         }
                     }
                     const uint32_t sc = cvt_e4m3x2_f16x2(s2);
-                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-                    uint8_t* to = V + (g >> 2) * (KVT_KEYS * 128);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ch = (g & 3) * 2 + (i & 1), kk = key + (i >> 1);
-                        uint32_t v[4];
-                        cvt_e2m1x8_f16(w[i], v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
-                        *reinterpret_cast<uint4*>(to + kk * 128 + ((ch ^ (kk & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    constexpr int W = D / 64;           // words of a token's
+                    uint32_t code[2 * W];
+                    if constexpr (D == 128) {
+                        const uint4 cw = *reinterpret_cast<const uint4*>(B + F::VC + hf * 512 + lane * 16);
+                        code[0] = cw.x; code[1] = cw.y; code[2] = cw.z; code[3] = cw.w;
+                    } else {
+                        const uint2 cw = *reinterpret_cast<const uint2*>(B + F::VC + hf * 256 + lane * 8);
+                        code[0] = cw.x; code[1] = cw.y;
                     }
-                } else {
-                    // 16 tokens of 64 channels: (half, group eighth, pair) pieces of 8 bytes, a token's 8 channels 4 bytes
-                    const int bk = tid >> 6, hf2 = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
-                    const uint8_t* B = R + bk * F::BLOCK;
-                    const uint2 c = *reinterpret_cast<const uint2*>(B + F::VC + hf2 * 256 + lane * 8);
-                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::VS + ((g >> 1) * 4 + tp) * 4 + hf2 * 2);
-                    const int key = bk * 16 + hf2 * 8 + 2 * tp;
-                    if (masked) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const bool out = (miss >> bk & 1u) || key0 + key + e >= req.ctx + req.t, nan = (s2 >> (8 * e) & 0x7fu) == 0x7fu;
-                            if (nan && !out) {
-                                *nan_any = 1;
-                                atomicOr(nan_tok + (g >> 1), 1ull << (key + e));
-                            }
-                            if (nan || out) s2 &= ~(0xffu << (8 * e));
-                        }
-                    }
-                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
-                    const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int kk = key + i;
+                    for (int i = 0; i < 2 * W; ++i) {
+                        // channels 8 ch ..; at D = 128 every other lane's two pieces change places, so that eight lanes' stores
+                        // fall on different banks
+                        const int kk = key + i / W, piece = D == 128 ? (i ^ g) & 1 : 0, ch = D == 128 ? (g & 3) * 2 + piece : g;
+                        const uint32_t word = D == 128 ? (piece ? code[(i & 2) + 1] : code[i & 2]) : code[i];
                         uint32_t v[4];
-                        cvt_e2m1x8_f16(w[i], v);
+                        cvt_e2m1x8_f16(word, v);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = i < 1 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
-                        *reinterpret_cast<uint4*>(V + kk * 128 + ((g ^ (kk & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        for (int e = 0; e < 4; ++e) v[e] = i < W ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
+                        *reinterpret_cast<uint4*>(V + (D == 128 ? g >> 2 : 0) * (KVT_KEYS * 128) + kk * 128 + ((ch ^ (kk & 7)) << 4)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
             }
-            // ---- scores to probabilities ----
-            // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(bar_s, phase(KVT_STAGES)));
-            if (ok) phases ^= 1u << KVT_STAGES;
+            if (alive) {                // the last unit's probabilities and values
+                fence_proxy_async_smem();
+                tc_fence_before();
+                alive = __syncthreads_and(ok);
+                if (alive) find_nan(b1 - 1);
+            }
+            // ---- the part's sums ----
+            if (alive) {
+                ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
+                if (ok) phases ^= 1u << (KVT_STAGES + 1);
+            }
+            half_max[half * KVT_ROWS + row] = l;
+            alive = __syncthreads_and(alive && ok);
             tc_fence_after();
-            float s[32], top = -INFINITY;
-            if (ok) {
-                tmem_ld32(tm_s + lane_base + 32 * half, s);
-                if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int at = 32 * half + i;
-                        if (!sees(key0 + at) || (miss >> (at >> 4) & 1u)) s[i] = -INFINITY;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i]);
+            if (alive) {
+                l += half_max[(half ^ 1) * KVT_ROWS + row];
+            } else {                    // a wait ran out: nothing of this part
+                m = -FLT_MAX;
+                l = 0.f;
             }
-            half_max[half * KVT_ROWS + row] = top;
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-            if (ok) {
-                const float c = rowf[row];
-                top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]) * c;
-                const bool grow = top > m + KV4_SLACK;
-                if (__any_sync(0xffffffffu, grow)) {        // both warps alike: the same rows
-                    const float f = grow ? ex2f(m - top) : 1.f;
-                    if (grow) m = top;
-                    l *= f;
-                    if (b > b0) {
+            // through shared memory (queries to probabilities are done with), 16-byte pieces at their place xor (row % 8)
+            const bool whole = is_whole(w);
+            float4* tile = reinterpret_cast<float4*>(smem);
+            {
+                const uint32_t nan_groups = row_nan[row];
+                const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            const uint32_t at = tm_o + lane_base + half * (D / 2) + 16 * k;
-                            float o[16];
-                            tmem_ld16(at, o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= f;
-                            tmem_st16(at, o);
-                        }
-                    }
-                }
-                const float neg = KV4_LIFT - m;
-                uint8_t* to = P + row * 128;
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 x = __ffma2_rn(make_float2(s[i + 2 * e], s[i + 2 * e + 1]), make_float2(c, c), make_float2(neg, neg));
-                        const float x0 = ex2f(x.x), x1 = ex2f(x.y);
-                        l += x0 + x1;
-                        const __half2 hh = __floats2half2_rn(x0, x1);
-                        hi[e] = *reinterpret_cast<const uint32_t*>(&hh);
-                        if constexpr (SPLIT) {
-                            const float2 f = __half22float2(hh);
-                            const __half2 rest = __floats2half2_rn(x0 - f.x, x1 - f.y);
-                            lo[e] = *reinterpret_cast<const uint32_t*>(&rest);
-                        }
-                    }
-                    uint4* at = reinterpret_cast<uint4*>(to + (((half * 4 + i / 8) ^ (row & 7)) << 4));
-                    *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if constexpr (SPLIT) at[SM::P / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            alive = __syncthreads_and(ok);      // the unit's codes are read, its probabilities written
-            if (!alive) break;
-            if (tid == 0) {
-                tc_fence_after();
-                constexpr uint32_t idesc = tc_idesc(KVT_ROWS, D, true);
-#pragma unroll
-                for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-#pragma unroll
-                    for (int k = 0; k < KVT_KEYS / 16; ++k)
-                        tc_mma(tm_o, tc_desc(aP + part * SM::P + k * 32, 16), tc_desc(aV + k * 2048, KVT_KEYS * 128), idesc,
-                               b > b0 || part + k > 0);
-                tc_commit(bar_o);
-            }
-            pending = true;
-            if (warp == 0 && b + KVT_STAGES < b1) fetch(b + KVT_STAGES);
-            if (*nan_any != 0) {        // a NaN among values that not all rows see
-#pragma unroll 1
-                for (int g = 0; g < D / 16; ++g)
-                    for (unsigned long long t = nan_tok[g]; t != 0; t &= t - 1)
-                        if (sees(key0 + __ffsll((long long)t) - 1)) nan_groups |= 1u << g;
-                __syncthreads();
-                if (tid < 8) nan_tok[tid] = 0;      // the next unit's are set behind the next barrier
-                if (tid == 0) *nan_any = 0;
-            }
-        }
-        // ---- the part's sums ----
-        if (alive && pending) {
-            const bool ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
-            if (ok) phases ^= 1u << (KVT_STAGES + 1);
-            alive = __syncthreads_and(ok);
-        }
-        tc_fence_after();
-        half_max[half * KVT_ROWS + row] = l;
-        __syncthreads();
-        if (alive) {
-            l += half_max[(half ^ 1) * KVT_ROWS + row];
-        } else {                        // a wait ran out: nothing of this part
-            m = -FLT_MAX;
-            l = 0.f;
-        }
-        {
-            const bool whole = b0 == 0 && b1 == req.units;
-            float* part = p.partials + (int64_t)(2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * KvtPart<D>::FLOATS;
-            const int j = (i0 + row) / p.grp;
-            const int64_t out = ((int64_t)(req.tok0 + j) * p.h_q + h * p.grp + (i0 + row) - j * p.grp) * D;
-            const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                float o[16];
-                const int d0 = half * (D / 2) + 16 * k;
-                tmem_ld16(tm_o + lane_base + d0, o);
-                if (row < rows) {
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[16];
+                    const int d0 = half * (D / 2) + 16 * k;
+                    tmem_ld16(tm_o() + lane_base + d0, o);
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
-                        float4 v = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        float4 v = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
                         if (l == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (nan_groups >> ((d0 + i) >> 4) & 1u) v = make_float4(NAN, NAN, NAN, NAN);
-                        if (whole) st_elem4(p.o, out + d0 + i, p.dtype, v.x * f, v.y * f, v.z * f, v.w * f);
-                        else __stcg(reinterpret_cast<float4*>(part + row * D + d0 + i), v);
+                        if (nan_groups >> (d0 >> 4) & 1u) v = make_float4(NAN, NAN, NAN, NAN);
+                        tile[row * (D / 4) + (((d0 + i) / 4) ^ (row & 7))] = v;
                     }
                 }
             }
+            float* part = part_at(w);
             if (!whole && half == 0 && row < rows) __stcg(reinterpret_cast<float2*>(part + KVT_ROWS * D) + row, make_float2(m, l));
+            asm volatile("bar.sync 5, 256;" ::: "memory");
+            for (int i = tid; i < rows * (D / 4); i += 32 * KVT_WARPS) {
+                const int x = i / (D / 4), c = i % (D / 4);
+                const float4 v = tile[x * (D / 4) + (c ^ (x & 7))];
+                if (whole) st_elem4(p.o, out_at(w, x) + 4 * c, p.dtype, v.x, v.y, v.z, v.w);
+                else __stcg(reinterpret_cast<float4*>(part) + i, v);
+            }
         }
         if (!alive && tid == 0) atomicCAS(p.status, 0, STATUS_TIMEOUT);
-        if (!alive) {
+        if (!alive && warp < KVT_WARPS) {
             // copies and products in flight end (or time out) before their memory is used again; nothing more is begun
-            (void)mbar_wait(bar_raw, phase(0));
-            (void)mbar_wait(bar_raw + 1, phase(1));
+            for (int i = 0; i < KVT_STAGES; ++i) (void)mbar_wait(bar_raw + i, phase(i));
             (void)mbar_wait(bar_s, phase(KVT_STAGES));
             (void)mbar_wait(bar_o, phase(KVT_STAGES + 1));
         }
         tc_fence_before();
-        __syncthreads();                // tensor memory, queries and the walk are free
+        __syncthreads();                // tensor memory, queries and this part's walk are free
         tc_fence_after();
         if (!alive) break;
-        if (tid == 0) *have_s = walk.next(p);
-        __syncthreads();
-        have = *have_s & 1;
     }
-    if (!alive && have) {               // the share's other parts: as if they saw no key
+    if (!alive) {                       // the share's other parts: as if they saw no key
+        KvtWalk& w = walk(cur);
         for (;;) {
-            if (tid == 0) *have_s = walk.next(p);
+            if (tid == 0) w.valid = w.next(p);
             __syncthreads();
-            const bool more = *have_s & 1;
-            if (!more) break;
-            const bool whole = walk.b0 == 0 && walk.b1 == walk.q.units;
-            const int rows = min(KVT_ROWS, walk.q.t * p.grp - walk.i0);
-            float* part = p.partials + (int64_t)(2 * blockIdx.x + (walk.b0 == 0 ? 1 : 0)) * KvtPart<D>::FLOATS;
+            if (!w.valid) break;
+            const int rows = min(KVT_ROWS, w.q.t * p.grp - w.i0);
+            float* part = part_at(w);
             for (int i = tid; i < rows * (D / 4); i += KVT_THREADS) {
-                const int x = walk.i0 + i / (D / 4), j = x / p.grp, d = i % (D / 4) * 4;
-                if (whole) st_elem4(p.o, ((int64_t)(walk.q.tok0 + j) * p.h_q + walk.h * p.grp + x - j * p.grp) * D + d, p.dtype, 0.f, 0.f, 0.f, 0.f);
-                else __stcg(reinterpret_cast<float4*>(part + i / (D / 4) * D + d), make_float4(0.f, 0.f, 0.f, 0.f));
-                if (!whole && d == 0) __stcg(reinterpret_cast<float2*>(part + KVT_ROWS * D) + i / (D / 4), make_float2(-FLT_MAX, 0.f));
+                const int x = i / (D / 4), d = i % (D / 4) * 4;
+                if (is_whole(w)) st_elem4(p.o, out_at(w, x) + d, p.dtype, 0.f, 0.f, 0.f, 0.f);
+                else __stcg(reinterpret_cast<float4*>(part + x * D + d), make_float4(0.f, 0.f, 0.f, 0.f));
+                if (!is_whole(w) && d == 0) __stcg(reinterpret_cast<float2*>(part + KVT_ROWS * D) + x, make_float2(-FLT_MAX, 0.f));
             }
             __syncthreads();
         }
     }
     __syncthreads();
-    if (warp == 1) tmem_free(tmem, KVT_TMEM);
+    if (warp == 1) tmem_free(tm_s(), KVT_TMEM);
 }
 
 // Joins the parts of the tiles that more than one CTA of kda_kv4_tree_kernel

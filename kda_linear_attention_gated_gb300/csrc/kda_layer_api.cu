@@ -82,8 +82,9 @@ int launch_tree(kda::Kv4AttendParams& prm, int64_t list, uint32_t flags, cudaStr
     int occ = 0, sms = 0;
     const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::KVT_THREADS, SM::BYTES, &occ, &sms);
     if (rc != KDA_OK) return rc;
-    // two CTAs' tensor memory fits an SM; none without four units
-    int64_t grid = std::min<int64_t>((int64_t)std::min(occ, 2) * sms, kda::KVT_MAX_CTAS);
+    // every CTA resident (the occupancy call does not know how much tensor memory a kernel takes and answers 1); none
+    // without four units
+    int64_t grid = std::min<int64_t>((int64_t)SM::CTAS * sms, kda::KVT_MAX_CTAS);
     grid = std::max<int64_t>(1, std::min(grid, list / 4));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
