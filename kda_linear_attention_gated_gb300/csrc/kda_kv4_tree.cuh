@@ -38,6 +38,21 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)more) : "memory");
 }
+// The same with a in tensor memory: a row a lane, two of its elements a column.
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool more) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)more) : "memory");
+}
+// A phase that is most likely complete: one test without the scheduler's help first.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0 || mbar_wait(bar, parity);
+}
 // 32 columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&x)[32]) {
     uint32_t r[32];
@@ -65,10 +80,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&x)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&x)[16]) {
-    uint32_t r[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n\t"
         "tcgen05.wait::st.sync.aligned;"
@@ -106,17 +118,19 @@ constexpr int KVT_TMEM = 256;            // columns: scores and sums; two CTAs a
 
 template <int D, bool SPLIT> struct KvtSmem {
     static constexpr int SLABS = D / 64;                         // 64-channel stretches, 128 bytes a row
-    static constexpr int Q = SLABS * KVT_ROWS * 128, K = SLABS * KVT_KEYS * 128, P = KVT_ROWS * 128;
+    static constexpr int Q = SLABS * KVT_ROWS * 128, K = SLABS * KVT_KEYS * 128;
     static constexpr int STAGE = 4 * Kv4<D>::BLOCK;
-    static constexpr int OFF_Q = 0, OFF_K = OFF_Q + Q * (SPLIT ? 2 : 1), OFF_V = OFF_K + K, OFF_P = OFF_V + K,
-                         OFF_RAW = OFF_P + P * (SPLIT ? 2 : 1), OFF_ROWF = OFF_RAW + KVT_STAGES * STAGE,
+    static constexpr int OFF_Q = 0, OFF_K = OFF_Q + Q * (SPLIT ? 2 : 1), OFF_V = OFF_K + 2 * K,       // keys of even and odd units
+                         OFF_RAW = OFF_V + K, OFF_ROWF = OFF_RAW + KVT_STAGES * STAGE,
                          OFF_MAX = OFF_ROWF + KVT_ROWS * 4,      // [2][128] halves' maxima, then sums
                          OFF_ROWNAN = OFF_MAX + 2 * KVT_ROWS * 4,     // [128] value groups in which a row has seen a NaN
                          OFF_NAN = OFF_ROWNAN + KVT_ROWS * 4,    // [2][8] tokens of an even or odd unit whose value group is NaN
                          OFF_BAR = OFF_NAN + 2 * 8 * 8,              // raw [stages], scores, sums
                          OFF_MISC = OFF_BAR + 8 * 8,             // tensor memory base, blocks not there [stages]
                          OFF_WALK = OFF_MISC + 32, BYTES = OFF_WALK + 2 * 128 + 1024;       // and 1024 to align
-    static_assert(KVT_ROWS * D * (SPLIT ? 4 : 2) <= OFF_RAW - OFF_K, "a tile's queries as they come");
+    // rows of a tile's queries that are fetched together, as they come, to where keys and values will be
+    static __host__ __device__ constexpr int fetched(int es) { return KVT_ROWS * D * es <= OFF_RAW - OFF_K ? KVT_ROWS : KVT_ROWS / 2; }
+    static_assert(KVT_ROWS / 2 * D * (SPLIT ? 4 : 2) <= OFF_RAW - OFF_K && KVT_ROWS * D * 4 <= OFF_RAW, "queries in, sums out");
     // CTAs an SM (228 KB of shared memory, 1 KB of it taken for each)
     static constexpr int CTAS = 2 * (BYTES + 1024) <= 228 * 1024 ? 2 : 1;
 };
@@ -139,6 +153,15 @@ template <int N> __device__ __forceinline__ void ld_shared(const void* p, int i,
         x[e] = f.x;
         x[e + 1] = f.y;
     }
+}
+
+// Whether any thread of two warps says so; barrier `id` is theirs.
+__device__ __forceinline__ bool pair_any(int id, bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"((uint32_t)yes) : "memory");
+    return r != 0;
 }
 
 // One request's part of the work (see Kv4Req), units of 64 keys.
@@ -289,7 +312,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint8_t *Q = smem + SM::OFF_Q, *K = smem + SM::OFF_K, *V = smem + SM::OFF_V, *P = smem + SM::OFF_P, *raw = smem + SM::OFF_RAW;
+    uint8_t *Q = smem + SM::OFF_Q, *K = smem + SM::OFF_K, *V = smem + SM::OFF_V, *raw = smem + SM::OFF_RAW;
     float* rowf = reinterpret_cast<float*>(smem + SM::OFF_ROWF);
     uint32_t* row_nan = reinterpret_cast<uint32_t*>(smem + SM::OFF_ROWNAN);
     float* half_max = reinterpret_cast<float*>(smem + SM::OFF_MAX);
@@ -355,6 +378,8 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
     // read again where it is needed: registers are short
     auto tm_s = [&]() { return *static_cast<volatile uint32_t*>(misc); };
     auto tm_o = [&]() { return tm_s() + KVT_KEYS; };
+    auto tm_p = [&]() { return tm_o() + D; };       // probabilities, two a column, and with SPLIT their remainders
+    static_assert(KVT_KEYS + D + (SPLIT ? 2 : 1) * KVT_KEYS / 2 <= KVT_TMEM, "tensor memory");
     if (*any_empty) {   // requests without a visible key: zero rows
         for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
             const Kv4Req q = kvt_request(p, r);
@@ -420,37 +445,44 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             }
             __syncwarp();
             constexpr uint32_t id_s = tc_idesc(KVT_ROWS, KVT_KEYS, false), id_o = tc_idesc(KVT_ROWS, D, true);
-            const uint32_t s_at = tm_s(), o_at = tm_o();
-            const uint64_t dQ = tc_desc(smem_u32(Q), 16), dK = tc_desc(smem_u32(K), 16), dP = tc_desc(smem_u32(P), 16),
-                           dV = tc_desc(smem_u32(V), KVT_KEYS * 128);
+            const uint32_t s_at = tm_s(), o_at = tm_o(), p_at = tm_p();
+            const uint64_t dQ = tc_desc(smem_u32(Q), 16), dK = tc_desc(smem_u32(K), 16), dV = tc_desc(smem_u32(V), KVT_KEYS * 128);
             auto add_values = [&](bool more) {
 #pragma unroll
                 for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
                     for (int k = 0; k < KVT_KEYS / 16; ++k)
-                        tc_mma(o_at, tc_step(dP, part * SM::P + k * 32), tc_step(dV, k * 2048), id_o, more || part + k > 0);
+                        tc_mma_ta(o_at, p_at + part * (KVT_KEYS / 2) + k * 8, tc_step(dV, k * 2048), id_o, more || part + k > 0);
                 tc_commit(bar_o);
             };
-            for (int b = b0; b <= b1; ++b) {
-                alive = __syncthreads_and(true);
+            int ready = 0;              // the stage of unit b + 1
+            for (int b = b0 - 1; b <= b1; ++b) {
+                bool ok = true;         // codes b + 1 are there
+                if (b + 1 < b1) {
+                    ok = mbar_wait(bar_raw + ready, phase(ready));
+                    if (ok) phases ^= 1u << ready;
+                    ready = ready + 1 == KVT_STAGES ? 0 : ready + 1;
+                }
+                alive = __syncthreads_and(ok);
                 if (!alive) break;
+                const bool rare = nan_any[(b - 1) & 1] != 0;
                 if (tc_elect()) {
                     tc_fence_after();
-                    if (b < b1) {
+                    if (b >= b0 && b < b1) {
+                        const uint64_t dKb = tc_step(dK, (b & 1) * SM::K);
 #pragma unroll
                         for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k)
                                 tc_mma(s_at, tc_step(dQ, part * SM::Q + k / 4 * (KVT_ROWS * 128) + k % 4 * 32),
-                                       tc_step(dK, k / 4 * (KVT_KEYS * 128) + k % 4 * 32), id_s, part + k > 0);
+                                       tc_step(dKb, k / 4 * (KVT_KEYS * 128) + k % 4 * 32), id_s, part + k > 0);
                         tc_commit(bar_s);
                     }
                     if (b > b0) add_values(b > b0 + 1);
                 }
                 __syncwarp();
-                const bool rare = nan_any[(b - 1) & 1] != 0;
-                if (b + 2 < b1) fetch(b + 2);           // into the stage of the unit before
-                if (rare) __syncthreads();              // the others look through that unit's tokens
+                if (b >= b0 && b + 2 < b1) fetch(b + 2);        // into the stage of unit b - 1
+                if (rare) __syncthreads();                      // the others look through that unit's tokens
             }
             alive = __syncthreads_and(alive);
         } else {
@@ -461,75 +493,79 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             {
                 const int es = p.dtype == 0 ? 4 : 2, chunks = D * es / 16;       // 16-byte pieces of a row
                 const uint32_t hold = smem_u32(K);
-#pragma unroll 4
-                for (int i = tid; i < rows * chunks; i += 32 * KVT_WARPS) {
-                    const int x = i / chunks, c = i - x * chunks, j = (w.i0 + x) / p.grp;
-                    const int64_t at = (int64_t)(req.tok0 + j) * p.q_stride + (int64_t)(w.h * p.grp + w.i0 + x - j * p.grp) * D;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                 ::"r"(hold + i * 16), "l"(static_cast<const char*>(p.q) + at * es + c * 16) : "memory");
-                }
-                const int hr = p.rot >> 1, w0 = warp * (KVT_ROWS / KVT_WARPS);
-                int pos = 0;            // of the lane's row of the warp's
-                if (lane < KVT_ROWS / KVT_WARPS && w0 + lane < rows) {
-                    const int j = (w.i0 + w0 + lane) / p.grp;
-                    pos = req.ctx + __popcll(tree_mask(p.tree, req.tok0 + j, j)) - 1;
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                asm volatile("bar.sync 5, 256;" ::: "memory");
+                const int most = SM::fetched(es), hr = p.rot >> 1;
                 constexpr int E = D / 32;
                 const int d = lane * E;
                 const bool first = d < hr;
+#pragma unroll 1
+                for (int from = 0; from < KVT_ROWS; from += most) {
 #pragma unroll 4
-                for (int k = 0; k < KVT_ROWS / KVT_WARPS; ++k) {
-                    const int i = w0 + k;
-                    float x[E] = {}, y[E] = {}, cs[E], sn[E] = {};
+                    for (int i = tid; i < min(most, rows - from) * chunks; i += 32 * KVT_WARPS) {
+                        const int x = i / chunks, c = i - x * chunks, y = w.i0 + from + x, j = y / p.grp;
+                        const int64_t at = (int64_t)(req.tok0 + j) * p.q_stride + (int64_t)(w.h * p.grp + y - j * p.grp) * D;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                     ::"r"(hold + i * 16), "l"(static_cast<const char*>(p.q) + at * es + c * 16) : "memory");
+                    }
+                    const int each = most / KVT_WARPS, w0 = from + warp * each;
+                    int pos = 0;            // of the lane's row of the warp's
+                    if (lane < each && w0 + lane < rows) {
+                        const int j = (w.i0 + w0 + lane) / p.grp;
+                        pos = req.ctx + __popcll(tree_mask(p.tree, req.tok0 + j, j)) - 1;
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    asm volatile("bar.sync 5, 256;" ::: "memory");
+#pragma unroll 4
+                    for (int k = 0; k < each; ++k) {
+                        const int i = w0 + k;
+                        float x[E] = {}, y[E] = {}, cs[E], sn[E] = {};
 #pragma unroll
-                    for (int e = 0; e < E; ++e) cs[e] = 1.f;
-                    const int64_t at = (int64_t)__shfl_sync(0xffffffffu, pos, k) * hr;
-                    if (i < rows) {
-                        ld_shared<E>(K, i * D + d, p.dtype, x);
-                        if (d < p.rot) {
-                            if (p.inter) {
-                                ld_elems<E / 2>(p.cos, at + d / 2, 0, cs);
-                                ld_elems<E / 2>(p.sin, at + d / 2, 0, sn);
+                        for (int e = 0; e < E; ++e) cs[e] = 1.f;
+                        const int64_t at = (int64_t)__shfl_sync(0xffffffffu, pos, k) * hr;
+                        if (i < rows) {
+                            ld_shared<E>(K, (i - from) * D + d, p.dtype, x);
+                            if (d < p.rot) {
+                                if (p.inter) {
+                                    ld_elems<E / 2>(p.cos, at + d / 2, 0, cs);
+                                    ld_elems<E / 2>(p.sin, at + d / 2, 0, sn);
 #pragma unroll
-                                for (int e = E / 2 - 1; e >= 0; --e) {
-                                    const float a = x[2 * e], b = x[2 * e + 1];
-                                    x[2 * e] = a * cs[e] - b * sn[e];
-                                    x[2 * e + 1] = b * cs[e] + a * sn[e];
+                                    for (int e = E / 2 - 1; e >= 0; --e) {
+                                        const float a = x[2 * e], b = x[2 * e + 1];
+                                        x[2 * e] = a * cs[e] - b * sn[e];
+                                        x[2 * e + 1] = b * cs[e] + a * sn[e];
+                                    }
+                                } else {
+                                    ld_shared<E>(K, (i - from) * D + (first ? d + hr : d - hr), p.dtype, y);
+                                    ld_elems<E>(p.cos, at + (first ? d : d - hr), 0, cs);
+                                    ld_elems<E>(p.sin, at + (first ? d : d - hr), 0, sn);
+#pragma unroll
+                                    for (int e = 0; e < E; ++e) x[e] = x[e] * cs[e] + (first ? -y[e] : y[e]) * sn[e];
                                 }
-                            } else {
-                                ld_shared<E>(K, i * D + (first ? d + hr : d - hr), p.dtype, y);
-                                ld_elems<E>(p.cos, at + (first ? d : d - hr), 0, cs);
-                                ld_elems<E>(p.sin, at + (first ? d : d - hr), 0, sn);
-#pragma unroll
-                                for (int e = 0; e < E; ++e) x[e] = x[e] * cs[e] + (first ? -y[e] : y[e]) * sn[e];
                             }
                         }
-                    }
-                    float amax = 0.f;
+                        float amax = 0.f;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
+                        for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    // as in kda_kv4_attend_kernel
-                    const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
-                    const float down =
-                        __uint_as_float(amax < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
-                    uint8_t* to = Q + (d / 64) * (KVT_ROWS * 128) + i * 128 + (((d % 64 / 8) ^ (i & 7)) << 4) + d % 8 * 2;
+                        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        // as in kda_kv4_attend_kernel
+                        const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
+                        const float down =
+                            __uint_as_float(amax < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
+                        uint8_t* to = Q + (d / 64) * (KVT_ROWS * 128) + i * 128 + (((d % 64 / 8) ^ (i & 7)) << 4) + d % 8 * 2;
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float u = x[e] * down, v = x[e + 1] * down;
-                        const __half2 hi = __floats2half2_rn(u, v);
-                        *reinterpret_cast<__half2*>(to + e * 2) = hi;
-                        if constexpr (SPLIT) {
-                            const float2 f = __half22float2(hi);
-                            *reinterpret_cast<__half2*>(to + SM::Q + e * 2) = __floats2half2_rn(u - f.x, v - f.y);
+                        for (int e = 0; e < E; e += 2) {
+                            const float u = x[e] * down, v = x[e + 1] * down;
+                            const __half2 hi = __floats2half2_rn(u, v);
+                            *reinterpret_cast<__half2*>(to + e * 2) = hi;
+                            if constexpr (SPLIT) {
+                                const float2 f = __half22float2(hi);
+                                *reinterpret_cast<__half2*>(to + SM::Q + e * 2) = __floats2half2_rn(u - f.x, v - f.y);
+                            }
                         }
+                        if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
                     }
-                    if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
+                    asm volatile("bar.sync 5, 256;" ::: "memory");      // other queries, or keys, go there
                 }
-                asm volatile("bar.sync 5, 256;" ::: "memory");      // the keys go where the queries were
             }
             // ---- what this thread's row sees of the tree and of the context ----
             uint64_t own = 0;
@@ -547,6 +583,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             };
             float m = -FLT_MAX, l = 0.f;
             if (half == 0) row_nan[row] = 0;
+            const float c = rowf[row];
             bool ok = true;
             int st = 0;                 // the stage of unit b + 1, whose keys are next
 
@@ -566,21 +603,14 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             // Unit b's scores and values, and unit b + 1's keys while the tensor cores are on the scores.
 #pragma unroll 1
             for (int b = b0 - 1; b < b1; ++b) {
-                if (b >= b0) {
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    alive = __syncthreads_and(ok);      // keys b, probabilities and values b - 1 are written, codes b - 1 read
-                    if (!alive) break;
-                    find_nan(b - 1);
-                    ok = mbar_wait(bar_s, phase(KVT_STAGES));
-                    if (ok) phases ^= 1u << KVT_STAGES;
-                    tc_fence_after();
-                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                alive = __syncthreads_and(ok);      // keys b, probabilities and values b - 1 are written, codes b - 1 read, codes b + 1 there
+                if (!alive) break;
+                if (b > b0) find_nan(b - 1);
                 // ---- keys: a token's quarter a thread ----
                 if (b + 1 < b1) {
-                    if (ok) ok = mbar_wait(bar_raw + st, phase(st));
-                    if (ok) {
-                        phases ^= 1u << st;
+                    {
                         const int key = tid >> 2, q = tid & 3;
                         const uint8_t* B = raw + st * SM::STAGE + (key >> 4) * F::BLOCK;
                         const bool gone = missing[st] >> (key >> 4) & 1u;
@@ -590,7 +620,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                             if (gone) s2 = 0;
                             const uint32_t sc = cvt_e4m3x2_f16x2(s2);
                             const uint32_t code[4] = {c.x, c.y, c.z, c.w};
-                            uint8_t* to = K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
+                            uint8_t* to = K + ((b + 1) & 1) * SM::K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 uint32_t v[4];
@@ -611,7 +641,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                                 cvt_e2m1x8_f16(code[i], v);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) v[e] = hmul2_half<false>(v[e], sc);
-                                *reinterpret_cast<uint4*>(K + key * 128 + (((q * 2 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                                *reinterpret_cast<uint4*>(K + ((b + 1) & 1) * SM::K + key * 128 + (((q * 2 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                             }
                         }
                     }
@@ -624,8 +654,10 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 // keys that every row sees: [ctx + t - window, ctx)
                 const bool masked = key0 + KVT_KEYS > req.ctx || (p.window > 0 && key0 < req.ctx + req.t - p.window) || miss != 0;
                 // ---- scores to probabilities, when the last unit's are done with ----
+                ok = mbar_poll(bar_s, phase(KVT_STAGES));
+                if (ok) phases ^= 1u << KVT_STAGES;
                 if (ok && b > b0) {
-                    ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
+                    ok = mbar_poll(bar_o, phase(KVT_STAGES + 1));
                     if (ok) phases ^= 1u << (KVT_STAGES + 1);
                 }
                 // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
@@ -644,50 +676,55 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(s[i], s[i + 1]), top);
                 }
-                half_max[half * KVT_ROWS + row] = top;
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-                if (ok) {
-                    const float c = rowf[row];
-                    top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]) * c;
+                top *= c;
+                // seldom: a score above its row's running maximum by more than the slack, in either half
+                if (pair_any(1 + (warp & 3), top > m + KV4_SLACK)) {
+                    half_max[half * KVT_ROWS + row] = top;
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+                    top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]);
                     const bool grow = top > m + KV4_SLACK;
-                    if (__any_sync(0xffffffffu, grow)) {        // both warps alike: the same rows
-                        const float f = grow ? ex2f(m - top) : 1.f;
-                        if (grow) m = top;
-                        l *= f;
-                        if (b > b0) {
+                    const float f = grow ? ex2f(m - top) : 1.f;
+                    if (grow) m = top;
+                    l *= f;
+                    if (ok && b > b0) {
 #pragma unroll 1
-                            for (int k = 0; k < D / 32; ++k) {
-                                const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
-                                float o[16];
-                                tmem_ld16(at, o);
+                        for (int k = 0; k < D / 32; ++k) {
+                            const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
+                            float o[16];
+                            uint32_t r[16];
+                            tmem_ld16(at, o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= f;
-                                tmem_st16(at, o);
-                            }
+                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * f);
+                            tmem_st16(at, r);
                         }
                     }
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");      // half_max is read
+                }
+                if (ok) {
                     const float neg = KV4_LIFT - m;
                     float2 sum = make_float2(l, 0.f);
-                    uint8_t* to = P + row * 128;
+                    uint32_t hi[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 x = __ffma2_rn(make_float2(s[i + 2 * e], s[i + 2 * e + 1]), make_float2(c, c), make_float2(neg, neg));
-                            const float x0 = ex2f(x.x), x1 = ex2f(x.y);
-                            sum = __fadd2_rn(sum, make_float2(x0, x1));
-                            const __half2 hh = __floats2half2_rn(x0, x1);
-                            hi[e] = *reinterpret_cast<const uint32_t*>(&hh);
-                            if constexpr (SPLIT) {
-                                const float2 f = __half22float2(hh);
-                                const __half2 rest = __floats2half2_rn(x0 - f.x, x1 - f.y);
-                                lo[e] = *reinterpret_cast<const uint32_t*>(&rest);
-                            }
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(c, c), make_float2(neg, neg));
+                        const float x0 = ex2f(x.x), x1 = ex2f(x.y);
+                        sum = __fadd2_rn(sum, make_float2(x0, x1));
+                        const __half2 hh = __floats2half2_rn(x0, x1);
+                        hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
+                        if constexpr (SPLIT) {
+                            const float2 f = __half22float2(hh);
+                            s[2 * i] = x0 - f.x;
+                            s[2 * i + 1] = x1 - f.y;
                         }
-                        uint4* at = reinterpret_cast<uint4*>(to + (((half * 4 + i / 8) ^ (row & 7)) << 4));
-                        *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if constexpr (SPLIT) at[SM::P / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    tmem_st16(tm_p() + lane_base + 16 * half, hi);
+                    if constexpr (SPLIT) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const __half2 rest = __floats2half2_rn(s[2 * i], s[2 * i + 1]);
+                            hi[i] = *reinterpret_cast<const uint32_t*>(&rest);
+                        }
+                        tmem_st16(tm_p() + lane_base + KVT_KEYS / 2 + 16 * half, hi);
                     }
                     l = sum.x + sum.y;
                     // ---- values: 16 channels (64: 8) of two tokens a thread ----
@@ -733,7 +770,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                     }
                 }
             }
-            if (alive) {                // the last unit's probabilities and values
+            if (alive) {                // the last unit's
                 fence_proxy_async_smem();
                 tc_fence_before();
                 alive = __syncthreads_and(ok);
@@ -784,11 +821,14 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             }
         }
         if (!alive && tid == 0) atomicCAS(p.status, 0, STATUS_TIMEOUT);
-        if (!alive && warp < KVT_WARPS) {
+        if (!alive) {
             // copies and products in flight end (or time out) before their memory is used again; nothing more is begun
-            for (int i = 0; i < KVT_STAGES; ++i) (void)mbar_wait(bar_raw + i, phase(i));
-            (void)mbar_wait(bar_s, phase(KVT_STAGES));
-            (void)mbar_wait(bar_o, phase(KVT_STAGES + 1));
+            if (warp == KVT_WARPS) {
+                for (int i = 0; i < KVT_STAGES; ++i) (void)mbar_wait(bar_raw + i, phase(i));
+            } else {
+                (void)mbar_wait(bar_s, phase(KVT_STAGES));
+                (void)mbar_wait(bar_o, phase(KVT_STAGES + 1));
+            }
         }
         tc_fence_before();
         __syncthreads();                // tensor memory, queries and this part's walk are free
