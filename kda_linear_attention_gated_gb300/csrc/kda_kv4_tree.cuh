@@ -111,7 +111,7 @@ constexpr int KVT_STAGES = 3;            // units of codes in flight
 constexpr int KVT_PART = 6;              // what beginning and ending a part costs a CTA, in units
 constexpr int KVT_FIRST = KVT_PART + 2, KVT_LAST = 2;   // what a cut leaves before and after it in a tile (see Kv4Shape)
 constexpr int KVT_MAX_CTAS = 304;        // two for each of 152 SMs
-constexpr int KVT_MIN_ROWS = 32;         // narrower trees go to kda_kv4_attend_kernel
+constexpr int KVT_MIN_ROWS = 48;         // narrower trees go to kda_kv4_attend_kernel
 constexpr int KVT_JOIN_GROUPS = 16;      // CTAs that join a tile
 constexpr int KVT_COUNTERS = 4096;       // bytes at the head of the workspace that kda_kv4_attend_kernel's counters take
 constexpr int KVT_TMEM = 256;            // columns: scores and sums; two CTAs an SM share 512
@@ -512,57 +512,95 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                         const int j = (w.i0 + w0 + lane) / p.grp;
                         pos = req.ctx + __popcll(tree_mask(p.tree, req.tok0 + j, j)) - 1;
                     }
+                    // the rotation's rows into the first-level cache, a line a load, all at once
+                    const int lines = 2 * ((hr + 31) / 32);
+                    for (int e0 = 0; e0 < each * lines; e0 += 32) {
+                        const int e = min(e0 + lane, each * lines - 1), k = e / lines, line = e - k * lines;
+                        const float* entry = (line & 1 ? p.sin : p.cos) + (int64_t)__shfl_sync(0xffffffffu, pos, k) * hr + (line >> 1) * 32;
+                        float x;
+                        asm volatile("ld.global.ca.f32 %0, [%1];" : "=f"(x) : "l"(entry));
+                    }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     asm volatile("bar.sync 5, 256;" ::: "memory");
-#pragma unroll 4
-                    for (int k = 0; k < each; ++k) {
-                        const int i = w0 + k;
-                        float x[E] = {}, y[E] = {}, cs[E], sn[E] = {};
+                    // four rows at a time, step by step, so that their latencies overlap
+                    constexpr int G = 4;
+                    const int dtype = SPLIT ? p.dtype : 2;
+                    const bool turns = d < p.rot;
+#pragma unroll 1
+                    for (int k = 0; k < each; k += G) {
+                        float x[G][E];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) cs[e] = 1.f;
-                        const int64_t at = (int64_t)__shfl_sync(0xffffffffu, pos, k) * hr;
-                        if (i < rows) {
-                            ld_shared<E>(K, (i - from) * D + d, p.dtype, x);
-                            if (d < p.rot) {
-                                if (p.inter) {
-                                    ld_elems<E / 2>(p.cos, at + d / 2, 0, cs);
-                                    ld_elems<E / 2>(p.sin, at + d / 2, 0, sn);
+                        for (int r = 0; r < G; ++r) {
+                            ld_shared<E>(K, (w0 + k + r - from) * D + d, dtype, x[r]);
+                            if (w0 + k + r >= rows)
 #pragma unroll
-                                    for (int e = E / 2 - 1; e >= 0; --e) {
-                                        const float a = x[2 * e], b = x[2 * e + 1];
-                                        x[2 * e] = a * cs[e] - b * sn[e];
-                                        x[2 * e + 1] = b * cs[e] + a * sn[e];
-                                    }
-                                } else {
-                                    ld_shared<E>(K, (i - from) * D + (first ? d + hr : d - hr), p.dtype, y);
-                                    ld_elems<E>(p.cos, at + (first ? d : d - hr), 0, cs);
-                                    ld_elems<E>(p.sin, at + (first ? d : d - hr), 0, sn);
+                                for (int e = 0; e < E; ++e) x[r][e] = 0.f;
+                        }
+                        int64_t at[G];
 #pragma unroll
-                                    for (int e = 0; e < E; ++e) x[e] = x[e] * cs[e] + (first ? -y[e] : y[e]) * sn[e];
+                        for (int r = 0; r < G; ++r) at[r] = (int64_t)__shfl_sync(0xffffffffu, pos, k + r) * hr;
+                        if (turns && p.inter) {
+                            float cs[G][E / 2], sn[G][E / 2];
+#pragma unroll
+                            for (int r = 0; r < G; ++r) {
+                                ld_elems<E / 2>(p.cos, at[r] + d / 2, 0, cs[r]);
+                                ld_elems<E / 2>(p.sin, at[r] + d / 2, 0, sn[r]);
+                            }
+#pragma unroll
+                            for (int r = 0; r < G; ++r)
+#pragma unroll
+                                for (int e = 0; e < E / 2; ++e) {
+                                    const float a = x[r][2 * e], b = x[r][2 * e + 1];
+                                    x[r][2 * e] = a * cs[r][e] - b * sn[r][e];
+                                    x[r][2 * e + 1] = b * cs[r][e] + a * sn[r][e];
+                                }
+                        } else if (turns) {
+                            float cs[G][E], sn[G][E], y[G][E];
+                            const int pair = first ? d + hr : d - hr, entry = first ? d : d - hr;
+#pragma unroll
+                            for (int r = 0; r < G; ++r) {
+                                ld_elems<E>(p.cos, at[r] + entry, 0, cs[r]);
+                                ld_elems<E>(p.sin, at[r] + entry, 0, sn[r]);
+                                ld_shared<E>(K, (w0 + k + r - from) * D + pair, dtype, y[r]);
+                            }
+#pragma unroll
+                            for (int r = 0; r < G; ++r)
+#pragma unroll
+                                for (int e = 0; e < E; ++e) {
+                                    const float v = x[r][e] * cs[r][e] + (first ? -y[r][e] : y[r][e]) * sn[r][e];
+                                    x[r][e] = w0 + k + r < rows ? v : 0.f;
+                                }
+                        }
+                        float amax[G];
+#pragma unroll
+                        for (int r = 0; r < G; ++r) {
+                            amax[r] = 0.f;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) amax[r] = fmaxf(amax[r], fabsf(x[r][e]));
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                            for (int r = 0; r < G; ++r) amax[r] = fmaxf(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], o));
+#pragma unroll
+                        for (int r = 0; r < G; ++r) {
+                            // as in kda_kv4_attend_kernel
+                            const int i = w0 + k + r, z = amax[r] > 1e-30f && amax[r] < 1e37f ? (int)(__float_as_uint(amax[r]) >> 23) - 126 : 0;
+                            const float down = __uint_as_float(
+                                amax[r] < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
+                            uint8_t* to = Q + (d / 64) * (KVT_ROWS * 128) + i * 128 + (((d % 64 / 8) ^ (i & 7)) << 4) + d % 8 * 2;
+#pragma unroll
+                            for (int e = 0; e < E; e += 2) {
+                                const float u = x[r][e] * down, v = x[r][e + 1] * down;
+                                const __half2 hi = __floats2half2_rn(u, v);
+                                *reinterpret_cast<__half2*>(to + e * 2) = hi;
+                                if constexpr (SPLIT) {
+                                    const float2 f = __half22float2(hi);
+                                    *reinterpret_cast<__half2*>(to + SM::Q + e * 2) = __floats2half2_rn(u - f.x, v - f.y);
                                 }
                             }
+                            if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
                         }
-                        float amax = 0.f;
-#pragma unroll
-                        for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                        // as in kda_kv4_attend_kernel
-                        const int z = amax > 1e-30f && amax < 1e37f ? (int)(__float_as_uint(amax) >> 23) - 126 : 0;
-                        const float down =
-                            __uint_as_float(amax < 1e37f ? (uint32_t)(127 - z) << 23 | (__float_as_uint(p.scale_log2) & 0x80000000u) : 0x7fffffffu);
-                        uint8_t* to = Q + (d / 64) * (KVT_ROWS * 128) + i * 128 + (((d % 64 / 8) ^ (i & 7)) << 4) + d % 8 * 2;
-#pragma unroll
-                        for (int e = 0; e < E; e += 2) {
-                            const float u = x[e] * down, v = x[e + 1] * down;
-                            const __half2 hi = __floats2half2_rn(u, v);
-                            *reinterpret_cast<__half2*>(to + e * 2) = hi;
-                            if constexpr (SPLIT) {
-                                const float2 f = __half22float2(hi);
-                                *reinterpret_cast<__half2*>(to + SM::Q + e * 2) = __floats2half2_rn(u - f.x, v - f.y);
-                            }
-                        }
-                        if (lane == 0) rowf[i] = fmaxf(1e-30f, fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + z) << 23));
                     }
                     asm volatile("bar.sync 5, 256;" ::: "memory");      // other queries, or keys, go there
                 }
