@@ -6,6 +6,8 @@
 // only bits up to j are looked at.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_common.cuh"
 #include "kda_conv.cuh"
 
@@ -189,10 +191,10 @@ constexpr int TREE_WARPS_MAX = 4;
 // Shared memory of a CTA of `warps` warps with at most t tokens a request.
 template <typename ST> struct TreeSmem {
     static constexpr int VEC = StateVec<ST>::VEC, CW = 2 * VEC;   // columns of a lane, of a warp
-    static __host__ __device__ constexpr int vecs(int t) { return 3 * t * KMAX * 4; }              // k, alpha, q of each token
+    static __host__ __device__ constexpr int vecs(int t, int k) { return 3 * t * k * 4; }          // k, alpha, q of each token
     static __host__ __device__ constexpr int delta(int t, int warps) { return t * warps * CW * 4; }
-    static __host__ __device__ constexpr int bytes(int t, int warps) {
-        return vecs(t) + delta(t, warps) + warps * 32 * 8 * 16 + t * (8 + 8 + 8 + 4);
+    static __host__ __device__ constexpr int bytes(int t, int k, int warps) {
+        return vecs(t, k) + delta(t, warps) + warps * 32 * 8 * 16 + t * (8 + 8 + 8 + 4);
     }
 };
 
@@ -213,16 +215,20 @@ template <typename ST> struct TreeSmem {
 // element and ancestor, no sums, the same bits as on the way there.  So states
 // carry fp32 along every path whatever the pool's type, and do not depend on
 // the order of siblings.
-template <typename ST, typename QT>
-__global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const StepParams p, const uint64_t* tree) {
+//
+// FULL: K = V = 128, so that every lane has all its rows and columns and the
+// places of a tile are constants.
+template <typename ST, typename QT, bool FULL>
+__global__ void __launch_bounds__(TREE_WARPS_MAX * 32, 3) kda_tree_kernel(const StepParams p, const uint64_t* tree) {
     using SV = StateVec<ST>;
     constexpr int VEC = SV::VEC, CW = 2 * VEC, NV = 2 * VEC, P2 = VEC / 2;
     extern __shared__ __align__(128) uint8_t smem[];
+    const int KD = FULL ? KMAX : p.k, VD = FULL ? KMAX : p.v;
     const int warps = blockDim.x >> 5, BV = warps * CW;
     float* kh = reinterpret_cast<float*>(smem);
-    float* al = kh + p.t * KMAX;
-    float* qh = al + p.t * KMAX;
-    float* du = qh + p.t * KMAX;                                            // [t][BV]: v, then delta
+    float* al = kh + p.t * KD;
+    float* qh = al + p.t * KD;
+    float* du = qh + p.t * KD;                                             // [t][BV]: v, then delta
     uint4* stash = reinterpret_cast<uint4*>(du + p.t * BV);                 // [8][threads]
     unsigned long long* masks = reinterpret_cast<unsigned long long*>(stash + 8 * blockDim.x);
     unsigned long long* child = masks + p.t;
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
     int32_t* snaps = reinterpret_cast<int32_t*>(sc + p.t);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cblocks = (p.v + BV - 1) / BV;
+    const int cblocks = (VD + BV - 1) / BV;
     const int cb = (int)blockIdx.x % cblocks, nh = (int)blockIdx.x / cblocks, n = nh / p.hv, h = nh - n * p.hv;
     for (int j = tid; j < p.t; j += blockDim.x) child[j] = 0;
     cudaTriggerProgrammaticLaunchCompletion();
@@ -262,20 +268,20 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
     }
     const int c0 = cb * BV + warp * CW + (lane & 1) * VEC;                  // the lane's first column
     const int r0 = (lane >> 1) * 4;                                         // and row; its i-th is r0 + i % 4 + 64 (i / 4)
-    const bool mine = c0 < p.v;
+    const bool mine = c0 < VD;
     if (slot < 0) {     // a padding request
         for (int i = tid; i < T * BV; i += blockDim.x) {
             const int j = i / BV, c = cb * BV + i - j * BV;
-            if (c < p.v) p.o[((int64_t)(tb + j) * p.hv + h) * p.v + c] = 0.f;
+            if (c < VD) p.o[((int64_t)(tb + j) * p.hv + h) * VD + c] = 0.f;
         }
         return;
     }
     const bool rst = p.reset != nullptr && __ldg(p.reset + n) != 0;
     // half 0 and half 1 of the lane's rows are in the state
-    const bool live[2] = {mine && r0 < p.k, mine && r0 + 64 < p.k};
+    const bool live[2] = {FULL || (mine && r0 < KD), FULL || (mine && r0 + 64 < KD)};
     ST* pool = static_cast<ST*>(p.pool);
-    const int64_t tile = (int64_t)r0 * p.v + c0;
-    auto at_row = [&](int i) { return (int64_t)((i & 3) + 64 * (i >> 2)) * p.v; };
+    const int64_t tile = (int64_t)r0 * VD + c0;
+    auto at_row = [&](int i) { return (int64_t)((i & 3) + 64 * (i >> 2)) * VD; };
     uint4 raw[8];
     {
         const ST* from = pool + state_at(p, slot, h) + tile;
@@ -290,60 +296,84 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
     const float gate = scaled ? expf(__ldg(p.a_log + h)) : 1.f;
     constexpr int AHEAD = 4;        // tokens whose loads a warp has on their way
     const int d = 4 * lane;
-    const bool on = d < p.k;
+    const bool on = d < KD;
     float bias[4] = {};
     if (on && scaled && p.dt_bias != nullptr) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) bias[e] = __ldg(p.dt_bias + h * p.k + d + e);
+        for (int e = 0; e < 4; ++e) bias[e] = __ldg(p.dt_bias + h * KD + d + e);
     }
     using QIO = ConvIO<QT, 4>;
     for (int j0 = warp; j0 < T; j0 += AHEAD * warps) {
         typename QIO::R kr[AHEAD], qr[AHEAD];
         float4 ar[AHEAD];
-        float br[AHEAD], vr[AHEAD];
+        float br[AHEAD], vr[AHEAD], vr2[AHEAD];      // a CTA has at most 64 columns
+        static_assert(TREE_WARPS_MAX * CW <= 64, "columns");
         unsigned long long mr[AHEAD];
 #pragma unroll
         for (int x = 0; x < AHEAD; ++x) {
             const int j = min(j0 + x * warps, T - 1);
-            const int64_t tok = tb + j, at = (tok * p.hqk + hq) * p.k + (on ? d : 0);
+            const int64_t tok = tb + j, at = (tok * p.hqk + hq) * KD + (on ? d : 0);
             kr[x] = QIO::ld(static_cast<const QT*>(p.kk) + at);
             qr[x] = QIO::ld(static_cast<const QT*>(p.q) + at);
-            ar[x] = __ldg(reinterpret_cast<const float4*>(p.a + (tok * p.hv + h) * p.k + (on ? d : 0)));
+            ar[x] = __ldg(reinterpret_cast<const float4*>(p.a + (tok * p.hv + h) * KD + (on ? d : 0)));
             br[x] = __ldg(p.b + tok * p.hv + h);
             mr[x] = tree_mask(tree, tok, j) ^ (1ull << j);
-            vr[x] = lane < BV && cb * BV + lane < p.v ? to_f32(static_cast<const QT*>(p.vv)[(tok * p.hv + h) * p.v + cb * BV + lane]) : 0.f;
+const QT* vt = static_cast<const QT*>(p.vv) + (tok * p.hv + h) * VD + cb * BV + lane;
+            vr[x] = lane < BV && cb * BV + lane < VD ? to_f32(vt[0]) : 0.f;
+            vr2[x] = lane + 32 < BV && cb * BV + lane + 32 < VD ? to_f32(vt[32]) : 0.f;
+        }
+        // step by step for all of them, so that their latencies overlap; behind the last token it is done again
+        float k4[AHEAD][4], q4[AHEAD][4], kk[AHEAD], qq[AHEAD], kq[AHEAD];
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) {
+            QIO::widen(kr[x], k4[x]);
+            QIO::widen(qr[x], q4[x]);
+            kk[x] = qq[x] = kq[x] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!on) k4[x][e] = q4[x][e] = 0.f;
+                kk[x] = fmaf(k4[x][e], k4[x][e], kk[x]);
+                qq[x] = fmaf(q4[x][e], q4[x][e], qq[x]);
+                kq[x] = fmaf(k4[x][e], q4[x][e], kq[x]);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                kk[x] += __shfl_xor_sync(0xffffffffu, kk[x], o);
+                qq[x] += __shfl_xor_sync(0xffffffffu, qq[x], o);
+                kq[x] += __shfl_xor_sync(0xffffffffu, kq[x], o);
+            }
+        float g[AHEAD][4];
+        if (scaled) {       // one branch for all
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                const float a[4] = {ar[x].x, ar[x].y, ar[x].z, ar[x].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[x][e] = gate_alpha(a[e], true, gate, bias[e]);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                const float a[4] = {ar[x].x, ar[x].y, ar[x].z, ar[x].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[x][e] = gate_alpha(a[e], false, gate, bias[e]);
+            }
         }
 #pragma unroll
         for (int x = 0; x < AHEAD; ++x) {
-            const int j = j0 + x * warps;
-            if (j >= T) break;
-            float k4[4], q4[4];
-            QIO::widen(kr[x], k4);
-            QIO::widen(qr[x], q4);
-            float kk = 0.f, qq = 0.f, kq = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (!on) k4[e] = q4[e] = 0.f;
-                kk = fmaf(k4[e], k4[e], kk);
-                qq = fmaf(q4[e], q4[e], qq);
-                kq = fmaf(k4[e], q4[e], kq);
+            const int j = min(j0 + x * warps, T - 1);
+            const float rk = __frsqrt_rn(kk[x] + L2_EPS), rq = __frsqrt_rn(qq[x] + L2_EPS);
+            if (FULL || on) {
+                *reinterpret_cast<float4*>(kh + j * KD + d) = make_float4(k4[x][0] * rk, k4[x][1] * rk, k4[x][2] * rk, k4[x][3] * rk);
+                *reinterpret_cast<float4*>(qh + j * KD + d) = make_float4(q4[x][0] * rq, q4[x][1] * rq, q4[x][2] * rq, q4[x][3] * rq);
+                *reinterpret_cast<float4*>(al + j * KD + d) = make_float4(g[x][0], g[x][1], g[x][2], g[x][3]);
             }
-            kk = warp_sum(kk);
-            qq = warp_sum(qq);
-            kq = warp_sum(kq);
-            const float rk = __frsqrt_rn(kk + L2_EPS), rq = __frsqrt_rn(qq + L2_EPS);
-            const float a[4] = {ar[x].x, ar[x].y, ar[x].z, ar[x].w};
-            float g[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) g[e] = on ? gate_alpha(a[e], scaled, gate, bias[e]) : 0.f;
-            *reinterpret_cast<float4*>(kh + j * KMAX + d) = make_float4(k4[0] * rk, k4[1] * rk, k4[2] * rk, k4[3] * rk);
-            *reinterpret_cast<float4*>(qh + j * KMAX + d) = make_float4(q4[0] * rq, q4[1] * rq, q4[2] * rq, q4[3] * rq);
-            *reinterpret_cast<float4*>(al + j * KMAX + d) = make_float4(g[0], g[1], g[2], g[3]);
             if (lane < BV) du[j * BV + lane] = vr[x];
-            for (int c = lane + 32; c < BV; c += 32)
-                du[j * BV + c] = cb * BV + c < p.v ? to_f32(static_cast<const QT*>(p.vv)[((int64_t)(tb + j) * p.hv + h) * p.v + cb * BV + c]) : 0.f;
+            if (lane + 32 < BV) du[j * BV + lane + 32] = vr2[x];
             if (lane == 0) {
-                sc[j] = make_float2(sigmoid_neg(-br[x]), kq * rk * rq);
+                sc[j] = make_float2(sigmoid_neg(-br[x]), kq[x] * rk * rq);
                 masks[j] = mr[x];
                 if (mr[x] != 0) atomicOr(child + tree_top(mr[x]), 1ull << j);
             }
@@ -362,11 +392,19 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
     constexpr int SB = VEC == 4 ? 2 : 1;
     const int vc = lane >> (SB + 1), second = lane >> SB & 1;
     const int my_col = warp * CW + (lane & 1) * VEC + vc;
-    const bool first_of = VEC == 8 || (lane & 2) == 0, live_col = cb * BV + my_col < p.v && first_of;
+    const bool first_of = VEC == 8 || (lane & 2) == 0, live_col = cb * BV + my_col < VD && first_of;
+    // a lane without rows there reads other rows', and k as zero: its states stay zero
+    const int at0 = r0 < KD ? r0 : 0, at1 = r0 + 64 < KD ? r0 + 64 : 0;
     auto vec8 = [&](const float* v, int j, float (&x)[8]) {
-        const float4 lo = *reinterpret_cast<const float4*>(v + j * KMAX + r0), hi = *reinterpret_cast<const float4*>(v + j * KMAX + 64 + r0);
+        const float4 lo = *reinterpret_cast<const float4*>(v + j * KD + at0), hi = *reinterpret_cast<const float4*>(v + j * KD + at1);
         x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
         x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+    };
+    auto key8 = [&](int j, float (&x)[8]) {
+        vec8(kh, j, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!FULL && r0 + 64 * (i >> 2) >= KD) x[i] = 0.f;
     };
     auto deltas = [&](int j, float2 (&d)[P2]) {
 #pragma unroll
@@ -381,24 +419,30 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
         float a[8], k[8];
         float2 d[P2];
         vec8(al, i, a);
-        vec8(kh, i, k);
+        key8(i, k);
         deltas(i, d);
 #pragma unroll
         for (int r = 0; r < 8; ++r)
 #pragma unroll
             for (int x = 0; x < P2; ++x) S[r][x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], __fmul2_rn(S[r][x], make_float2(a[r], a[r])));
     };
-    // Token j, a child of the token whose state S is: outputs, and the state to its snapshot; keep: and to S.
-    auto step = [&](int j, bool keep) {
-        float a[8], k[8];
-        vec8(al, j, a);
-        vec8(kh, j, k);
-        float2 su[P2], sq[P2];
+    // Tokens j[0 .. N), children of the token whose state S is: their outputs, and their deltas to du.  Step by step
+    // for all of them, so that their latencies overlap.
+    auto sums = [&](auto n_of, const int* j) {
+        constexpr int N = decltype(n_of)::value;
+        float f[N][NV], v[N];
+        float2 bs[N];
 #pragma unroll
-        for (int x = 0; x < P2; ++x) su[x] = sq[x] = make_float2(0.f, 0.f);
-        {
-            float q[8];
-            vec8(qh, j, q);
+        for (int i = 0; i < N; ++i) {
+            float a[8], k[8], q[8];
+            vec8(al, j[i], a);
+            vec8(kh, j[i], k);
+            vec8(qh, j[i], q);
+            v[i] = du[j[i] * BV + my_col];
+            bs[i] = sc[j[i]];
+            float2 su[P2], sq[P2];
+#pragma unroll
+            for (int x = 0; x < P2; ++x) su[x] = sq[x] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const float ak = a[r] * k[r], aq = a[r] * q[r];
@@ -408,37 +452,49 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
                     sq[x] = __ffma2_rn(S[r][x], make_float2(aq, aq), sq[x]);
                 }
             }
-        }
-        const float v = du[j * BV + my_col];
-        const float2 bs = sc[j];
-        // sums over the 16 row groups (lane bits 4 .. 1), scattered: value 2 c + s of column c
-        float f[NV];
 #pragma unroll
-        for (int x = 0; x < P2; ++x) {
-            f[4 * x] = su[x].x;
-            f[4 * x + 1] = sq[x].x;
-            f[4 * x + 2] = su[x].y;
-            f[4 * x + 3] = sq[x].y;
+            for (int x = 0; x < P2; ++x) {
+                f[i][4 * x] = su[x].x;
+                f[i][4 * x + 1] = sq[x].x;
+                f[i][4 * x + 2] = su[x].y;
+                f[i][4 * x + 3] = sq[x].y;
+            }
         }
+        // over the 16 row groups (lane bits 4 .. 1), scattered: value 2 c + s of column c
         int m = 16;
 #pragma unroll
         for (int cnt = NV; cnt > 1; cnt >>= 1, m >>= 1) {
             const bool upper = (lane & m) != 0;
 #pragma unroll
-            for (int x = 0; x < cnt / 2; ++x) {
-                const float send = upper ? f[x] : f[x + cnt / 2], keep_f = upper ? f[x + cnt / 2] : f[x];
-                f[x] = keep_f + __shfl_xor_sync(0xffffffffu, send, m);
-            }
+            for (int x = 0; x < cnt / 2; ++x)
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float send = upper ? f[i][x] : f[i][x + cnt / 2], keep = upper ? f[i][x + cnt / 2] : f[i][x];
+                    f[i][x] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                }
         }
-        if constexpr (VEC == 4) f[0] += __shfl_xor_sync(0xffffffffu, f[0], 2);
-        const float other = __shfl_xor_sync(0xffffffffu, f[0], 1 << SB);
-        const float u = second ? other : f[0], pq = second ? f[0] : other;
-        const float delta = bs.x * (v - u);
+        if constexpr (VEC == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i][0] += __shfl_xor_sync(0xffffffffu, f[i][0], 2);
+        }
+        float other[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) other[i] = __shfl_xor_sync(0xffffffffu, f[i][0], 1 << SB);
         __syncwarp();       // v is read
-        if (!second && first_of) du[j * BV + my_col] = delta;
-        if (second && live_col) p.o[((int64_t)(tb + j) * p.hv + h) * p.v + cb * BV + my_col] = fmaf(bs.y, delta, pq) * p.inv_sqrt_k;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float u = second ? other[i] : f[i][0], pq = second ? f[i][0] : other[i], delta = bs[i].x * (v[i] - u);
+            if (!second && first_of) du[j[i] * BV + my_col] = delta;
+            if (second && live_col) p.o[((int64_t)(tb + j[i]) * p.hv + h) * VD + cb * BV + my_col] = fmaf(bs[i].y, delta, pq) * p.inv_sqrt_k;
+        }
         __syncwarp();
+    };
+    // Token j's state, from its parent's in S, to its snapshot; keep: and to S.
+    auto store = [&](int j, bool keep) {
+        float a[8], k[8];
         float2 d[P2];
+        vec8(al, j, a);
+        key8(j, k);
         deltas(j, d);
         const int32_t snap = snaps[j];
         ST* to = pool + state_at(p, snap, h) + tile;
@@ -481,11 +537,24 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32) kda_tree_kernel(const Ste
             for (unsigned long long m = above; m != 0; m &= m - 1) again(__ffsll((long long)m) - 1);
             kids = above != 0 ? child[tree_top(above)] & todo : 1ull << j;
         }
-        const unsigned long long ends = kids & leaves;
-        const int j = __ffsll((long long)(ends != 0 ? ends : kids)) - 1;
-        step(j, ends == 0);
-        todo &= ~(1ull << j);
-        if (ends == 0) kids = child[j];
+        // leaves two at a time, then an inner child; a leaf and the inner child go together too
+        const unsigned long long ends = kids & leaves, inner = kids & ~leaves;
+        int j[2];
+        j[0] = __ffsll((long long)(ends != 0 ? ends : inner)) - 1;
+        const unsigned long long left = ends & (ends - 1);
+        const bool down = ends == 0 || (left == 0 && inner != 0);       // the last of this token's children that are taken from S
+        j[1] = left != 0 ? __ffsll((long long)left) - 1 : inner != 0 && ends != 0 ? __ffsll((long long)inner) - 1 : -1;
+        if (j[1] >= 0) {
+            sums(std::integral_constant<int, 2>{}, j);
+            store(j[0], false);
+            store(j[1], down);
+            todo &= ~(1ull << j[1]);
+        } else {
+            sums(std::integral_constant<int, 1>{}, j);
+            store(j[0], down);
+        }
+        todo &= ~(1ull << j[0]);
+        if (down) kids = child[j[1] >= 0 ? j[1] : j[0]];
     }
 }
 

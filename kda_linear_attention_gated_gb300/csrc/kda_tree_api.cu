@@ -29,21 +29,21 @@ constexpr int kSms = 152;
 template <typename QT>
 int launch_tree(const kda::StepParams& prm, const uint64_t* tree, uint32_t flags, cudaStream_t stream) {
     using SM = kda::TreeSmem<state_t>;
-    auto kernel = kda::kda_tree_kernel<state_t, QT>;
-    // four warps a CTA share the tokens' vectors; fewer while the grid is below two CTAs for each SM
+    auto kernel = prm.k == kda::KMAX && prm.v == kda::KMAX ? kda::kda_tree_kernel<state_t, QT, true> : kda::kda_tree_kernel<state_t, QT, false>;
+    // Up to four warps a CTA share the tokens' vectors; fewer while that leaves an SM without a CTA.
     const int64_t heads = (int64_t)prm.n * prm.hv;
     int warps = kda::TREE_WARPS_MAX;
     auto ctas = [&](int w) { return heads * ((prm.v + w * SM::CW - 1) / (w * SM::CW)); };
-    while (warps > 1 && (ctas(warps) < 2 * kSms || (warps / 2) * SM::CW >= prm.v)) warps /= 2;
+    while (warps > 1 && (ctas(warps) < kSms || (warps / 2) * SM::CW >= prm.v)) warps /= 2;
     if (ctas(warps) > 0x7fffffffLL) return KDA_ERR_SHAPE;
     int occ = 0, sms = 0;   // raises the kernel's limit to the most that any call takes
     const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::TREE_WARPS_MAX * 32,
-                             SM::bytes(kda::TREE_MAX, kda::TREE_WARPS_MAX), &occ, &sms);
+                             SM::bytes(kda::TREE_MAX, kda::KMAX, kda::TREE_WARPS_MAX), &occ, &sms);
     if (rc != KDA_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas(warps), 1, 1);
     cfg.blockDim = dim3((unsigned)(32 * warps), 1, 1);
-    cfg.dynamicSmemBytes = SM::bytes(prm.t, warps);
+    cfg.dynamicSmemBytes = SM::bytes(prm.t, prm.k, warps);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     set_pdl(cfg, &attr, flags);
