@@ -186,56 +186,87 @@ __global__ void __launch_bounds__(CONV_TREE_CH * CONV_TREE_GROUPS) kda_conv_tree
 // ---------------------------------------------------------------------------
 // Recurrence
 // ---------------------------------------------------------------------------
-constexpr int TREE_WARPS_MAX = 4;
+// Most column groups of a CTA, of W = 1 or 4 warps each.
+__host__ __device__ constexpr int tree_groups(int w) { return w == 4 ? 2 : 4; }
+constexpr int TREE_CW = 16;             // columns of a group
 
-// Shared memory of a CTA of `warps` warps with at most t tokens a request.
+// Four neighbouring state elements of a row.
+template <typename ST> struct TreeVec;
+template <> struct TreeVec<float> {
+    using R = uint4;
+    static __device__ __forceinline__ void widen(const R& r, float2 (&x)[2]) {
+        x[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+        x[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+    }
+    static __device__ __forceinline__ R narrow(const float2 (&x)[2]) {
+        return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+    }
+    static __device__ __forceinline__ R zero() { return make_uint4(0, 0, 0, 0); }
+};
+template <> struct TreeVec<__half> {
+    using R = uint2;
+    static __device__ __forceinline__ void widen(const R& r, float2 (&x)[2]) {      // exact
+        x[0] = StateVec<__half>::w2(r.x);
+        x[1] = StateVec<__half>::w2(r.y);
+    }
+    static __device__ __forceinline__ R narrow(const float2 (&x)[2]) {              // to nearest even
+        return make_uint2(StateVec<__half>::n2(x[0].x, x[0].y), StateVec<__half>::n2(x[1].x, x[1].y));
+    }
+    static __device__ __forceinline__ R zero() { return make_uint2(0, 0); }
+};
+
+// Shared memory of a CTA of `groups` column groups with at most t tokens a request.
 template <typename ST> struct TreeSmem {
-    static constexpr int VEC = StateVec<ST>::VEC, CW = 2 * VEC;   // columns of a lane, of a warp
-    static __host__ __device__ constexpr int vecs(int t, int k) { return 3 * t * k * 4; }          // k, alpha, q of each token
-    static __host__ __device__ constexpr int delta(int t, int warps) { return t * warps * CW * 4; }
-    static __host__ __device__ constexpr int bytes(int t, int k, int warps) {
-        return vecs(t, k) + delta(t, warps) + warps * 32 * 8 * 16 + t * (8 + 8 + 8 + 4);
+    static __host__ __device__ constexpr int bytes(int t, int k, int groups, int w) {
+        return 3 * t * k * 4                                                        // khat, alpha, qhat of each token
+               + t * groups * TREE_CW * 4                                           // v, then delta
+               + groups * KMAX * 4 * (int)sizeof(typename TreeVec<ST>::R)           // the initial state
+               + 2 * 2 * groups * w * 2 * TREE_CW * 4                               // the warps' sums
+               + t * (8 + 8 + 8 + 4);                                               // masks, children, beta and khat . qhat, slots
     }
 };
 
-// One CTA: one request, one value head, `warps` times 32 bytes' worth of state
-// columns.  A warp owns its columns whole: lane l holds VEC columns of the rows
-// 4 (l / 2) .. + 3 and 64 more, so the sums over K are shuffles within the
-// warp and nothing waits for another warp once the tokens' vectors are in
-// shared memory.
+// One CTA: one request, one value head, `groups` times 16 state columns.  W
+// warps share a group's columns, 128 / W rows each; lane l of a warp holds 4
+// columns (l % 4) of 16 / W rows, four neighbouring ones (l / 4) of every 32.
+// The sums over K are three shuffles in a warp and W terms over the warps,
+// through shared memory behind a barrier of the group: more warps shorten a
+// token's way, fewer save instructions.
 //
 // A token's state is S_j = diag(alpha_j) S_parent + khat_j delta_j^T with
 // delta_j = beta_j (v_j - S_parent^T diag(alpha_j) khat_j), and both of its sums
 // are over the parent's state, which is in registers.  Tokens are taken depth
 // first: of a token's children first the leaves, whose states only pass
-// through on their way out, then the first of the others, in place.  Where
-// another branch begins its parent's state is built again from the initial
-// state (kept on chip as it was loaded: its slot may be one of the
-// snapshots') with the ancestors' deltas, which are kept: two operations an
-// element and ancestor, no sums, the same bits as on the way there.  So states
-// carry fp32 along every path whatever the pool's type, and do not depend on
-// the order of siblings.
+// through on their way out, then the first of the others, in place; two
+// children at a time.  Where another branch begins its parent's state is built
+// again from the initial state (kept on chip as it was loaded: its slot may be
+// one of the snapshots') with the ancestors' deltas, which are kept: two
+// operations an element and ancestor, no sums, the same bits as on the way
+// there.  So states carry fp32 along every path whatever the pool's type, and
+// do not depend on the order of siblings.
 //
 // FULL: K = V = 128, so that every lane has all its rows and columns and the
 // places of a tile are constants.
-template <typename ST, typename QT, bool FULL>
-__global__ void __launch_bounds__(TREE_WARPS_MAX * 32, 3) kda_tree_kernel(const StepParams p, const uint64_t* tree) {
-    using SV = StateVec<ST>;
-    constexpr int VEC = SV::VEC, CW = 2 * VEC, NV = 2 * VEC, P2 = VEC / 2;
+template <typename ST, typename QT, int W, bool FULL>
+__global__ void __launch_bounds__(tree_groups(W) * W * 32, W == 1 ? 3 : 2) kda_tree_kernel(const StepParams p, const uint64_t* tree) {
+    using SV = TreeVec<ST>;
+    using R = typename SV::R;
     extern __shared__ __align__(128) uint8_t smem[];
     const int KD = FULL ? KMAX : p.k, VD = FULL ? KMAX : p.v;
-    const int warps = blockDim.x >> 5, BV = warps * CW;
+    constexpr int RL = 16 / W;              // rows of a lane: r0 + i % 4 + 32 (i / 4)
+    const int groups = blockDim.x / (32 * W), BV = groups * TREE_CW;
     float* kh = reinterpret_cast<float*>(smem);
     float* al = kh + p.t * KD;
     float* qh = al + p.t * KD;
-    float* du = qh + p.t * KD;                                             // [t][BV]: v, then delta
-    uint4* stash = reinterpret_cast<uint4*>(du + p.t * BV);                 // [8][threads]
-    unsigned long long* masks = reinterpret_cast<unsigned long long*>(stash + 8 * blockDim.x);
+    float* du = qh + p.t * KD;                                              // [t][BV]: v, then delta
+    R* stash = reinterpret_cast<R*>(du + p.t * BV);                         // [RL][threads]
+    float* red = reinterpret_cast<float*>(stash + RL * blockDim.x);         // [2][2][groups][W][2][16]
+    unsigned long long* masks = reinterpret_cast<unsigned long long*>(red + 2 * 2 * groups * W * 2 * TREE_CW);
     unsigned long long* child = masks + p.t;
     float2* sc = reinterpret_cast<float2*>(child + p.t);                    // beta, khat . qhat
     int32_t* snaps = reinterpret_cast<int32_t*>(sc + p.t);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = warp / W, share = warp % W;
     const int cblocks = (VD + BV - 1) / BV;
     const int cb = (int)blockIdx.x % cblocks, nh = (int)blockIdx.x / cblocks, n = nh / p.hv, h = nh - n * p.hv;
     for (int j = tid; j < p.t; j += blockDim.x) child[j] = 0;
@@ -266,9 +297,8 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32, 3) kda_tree_kernel(const 
         if (tid == 0) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
         return;
     }
-    const int c0 = cb * BV + warp * CW + (lane & 1) * VEC;                  // the lane's first column
-    const int r0 = (lane >> 1) * 4;                                         // and row; its i-th is r0 + i % 4 + 64 (i / 4)
-    const bool mine = c0 < VD;
+    const int lc = grp * TREE_CW + (lane & 3) * 4, c0 = cb * BV + lc;       // the lane's first column: of the CTA's, of all
+    const int r0 = share * (KMAX / W) + (lane >> 2) * 4;                    // its first row
     if (slot < 0) {     // a padding request
         for (int i = tid; i < T * BV; i += blockDim.x) {
             const int j = i / BV, c = cb * BV + i - j * BV;
@@ -277,37 +307,39 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32, 3) kda_tree_kernel(const 
         return;
     }
     const bool rst = p.reset != nullptr && __ldg(p.reset + n) != 0;
-    // half 0 and half 1 of the lane's rows are in the state
-    const bool live[2] = {FULL || (mine && r0 < KD), FULL || (mine && r0 + 64 < KD)};
+    // its rows and columns are in the state
+    auto row_at = [](int i) { return (i & 3) + 32 * (i >> 2); };
+    auto has = [&](int i) { return FULL || r0 + 32 * (i >> 2) < KD; };
+    auto live = [&](int i) { return FULL || (has(i) && c0 < VD); };
     ST* pool = static_cast<ST*>(p.pool);
     const int64_t tile = (int64_t)r0 * VD + c0;
-    auto at_row = [&](int i) { return (int64_t)((i & 3) + 64 * (i >> 2)) * VD; };
-    uint4 raw[8];
+    // the initial state goes straight to shared memory, each thread's own
     {
         const ST* from = pool + state_at(p, slot, h) + tile;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            raw[i] = live[i >> 2] && !rst ? *reinterpret_cast<const uint4*>(from + at_row(i)) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < RL; ++i) {
+            R* to = stash + i * blockDim.x + tid;
+            if (live(i) && !rst)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from + row_at(i) * VD), "n"(sizeof(R)) : "memory");
+            else
+                *to = SV::zero();
+        }
     }
     __syncthreads();    // child is zero
-    // ---- the tokens' vectors, a token a warp at a time ----
-    const int hq = h / (p.hv / p.hqk);
+    // ---- the tokens' vectors, two tokens a warp at a time ----
+    const int hq = h / (p.hv / p.hqk), warps = blockDim.x >> 5;
     const bool scaled = p.a_log != nullptr;
     const float gate = scaled ? expf(__ldg(p.a_log + h)) : 1.f;
-    constexpr int AHEAD = 4;        // tokens whose loads a warp has on their way
+    constexpr int AHEAD = 2;
     const int d = 4 * lane;
-    const bool on = d < KD;
-    float bias[4] = {};
-    if (on && scaled && p.dt_bias != nullptr) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bias[e] = __ldg(p.dt_bias + h * KD + d + e);
-    }
+    const bool on = FULL || d < KD;
+    const float* bias = scaled && p.dt_bias != nullptr ? p.dt_bias + h * KD + (on ? d : 0) : nullptr;
     using QIO = ConvIO<QT, 4>;
     for (int j0 = warp; j0 < T; j0 += AHEAD * warps) {
         typename QIO::R kr[AHEAD], qr[AHEAD];
         float4 ar[AHEAD];
-        float br[AHEAD], vr[AHEAD], vr2[AHEAD];      // a CTA has at most 64 columns
-        static_assert(TREE_WARPS_MAX * CW <= 64, "columns");
+        float br[AHEAD], vr[AHEAD][2];          // a CTA has at most 64 columns
+        static_assert(tree_groups(W) * TREE_CW <= 64, "columns");
         unsigned long long mr[AHEAD];
 #pragma unroll
         for (int x = 0; x < AHEAD; ++x) {
@@ -318,11 +350,11 @@ __global__ void __launch_bounds__(TREE_WARPS_MAX * 32, 3) kda_tree_kernel(const 
             ar[x] = __ldg(reinterpret_cast<const float4*>(p.a + (tok * p.hv + h) * KD + (on ? d : 0)));
             br[x] = __ldg(p.b + tok * p.hv + h);
             mr[x] = tree_mask(tree, tok, j) ^ (1ull << j);
-const QT* vt = static_cast<const QT*>(p.vv) + (tok * p.hv + h) * VD + cb * BV + lane;
-            vr[x] = lane < BV && cb * BV + lane < VD ? to_f32(vt[0]) : 0.f;
-            vr2[x] = lane + 32 < BV && cb * BV + lane + 32 < VD ? to_f32(vt[32]) : 0.f;
+            const QT* vt = static_cast<const QT*>(p.vv) + (tok * p.hv + h) * VD + cb * BV + lane;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) vr[x][y] = lane + 32 * y < BV && cb * BV + lane + 32 * y < VD ? to_f32(vt[32 * y]) : 0.f;
         }
-        // step by step for all of them, so that their latencies overlap; behind the last token it is done again
+        // step by step for both, so that their latencies overlap; behind the last token it is done again
         float k4[AHEAD][4], q4[AHEAD][4], kk[AHEAD], qq[AHEAD], kq[AHEAD];
 #pragma unroll
         for (int x = 0; x < AHEAD; ++x) {
@@ -346,32 +378,24 @@ const QT* vt = static_cast<const QT*>(p.vv) + (tok * p.hv + h) * VD + cb * BV + 
                 kq[x] += __shfl_xor_sync(0xffffffffu, kq[x], o);
             }
         float g[AHEAD][4];
-        if (scaled) {       // one branch for all
 #pragma unroll
-            for (int x = 0; x < AHEAD; ++x) {
-                const float a[4] = {ar[x].x, ar[x].y, ar[x].z, ar[x].w};
+        for (int x = 0; x < AHEAD; ++x) {
+            const float a[4] = {ar[x].x, ar[x].y, ar[x].z, ar[x].w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) g[x][e] = gate_alpha(a[e], true, gate, bias[e]);
-            }
-        } else {
-#pragma unroll
-            for (int x = 0; x < AHEAD; ++x) {
-                const float a[4] = {ar[x].x, ar[x].y, ar[x].z, ar[x].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[x][e] = gate_alpha(a[e], false, gate, bias[e]);
-            }
+            for (int e = 0; e < 4; ++e) g[x][e] = gate_alpha(a[e], scaled, gate, bias != nullptr ? __ldg(bias + e) : 0.f);
         }
 #pragma unroll
         for (int x = 0; x < AHEAD; ++x) {
             const int j = min(j0 + x * warps, T - 1);
             const float rk = __frsqrt_rn(kk[x] + L2_EPS), rq = __frsqrt_rn(qq[x] + L2_EPS);
-            if (FULL || on) {
+            if (on) {
                 *reinterpret_cast<float4*>(kh + j * KD + d) = make_float4(k4[x][0] * rk, k4[x][1] * rk, k4[x][2] * rk, k4[x][3] * rk);
                 *reinterpret_cast<float4*>(qh + j * KD + d) = make_float4(q4[x][0] * rq, q4[x][1] * rq, q4[x][2] * rq, q4[x][3] * rq);
                 *reinterpret_cast<float4*>(al + j * KD + d) = make_float4(g[x][0], g[x][1], g[x][2], g[x][3]);
             }
-            if (lane < BV) du[j * BV + lane] = vr[x];
-            if (lane + 32 < BV) du[j * BV + lane + 32] = vr2[x];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                if (lane + 32 * y < BV) du[j * BV + lane + 32 * y] = vr[x][y];
             if (lane == 0) {
                 sc[j] = make_float2(sigmoid_neg(-br[x]), kq[x] * rk * rq);
                 masks[j] = mr[x];
@@ -379,141 +403,145 @@ const QT* vt = static_cast<const QT*>(p.vv) + (tok * p.hv + h) * VD + cb * BV + 
             }
         }
     }
-    float2 S[8][P2];
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float2 S[RL][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        SV::widen2(raw[i], S[i]);
-        stash[i * blockDim.x + tid] = raw[i];
-    }
+    for (int i = 0; i < RL; ++i) SV::widen(stash[i * blockDim.x + tid], S[i]);
     __syncthreads();
 
-    // which of the warp's sums this lane ends up with: lane bits 4.. down to SB count columns, bit SB is
-    // 0 for the sum with khat and 1 for the one with qhat, bit 0 the column half
-    constexpr int SB = VEC == 4 ? 2 : 1;
-    const int vc = lane >> (SB + 1), second = lane >> SB & 1;
-    const int my_col = warp * CW + (lane & 1) * VEC + vc;
-    const bool first_of = VEC == 8 || (lane & 2) == 0, live_col = cb * BV + my_col < VD && first_of;
-    // a lane without rows there reads other rows', and k as zero: its states stay zero
-    const int at0 = r0 < KD ? r0 : 0, at1 = r0 + 64 < KD ? r0 + 64 : 0;
-    auto vec8 = [&](const float* v, int j, float (&x)[8]) {
-        const float4 lo = *reinterpret_cast<const float4*>(v + j * KD + at0), hi = *reinterpret_cast<const float4*>(v + j * KD + at1);
-        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+    // rows r0 + 32 i .. + 3 of a vector; a lane without them reads the first ones, and k as zero: its states stay zero
+    auto vec4 = [&](const float* v, int j, int i) {
+        return *reinterpret_cast<const float4*>(v + j * KD + (has(4 * i) ? r0 + 32 * i : 0));
     };
-    auto key8 = [&](int j, float (&x)[8]) {
-        vec8(kh, j, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!FULL && r0 + 64 * (i >> 2) >= KD) x[i] = 0.f;
+    auto key4 = [&](int j, int i) {
+        const float4 k = vec4(kh, j, i);
+        return has(4 * i) ? k : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    auto deltas = [&](int j, float2 (&d)[P2]) {
+    auto times = [&](float2 x, float f) { return __fmul2_rn(x, make_float2(f, f)); };
+    auto plus = [&](float f, float2 y, float2 x) { return __ffma2_rn(make_float2(f, f), y, x); };
+    auto part = [](const float4& v, int r) { return r == 0 ? v.x : r == 1 ? v.y : r == 2 ? v.z : v.w; };
+    // row r of diag(alpha) S + khat delta^T, a and k of its four rows
+    auto next_row = [&](int r, const float4& a, const float4& k, const float2 (&dl)[2], float2 (&out)[2]) {
 #pragma unroll
-        for (int x = 0; x < P2; x += 2) {
-            const float4 f = *reinterpret_cast<const float4*>(du + j * BV + warp * CW + (lane & 1) * VEC + 2 * x);
-            d[x] = make_float2(f.x, f.y);
-            d[x + 1] = make_float2(f.z, f.w);
+        for (int x = 0; x < 2; ++x) out[x] = plus(part(k, r & 3), dl[x], times(S[r][x], part(a, r & 3)));
+    };
+    // an earlier token's step again
+    auto again = [&](int j) {
+        const float4 f = *reinterpret_cast<const float4*>(du + j * BV + lc);
+        const float2 dl[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
+#pragma unroll
+        for (int i = 0; i < RL / 4; ++i) {
+            const float4 a = vec4(al, j, i), k = key4(j, i);
+#pragma unroll
+            for (int r = 4 * i; r < 4 * i + 4; ++r) next_row(r, a, k, dl, S[r]);
         }
     };
-    // S <- diag(alpha_i) S + khat_i delta_i^T of an earlier token
-    auto again = [&](int i) {
-        float a[8], k[8];
-        float2 d[P2];
-        vec8(al, i, a);
-        key8(i, k);
-        deltas(i, d);
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int x = 0; x < P2; ++x) S[r][x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], __fmul2_rn(S[r][x], make_float2(a[r], a[r])));
-    };
-    // Tokens j[0 .. N), children of the token whose state S is: their outputs, and their deltas to du.  Step by step
-    // for all of them, so that their latencies overlap.
-    auto sums = [&](auto n_of, const int* j) {
+    int turn = 0;       // which half of `red`
+    // Tokens j[0 .. N), children of the token whose state S is: outputs, deltas, states to their snapshots; keep: the
+    // last one's to S.  Step by step for all of them, so that their latencies overlap.
+    auto step = [&](auto n_of, const int* j, bool keep) {
         constexpr int N = decltype(n_of)::value;
-        float f[N][NV], v[N];
-        float2 bs[N];
+        float f[N][8];
+        float4 v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float a[8], k[8], q[8];
-            vec8(al, j[i], a);
-            vec8(kh, j[i], k);
-            vec8(qh, j[i], q);
-            v[i] = du[j[i] * BV + my_col];
-            bs[i] = sc[j[i]];
-            float2 su[P2], sq[P2];
+        for (int x = 0; x < N; ++x) {
+            v[x] = *reinterpret_cast<const float4*>(du + j[x] * BV + lc);
+            float2 su[2], sq[2];
 #pragma unroll
-            for (int x = 0; x < P2; ++x) su[x] = sq[x] = make_float2(0.f, 0.f);
+            for (int i = 0; i < RL / 4; ++i) {
+                const float4 a = vec4(al, j[x], i), k = key4(j[x], i), q = vec4(qh, j[x], i);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float ak = a[r] * k[r], aq = a[r] * q[r];
+                for (int r = 0; r < 4; ++r) {
+                    const float ak = part(a, r) * part(k, r), aq = part(a, r) * part(q, r);
 #pragma unroll
-                for (int x = 0; x < P2; ++x) {
-                    su[x] = __ffma2_rn(S[r][x], make_float2(ak, ak), su[x]);
-                    sq[x] = __ffma2_rn(S[r][x], make_float2(aq, aq), sq[x]);
+                    for (int y = 0; y < 2; ++y) {
+                        su[y] = i + r == 0 ? times(S[0][y], ak) : plus(ak, S[4 * i + r][y], su[y]);
+                        sq[y] = i + r == 0 ? times(S[0][y], aq) : plus(aq, S[4 * i + r][y], sq[y]);
+                    }
                 }
             }
 #pragma unroll
-            for (int x = 0; x < P2; ++x) {
-                f[i][4 * x] = su[x].x;
-                f[i][4 * x + 1] = sq[x].x;
-                f[i][4 * x + 2] = su[x].y;
-                f[i][4 * x + 3] = sq[x].y;
+            for (int y = 0; y < 2; ++y) {
+                f[x][2 * y] = su[y].x;
+                f[x][2 * y + 1] = su[y].y;
+                f[x][4 + 2 * y] = sq[y].x;
+                f[x][4 + 2 * y + 1] = sq[y].y;
             }
         }
-        // over the 16 row groups (lane bits 4 .. 1), scattered: value 2 c + s of column c
+        // over the 8 row groups (lane bits 4 .. 2), scattered: lane bit 4 tells the sum, bits 3 and 2 the column
         int m = 16;
 #pragma unroll
-        for (int cnt = NV; cnt > 1; cnt >>= 1, m >>= 1) {
+        for (int cnt = 8; cnt > 1; cnt >>= 1, m >>= 1) {
             const bool upper = (lane & m) != 0;
 #pragma unroll
-            for (int x = 0; x < cnt / 2; ++x)
+            for (int y = 0; y < cnt / 2; ++y)
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float send = upper ? f[i][x] : f[i][x + cnt / 2], keep = upper ? f[i][x + cnt / 2] : f[i][x];
-                    f[i][x] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                for (int x = 0; x < N; ++x) {
+                    const float send = upper ? f[x][y] : f[x][y + cnt / 2], mine = upper ? f[x][y + cnt / 2] : f[x][y];
+                    f[x][y] = mine + __shfl_xor_sync(0xffffffffu, send, m);
                 }
         }
-        if constexpr (VEC == 4) {
+        float* sums = red + (turn * 2 * groups + grp) * W * 2 * TREE_CW;        // token x: x * groups * W * 2 * 16 on
+        turn ^= 1;
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i][0] += __shfl_xor_sync(0xffffffffu, f[i][0], 2);
-        }
-        float other[N];
+        for (int x = 0; x < N; ++x)
+            sums[(x * groups * W + share) * 2 * TREE_CW + (lane >> 4) * TREE_CW + (lane & 3) * 4 + (lane >> 2 & 3)] = f[x][0];
+        if constexpr (W == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * W) : "memory");
+        // the group's sums are there, and its v read
+        float2 dl[N][2];
 #pragma unroll
-        for (int i = 0; i < N; ++i) other[i] = __shfl_xor_sync(0xffffffffu, f[i][0], 1 << SB);
-        __syncwarp();       // v is read
+        for (int x = 0; x < N; ++x) {
+            const float* of = sums + x * groups * W * 2 * TREE_CW + (lane & 3) * 4;
+            auto over_warps = [&](const float* y) {
+                float4 s = *reinterpret_cast<const float4*>(y);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float u = second ? other[i] : f[i][0], pq = second ? f[i][0] : other[i], delta = bs[i].x * (v[i] - u);
-            if (!second && first_of) du[j[i] * BV + my_col] = delta;
-            if (second && live_col) p.o[((int64_t)(tb + j[i]) * p.hv + h) * VD + cb * BV + my_col] = fmaf(bs[i].y, delta, pq) * p.inv_sqrt_k;
-        }
-        __syncwarp();
-    };
-    // Token j's state, from its parent's in S, to its snapshot; keep: and to S.
-    auto store = [&](int j, bool keep) {
-        float a[8], k[8];
-        float2 d[P2];
-        vec8(al, j, a);
-        key8(j, k);
-        deltas(j, d);
-        const int32_t snap = snaps[j];
-        ST* to = pool + state_at(p, snap, h) + tile;
-        if (keep) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-#pragma unroll
-                for (int x = 0; x < P2; ++x) S[r][x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], __fmul2_rn(S[r][x], make_float2(a[r], a[r])));
-                if (snap >= 0 && live[r >> 2]) *reinterpret_cast<uint4*>(to + at_row(r)) = SV::narrow2(S[r]);
+                for (int z = 1; z < W; ++z) {
+                    const float4 t = *reinterpret_cast<const float4*>(y + z * 2 * TREE_CW);
+                    s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+                }
+                return s;
+            };
+            const float4 u = over_warps(of);
+            const float2 bs = sc[j[x]];
+            const float4 dt = make_float4(bs.x * (v[x].x - u.x), bs.x * (v[x].y - u.y), bs.x * (v[x].z - u.z), bs.x * (v[x].w - u.w));
+            dl[x][0] = make_float2(dt.x, dt.y);
+            dl[x][1] = make_float2(dt.z, dt.w);
+            if (lane < 4 && share == x % W) {       // one lane of the columns
+                *reinterpret_cast<float4*>(du + j[x] * BV + lc) = dt;
+                const float4 pq = over_warps(of + TREE_CW);
+                float* o = p.o + ((int64_t)(tb + j[x]) * p.hv + h) * VD + c0;
+                const float4 out = make_float4(fmaf(bs.y, dt.x, pq.x) * p.inv_sqrt_k, fmaf(bs.y, dt.y, pq.y) * p.inv_sqrt_k,
+                                               fmaf(bs.y, dt.z, pq.z) * p.inv_sqrt_k, fmaf(bs.y, dt.w, pq.w) * p.inv_sqrt_k);
+                if (FULL || c0 < VD) {              // o has the alignment of floats
+                    o[0] = out.x;
+                    o[1] = out.y;
+                    o[2] = out.z;
+                    o[3] = out.w;
+                }
             }
-        } else if (snap >= 0) {
+        }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                float2 out[P2];
+        for (int x = 0; x < N; ++x) {
+            const int32_t snap = snaps[j[x]];
+            const bool stay = x == N - 1 && keep;
+            ST* to = pool + state_at(p, snap, h) + tile;
 #pragma unroll
-                for (int x = 0; x < P2; ++x) out[x] = __ffma2_rn(make_float2(k[r], k[r]), d[x], __fmul2_rn(S[r][x], make_float2(a[r], a[r])));
-                if (live[r >> 2]) *reinterpret_cast<uint4*>(to + at_row(r)) = SV::narrow2(out);
+            for (int i = 0; i < RL / 4; ++i) {
+                const float4 a = vec4(al, j[x], i), k = key4(j[x], i);
+#pragma unroll
+                for (int r = 4 * i; r < 4 * i + 4; ++r) {
+                    float2 out[2];
+                    next_row(r, a, k, dl[x], out);
+                    if (snap >= 0 && live(r)) *reinterpret_cast<R*>(to + row_at(r) * VD) = SV::narrow(out);
+                    if (stay) {
+                        S[r][0] = out[0];
+                        S[r][1] = out[1];
+                    }
+                }
             }
         }
+        if constexpr (W == 1) __syncwarp();     // du is written for all lanes
     };
     // ---- depth first ----
     unsigned long long todo, leaves, kids;      // kids: of the token whose state S is (at first the context)
@@ -529,29 +557,25 @@ const QT* vt = static_cast<const QT*>(p.vv) + (tok * p.hv + h) * VD + cb * BV + 
     while (todo != 0) {
         kids &= todo;
         if (kids == 0) {
-            // another branch: the lowest token left, whose parent is done
+            // another branch: the lowest token left, whose parent is done (two steps ago or more: its delta is there)
             const int j = __ffsll((long long)todo) - 1;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) SV::widen2(stash[i * blockDim.x + tid], S[i]);
+            for (int i = 0; i < RL; ++i) SV::widen(stash[i * blockDim.x + tid], S[i]);
             const unsigned long long above = masks[j];
             for (unsigned long long m = above; m != 0; m &= m - 1) again(__ffsll((long long)m) - 1);
             kids = above != 0 ? child[tree_top(above)] & todo : 1ull << j;
         }
-        // leaves two at a time, then an inner child; a leaf and the inner child go together too
-        const unsigned long long ends = kids & leaves, inner = kids & ~leaves;
+        // leaves two at a time, then an inner child; the last leaf and the inner child go together
+        const unsigned long long ends = kids & leaves, inner = kids & ~leaves, left = ends & (ends - 1);
+        const bool down = ends == 0 || (left == 0 && inner != 0);       // the last of these is the one to go on from
         int j[2];
         j[0] = __ffsll((long long)(ends != 0 ? ends : inner)) - 1;
-        const unsigned long long left = ends & (ends - 1);
-        const bool down = ends == 0 || (left == 0 && inner != 0);       // the last of this token's children that are taken from S
         j[1] = left != 0 ? __ffsll((long long)left) - 1 : inner != 0 && ends != 0 ? __ffsll((long long)inner) - 1 : -1;
         if (j[1] >= 0) {
-            sums(std::integral_constant<int, 2>{}, j);
-            store(j[0], false);
-            store(j[1], down);
+            step(std::integral_constant<int, 2>{}, j, down);
             todo &= ~(1ull << j[1]);
         } else {
-            sums(std::integral_constant<int, 1>{}, j);
-            store(j[0], down);
+            step(std::integral_constant<int, 1>{}, j, down);
         }
         todo &= ~(1ull << j[0]);
         if (down) kids = child[j[1] >= 0 ? j[1] : j[0]];

@@ -26,28 +26,39 @@ using state_t = float;
 
 constexpr int kSms = 152;
 
-template <typename QT>
-int launch_tree(const kda::StepParams& prm, const uint64_t* tree, uint32_t flags, cudaStream_t stream) {
+template <typename QT, int W>
+int launch_tree_warps(const kda::StepParams& prm, const uint64_t* tree, int groups, uint32_t flags, cudaStream_t stream) {
     using SM = kda::TreeSmem<state_t>;
-    auto kernel = prm.k == kda::KMAX && prm.v == kda::KMAX ? kda::kda_tree_kernel<state_t, QT, true> : kda::kda_tree_kernel<state_t, QT, false>;
-    // Up to four warps a CTA share the tokens' vectors; fewer while that leaves an SM without a CTA.
-    const int64_t heads = (int64_t)prm.n * prm.hv;
-    int warps = kda::TREE_WARPS_MAX;
-    auto ctas = [&](int w) { return heads * ((prm.v + w * SM::CW - 1) / (w * SM::CW)); };
-    while (warps > 1 && (ctas(warps) < kSms || (warps / 2) * SM::CW >= prm.v)) warps /= 2;
-    if (ctas(warps) > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    auto kernel = prm.k == kda::KMAX && prm.v == kda::KMAX ? kda::kda_tree_kernel<state_t, QT, W, true>
+                                                           : kda::kda_tree_kernel<state_t, QT, W, false>;
+    const int64_t grid = (int64_t)prm.n * prm.hv * ((prm.v + groups * kda::TREE_CW - 1) / (groups * kda::TREE_CW));
+    if (grid > 0x7fffffffLL) return KDA_ERR_SHAPE;
     int occ = 0, sms = 0;   // raises the kernel's limit to the most that any call takes
-    const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::TREE_WARPS_MAX * 32,
-                             SM::bytes(kda::TREE_MAX, kda::KMAX, kda::TREE_WARPS_MAX), &occ, &sms);
+    const int rc = occupancy(reinterpret_cast<const void*>(kernel), kda::tree_groups(W) * W * 32,
+                             SM::bytes(kda::TREE_MAX, kda::KMAX, kda::tree_groups(W), W), &occ, &sms);
     if (rc != KDA_OK) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas(warps), 1, 1);
-    cfg.blockDim = dim3((unsigned)(32 * warps), 1, 1);
-    cfg.dynamicSmemBytes = SM::bytes(prm.t, prm.k, warps);
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)(32 * W * groups), 1, 1);
+    cfg.dynamicSmemBytes = SM::bytes(prm.t, prm.k, groups, W);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     set_pdl(cfg, &attr, flags);
     return cudaLaunchKernelEx(&cfg, kernel, prm, tree) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+template <typename QT>
+int launch_tree(const kda::StepParams& prm, const uint64_t* tree, uint32_t flags, cudaStream_t stream) {
+    const int64_t heads = (int64_t)prm.n * prm.hv, all = heads * ((prm.v + kda::TREE_CW - 1) / kda::TREE_CW);
+    // Few column groups: four warps each, for the time that a token takes; many: one, for the instructions.  12 heads of
+    // 128, four against one, us (fp16 pool, trees of 32): 1 request 31, 61; 2: 35, 64; 4 (384 groups): 41, 49; 8: 64, 53;
+    // 16: 104, 70.  (fp32: 31, 63; 35, 64; 45, 53; 70, 61; 115, 96.)  Two warps gain nothing between.
+    const bool few = all <= 3 * kSms;
+    // Groups of a CTA share the tokens' vectors; fewer while that leaves an SM without a CTA.
+    int groups = kda::tree_groups(few ? 4 : 1);
+    auto ctas = [&](int g) { return heads * ((prm.v + g * kda::TREE_CW - 1) / (g * kda::TREE_CW)); };
+    while (groups > 1 && (ctas(groups) < kSms || (groups / 2) * kda::TREE_CW >= prm.v)) groups /= 2;
+    return few ? launch_tree_warps<QT, 4>(prm, tree, groups, flags, stream) : launch_tree_warps<QT, 1>(prm, tree, groups, flags, stream);
 }
 
 template <typename ET, int VC, int KWM>
