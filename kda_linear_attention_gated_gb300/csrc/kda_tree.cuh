@@ -26,14 +26,15 @@ __device__ __forceinline__ int tree_top(uint64_t m) { return 63 - __clzll((long 
 // ---------------------------------------------------------------------------
 // Convolution
 // ---------------------------------------------------------------------------
-constexpr int CONV_TREE_CH = 64;        // channel vectors of a CTA
+constexpr int CONV_TREE_CH = 32;        // channel vectors of a CTA
 constexpr int CONV_TREE_GROUPS = 4;     // threads of a channel vector, which share the tokens
 
 // Shared memory of a CTA: a row for each history entry and token, and the rows
 // of each token's taps.
 template <typename ET, int VC> struct ConvTreeSmem {
     static constexpr int ROW = CONV_TREE_CH * VC * (int)sizeof(ET);
-    static __host__ __device__ constexpr int bytes(int t) { return (CONV_KW_MAX - 1 + t) * ROW + t * 8; }
+    static constexpr int WEIGHTS = CONV_TREE_CH * VC * 16;       // four taps a channel
+    static __host__ __device__ constexpr int bytes(int t) { return WEIGHTS + (CONV_KW_MAX - 1 + t) * ROW + t * 8; }
 };
 
 // silu_fast in five instructions: the exponential and the reciprocal without
@@ -61,14 +62,25 @@ __global__ void __launch_bounds__(CONV_TREE_CH * CONV_TREE_GROUPS) kda_conv_tree
     using IO = ConvIO<ET, VC>;
     using R = typename IO::R;
     extern __shared__ __align__(128) uint8_t smem[];
-    R* rows = reinterpret_cast<R*>(smem);       // [KW - 1 + T][64]
+    float4* wide = reinterpret_cast<float4*>(smem);     // [vectors][VC]: a channel's four taps, at their place xor the vector's
+    R* rows = reinterpret_cast<R*>(smem + ConvTreeSmem<ET, VC>::WEIGHTS);       // [KW - 1 + T][vectors]
     const int cblocks = (p.C / VC + CONV_TREE_CH - 1) / CONV_TREE_CH;
     const int cb = (int)blockIdx.x % cblocks, r = (int)blockIdx.x / cblocks;
     const int ch = threadIdx.x % CONV_TREE_CH, grp = threadIdx.x / CONV_TREE_CH, tid = threadIdx.x;
     const int c = (cb * CONV_TREE_CH + ch) * VC, KW = p.KW;
-    uint64_t* taps = reinterpret_cast<uint64_t*>(rows + (KW - 1 + p.t) * CONV_TREE_CH);   // rows are multiples of 128 bytes
+    uint64_t* taps = reinterpret_cast<uint64_t*>(rows + (KW - 1 + p.t) * CONV_TREE_CH);
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
+    // a channel's weights are 16 bytes: fetched in order, read back by vector
+    const bool four = VC % 4 == 0 && KWM == 4 && KW == 4 && (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0;
+    auto place = [](int v, int c) { return v * VC + (c ^ (VC == 8 ? v & 7 : v >> 1 & 3)); };
+    auto copy16 = [](void* to, const void* from) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    };
+    if (four) {
+        for (int i = tid; i < CONV_TREE_CH * VC; i += CONV_TREE_CH * CONV_TREE_GROUPS)
+            if (cb * CONV_TREE_CH * VC + i < p.C) copy16(wide + place(i / VC, i % VC), reinterpret_cast<const float4*>(p.w) + cb * CONV_TREE_CH * VC + i);
+    }
     int tb = r * p.t, T = p.t;
     if (p.cu != nullptr) {
         tb = __ldg(p.cu + r);
@@ -95,17 +107,16 @@ __global__ void __launch_bounds__(CONV_TREE_CH * CONV_TREE_GROUPS) kda_conv_tree
     if (on) {
         const ET* x = static_cast<const ET*>(p.x) + (int64_t)tb * p.C + c;
         const ET* W = static_cast<const ET*>(p.window) + (int64_t)slot * p.slot_stride + (int64_t)acc * p.C + c;
-        for (int i = grp; i < KW - 1; i += CONV_TREE_GROUPS) rows[i * CONV_TREE_CH + ch] = rst ? IO::narrow(zero) : IO::ld(W + (int64_t)i * p.C);
-        constexpr int U = 8;
-        int j = grp;
-        for (; j + (U - 1) * CONV_TREE_GROUPS < T; j += U * CONV_TREE_GROUPS) {
-            R v[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) v[i] = IO::ld(x + (int64_t)(j + i * CONV_TREE_GROUPS) * p.C);
-#pragma unroll
-            for (int i = 0; i < U; ++i) rows[(KW - 1 + j + i * CONV_TREE_GROUPS) * CONV_TREE_CH + ch] = v[i];
+        auto copy = [&](int to, const ET* from) {
+            if constexpr (sizeof(R) == 16) copy16(rows + to * CONV_TREE_CH + ch, from);
+            else rows[to * CONV_TREE_CH + ch] = IO::ld(from);
+        };
+        for (int i = grp; i < KW - 1; i += CONV_TREE_GROUPS) {
+            if (rst) rows[i * CONV_TREE_CH + ch] = IO::narrow(zero);
+            else copy(i, W + (int64_t)i * p.C);
         }
-        for (; j < T; j += CONV_TREE_GROUPS) rows[(KW - 1 + j) * CONV_TREE_CH + ch] = IO::ld(x + (int64_t)j * p.C);
+#pragma unroll 8
+        for (int j = grp; j < T; j += CONV_TREE_GROUPS) copy(KW - 1 + j, x + (int64_t)j * p.C);
     }
     if (tid < T) {
         // byte i: the row of tap i
@@ -124,62 +135,85 @@ __global__ void __launch_bounds__(CONV_TREE_CH * CONV_TREE_GROUPS) kda_conv_tree
         }
         taps[tid] = packed;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    if (!on) return;
     // taps right-aligned: place i of KWM holds tap i - (KWM - KW)
     const int pad = KWM - KW;
     float w[KWM][VC], bias[VC];
-    if (on) {
-        const float* wp = p.w + (int64_t)c * KW;
-        if (VC % 4 == 0 && KWM == 4 && KW == 4 && (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0) {
+    if (four) {
 #pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(wp) + v);
-                w[0][v] = f.x;
-                w[1 % KWM][v] = f.y;
-                w[2 % KWM][v] = f.z;
-                w[3 % KWM][v] = f.w;
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < VC; ++v)
-#pragma unroll
-                for (int i = 0; i < KWM; ++i) w[i][v] = i >= pad ? __ldg(wp + v * KW + i - pad) : 0.f;
+        for (int v = 0; v < VC; ++v) {
+            const float4 f = wide[place(ch, v)];
+            w[0][v] = f.x;
+            w[1 % KWM][v] = f.y;
+            w[2 % KWM][v] = f.z;
+            w[3 % KWM][v] = f.w;
         }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VC; ++v)
+#pragma unroll
+            for (int i = 0; i < KWM; ++i) w[i][v] = i >= pad ? __ldg(p.w + (int64_t)(c + v) * KW + i - pad) : 0.f;
+    }
+    if (VC % 4 == 0 && p.bias != nullptr && (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0) {
+#pragma unroll
+        for (int v = 0; v < VC; v += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(p.bias + c + v));
+            bias[v] = f.x;
+            bias[(v + 1) % VC] = f.y;
+            bias[(v + 2) % VC] = f.z;
+            bias[(v + 3) % VC] = f.w;
+        }
+    } else {
 #pragma unroll
         for (int v = 0; v < VC; ++v) bias[v] = p.bias != nullptr ? __ldg(p.bias + c + v) : 0.f;
     }
-    __syncthreads();
-    if (!on) return;
-    for (int j = grp; j < T; j += CONV_TREE_GROUPS) {
-        const uint64_t packed = taps[j] << (8 * pad);
-        R z[KWM];
+    // two tokens at a time, step by step, so that their latencies overlap
+    constexpr int N = VC * KWM <= 32 ? 2 : 1;
+    for (int j = grp; j < T; j += N * CONV_TREE_GROUPS) {
+        R z[N][KWM];
 #pragma unroll
-        for (int i = 0; i < KWM; ++i)
-            if (i >= pad) z[i] = rows[(int)(packed >> (8 * i) & 0xffu) * CONV_TREE_CH + ch];
-        float s[VC];
+        for (int x = 0; x < N; ++x) {
+            const uint64_t packed = taps[min(j + x * CONV_TREE_GROUPS, T - 1)] << (8 * pad);
 #pragma unroll
-        for (int v = 0; v < VC; ++v) s[v] = bias[v];
+            for (int i = 0; i < KWM; ++i)
+                if (i >= pad) z[x][i] = rows[(int)(packed >> (8 * i) & 0xffu) * CONV_TREE_CH + ch];
+        }
+        float s[N][VC];
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+#pragma unroll
+            for (int v = 0; v < VC; ++v) s[x][v] = bias[v];
 #pragma unroll
         for (int i = 0; i < KWM; ++i) {
             if (i < pad) continue;
-            float f[VC];
-            IO::widen(z[i], f);
-            if constexpr (VC % 2 == 0) {    // two at a time, each as fmaf rounds
 #pragma unroll
-                for (int v = 0; v < VC; v += 2) {
-                    const float2 t = __ffma2_rn(make_float2(w[i][v], w[i][v + 1]), make_float2(f[v], f[v + 1]), make_float2(s[v], s[v + 1]));
-                    s[v] = t.x;
-                    s[v + 1] = t.y;
+            for (int x = 0; x < N; ++x) {
+                float f[VC];
+                IO::widen(z[x][i], f);
+                if constexpr (VC % 2 == 0) {    // two channels at a time, each as fmaf rounds
+#pragma unroll
+                    for (int v = 0; v < VC; v += 2) {
+                        const float2 t = __ffma2_rn(make_float2(w[i][v], w[i][v + 1]), make_float2(f[v], f[v + 1]), make_float2(s[x][v], s[x][v + 1]));
+                        s[x][v] = t.x;
+                        s[x][v + 1] = t.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < VC; ++v) s[x][v] = fmaf(w[i][v], f[v], s[x][v]);
                 }
-            } else {
-#pragma unroll
-                for (int v = 0; v < VC; ++v) s[v] = fmaf(w[i][v], f[v], s[v]);
             }
         }
         if (p.silu) {
 #pragma unroll
-            for (int v = 0; v < VC; ++v) s[v] = silu_short(s[v]);
+            for (int x = 0; x < N; ++x)
+#pragma unroll
+                for (int v = 0; v < VC; ++v) s[x][v] = silu_short(s[x][v]);
         }
-        IO::st(y + (int64_t)j * p.C, IO::narrow(s));
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+            if (j + x * CONV_TREE_GROUPS < T) IO::st(y + (int64_t)(j + x * CONV_TREE_GROUPS) * p.C, IO::narrow(s[x]));
     }
 }
 
