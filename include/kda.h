@@ -101,17 +101,18 @@ typedef enum kda_status {
 
 /*
  * KDA_LAUNCH_TEST_WITHHOLD_STATE: a test hook of kda_decode_step,
- *   kda_spec_verify, kda_step and kda_kv4_attend, for the timeout path only;
- *   never for production calls, and refused by every other entry point.  Each
+ *   kda_spec_verify, kda_step, kda_kv4_attend and kda_kv4_attend_tree, for the
+ *   timeout path only; never for production calls, and refused by every other
+ *   entry point.  Each
  *   tile arms
  *   its state tile's barrier but withholds the copy, so every wait on it gives
  *   up at its 1 s bound: the call then reports KDA_ERR_TIMEOUT through
  *   dev_status (after about 2 s: the wait, then a bounded drain), writes
  *   neither those tiles' states nor their outputs, and the context stays
  *   usable.  Requests that reset (no state read) are not affected.
- *   kda_kv4_attend withholds its block copies: it reports KDA_ERR_TIMEOUT
- *   after about 4 s, its output rows are zero or those of the keys worked on
- *   before, and the workspace is ready for the next call.
+ *   kda_kv4_attend and kda_kv4_attend_tree withhold their block copies: they
+ *   report KDA_ERR_TIMEOUT after about 4 s, output rows are zero or those of the keys
+ *   worked on before, and the workspace is ready for the next call.
  */
 #define KDA_LAUNCH_TEST_WITHHOLD_STATE (1u << 30)
 

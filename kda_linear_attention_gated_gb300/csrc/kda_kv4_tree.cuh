@@ -414,14 +414,16 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             const int32_t* table = p.table + (int64_t)w.r * p.cols;
             const uint8_t* base = p.pages + (int64_t)w.h * bpp * F::BLOCK;
             // the lane's next block, by page and place in it
-            int blk = (req.first + b0) * 4 + lane, pg = blk / bpp, in = blk - pg * bpp, stage = 0, page = -1;
+            int blk = (req.first + b0) * 4 + lane, pg = blk / bpp, in = blk - pg * bpp, stage = 0, page = 0;
+            bool wanted = false;
             const int low_end = p.window > 0 ? req.ctx - p.window + 1 : -1;     // blocks that end there are in no window
             auto look = [&](int b) {
-                page = b < b1 && lane < 4 && blk * 16 < last && low_end < (blk + 1) * 16 ? __ldg(table + pg) : -2;      // -2: not wanted
+                wanted = b < b1 && lane < 4 && blk * 16 < last && low_end < (blk + 1) * 16;
+                if (wanted) page = __ldg(table + pg);
             };
             auto fetch = [&](int b) {
-                const bool ok = page >= 0 && page < p.num_pages;
-                if (!ok && page != -2) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
+                const bool ok = wanted && page >= 0 && page < p.num_pages;
+                if (wanted && !ok) atomicCAS(p.status, 0, STATUS_SLOT_RANGE);
                 const uint32_t there = __ballot_sync(0xffffffffu, ok);
                 if (lane == 0) {
                     missing[stage] = there ^ 15u;

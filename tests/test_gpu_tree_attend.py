@@ -228,3 +228,135 @@ def test_attend_tree_captured_beside_another_step(lib, workspace):
             gr.replay()
     torch.cuda.synchronize()
     assert st.item() == 0 and torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+
+
+# -- wide trees: the rows of a key/value head past 48 go to the tensor cores' other kernel --------------------------
+WIDE = [("wide", 32, BF16, 128), ("wide", 32, F32, 128), ("forest", 24, F16, 64), ("chain", 24, BF16, 64), ("star", 40, F32, 64)]
+
+
+@pytest.mark.parametrize("shape,grp,dtype,dim", WIDE)
+@pytest.mark.parametrize("ctx", [0, 1, 63, 64, 65, 200])
+def test_wide_tree_contexts_around_a_unit_of_keys(lib, workspace, shape, grp, dtype, dim, ctx):
+    run(lib, workspace, 1, grp, dim, 16, [ctx], trees((3, shape)), dtype, dim, False, seed=ctx + grp)
+
+
+@pytest.mark.parametrize("dtype,dim,inter", [(BF16, 128, True), (F32, 128, True), (F32, 128, False), (F16, 128, False), (BF16, 64, False), (F32, 64, True)])
+def test_wide_tree_rows_around_a_tile(lib, workspace, dtype, dim, inter):
+    """127, 128, 129 and 256 rows, and one head of many."""
+    for t, grp in ((1, 127), (16, 8), (43, 3), (64, 4)):
+        run(lib, workspace, 1, grp, dim, 32, [70], trees((t, "wide")), dtype, dim // 2, inter, seed=t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_wide_trees_of_many_ragged_requests(lib, workspace, dtype):
+    """40 requests and more, some empty, some padding: shares that begin and end anywhere in the list."""
+    shapes = [(0 if r % 7 == 3 else 1 + (5 * r) % 9, ("wide", "chain", "star")[r % 3]) for r in range(43)]
+    ctx = [-shapes[r][0] if r % 11 == 5 else (37 * r) % 150 for r in range(43)]
+    run(lib, workspace, 1, 8, 64, 16, ctx, trees(*shapes), dtype, 64, False, seed=4)
+
+
+def test_wide_tree_one_long_context_over_the_card(lib, workspace):
+    run(lib, workspace, 1, 10, 128, 64, [20011], trees((7, "wide")), BF16, 128, False, seed=5)
+    run(lib, workspace, 2, 26, 64, 64, [9000, 64], trees((2, "wide"), (5, "wide")), F32, 64, False, window=700, seed=6)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, F32), (64, BF16), (128, BF16), (128, F16)])
+def test_wide_tree_nan_stays_with_the_rows_that_see_it(lib, workspace, dim, dtype):
+    """NaN in a drafted token's key or value, and in the value of a context token that a window hides from deep rows."""
+    par = [-1, 0, 0, 1, 2, 4, 0, 6]
+    for which in (0, 1):
+        def poison(r, sk, sv):
+            (sk, sv)[which][50 + 2, 0, 1] = 0x7F
+        got, want = run(lib, workspace, 1, 16, dim, 16, [50], [par], dtype, 64, False, poison=poison)
+        assert want.isnan().flatten(1).any(1).tolist() == [False, False, True, False, True, True, False, False]
+    def early(r, sk, sv):
+        sv[11, 0, dim // 16 - 1] = 0x7F
+        sv[30, 0, 0] = 0x7F
+    got, want = run(lib, workspace, 1, 16, dim, 16, [50], [par], dtype, 64, False, poison=early, window=40)
+    assert want[:, :, dim - 1].isnan().all(1).tolist() == [True] + [False] * 7        # key 11 is in the root's window alone
+    assert want[:, :, 0].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_wide_tree_queries_far_from_one_and_not_finite(lib, workspace, dtype):
+    def edit(q):
+        q[0] *= 40.0
+        q[1] = 0.0
+        q[2] *= 2.0 ** -60
+        q[3, 5, 7] = float("nan")
+        q[4, 20, 0] = float("inf")
+        q[5, 31, 9] = -float("inf")
+    g = torch.Generator().manual_seed(3)
+    cache = ref.Cache([157], 1, 128, 16, g)
+    q = (torch.randn(7, 32, 128, generator=g) * 1.5).to(dtype)
+    edit(q)
+    o, st = torch.zeros(7, 32, 128, dtype=dtype, device="cuda"), i32([0])
+    par = [ref_par for ref_par in trees((7, "wide"))]
+    lib.kda_kv4_attend_tree(cache.pages.cuda(), cache.table.cuda(), i32([150]), q.cuda(), tree_ref.masks(par), o, workspace, st)
+    bad = torch.zeros(7, 32, dtype=torch.bool)
+    bad[3, 5] = bad[4, 20] = bad[5, 31] = True
+    got = o.cpu().double()
+    assert st.item() == 0 and torch.equal(got.isnan().all(-1), bad) and torch.equal(got.isnan().any(-1), bad)
+    want, err, big, top = tree_ref.attend(cache, [150], par, torch.where(bad[..., None], torch.zeros_like(q), q), None, None, False)
+    lim = ref.attend_tolerance(want, err, big, top, dtype, dtype != BF16)
+    assert ((got - want).abs() <= lim)[~bad].all()
+
+
+def test_wide_tree_bad_contexts_tables_and_pages(lib, workspace):
+    dim = 64
+    pages = torch.full((4, 1, 1, 18 * dim), 0x11, dtype=torch.uint8, device="cuda")
+    table = i32([[0, 1], [2, 3], [3, 1]])
+    pars = trees((3, "star"), (3, "star"), (3, "star"))
+    q = torch.randn(9, 20, dim, device="cuda")
+    cos, sin = (t.cuda() for t in ref.tables(20, 32))
+
+    def go(table, ctx, rot=True, cu=None):
+        o, st = torch.full_like(q, 5.0), i32([0])
+        lib.kda_kv4_attend_tree(pages, table, i32(ctx), q, tree_ref.masks(pars), o, workspace, st, cu_seqlens=None if cu is None else i32(cu),
+                                max_t=3, cos=cos if rot else None, sin=sin if rot else None)
+        torch.cuda.synchronize()
+        rows = lambda v: (o == v).flatten(1).all(1).view(3, 3).all(1).tolist()  # noqa: E731
+        return st.item(), rows(0), rows(5)
+
+    assert go(table, [4, 4, 4]) == (kda.KDA_OK, [False] * 3, [False] * 3)
+    assert go(table, [4, -1, 4]) == (kda.KDA_ERR_ARG, [False, True, False], [False] * 3)
+    assert go(table, [4, -3, 4]) == (kda.KDA_OK, [False, True, False], [False] * 3)
+    assert go(table, [4, 18, 4]) == (kda.KDA_ERR_ARG, [False, True, False], [False] * 3)
+    assert go(table, [4, 30, 4], rot=False) == (kda.KDA_ERR_ARG, [False, True, False], [False] * 3)
+    assert go(table, [4, 2 ** 31 - 1, 4], rot=False) == (kda.KDA_ERR_ARG, [False, True, False], [False] * 3)
+    for page in (4, -1, -2, 2 ** 31 - 1, -2 ** 31):
+        bad = table.clone()
+        bad[1, 0] = page
+        assert go(bad, [4, 4, 4]) == (kda.KDA_ERR_SLOT_RANGE, [False, True, False], [False] * 3), page
+    st, zero, kept = go(table, [4, 4, 4], cu=[0, 3, 7, 9])      # four tokens: that request is skipped
+    assert st == kda.KDA_ERR_ARG and zero == [False] * 3
+    # a page that is missing inside a context: its keys are not seen, the others are
+    big = torch.randint(0, 256, (8, 1, 4, 18 * dim), generator=torch.Generator().manual_seed(1)).to(torch.uint8)
+    big[..., 16 * dim:] = 0x30
+    big = big.cuda()
+    qs = torch.randn(3, 20, dim, device="cuda")
+    outs = []
+    for tab, ctx in ((i32([[0, 99, 2]]), 130), (i32([[0, 2]]), 66)):
+        o, st = torch.zeros_like(qs), i32([0])
+        lib.kda_kv4_attend_tree(big, tab, i32([ctx]), qs, tree_ref.masks(trees((3, "star"))), o, workspace, st)
+        outs.append(o)
+        assert st.item() == (kda.KDA_ERR_SLOT_RANGE if ctx == 130 else 0)
+    assert (outs[0] - outs[1]).abs().max() <= 1e-5 * outs[1].abs().max()
+
+
+@pytest.mark.parametrize("grp,dtype", [(4, BF16), (20, BF16), (20, F32)])
+def test_attend_tree_reports_a_wait_that_runs_out(lib, workspace, grp, dtype):
+    """Copies withheld by the test hook: the status, no fault, and the same workspace right again."""
+    g = torch.Generator().manual_seed(2)
+    cache = ref.Cache([203], 2, 64, 16, g)
+    q, o = torch.randn(3, 2 * grp, 64, generator=g).to(dtype).cuda(), torch.full((3, 2 * grp, 64), 5.0, dtype=dtype, device="cuda")
+    st, tree = i32([0]), tree_ref.masks(trees((3, "star")))
+    common = (cache.pages.cuda(), cache.table.cuda(), i32([200]), q, tree, o, workspace, st)
+    lib.kda_kv4_attend_tree(*common, flags=kda.KDA_LAUNCH_TEST_WITHHOLD_STATE)
+    torch.cuda.synchronize()
+    assert st.item() == kda.KDA_ERR_TIMEOUT and (o == 0).all()
+    st.zero_()
+    lib.kda_kv4_attend_tree(*common)
+    want, err, big, top = tree_ref.attend(cache, [200], trees((3, "star")), q.cpu(), None, None, False)
+    assert st.item() == 0
+    assert ((o.cpu().double() - want).abs() <= ref.attend_tolerance(want, err, big, top, dtype, dtype != BF16)).all()

@@ -100,6 +100,10 @@ class Step:
     ([(9, "forest")] * 3, 3, 1, 16, 16, BF16, True),
     ([(7, "wide")] * 13, 6, 3, 112, 32, F32, False),
     ([(4, "wide")] * 40, 8, 8, 32, 128, F16, False),
+    # enough column groups for one warp each, whole tiles and not
+    ([(9, "wide")] * 8, 8, 4, 128, 128, BF16, False),
+    ([(33, "forest")], 58, 58, 128, 128, F16, True),
+    ([(13, "wide"), (64, "chain")], 50, 25, 64, 80, F32, False),
 ])
 def test_step_tree_against_fp64(libs, pool_dtype, shapes, hv, hqk, kd, vd, dtype, learned):
     s = Step([ref.parents(t, k, i) for i, (t, k) in enumerate(shapes)], hv, hqk, kd, vd, pool_dtype, dtype, learned, seed=hv + kd)
