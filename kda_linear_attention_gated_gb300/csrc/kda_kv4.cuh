@@ -730,9 +730,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const int i = i0 + warp + k * KV4_WARPS, j = i / p.grp;
-            int pos = get.q.ctx + j;
-            if constexpr (TREE)
-                if (j < get.q.t) pos = get.q.ctx + __popcll(tree_mask(p.tree, get.q.tok0 + j, j)) - 1;
+            const int pos = get.q.ctx + (TREE && j < get.q.t ? __popcll(tree_mask(p.tree, get.q.tok0 + j, j)) - 1 : j);
             const int64_t base = (int64_t)(get.q.tok0 + j) * p.q_stride + (int64_t)(h * p.grp + i - j * p.grp) * D;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -874,10 +872,11 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
     // registers
     auto row_pos = [&](int i) { return cur.q.ctx + (cur.i0 + i) / p.grp; };
     // (a tree's row may see any token of the request: the last one)
-    auto last_row_pos = [&]() { return cur.q.ctx + (TREE ? cur.q.t - 1 : min(cur.q.t - 1, (cur.i0 + ROWS - 1) / p.grp)); };
-    // whether a row sees a key: a chain's by their positions
-    auto sees_chain = [&](int pos, int key) { return key <= pos && (p.window <= 0 || key > pos - p.window); };
-    // a tree's by row i's mask, of which a window leaves the last ones, and the first key of the context that it sees
+    auto last_row_pos = [&]() {
+        if constexpr (TREE) return cur.q.ctx + cur.q.t - 1;
+        return cur.q.ctx + min(cur.q.t - 1, (cur.i0 + ROWS - 1) / p.grp);
+    };
+    // a tree's row sees keys by its mask, of which a window leaves the last ones, and the first key of the context that it sees
     auto tree_row = [&](int i, uint64_t& own, int& low) {
         const int j = (cur.i0 + i) / p.grp;
         own = 0;
@@ -991,14 +990,21 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                 if (masked) {
 #pragma unroll
                     for (int a = 0; a < 2 * NB; ++a) {
+                        if constexpr (TREE) {
+                            uint64_t own;
+                            int low;
+                            tree_row(row_of(a), own, low);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (!sees_tree(own, low, unit * KV4_KEYS + i * 8 + g) || (miss >> (i >> 1) & 1u))
+                                    s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
+                            continue;
+                        }
                         const int pos = row_pos(row_of(a));
-                        uint64_t own = 0;
-                        int low = 0;
-                        if constexpr (TREE) tree_row(row_of(a), own, low);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int key = unit * KV4_KEYS + i * 8 + g;
-                            if (!(TREE ? sees_tree(own, low, key) : sees_chain(pos, key)) || (miss >> (i >> 1) & 1u))
+                            if (key > pos || (p.window > 0 && key <= pos - p.window) || (miss >> (i >> 1) & 1u))
                                 s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
                         }
                     }
@@ -1082,11 +1088,15 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
                                 if ((W[kv4_v_scale<D>(w, grp)] & 0x7f) != 0x7f || key0 + w > to) continue;
 #pragma unroll
                                 for (int a = 0; a < 2 * NB; ++a) {
+                                    if constexpr (TREE) {
+                                        uint64_t own;
+                                        int low;
+                                        tree_row(row_of(a), own, low);
+                                        if (sees_tree(own, low, key0 + w)) hit |= 1u << a;
+                                        continue;
+                                    }
                                     const int pos = row_pos(row_of(a));
-                                    uint64_t own = 0;
-                                    int low = 0;
-                                    if constexpr (TREE) tree_row(row_of(a), own, low);
-                                    if (TREE ? sees_tree(own, low, key0 + w) : sees_chain(pos, key0 + w)) hit |= 1u << a;
+                                    if (key0 + w <= pos && (p.window <= 0 || key0 + w > pos - p.window)) hit |= 1u << a;
                                 }
                             }
 #pragma unroll
