@@ -103,16 +103,15 @@ typedef enum kda_status {
  * KDA_LAUNCH_TEST_WITHHOLD_STATE: a test hook of kda_decode_step,
  *   kda_spec_verify, kda_step, kda_kv4_attend and kda_kv4_attend_tree, for the
  *   timeout path only; never for production calls, and refused by every other
- *   entry point.  Each
- *   tile arms
- *   its state tile's barrier but withholds the copy, so every wait on it gives
- *   up at its 1 s bound: the call then reports KDA_ERR_TIMEOUT through
- *   dev_status (after about 2 s: the wait, then a bounded drain), writes
- *   neither those tiles' states nor their outputs, and the context stays
- *   usable.  Requests that reset (no state read) are not affected.
- *   kda_kv4_attend and kda_kv4_attend_tree withhold their block copies: they
- *   report KDA_ERR_TIMEOUT after about 4 s, output rows are zero or those of the keys
- *   worked on before, and the workspace is ready for the next call.
+ *   entry point.  Each tile arms its state tile's barrier but withholds the
+ *   copy, so every wait on it gives up at its 1 s bound: the call then reports
+ *   KDA_ERR_TIMEOUT through dev_status (after about 2 s: the wait, then a
+ *   bounded drain), writes neither those tiles' states nor their outputs, and
+ *   the context stays usable.  Requests that reset (no state read) are not
+ *   affected.  kda_kv4_attend and kda_kv4_attend_tree withhold their block
+ *   copies: they report KDA_ERR_TIMEOUT after about 4 s, output rows are zero
+ *   or those of the keys worked on before, and the workspace is ready for the
+ *   next call.
  */
 #define KDA_LAUNCH_TEST_WITHHOLD_STATE (1u << 30)
 
@@ -900,8 +899,9 @@ int kda_kv4_attend_tree(const kda_kv4_cache* cache, const kda_kv4_attend_args* a
  * 1.  Where no child is left, the next token is the lowest i with W(i) > 0 and
  * sum_{l <= i} W(l) > u_last sum W, or, if rounding leaves none, the last with
  * W(i) > 0; if W is zero throughout, W is the row of p again.  Accepted tokens
- * and the next one are distributed as the target's own.  Sums are held in 48
- * bits or more, tests in 53.
+ * and the next one are distributed as the target's own.  Sums and the sides of
+ * the tests are pairs of floats, 46 bits or more; the test of a token's first
+ * child, u q(x) < p(x), is exact.
  *   accepted  [n]         tokens accepted, token 0 among them; 0 without tokens
  *   node      [n]         1 + the last one's place in its request (kda_step_tree's
  *                         `accepted` in the next step, where its columns are); 0 without tokens

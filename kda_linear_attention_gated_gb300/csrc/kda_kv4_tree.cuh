@@ -107,12 +107,29 @@ constexpr int KVT_ROWS = 128;            // query rows of a tile: the tensor cor
 constexpr int KVT_KEYS = 64;             // keys of a unit of work: four blocks
 constexpr int KVT_WARPS = 8;              // that compute; one more fetches the codes and starts the products
 constexpr int KVT_THREADS = 32 * (KVT_WARPS + 1);
-constexpr int KVT_STAGES = 3;            // units of codes in flight
-constexpr int KVT_PART = 6;              // what beginning and ending a part costs a CTA, in units
+constexpr int KVT_STAGES = 3;            // units of codes: one read for its values, one for its keys, one on its way; a
+                                         // fourth would leave an SM's second CTA without shared memory
+// What beginning and ending a part costs a CTA, in units.  3, 6, 10, us: 32
+// requests of up to 16 tokens, 16383 keys 123, 94, 92; 8 of 64 tokens, 8192
+// keys 135, 133, 135; 4 of 32, 4000 keys 46, 46, 49; 1 of 64, 20000 67.6, 64.5,
+// 65.5.
+constexpr int KVT_PART = 6;
 constexpr int KVT_FIRST = KVT_PART + 2, KVT_LAST = 2;   // what a cut leaves before and after it in a tile (see Kv4Shape)
 constexpr int KVT_MAX_CTAS = 304;        // two for each of 152 SMs
-constexpr int KVT_MIN_ROWS = 48;         // narrower trees go to kda_kv4_attend_kernel
-constexpr int KVT_JOIN_GROUPS = 16;      // CTAs that join a tile
+// Calls with at most so many query rows a head (tokens times query heads of a
+// key/value head) go to kda_kv4_attend_kernel, whose time grows with the rows;
+// this one's is that of 128 rows.  That kernel / this one at 32, 48, 64 and 128
+// rows, us: 16 requests, 8192 keys, 8 heads of 128, bf16 101/122, 139/124,
+// 177/127, 330/133; fp16 (two products) 156/203, 222/205, 291/207, 559/215;
+// heads of 64, bf16 70/98, 96/98, 121/100, 222/103; fp32 101/115, 143/117,
+// 186/119, 354/123; one request, 8 heads of 128, bf16, 100000 keys 80/104,
+// 113/106, 131/109, 242/113; 8192 keys 31/35, 33/36, 35/36, 43/38.  Short
+// contexts would gain from staying there (500 keys, fp16, 64 rows 25/37), but
+// their lengths are on the device.
+constexpr int KVT_MIN_ROWS = 48;
+// CTAs that join a tile.  1, 4, 16, us: one request of 24 tokens, 131071 keys
+// (76 CTAs a tile) 381, 146, 88; 32 of up to 16, 16383 keys 128, 99, 94.
+constexpr int KVT_JOIN_GROUPS = 16;
 constexpr int KVT_COUNTERS = 4096;       // bytes at the head of the workspace that kda_kv4_attend_kernel's counters take
 constexpr int KVT_TMEM = 256;            // columns: scores and sums; two CTAs an SM share 512
 
@@ -296,12 +313,28 @@ template <int D> struct KvtPart {
 // remainders, and probabilities with theirs, as second operands into the same
 // sums.
 //
-// A unit of 64 keys: all threads write K's values to shared memory in the
-// tensor cores' layout; while they take the scores, all write V's; two threads a
-// row then take its scores to probabilities, to shared memory again; while the
-// tensor cores add P V, the next unit's keys are on.  The other CTA of the SM
-// fills what one leaves idle.  V is used as it lies, keys by channels (its rows
-// run along N).
+// A unit of 64 keys is a step between two barriers of the CTA.  Behind the
+// first the control warp starts the unit's scores and the last unit's P V;
+// meanwhile the eight others write the next unit's keys to shared memory in the
+// tensor cores' layout (two places, in turn).  They then take the scores to
+// probabilities, a thread half a row, back into tensor memory, where the tensor
+// cores read them, and write this unit's values.  V is used as it lies, keys by
+// channels (its rows run along N).  A running maximum moves only past a slack of
+// KV4_SLACK, so O is seldom scaled.  The other CTA of the SM fills what one
+// leaves idle.
+//
+// Measured, us: 8 requests of 64 tokens, 8192 keys, 4 query heads on each of 8
+// heads of 128, bf16: 130.5, where the products take 36.2 at the measured rate
+// and the codes 12.5; 32 of up to 16 tokens, 6 query heads on each of 8, 16383
+// keys at most: 92.1 (8.7 and 12.7; most of the 128 rows are empty); 1 of 24,
+// 131071 keys, 4 heads of 64, fp16: 87.1 (13.5 and 5.6).  The two CTAs of an SM
+// issue in 45 of 100 cycles, 440 instructions a warp and unit, the tensor cores
+// are busy in 23: bound by a step's chain, scores - probabilities - barrier,
+// and by issue.  Values written while the scores are on their way from tensor
+// memory: the same.  The first size on the way here: warp products of 16 rows
+// 324; tensor cores, a barrier between any two steps 259; one barrier a unit, a
+// warp for copies and products 141; probabilities in tensor memory and two places
+// for keys 135; queries four rows at a time 130 (the second size 105, then 92).
 //
 // Parts of a (request, head, tile) that several CTAs share go to the
 // workspace, and kda_kv4_tree_join_kernel adds them in order.
