@@ -195,6 +195,8 @@ int attend(const kda_kv4_cache* cache, const kda_kv4_attend_args* args, const ui
     if (g.reserved != 0 || g.window < 0 || !std::isfinite(g.scale)) return KDA_ERR_ARG;
     if (g.h_q < 1 || g.h_q % cache->heads != 0 || g.max_t > (TREE ? kda::TREE_MAX : KDA_KV4_MAX_TOKENS) || g.q_stride < (int64_t)g.h_q * cache->dim)
         return KDA_ERR_SHAPE;
+    // the wide tree's units of keys, too, end below 2^31
+    if (TREE && (int64_t)g.table_cols * cache->page_tokens > 0x7fffffffLL - kda::KVT_KEYS) return KDA_ERR_SHAPE;
     const int grp = g.h_q / cache->heads;
     // rows of a tile and their rounding (kda_kv4.cuh)
     const int mode = g.dtype != KDA_BF16 ? kda::KV4_REST : (int64_t)g.max_t * grp <= 8 ? kda::KV4_8 : kda::KV4_16;

@@ -115,6 +115,16 @@ def test_kv4_tree_refusals(lib):
         assert call(P, rope_rows=0) == E.KDA_ERR_SHAPE
         assert call(P, flags=kda.KDA_LAUNCH_PDL_EARLY_STATE) == E.KDA_ERR_ARG
         assert call(None, n=0, total=0) == E.KDA_OK
+    for small in (0, kda.KDA_KV4_WORKSPACE_BYTES, kda.KDA_KV4_TREE_WORKSPACE_BYTES - 1):
+        args = attend_args(workspace_bytes=small)
+        assert lib.lib.kda_kv4_attend_tree(ctypes.byref(cache_desc()), ctypes.byref(args), P, P, 0, None) == E.KDA_ERR_SHAPE
+
+
+def test_kv4_tree_tables_next_to_2_31_tokens_are_refused(lib):
+    """The end of the last unit of 64 keys stays below 2^31."""
+    one = cache_desc(heads=1, page_tokens=16)
+    args = attend_args(table_cols=(2 ** 31 - 48) // 16, h_q=1, rot_dim=0, n=0, total=0)
+    assert lib.lib.kda_kv4_attend_tree(ctypes.byref(one), ctypes.byref(args), P, P, 0, None) == E.KDA_ERR_SHAPE
 
 
 def test_cpu_tensors_and_missing_trees_are_refused(lib):
