@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 const bool rare = nan_any[(b - 1) & 1] != 0;
                 if (tc_elect()) {
                     tc_fence_after();
+                    if (b > b0) add_values(b > b0 + 1);
                     if (b >= b0 && b < b1) {
                         const uint64_t dKb = tc_step(dK, (b & 1) * SM::K);
 #pragma unroll
@@ -513,7 +514,6 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                                        tc_step(dKb, k / 4 * (KVT_KEYS * 128) + k % 4 * 32), id_s, part + k > 0);
                         tc_commit(bar_s);
                     }
-                    if (b > b0) add_values(b > b0 + 1);
                 }
                 __syncwarp();
                 if (b >= b0 && b + 2 < b1) fetch(b + 2);        // into the stage of unit b - 1
@@ -523,6 +523,8 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
         } else {
             const int &b0 = w.b0, &b1 = w.b1;
             const int rows = min(KVT_ROWS, req.t * p.grp - w.i0);
+            // rows of the warps that have any; what the others' are is seen nowhere, since a row is a row in both products
+            const int live = (rows + 31) & ~31;
             // ---- queries: fetched together, where keys, values and probabilities will be; then rotated, scaled to
             // below 1 by a power of two, rounded: 16 neighbouring rows a warp, a row at a time ----
             {
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                     const int dtype = SPLIT ? p.dtype : 2;
                     const bool turns = d < p.rot;
 #pragma unroll 1
-                    for (int k = 0; k < each; k += G) {
+                    for (int k = 0; k < each && w0 + k < live; k += G) {
                         float x[G][E];
 #pragma unroll
                         for (int r = 0; r < G; ++r) {
@@ -657,6 +659,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             float m = -FLT_MAX, l = 0.f;
             if (half == 0) row_nan[row] = 0;
             const float c = rowf[row];
+            const bool idle = 32 * (warp & 3) >= live;
             bool ok = true;
             int st = 0;                 // the stage of unit b + 1, whose keys are next
 
@@ -726,81 +729,12 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 const uint32_t miss = missing[sv];
                 // keys that every row sees: [ctx + t - window, ctx)
                 const bool masked = key0 + KVT_KEYS > req.ctx || (p.window > 0 && key0 < req.ctx + req.t - p.window) || miss != 0;
-                // ---- scores to probabilities, when the last unit's are done with ----
-                ok = mbar_poll(bar_s, phase(KVT_STAGES));
-                if (ok) phases ^= 1u << KVT_STAGES;
-                if (ok && b > b0) {
+                // ---- values, when the last unit's products are done with: 16 channels (64: 8) of two tokens a thread ----
+                if (b > b0) {
                     ok = mbar_poll(bar_o, phase(KVT_STAGES + 1));
                     if (ok) phases ^= 1u << (KVT_STAGES + 1);
                 }
-                // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
-                ok = __all_sync(0xffffffffu, ok);
-                tc_fence_after();
-                float s[32], top = -INFINITY;
                 if (ok) {
-                    tmem_ld32(tm_s() + lane_base + 32 * half, s);
-                    if (masked) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int at = 32 * half + i;
-                            if (!sees(key0 + at) || (miss >> (at >> 4) & 1u)) s[i] = -INFINITY;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(s[i], s[i + 1]), top);
-                }
-                top *= c;
-                // seldom: a score above its row's running maximum by more than the slack, in either half
-                if (pair_any(1 + (warp & 3), top > m + KV4_SLACK)) {
-                    half_max[half * KVT_ROWS + row] = top;
-                    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-                    top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]);
-                    const bool grow = top > m + KV4_SLACK;
-                    const float f = grow ? ex2f(m - top) : 1.f;
-                    if (grow) m = top;
-                    l *= f;
-                    if (ok && b > b0) {
-#pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
-                            const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
-                            float o[16];
-                            uint32_t r[16];
-                            tmem_ld16(at, o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * f);
-                            tmem_st16(at, r);
-                        }
-                    }
-                    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");      // half_max is read
-                }
-                if (ok) {
-                    const float neg = KV4_LIFT - m;
-                    float2 sum = make_float2(l, 0.f);
-                    uint32_t hi[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(c, c), make_float2(neg, neg));
-                        const float x0 = ex2f(x.x), x1 = ex2f(x.y);
-                        sum = __fadd2_rn(sum, make_float2(x0, x1));
-                        const __half2 hh = __floats2half2_rn(x0, x1);
-                        hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
-                        if constexpr (SPLIT) {
-                            const float2 f = __half22float2(hh);
-                            s[2 * i] = x0 - f.x;
-                            s[2 * i + 1] = x1 - f.y;
-                        }
-                    }
-                    tmem_st16(tm_p() + lane_base + 16 * half, hi);
-                    if constexpr (SPLIT) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const __half2 rest = __floats2half2_rn(s[2 * i], s[2 * i + 1]);
-                            hi[i] = *reinterpret_cast<const uint32_t*>(&rest);
-                        }
-                        tmem_st16(tm_p() + lane_base + KVT_KEYS / 2 + 16 * half, hi);
-                    }
-                    l = sum.x + sum.y;
-                    // ---- values: 16 channels (64: 8) of two tokens a thread ----
                     const int bk = tid >> 6, hf = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
                     const uint8_t* B = raw + sv * SM::STAGE + bk * F::BLOCK;
                     const int key = bk * 16 + hf * 8 + 2 * tp, grp = D == 128 ? g : g >> 1;     // its first token, its scale group
@@ -842,6 +776,81 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                             make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
+                // ---- scores to probabilities ----
+                if (ok) {
+                    ok = mbar_poll(bar_s, phase(KVT_STAGES));
+                    if (ok) phases ^= 1u << KVT_STAGES;
+                }
+                // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                if (!idle) {
+                    float s[32], top = -INFINITY;
+                    if (ok) {
+                        tmem_ld32(tm_s() + lane_base + 32 * half, s);
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int at = 32 * half + i;
+                                if (!sees(key0 + at) || (miss >> (at >> 4) & 1u)) s[i] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(s[i], s[i + 1]), top);
+                    }
+                    top *= c;
+                    // seldom: a score above its row's running maximum by more than the slack, in either half
+                    if (pair_any(1 + (warp & 3), top > m + KV4_SLACK)) {
+                        half_max[half * KVT_ROWS + row] = top;
+                        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+                        top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]);
+                        const bool grow = top > m + KV4_SLACK;
+                        const float f = grow ? ex2f(m - top) : 1.f;
+                        if (grow) m = top;
+                        l *= f;
+                        if (ok && b > b0) {
+#pragma unroll 1
+                            for (int k = 0; k < D / 32; ++k) {
+                                const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
+                                float o[16];
+                                uint32_t r[16];
+                                tmem_ld16(at, o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * f);
+                                tmem_st16(at, r);
+                            }
+                        }
+                        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");      // half_max is read
+                    }
+                    if (ok) {
+                        const float neg = KV4_LIFT - m;
+                        float2 sum = make_float2(l, 0.f);
+                        uint32_t hi[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(c, c), make_float2(neg, neg));
+                            const float x0 = ex2f(x.x), x1 = ex2f(x.y);
+                            sum = __fadd2_rn(sum, make_float2(x0, x1));
+                            const __half2 hh = __floats2half2_rn(x0, x1);
+                            hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
+                            if constexpr (SPLIT) {
+                                const float2 f = __half22float2(hh);
+                                s[2 * i] = x0 - f.x;
+                                s[2 * i + 1] = x1 - f.y;
+                            }
+                        }
+                        tmem_st16(tm_p() + lane_base + 16 * half, hi);
+                        if constexpr (SPLIT) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const __half2 rest = __floats2half2_rn(s[2 * i], s[2 * i + 1]);
+                                hi[i] = *reinterpret_cast<const uint32_t*>(&rest);
+                            }
+                            tmem_st16(tm_p() + lane_base + KVT_KEYS / 2 + 16 * half, hi);
+                        }
+                        l = sum.x + sum.y;
+                    }
+                }
             }
             if (alive) {                // the last unit's
                 fence_proxy_async_smem();
@@ -871,6 +880,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
+                    if (idle) break;
                     float o[16];
                     const int d0 = half * (D / 2) + 16 * k;
                     tmem_ld16(tm_o() + lane_base + d0, o);
