@@ -694,8 +694,11 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                             const uint4 c = *reinterpret_cast<const uint4*>(B + F::KC + (key & 15) * 64 + q * 16);
                             uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::KS + (key & 15) * 8 + 2 * q);
                             if (gone) s2 = 0;
-                            const uint32_t sc = cvt_e4m3x2_f16x2(s2);
-                            const uint32_t code[4] = {c.x, c.y, c.z, c.w};
+                            // every other quarter takes its words from the middle on, so that eight lanes' stores fall on
+                            // different banks
+                            const bool swap = (q & 2) != 0;
+                            const uint32_t two = cvt_e4m3x2_f16x2(s2), sc = swap ? __byte_perm(two, two, 0x1032) : two;
+                            const uint32_t code[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
                             uint8_t* to = K + ((b + 1) & 1) * SM::K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                                 cvt_e2m1x8_f16(code[i], v);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
-                                *reinterpret_cast<uint4*>(to + ((((q & 1) * 4 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                                *reinterpret_cast<uint4*>(to + ((((q & 1) * 4 + i) ^ (q & 2) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                             }
                         } else {
                             const uint2 c = *reinterpret_cast<const uint2*>(B + F::KC + (key & 15) * 32 + q * 8);
