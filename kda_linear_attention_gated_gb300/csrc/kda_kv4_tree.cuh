@@ -118,14 +118,14 @@ constexpr int KVT_FIRST = KVT_PART + 2, KVT_LAST = 2;   // what a cut leaves bef
 constexpr int KVT_MAX_CTAS = 304;        // two for each of 152 SMs
 // Calls with at most so many query rows a head (tokens times query heads of a
 // key/value head) go to kda_kv4_attend_kernel, whose time grows with the rows;
-// this one's is that of 128 rows.  That kernel / this one at 32, 48, 64 and 128
-// rows, us: 16 requests, 8192 keys, 8 heads of 128, bf16 101/122, 139/124,
-// 177/127, 330/133; fp16 (two products) 156/203, 222/205, 291/207, 559/215;
-// heads of 64, bf16 70/98, 96/98, 121/100, 222/103; fp32 101/115, 143/117,
-// 186/119, 354/123; one request, 8 heads of 128, bf16, 100000 keys 80/104,
-// 113/106, 131/109, 242/113; 8192 keys 31/35, 33/36, 35/36, 43/38.  Short
-// contexts would gain from staying there (500 keys, fp16, 64 rows 25/37), but
-// their lengths are on the device.
+// this one's is nearly that of 128 rows.  That kernel / this one at 32, 48, 64
+// and 128 rows, us: 16 requests, 8192 keys, 8 heads of 128, bf16 101/111,
+// 139/117, 177/117, 330/129; fp16 (two products) 156/207, 222/207, 291/207,
+// 559/213; heads of 64, bf16 70/92, 96/97, 121/98, 222/104; fp32 101/102,
+// 143/113, 186/113, 354/123; one request, 8 heads of 128, bf16, 100000 keys
+// 80/96, 113/100, 131/100, 242/109; 8192 keys 31/35, 33/35, 35/35, 43/38; 500
+// keys 22/30, 22/30, 31/34, 30/36.  At 48 rows short contexts gain by staying
+// there and long ones lose; their lengths are on the device.
 constexpr int KVT_MIN_ROWS = 48;
 // CTAs that join a tile.  1, 4, 16, us: one request of 24 tokens, 131071 keys
 // (76 CTAs a tile) 381, 146, 88; 32 of up to 16, 16383 keys 128, 99, 94.
@@ -314,27 +314,31 @@ template <int D> struct KvtPart {
 // sums.
 //
 // A unit of 64 keys is a step between two barriers of the CTA.  Behind the
-// first the control warp starts the unit's scores and the last unit's P V;
+// first the control warp starts the last unit's P V and the unit's scores;
 // meanwhile the eight others write the next unit's keys to shared memory in the
-// tensor cores' layout (two places, in turn).  They then take the scores to
-// probabilities, a thread half a row, back into tensor memory, where the tensor
-// cores read them, and write this unit's values.  V is used as it lies, keys by
+// tensor cores' layout (two places, in turn) and, once P V is done, this unit's
+// values.  They then take the scores to probabilities, a thread half a row, back
+// into tensor memory, where the tensor cores read them.  V is used as it lies, keys by
 // channels (its rows run along N).  A running maximum moves only past a slack of
 // KV4_SLACK, so O is seldom scaled.  The other CTA of the SM fills what one
 // leaves idle.
 //
 // Measured, us: 8 requests of 64 tokens, 8192 keys, 4 query heads on each of 8
-// heads of 128, bf16: 130.5, where the products take 36.2 at the measured rate
+// heads of 128, bf16: 126, where the products take 36.2 at the measured rate
 // and the codes 12.5; 32 of up to 16 tokens, 6 query heads on each of 8, 16383
-// keys at most: 92.1 (8.7 and 12.7; most of the 128 rows are empty); 1 of 24,
-// 131071 keys, 4 heads of 64, fp16: 87.1 (13.5 and 5.6).  The two CTAs of an SM
-// issue in 45 of 100 cycles, 440 instructions a warp and unit, the tensor cores
-// are busy in 23: bound by a step's chain, scores - probabilities - barrier,
-// and by issue.  Values written while the scores are on their way from tensor
-// memory: the same.  The first size on the way here: warp products of 16 rows
-// 324; tensor cores, a barrier between any two steps 259; one barrier a unit, a
-// warp for copies and products 141; probabilities in tensor memory and two places
-// for keys 135; queries four rows at a time 130 (the second size 105, then 92).
+// keys at most: 88 (8.7 and 12.7; most of the 128 rows are empty, and warps
+// without any skip the softmax); 1 of 24, 131071 keys, 4 heads of 64, fp16: 86
+// (13.5 and 5.6).  The two CTAs of an SM issue in 48 of 100 cycles, 460
+// instructions a warp and unit, and the tensor cores are busy in 24: bound by a
+// unit's chain.  Of its 3300 cycles (heads of 128) a warp spends 600 at the
+// barrier, 780 on the next keys, 350 waiting for the last P V, 350 on values,
+// 180 waiting for scores, 430 on fetching and comparing them, 430 on
+// probabilities.  The first size on the way here: warp products of 16 rows 324;
+// tensor cores, a barrier between any two steps 259; one barrier a unit, a warp
+// for copies and products 141; probabilities in tensor memory and two places for
+// keys 135; queries four rows at a time 131; P V before the scores, values
+// between them, keys' stores without bank conflicts 126.  Codes loaded ahead of
+// the wait for P V, scores fetched while values are written: the same.
 //
 // Parts of a (request, head, tile) that several CTAs share go to the
 // workspace, and kda_kv4_tree_join_kernel adds them in order.
@@ -676,7 +680,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 if (tid == 0) nan_any[b & 1] = 0;
             };
 
-            // Unit b's scores and values, and unit b + 1's keys while the tensor cores are on the scores.
+            // Unit b + 1's keys and unit b's values while the tensor cores are on, then unit b's scores.
 #pragma unroll 1
             for (int b = b0 - 1; b < b1; ++b) {
                 fence_proxy_async_smem();
