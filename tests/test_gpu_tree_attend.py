@@ -247,6 +247,19 @@ def test_wide_tree_rows_around_a_tile(lib, workspace, dtype, dim, inter):
         run(lib, workspace, 1, grp, dim, 32, [70], trees((t, "wide")), dtype, dim // 2, inter, seed=t)
 
 
+@pytest.mark.parametrize("dtype,dim", [(BF16, 128), (F32, 128), (F16, 64), (BF16, 64)])
+def test_wide_tree_rows_around_a_warp(lib, workspace, dtype, dim):
+    """Tiles whose rows end within, at and behind a warp's 32: the other warps have none, and what rows that are not there
+    hold is seen nowhere, also where a call before left NaN in every row."""
+    def nan_rows(q):
+        q[:] = float("nan")
+    run(lib, workspace, 8, 128, dim, 16, [80], trees((1, "chain")), dtype, dim, False, seed=3, edit=nan_rows)
+    run(lib, workspace, 2, 1, dim, 32, [70, 200, 5, 64, 0, 129, 33], trees((31, "wide"), (32, "chain"), (33, "wide"), (64, "forest"), (1, "chain"),
+        (63, "star"), (2, "wide")), dtype, dim, False, seed=11)
+    for grp in (65, 96, 97):
+        run(lib, workspace, 1, grp, dim, 16, [190], trees((1, "chain")), dtype, dim, False, seed=grp)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_wide_trees_of_many_ragged_requests(lib, workspace, dtype):
     """40 requests and more, some empty, some padding: shares that begin and end anywhere in the list."""
