@@ -900,8 +900,9 @@ int kda_kv4_attend_tree(const kda_kv4_cache* cache, const kda_kv4_attend_args* a
  * sum_{l <= i} W(l) > u_last sum W, or, if rounding leaves none, the last with
  * W(i) > 0; if W is zero throughout, W is the row of p again.  Accepted tokens
  * and the next one are distributed as the target's own.  Sums and the sides of
- * the tests are pairs of floats, 46 bits or more; the test of a token's first
- * child, u q(x) < p(x), is exact.
+ * the tests are pairs of floats: off by at most (160 + vocab / 256) 2^-48 of the
+ * magnitudes that they add up and take away (2^-37 for 2^18 entries; as a rule
+ * by 2^-46).  The test of a token's first child, u q(x) < p(x), is exact.
  *   accepted  [n]         tokens accepted, token 0 among them; 0 without tokens
  *   node      [n]         1 + the last one's place in its request (kda_step_tree's
  *                         `accepted` in the next step, where its columns are); 0 without tokens

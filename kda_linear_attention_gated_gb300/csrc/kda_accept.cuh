@@ -32,7 +32,10 @@ static_assert(ACC_SEGS == 64, "two pieces a lane");
 // scans in fp64: 70 us for 64 chains of 8 over 131072 tokens, where this takes
 // 25), and 32 bits lose the places next to a border between two tokens.
 struct Pair { float hi, lo; };
-// s += x (Knuth's exact sum of two floats; the errors add up in lo)
+// s += x (Knuth's exact sum of two floats; the errors add up in lo).  lo is a
+// plain float: a run of these has to be brought back into order by pair_norm
+// every few steps, or lo outgrows hi's step and loses its own last places (after
+// 1000 steps 2^-41 of the sum, 2^-30 for weights that all round the same way).
 __device__ __forceinline__ void pair_add(Pair& s, float x, float x_lo) {
     const float t = s.hi + x, b = t - s.hi;
     s.lo += ((s.hi - (t - b)) + (x - b)) + x_lo;
@@ -280,9 +283,13 @@ __global__ void __cluster_dims__(ACC_CTAS, 1, 1) __launch_bounds__(ACC_THREADS, 
                 if (v + 32 * x < v1) raw[x] = row.load(v + 32 * x);
 #pragma unroll
             for (int x = 0; x < U; ++x)
-                if (v + 32 * x < v1) row.weights(raw[x], v + 32 * x, add);
+                if (v + 32 * x < v1) {
+                    row.weights(raw[x], v + 32 * x, add);
+                    s[0] = pair_norm(s[0]);
+                    s[1] = pair_norm(s[1]);
+                }
         }
-        Pair d = pair_norm(s[0]) + pair_norm(s[1]);
+        Pair d = s[0] + s[1];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             // the lower lane's first: both get the same sum
@@ -366,8 +373,10 @@ __global__ void __cluster_dims__(ACC_CTAS, 1, 1) __launch_bounds__(ACC_THREADS, 
             const int g0 = min(row.vecs, seg * each), g1 = min(row.vecs, g0 + each), per = (each + ACC_THREADS - 1) / ACC_THREADS;
             const int a0 = min(g1, g0 + tid * per), a1 = min(g1, a0 + per);
             Pair mine = {0.f, 0.f};
-            for (int v = a0; v < a1; ++v) row.weights(row.load(v), v, [&](const Pair& w, int) { pair_add(mine, w.hi, w.lo); });
-            mine = pair_norm(mine);
+            for (int v = a0; v < a1; ++v) {
+                row.weights(row.load(v), v, [&](const Pair& w, int) { pair_add(mine, w.hi, w.lo); });
+                mine = pair_norm(mine);
+            }
             const Pair run = pair_scan(mine, lane);
             if (lane == 31) info.part[warp] = run;
             __syncthreads();
