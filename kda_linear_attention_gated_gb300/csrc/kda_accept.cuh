@@ -320,10 +320,12 @@ __global__ void __cluster_dims__(ACC_CTAS, 1, 1) __launch_bounds__(ACC_THREADS, 
             for (unsigned long long g = row.gone; g != 0; g &= g - 1)
                 if (info.tok[__ffsll((long long)g) - 1] == info.tok[i]) w = {0.f, 0.f};
         }
-        // u q is exact as a pair, and so the first child's test
+        // The first child's test is exact: u q is 48 bits, a pair down to 2^-100 (below it the lower half would leave fp32's
+        // range, and such a test is made in fp64).
         const float u = info.u[i], uq = u * qx;
-        const Pair bar = row.k == 0 && row.gone == 0 ? Pair{uq, fmaf(u, qx, -uq)} : (z * qx) * u;
-        if (bar < w) {
+        const bool first = row.k == 0 && row.gone == 0;
+        const Pair bar = first ? Pair{uq, fmaf(u, qx, -uq)} : (z * qx) * u;
+        if (first && uq < 0x1p-100f ? (double)u * (double)qx < (double)w.hi : bar < w) {
             cur = i;
             if (writer) path[count] = tb + i;
             ++count;
