@@ -54,7 +54,7 @@ __device__ __forceinline__ Pair operator-(Pair a, const Pair& b) {
     return pair_norm(a);
 }
 __device__ __forceinline__ Pair operator*(const Pair& a, float f) {
-    const float h = a.hi * f;
+    const float h = __fmul_rn(a.hi, f);     // never fused into the sums that it goes into: its error is added apart
     return pair_norm({h, fmaf(a.hi, f, -h) + a.lo * f});
 }
 __device__ __forceinline__ bool operator<(const Pair& a, const Pair& b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
@@ -148,7 +148,7 @@ template <typename T, bool DRAWN> struct AcceptRow {
                     const float d = w.hi - qf;
                     w = w.hi > qf ? Pair{d, (w.hi - d) - qf} : Pair{0.f, 0.f};
                 } else if (k > 1) {
-                    const float h = c.hi * qf;
+                    const float h = __fmul_rn(c.hi, qf);
                     pair_add(w, -h, -(fmaf(c.hi, qf, -h) + c.lo * qf));
                     w = pair_norm(w);
                     if (!(w.hi > 0.f)) w = {0.f, 0.f};
