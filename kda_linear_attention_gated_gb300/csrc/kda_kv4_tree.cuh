@@ -367,9 +367,10 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
         nan_any[0] = nan_any[1] = 0;
     }
     if (tid < 16) nan_tok[tid] = 0;
-    if (warp == 1) tmem_alloc(misc, KVT_TMEM);
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
+    // behind the wait: tensor memory that a CTA held there, a CTA of the launch before could be waiting for
+    if (warp == 1) tmem_alloc(misc, KVT_TMEM);
 
     // ---- this CTA's share ----
     if (warp == 0) {
