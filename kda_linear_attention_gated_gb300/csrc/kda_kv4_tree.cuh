@@ -87,6 +87,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
           "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr) : "memory");
 }
+__device__ __forceinline__ void tmem_st16f(uint32_t addr, const float (&x)[16]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+    tmem_st16(addr, r);
+}
 // Descriptor of a tile of 128-byte rows in shared memory, 16-byte pieces at
 // their place xor (row % 8) (the 128-byte swizzle), groups of eight rows 1024
 // bytes apart.  `lead`: bytes between 64-element stretches of the other
@@ -130,8 +136,18 @@ constexpr int KVT_MIN_ROWS = 48;
 // CTAs that join a tile.  1, 4, 16, us: one request of 24 tokens, 131071 keys
 // (76 CTAs a tile) 381, 146, 88; 32 of up to 16, 16383 keys 128, 99, 94.
 constexpr int KVT_JOIN_GROUPS = 16;
+// Units whose products with the values add up in one sum of the tensor cores,
+// before that is added to the part's others in fp32 (and a thread's sum of
+// probabilities likewise).  The tensor cores round towards zero at each
+// addition, 4 a unit and 8 with remainders, and a sum that grows evenly loses
+// up to 2^-24 of itself at each: 2^-10 after 2000 units in one sum, where here
+// it is 2^-17, 2^-15 and 2^-14 at most for fp32, fp16 and bf16 queries.  One sum
+// / these, us: 16 requests of 16 tokens, 8192 keys, 8 query heads on each of 8
+// heads of 128, fp32 212/215, fp16 209/209, bf16 127/127; heads of 64, fp32
+// 121/121; 64 of 32, 30000 keys, 4 on each of 8 of 128, fp16 2587/2611, bf16
+// 1342/1344.
+__host__ __device__ constexpr int kvt_chain(int dtype) { return dtype == 0 ? 16 : dtype == 1 ? 64 : 256; }
 constexpr int KVT_COUNTERS = 4096;       // bytes at the head of the workspace that kda_kv4_attend_kernel's counters take
-constexpr int KVT_TMEM = 256;            // columns: scores and sums; two CTAs an SM share 512
 
 template <int D, bool SPLIT> struct KvtSmem {
     static constexpr int SLABS = D / 64;                         // 64-channel stretches, 128 bytes a row
@@ -144,12 +160,19 @@ template <int D, bool SPLIT> struct KvtSmem {
                          OFF_NAN = OFF_ROWNAN + KVT_ROWS * 4,    // [2][8] tokens of an even or odd unit whose value group is NaN
                          OFF_BAR = OFF_NAN + 2 * 8 * 8,              // raw [stages], scores, sums
                          OFF_MISC = OFF_BAR + 8 * 8,             // tensor memory base, blocks not there [stages]
-                         OFF_WALK = OFF_MISC + 32, BYTES = OFF_WALK + 2 * 128 + 1024;       // and 1024 to align
+                         OFF_WALK = OFF_MISC + 32,
+                         OFF_KEPT = OFF_WALK + 2 * 128,          // [256] a thread's (maximum, sum) that were kept
+                         BYTES = OFF_KEPT + 32 * KVT_WARPS * 8 + 1024;      // and 1024 to align
     // rows of a tile's queries that are fetched together, as they come, to where keys and values will be
     static __host__ __device__ constexpr int fetched(int es) { return KVT_ROWS * D * es <= OFF_RAW - OFF_K ? KVT_ROWS : KVT_ROWS / 2; }
     static_assert(KVT_ROWS / 2 * D * (SPLIT ? 4 : 2) <= OFF_RAW - OFF_K && KVT_ROWS * D * 4 <= OFF_RAW, "queries in, sums out");
     // CTAs an SM (228 KB of shared memory, 1 KB of it taken for each)
     static constexpr int CTAS = 2 * (BYTES + 1024) <= 228 * 1024 ? 2 : 1;
+    // columns of tensor memory, of which an SM has 512: scores, sums, probabilities (two a column, SPLIT: and their
+    // remainders), and the sums that are kept apart where there is room for them
+    static constexpr int TMEM = 512 / CTAS, USED = KVT_KEYS + D + (SPLIT ? 2 : 1) * KVT_KEYS / 2;
+    static constexpr bool KEEP = USED + D <= TMEM;
+    static_assert(USED <= TMEM, "tensor memory");
 };
 
 // N (2 or 4) neighbouring elements of a typed array in shared memory, from a multiple of N.
@@ -370,7 +393,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
     // behind the wait: tensor memory that a CTA held there, a CTA of the launch before could be waiting for
-    if (warp == 1) tmem_alloc(misc, KVT_TMEM);
+    if (warp == 1) tmem_alloc(misc, SM::TMEM);
 
     // ---- this CTA's share ----
     if (warp == 0) {
@@ -417,7 +440,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
     auto tm_s = [&]() { return *static_cast<volatile uint32_t*>(misc); };
     auto tm_o = [&]() { return tm_s() + KVT_KEYS; };
     auto tm_p = [&]() { return tm_o() + D; };       // probabilities, two a column, and with SPLIT their remainders
-    static_assert(KVT_KEYS + D + (SPLIT ? 2 : 1) * KVT_KEYS / 2 <= KVT_TMEM, "tensor memory");
+    auto tm_k = [&]() { return tm_s() + SM::USED; };        // KEEP: sums that are kept apart
     if (*any_empty) {   // requests without a visible key: zero rows
         for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
             const Kv4Req q = kvt_request(p, r);
@@ -495,6 +518,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                         tc_mma_ta(o_at, p_at + part * (KVT_KEYS / 2) + k * 8, tc_step(dV, k * 2048), id_o, more || part + k > 0);
                 tc_commit(bar_o);
             };
+            const int chain = SPLIT ? kvt_chain(p.dtype) : kvt_chain(2);
             int ready = 0;              // the stage of unit b + 1
             for (int b = b0 - 1; b <= b1; ++b) {
                 bool ok = true;         // codes b + 1 are there
@@ -508,7 +532,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 const bool rare = nan_any[(b - 1) & 1] != 0;
                 if (tc_elect()) {
                     tc_fence_after();
-                    if (b > b0) add_values(b > b0 + 1);
+                    if (b > b0) add_values(((b - 1 - b0) & (chain - 1)) != 0);
                     if (b >= b0 && b < b1) {
                         const uint64_t dKb = tc_step(dK, (b & 1) * SM::K);
 #pragma unroll
@@ -662,6 +686,38 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 return at < 0 ? key >= low : at < TREE_MAX && (own >> at & 1u) != 0;
             };
             float m = -FLT_MAX, l = 0.f;
+            // sums that are kept: this thread's columns in tensor memory, or else in the part's place in the workspace; its
+            // row's maximum then and the sum of probabilities until then
+            const int chain = SPLIT ? kvt_chain(p.dtype) : kvt_chain(2);
+            float2* kept_ml = reinterpret_cast<float2*>(smem + SM::OFF_KEPT) + tid;
+            auto kept_at = [&](int k) { return tm_k() + lane_base + half * (D / 2) + 16 * k; };
+            auto kept_mem = [&](int k) { return reinterpret_cast<float4*>(part_at(w)) + tid + 4 * k * (32 * KVT_WARPS); };
+            auto add_kept = [&](int k, float g, float (&o)[16]) {       // o += g times 16 columns that were kept
+                if constexpr (SM::KEEP) {
+                    float old[16];
+                    tmem_ld16(kept_at(k), old);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = fmaf(old[i], g, o[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 old = __ldcg(kept_mem(k) + i * (32 * KVT_WARPS));
+                        o[4 * i] = fmaf(old.x, g, o[4 * i]);
+                        o[4 * i + 1] = fmaf(old.y, g, o[4 * i + 1]);
+                        o[4 * i + 2] = fmaf(old.z, g, o[4 * i + 2]);
+                        o[4 * i + 3] = fmaf(old.w, g, o[4 * i + 3]);
+                    }
+                }
+            };
+            auto keep = [&](int k, const float (&o)[16]) {
+                if constexpr (SM::KEEP) {
+                    tmem_st16f(kept_at(k), o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        __stcg(kept_mem(k) + i * (32 * KVT_WARPS), make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+                }
+            };
             if (half == 0) row_nan[row] = 0;
             const float c = rowf[row];
             const bool idle = 32 * (warp & 3) >= live;
@@ -681,184 +737,208 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 if (tid == 0) nan_any[b & 1] = 0;
             };
 
-            // Unit b + 1's keys and unit b's values while the tensor cores are on, then unit b's scores.
+            // Unit b + 1's keys and unit b's values while the tensor cores are on, then unit b's scores; every `chain` units the
+            // sums so far are kept apart.  (Two loops, so that the inner one's registers know nothing of it: in one, 3 % slower.)
+            int b = b0 - 1, next = b0 + chain + 1;
 #pragma unroll 1
-            for (int b = b0 - 1; b < b1; ++b) {
-                fence_proxy_async_smem();
-                tc_fence_before();
-                alive = __syncthreads_and(ok);      // keys b, probabilities and values b - 1 are written, codes b - 1 read, codes b + 1 there
-                if (!alive) break;
-                if (b > b0) find_nan(b - 1);
-                // ---- keys: a token's quarter a thread ----
-                if (b + 1 < b1) {
-                    {
-                        const int key = tid >> 2, q = tid & 3;
-                        const uint8_t* B = raw + st * SM::STAGE + (key >> 4) * F::BLOCK;
-                        const bool gone = missing[st] >> (key >> 4) & 1u;
-                        if constexpr (D == 128) {
-                            const uint4 c = *reinterpret_cast<const uint4*>(B + F::KC + (key & 15) * 64 + q * 16);
-                            uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::KS + (key & 15) * 8 + 2 * q);
-                            if (gone) s2 = 0;
-                            // every other quarter takes its words from the middle on, so that eight lanes' stores fall on
-                            // different banks
-                            const bool swap = (q & 2) != 0;
-                            const uint32_t two = cvt_e4m3x2_f16x2(s2), sc = swap ? __byte_perm(two, two, 0x1032) : two;
-                            const uint32_t code[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
-                            uint8_t* to = K + ((b + 1) & 1) * SM::K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
+            for (;;) {
+#pragma unroll 1
+                for (const int stop = min(b1, next); b < stop; ++b) {
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    // keys b, probabilities and values b - 1 are written, codes b - 1 read, codes b + 1 there
+                    alive = __syncthreads_and(ok);
+                    if (!alive) break;
+                    if (b > b0) find_nan(b - 1);
+                    // ---- keys: a token's quarter a thread ----
+                    if (b + 1 < b1) {
+                        {
+                            const int key = tid >> 2, q = tid & 3;
+                            const uint8_t* B = raw + st * SM::STAGE + (key >> 4) * F::BLOCK;
+                            const bool gone = missing[st] >> (key >> 4) & 1u;
+                            if constexpr (D == 128) {
+                                const uint4 c = *reinterpret_cast<const uint4*>(B + F::KC + (key & 15) * 64 + q * 16);
+                                uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::KS + (key & 15) * 8 + 2 * q);
+                                if (gone) s2 = 0;
+                                // every other quarter takes its words from the middle on, so that eight lanes' stores fall on
+                                // different banks
+                                const bool swap = (q & 2) != 0;
+                                const uint32_t two = cvt_e4m3x2_f16x2(s2), sc = swap ? __byte_perm(two, two, 0x1032) : two;
+                                const uint32_t code[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+                                uint8_t* to = K + ((b + 1) & 1) * SM::K + (q >> 1) * (KVT_KEYS * 128) + key * 128;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t v[4];
-                                cvt_e2m1x8_f16(code[i], v);
+                                for (int i = 0; i < 4; ++i) {
+                                    uint32_t v[4];
+                                    cvt_e2m1x8_f16(code[i], v);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
-                                *reinterpret_cast<uint4*>(to + ((((q & 1) * 4 + i) ^ (q & 2) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                            }
-                        } else {
-                            const uint2 c = *reinterpret_cast<const uint2*>(B + F::KC + (key & 15) * 32 + q * 8);
-                            uint32_t s2 = B[F::KS + (key & 15) * 4 + q];
-                            if (gone) s2 = 0;
-                            const uint32_t sc = cvt_e4m3x2_f16x2(s2);
-                            const uint32_t code[2] = {c.x, c.y};
+                                    for (int e = 0; e < 4; ++e) v[e] = i < 2 ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
+                                    *reinterpret_cast<uint4*>(to + ((((q & 1) * 4 + i) ^ (q & 2) ^ (key & 7)) << 4)) =
+                                        make_uint4(v[0], v[1], v[2], v[3]);
+                                }
+                            } else {
+                                const uint2 c = *reinterpret_cast<const uint2*>(B + F::KC + (key & 15) * 32 + q * 8);
+                                uint32_t s2 = B[F::KS + (key & 15) * 4 + q];
+                                if (gone) s2 = 0;
+                                const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                                const uint32_t code[2] = {c.x, c.y};
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                uint32_t v[4];
-                                cvt_e2m1x8_f16(code[i], v);
+                                for (int i = 0; i < 2; ++i) {
+                                    uint32_t v[4];
+                                    cvt_e2m1x8_f16(code[i], v);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) v[e] = hmul2_half<false>(v[e], sc);
-                                *reinterpret_cast<uint4*>(K + ((b + 1) & 1) * SM::K + key * 128 + (((q * 2 + i) ^ (key & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                                    for (int e = 0; e < 4; ++e) v[e] = hmul2_half<false>(v[e], sc);
+                                    *reinterpret_cast<uint4*>(K + ((b + 1) & 1) * SM::K + key * 128 + (((q * 2 + i) ^ (key & 7)) << 4)) =
+                                        make_uint4(v[0], v[1], v[2], v[3]);
+                                }
                             }
                         }
                     }
-                }
-                st = st + 1 == KVT_STAGES ? 0 : st + 1;
-                if (b < b0) continue;
-                const int sv = st >= 2 ? st - 2 : st + 1;               // the stage of unit b
-                const int key0 = (req.first + b) * KVT_KEYS;
-                const uint32_t miss = missing[sv];
-                // keys that every row sees: [ctx + t - window, ctx)
-                const bool masked = key0 + KVT_KEYS > req.ctx || (p.window > 0 && key0 < req.ctx + req.t - p.window) || miss != 0;
-                // ---- values, when the last unit's products are done with: 16 channels (64: 8) of two tokens a thread ----
-                if (b > b0) {
-                    ok = mbar_poll(bar_o, phase(KVT_STAGES + 1));
-                    if (ok) phases ^= 1u << (KVT_STAGES + 1);
-                }
-                if (ok) {
-                    const int bk = tid >> 6, hf = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
-                    const uint8_t* B = raw + sv * SM::STAGE + bk * F::BLOCK;
-                    const int key = bk * 16 + hf * 8 + 2 * tp, grp = D == 128 ? g : g >> 1;     // its first token, its scale group
-                    uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::VS + (grp * 4 + tp) * 4 + hf * 2);
-                    if (masked) {
-                        // tokens behind the end hold anything, and 0 * NaN is NaN: their scales become 0, and so do NaN
-                        // ones, whose groups of the rows that see them are then set by hand (a rare path)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const bool out = (miss >> bk & 1u) || key0 + key + e >= req.ctx + req.t, nan = (s2 >> (8 * e) & 0x7fu) == 0x7fu;
-                            if (nan && !out) {
-                                nan_any[b & 1] = 1;
-                                atomicOr(nan_tok + (b & 1) * 8 + grp, 1ull << (key + e));
-                            }
-                            if (nan || out) s2 &= ~(0xffu << (8 * e));
-                        }
+                    st = st + 1 == KVT_STAGES ? 0 : st + 1;
+                    if (b < b0) continue;
+                    const int sv = st >= 2 ? st - 2 : st + 1;               // the stage of unit b
+                    const int key0 = (req.first + b) * KVT_KEYS;
+                    const uint32_t miss = missing[sv];
+                    // keys that every row sees: [ctx + t - window, ctx)
+                    const bool masked = key0 + KVT_KEYS > req.ctx || (p.window > 0 && key0 < req.ctx + req.t - p.window) || miss != 0;
+                    // ---- values, when the last unit's products are done with: 16 channels (64: 8) of two tokens a thread ----
+                    if (b > b0) {
+                        ok = mbar_poll(bar_o, phase(KVT_STAGES + 1));
+                        if (ok) phases ^= 1u << (KVT_STAGES + 1);
                     }
-                    const uint32_t sc = cvt_e4m3x2_f16x2(s2);
-                    constexpr int W = D / 64;           // words of a token's
-                    uint32_t code[2 * W];
-                    if constexpr (D == 128) {
-                        const uint4 cw = *reinterpret_cast<const uint4*>(B + F::VC + hf * 512 + lane * 16);
-                        code[0] = cw.x; code[1] = cw.y; code[2] = cw.z; code[3] = cw.w;
-                    } else {
-                        const uint2 cw = *reinterpret_cast<const uint2*>(B + F::VC + hf * 256 + lane * 8);
-                        code[0] = cw.x; code[1] = cw.y;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2 * W; ++i) {
-                        // channels 8 ch ..; at D = 128 every other lane's two pieces change places, so that eight lanes' stores
-                        // fall on different banks
-                        const int kk = key + i / W, piece = D == 128 ? (i ^ g) & 1 : 0, ch = D == 128 ? (g & 3) * 2 + piece : g;
-                        const uint32_t word = D == 128 ? (piece ? code[(i & 2) + 1] : code[i & 2]) : code[i];
-                        uint32_t v[4];
-                        cvt_e2m1x8_f16(word, v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = i < W ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
-                        *reinterpret_cast<uint4*>(V + (D == 128 ? g >> 2 : 0) * (KVT_KEYS * 128) + kk * 128 + ((ch ^ (kk & 7)) << 4)) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                }
-                // ---- scores to probabilities ----
-                if (ok) {
-                    ok = mbar_poll(bar_s, phase(KVT_STAGES));
-                    if (ok) phases ^= 1u << KVT_STAGES;
-                }
-                // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
-                ok = __all_sync(0xffffffffu, ok);
-                tc_fence_after();
-                if (!idle) {
-                    float s[32], top = -INFINITY;
                     if (ok) {
-                        tmem_ld32(tm_s() + lane_base + 32 * half, s);
+                        const int bk = tid >> 6, hf = tid >> 5 & 1, g = lane >> 2, tp = lane & 3;
+                        const uint8_t* B = raw + sv * SM::STAGE + bk * F::BLOCK;
+                        const int key = bk * 16 + hf * 8 + 2 * tp, grp = D == 128 ? g : g >> 1;     // its first token, its scale group
+                        uint32_t s2 = *reinterpret_cast<const uint16_t*>(B + F::VS + (grp * 4 + tp) * 4 + hf * 2);
                         if (masked) {
+                            // tokens behind the end hold anything, and 0 * NaN is NaN: their scales become 0, and so do NaN
+                            // ones, whose groups of the rows that see them are then set by hand (a rare path)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int at = 32 * half + i;
-                                if (!sees(key0 + at) || (miss >> (at >> 4) & 1u)) s[i] = -INFINITY;
+                            for (int e = 0; e < 2; ++e) {
+                                const bool out = (miss >> bk & 1u) || key0 + key + e >= req.ctx + req.t, nan = (s2 >> (8 * e) & 0x7fu) == 0x7fu;
+                                if (nan && !out) {
+                                    nan_any[b & 1] = 1;
+                                    atomicOr(nan_tok + (b & 1) * 8 + grp, 1ull << (key + e));
+                                }
+                                if (nan || out) s2 &= ~(0xffu << (8 * e));
                             }
                         }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(s[i], s[i + 1]), top);
-                    }
-                    top *= c;
-                    // seldom: a score above its row's running maximum by more than the slack, in either half
-                    if (pair_any(1 + (warp & 3), top > m + KV4_SLACK)) {
-                        half_max[half * KVT_ROWS + row] = top;
-                        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-                        top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]);
-                        const bool grow = top > m + KV4_SLACK;
-                        const float f = grow ? ex2f(m - top) : 1.f;
-                        if (grow) m = top;
-                        l *= f;
-                        if (ok && b > b0) {
-#pragma unroll 1
-                            for (int k = 0; k < D / 32; ++k) {
-                                const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
-                                float o[16];
-                                uint32_t r[16];
-                                tmem_ld16(at, o);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * f);
-                                tmem_st16(at, r);
-                            }
+                        const uint32_t sc = cvt_e4m3x2_f16x2(s2);
+                        constexpr int W = D / 64;           // words of a token's
+                        uint32_t code[2 * W];
+                        if constexpr (D == 128) {
+                            const uint4 cw = *reinterpret_cast<const uint4*>(B + F::VC + hf * 512 + lane * 16);
+                            code[0] = cw.x; code[1] = cw.y; code[2] = cw.z; code[3] = cw.w;
+                        } else {
+                            const uint2 cw = *reinterpret_cast<const uint2*>(B + F::VC + hf * 256 + lane * 8);
+                            code[0] = cw.x; code[1] = cw.y;
                         }
-                        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");      // half_max is read
+#pragma unroll
+                        for (int i = 0; i < 2 * W; ++i) {
+                            // channels 8 ch ..; at D = 128 every other lane's two pieces change places, so that eight lanes' stores
+                            // fall on different banks
+                            const int kk = key + i / W, piece = D == 128 ? (i ^ g) & 1 : 0, ch = D == 128 ? (g & 3) * 2 + piece : g;
+                            const uint32_t word = D == 128 ? (piece ? code[(i & 2) + 1] : code[i & 2]) : code[i];
+                            uint32_t v[4];
+                            cvt_e2m1x8_f16(word, v);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = i < W ? hmul2_half<false>(v[e], sc) : hmul2_half<true>(v[e], sc);
+                            *reinterpret_cast<uint4*>(V + (D == 128 ? g >> 2 : 0) * (KVT_KEYS * 128) + kk * 128 + ((ch ^ (kk & 7)) << 4)) =
+                                make_uint4(v[0], v[1], v[2], v[3]);
+                        }
                     }
+                    // ---- scores to probabilities ----
                     if (ok) {
-                        const float neg = KV4_LIFT - m;
-                        float2 sum = make_float2(l, 0.f);
-                        uint32_t hi[16];
+                        ok = mbar_poll(bar_s, phase(KVT_STAGES));
+                        if (ok) phases ^= 1u << KVT_STAGES;
+                    }
+                    // the warp's verdict, not a lane's; the two warps of a row meet whatever it is
+                    ok = __all_sync(0xffffffffu, ok);
+                    tc_fence_after();
+                    if (!idle) {
+                        float s[32], top = -INFINITY;
+                        if (ok) {
+                            tmem_ld32(tm_s() + lane_base + 32 * half, s);
+                            if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(c, c), make_float2(neg, neg));
-                            const float x0 = ex2f(x.x), x1 = ex2f(x.y);
-                            sum = __fadd2_rn(sum, make_float2(x0, x1));
-                            const __half2 hh = __floats2half2_rn(x0, x1);
-                            hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
-                            if constexpr (SPLIT) {
-                                const float2 f = __half22float2(hh);
-                                s[2 * i] = x0 - f.x;
-                                s[2 * i + 1] = x1 - f.y;
+                                for (int i = 0; i < 32; ++i) {
+                                    const int at = 32 * half + i;
+                                    if (!sees(key0 + at) || (miss >> (at >> 4) & 1u)) s[i] = -INFINITY;
+                                }
                             }
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(s[i], s[i + 1]), top);
                         }
-                        tmem_st16(tm_p() + lane_base + 16 * half, hi);
-                        if constexpr (SPLIT) {
+                        top *= c;
+                        // seldom: a score above its row's running maximum by more than the slack, in either half
+                        if (pair_any(1 + (warp & 3), top > m + KV4_SLACK)) {
+                            half_max[half * KVT_ROWS + row] = top;
+                            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+                            top = fmaxf(top, half_max[(half ^ 1) * KVT_ROWS + row]);
+                            const bool grow = top > m + KV4_SLACK;
+                            const float f = grow ? ex2f(m - top) : 1.f;
+                            if (grow) m = top;
+                            l *= f;
+                            if (ok && b > b0) {
+#pragma unroll 1
+                                for (int k = 0; k < D / 32; ++k) {
+                                    const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
+                                    float o[16];
+                                    tmem_ld16(at, o);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] *= f;
+                                    tmem_st16f(at, o);
+                                }
+                            }
+                            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");      // half_max is read
+                        }
+                        if (ok) {
+                            const float neg = KV4_LIFT - m;
+                            float2 sum = make_float2(l, 0.f);
+                            uint32_t hi[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const __half2 rest = __floats2half2_rn(s[2 * i], s[2 * i + 1]);
-                                hi[i] = *reinterpret_cast<const uint32_t*>(&rest);
+                                const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), make_float2(c, c), make_float2(neg, neg));
+                                const float x0 = ex2f(x.x), x1 = ex2f(x.y);
+                                sum = __fadd2_rn(sum, make_float2(x0, x1));
+                                const __half2 hh = __floats2half2_rn(x0, x1);
+                                hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
+                                if constexpr (SPLIT) {
+                                    const float2 f = __half22float2(hh);
+                                    s[2 * i] = x0 - f.x;
+                                    s[2 * i + 1] = x1 - f.y;
+                                }
                             }
-                            tmem_st16(tm_p() + lane_base + KVT_KEYS / 2 + 16 * half, hi);
+                            tmem_st16(tm_p() + lane_base + 16 * half, hi);
+                            if constexpr (SPLIT) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const __half2 rest = __floats2half2_rn(s[2 * i], s[2 * i + 1]);
+                                    hi[i] = *reinterpret_cast<const uint32_t*>(&rest);
+                                }
+                                tmem_st16(tm_p() + lane_base + KVT_KEYS / 2 + 16 * half, hi);
+                            }
+                            l = sum.x + sum.y;
                         }
-                        l = sum.x + sum.y;
                     }
                 }
+                if (!alive || b != next) break;
+                // The products of the last unit, not begun yet, start new sums; those so far are kept.
+                if (ok && !idle) {
+                    const bool more = next > b0 + chain + 1;
+                    const float2 ml = more ? *kept_ml : make_float2(-FLT_MAX, 0.f);
+                    const float g = ex2f(ml.x - m);
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        float o[16];
+                        tmem_ld16(tm_o() + lane_base + half * (D / 2) + 16 * k, o);
+                        if (more) add_kept(k, g, o);
+                        keep(k, o);
+                    }
+                    *kept_ml = make_float2(m, fmaf(ml.y, g, l));
+                    l = 0.f;
+                }
+                next += chain;
             }
             if (alive) {                // the last unit's
                 fence_proxy_async_smem();
@@ -871,6 +951,9 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
                 ok = mbar_wait(bar_o, phase(KVT_STAGES + 1));
                 if (ok) phases ^= 1u << (KVT_STAGES + 1);
             }
+            const float2 ml_kept = b1 - b0 > chain ? *kept_ml : make_float2(-FLT_MAX, 0.f);
+            const float g = ex2f(ml_kept.x - m);
+            l = fmaf(ml_kept.y, g, l);
             half_max[half * KVT_ROWS + row] = l;
             alive = __syncthreads_and(alive && ok);
             tc_fence_after();
@@ -879,6 +962,16 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
             } else {                    // a wait ran out: nothing of this part
                 m = -FLT_MAX;
                 l = 0.f;
+            }
+            if (b1 - b0 > chain && !idle) {
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    const uint32_t at = tm_o() + lane_base + half * (D / 2) + 16 * k;
+                    float o[16];
+                    tmem_ld16(at, o);
+                    add_kept(k, g, o);
+                    tmem_st16f(at, o);
+                }
             }
             // through shared memory (queries to probabilities are done with), 16-byte pieces at their place xor (row % 8)
             const bool whole = is_whole(w);
@@ -944,7 +1037,7 @@ __global__ void __launch_bounds__(KVT_THREADS, KvtSmem<D, SPLIT>::CTAS) kda_kv4_
         }
     }
     __syncthreads();
-    if (warp == 1) tmem_free(tm_s(), KVT_TMEM);
+    if (warp == 1) tmem_free(tm_s(), SM::TMEM);
 }
 
 // Joins the parts of the tiles that more than one CTA of kda_kv4_tree_kernel
