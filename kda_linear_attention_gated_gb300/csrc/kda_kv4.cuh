@@ -470,6 +470,11 @@ constexpr int KV4_KEYS = 32;             // keys of a unit of work: two blocks
 // One value for all builds: the fp16 and fp32 ones, whose units take longer, would gain 5 % and 3 % with 12 and 16.
 constexpr int KV4_PART = 24;
 constexpr int KV4_MAX_CTAS = 512;        // counters at the head of the workspace
+// Units of a warp whose products with the values (fp16 and fp32 queries) add up
+// in one sum of the tensor cores, before that is added to the warp's others in
+// fp32.  The tensor cores round towards zero at each of a unit's four additions:
+// 2^-17 of a sum here, 2^-13 after 680 units in one.
+constexpr int KV4_CHAIN = 32;
 constexpr int KV4_AHEAD = 16;            // units whose pages a warp looks up at a time: lanes 2 i, 2 i + 1 a block each
 // The running maximum may lag by SLACK powers of two, and probabilities are held times 2^LIFT: at most
 // 2^15 in fp16, whose last step then stands for 2^-35 of the maximum's (unlifted, what many keys add behind
@@ -932,216 +937,255 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.f;
 
+        // Sums that are kept lie where the warp's are joined from, with their rows' (maximum, sum of probabilities).
+        auto kept_at = [&](int e, int k) {      // 16-byte piece k of this lane's channels of its row e
+            return reinterpret_cast<float4*>(merge + (warp * 8 + 2 * t + e) * D + ((g * (D / 32) + k) ^ t) * 4);
+        };
+        bool kept = false;
+        int unit = cur.q.first + cur.b0 + warp;
+        const int end = cur.q.first + cur.b1;
 #pragma unroll 1
-        for (int unit = cur.q.first + cur.b0 + warp, end = cur.q.first + cur.b1; unit < end; unit += KV4_WARPS) {
-            bool use = (flags & ALIVE) && (flags >> (8 + 2 * slot) & 3u) != 3u;
-            if (use) {
-                // the warp's verdict, not a lane's: a copy may land while some lanes give up
-                use = __all_sync(0xffffffffu, mbar_wait(bars + slot, flags >> slot & 1u));
+        for (;;) {
+#pragma unroll 1
+            for (const int stop = SPLIT ? min(end, unit + KV4_CHAIN * KV4_WARPS) : end; unit < stop; unit += KV4_WARPS) {
+                bool use = (flags & ALIVE) && (flags >> (8 + 2 * slot) & 3u) != 3u;
                 if (use) {
-                    flags ^= 1u << slot;
-                } else {
-                    flags &= ~(MORE | ALIVE);
-                    if (lane == 0) atomicCAS(p.status, 0, STATUS_TIMEOUT);
-                }
-            }
-            if (use) {
-                const uint8_t* B = ring + slot * (2 * F::BLOCK);
-                // ---- scores: s[blk][n][..] of keys 16 blk + g (0, 1) and g + 8 (2, 3) with the lane's rows ----
-                float s[2][NB][4];
-#pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
-                    const uint8_t* K = B + blk * F::BLOCK;
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) s[blk][n][0] = s[blk][n][1] = s[blk][n][2] = s[blk][n][3] = 0.f;
-                    uint32_t code[2][D / 32], sc[2];   // sc: scales of the lane's two groups (D = 64: of its one)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int key = hf * 8 + g;
-                        if constexpr (D == 128) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(K + F::KC + key * 64 + t * 16);
-                            code[hf][0] = w.x; code[hf][1] = w.y; code[hf][2] = w.z; code[hf][3] = w.w;
-                            sc[hf] = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(K + F::KS + key * 8 + 2 * t));
-                        } else {
-                            const uint2 w = *reinterpret_cast<const uint2*>(K + F::KC + key * 32 + t * 8);
-                            code[hf][0] = w.x; code[hf][1] = w.y;
-                            sc[hf] = cvt_e4m3x2_f16x2(K[F::KS + key * 4 + t]);
-                        }
-                    }
-#pragma unroll
-                    for (int w = 0; w < D / 32; ++w) {
-                        uint32_t k0[4], k1[4];
-                        cvt_e2m1x8_f16(code[0][w], k0);
-                        cvt_e2m1x8_f16(code[1][w], k1);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            k0[e] = w < 2 ? hmul2_half<false>(k0[e], sc[0]) : hmul2_half<true>(k0[e], sc[0]);
-                            k1[e] = w < 2 ? hmul2_half<false>(k1[e], sc[1]) : hmul2_half<true>(k1[e], sc[1]);
-                        }
-                        kv4_mma(s[blk][0], k0[0], k1[0], k0[1], k1[1], qa[w].x, qa[w].y);
-                        if constexpr (MODE != KV4_8) kv4_mma(s[blk][NB - 1], k0[0], k1[0], k0[1], k1[1], qb[w].x, qb[w].y);
-                        kv4_mma(s[blk][0], k0[2], k1[2], k0[3], k1[3], qa[w].z, qa[w].w);
-                        if constexpr (MODE != KV4_8) kv4_mma(s[blk][NB - 1], k0[2], k1[2], k0[3], k1[3], qb[w].z, qb[w].w);
+                    // the warp's verdict, not a lane's: a copy may land while some lanes give up
+                    use = __all_sync(0xffffffffu, mbar_wait(bars + slot, flags >> slot & 1u));
+                    if (use) {
+                        flags ^= 1u << slot;
+                    } else {
+                        flags &= ~(MORE | ALIVE);
+                        if (lane == 0) atomicCAS(p.status, 0, STATUS_TIMEOUT);
                     }
                 }
-                // ---- running softmax ----
-                const uint32_t miss = flags >> (8 + 2 * slot) & 3u;
-                const bool masked = unit < see0 || unit >= see1 || miss != 0;
-                if (masked) {
+                if (use) {
+                    const uint8_t* B = ring + slot * (2 * F::BLOCK);
+                    // ---- scores: s[blk][n][..] of keys 16 blk + g (0, 1) and g + 8 (2, 3) with the lane's rows ----
+                    float s[2][NB][4];
 #pragma unroll
-                    for (int a = 0; a < 2 * NB; ++a) {
-                        if constexpr (TREE) {
-                            uint64_t own;
-                            int low;
-                            tree_row(row_of(a), own, low);
+                    for (int blk = 0; blk < 2; ++blk) {
+                        const uint8_t* K = B + blk * F::BLOCK;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (!sees_tree(own, low, unit * KV4_KEYS + i * 8 + g) || (miss >> (i >> 1) & 1u))
-                                    s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
-                            continue;
-                        }
-                        const int pos = row_pos(row_of(a));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int key = unit * KV4_KEYS + i * 8 + g;
-                            if (key > pos || (p.window > 0 && key <= pos - p.window) || (miss >> (i >> 1) & 1u))
-                                s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
-                        }
-                    }
-                }
-                float top[2 * NB];
-                bool grow = false;
-#pragma unroll
-                for (int a = 0; a < 2 * NB; ++a) {
-                    const int n = a >> 1, e = a & 1;
-                    top[a] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
-                    if constexpr (NB == 1) grow |= top[a] > bar[a];
-                    else grow |= top[a] * rowf[row_of(a)] > m[a] + KV4_SLACK;
-                }
-                // rarely: a score above the running maximum by more than its slack
-                if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                    for (int a = 0; a < 2 * NB; ++a) {
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], o));
-                        const float c = rowf[row_of(a)];
-                        top[a] *= c;
-                        if (top[a] > m[a]) {
-                            if constexpr (NB == 1) bar[a] = (top[a] + KV4_SLACK) / c;
-                            const float f = ex2f(m[a] - top[a]);
-                            m[a] = top[a];
-                            l[a] *= f;
-#pragma unroll
-                            for (int j = 0; j < MT; ++j) {
-                                acc[a >> 1][j][a & 1] *= f;
-                                acc[a >> 1][j][2 + (a & 1)] *= f;
-                            }
-                        }
-                    }
-                }
-                uint32_t pf[2][NB][2], pr[SPLIT ? 2 : 1][2];   // B fragments of the probabilities, of their remainders
-#pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    // both rows at once (packed fp32)
-                    const float2 c = *reinterpret_cast<const float2*>(rowf + row_of(2 * n));
-                    const float2 neg = make_float2(KV4_LIFT - m[2 * n], KV4_LIFT - m[2 * n + 1]);
-                    float2 sum = make_float2(l[2 * n], l[2 * n + 1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 e = __ffma2_rn(make_float2(s[i >> 1][n][2 * (i & 1)], s[i >> 1][n][2 * (i & 1) + 1]), c, neg);
-                        const float x0 = ex2f(e.x), x1 = ex2f(e.y);
-                        sum = __fadd2_rn(sum, make_float2(x0, x1));
-                        const __half2 hi = __floats2half2_rn(x0, x1);
-                        pf[i >> 1][n][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&hi));
-                        if constexpr (SPLIT) {
-                            const float2 f = __half22float2(hi);
-                            const __half2 rest = __floats2half2_rn(x0 - f.x, x1 - f.y);
-                            pr[i >> 1][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&rest));
-                        }
-                    }
-                    l[2 * n] = sum.x;
-                    l[2 * n + 1] = sum.y;
-                }
-                // ---- values ----
-#pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
-                    const uint8_t* W = B + blk * F::BLOCK;
-                    const int grp = g * (D / 8) / 16;       // the lane's channels are of one scale group
-                    uint32_t vs4 = *reinterpret_cast<const uint32_t*>(W + F::VS + (grp * 4 + t) * 4);
-                    if (masked) {
-                        // A token that some row does not see may hold anything, and 0 * NaN is NaN:
-                        // scales behind the end become 0, and so do NaN ones, whose channels of the
-                        // rows that do see them are then set by hand (a rare path).
-                        const int key0 = unit * KV4_KEYS + blk * 16, to = (miss >> blk & 1u) ? -1 : last_row_pos();
-                        bool nan = false;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + (e >> 1) * 8 + 2 * t + (e & 1);
-                            const bool bad = (vs4 >> (8 * e) & 0x7fu) == 0x7fu;
-                            if (key > to || bad) vs4 &= ~(0xffu << (8 * e));
-                            nan |= bad && key <= to;
-                        }
-                        if (__any_sync(0xffffffffu, nan)) {
-                            uint32_t hit = 0;
-#pragma unroll 1
-                            for (int w = 0; w < 16; ++w) {
-                                if ((W[kv4_v_scale<D>(w, grp)] & 0x7f) != 0x7f || key0 + w > to) continue;
-#pragma unroll
-                                for (int a = 0; a < 2 * NB; ++a) {
-                                    if constexpr (TREE) {
-                                        uint64_t own;
-                                        int low;
-                                        tree_row(row_of(a), own, low);
-                                        if (sees_tree(own, low, key0 + w)) hit |= 1u << a;
-                                        continue;
-                                    }
-                                    const int pos = row_pos(row_of(a));
-                                    if (key0 + w <= pos && (p.window <= 0 || key0 + w > pos - p.window)) hit |= 1u << a;
-                                }
-                            }
-#pragma unroll
-                            for (int a = 0; a < 2 * NB; ++a)
-                                if (hit >> a & 1u)
-#pragma unroll
-                                    for (int j = 0; j < MT; ++j) acc[a >> 1][j][a & 1] = acc[a >> 1][j][2 + (a & 1)] = NAN;
-                        }
-                    }
-                    const uint32_t sv[2] = {cvt_e4m3x2_f16x2(vs4 & 0xffffu), cvt_e4m3x2_f16x2(vs4 >> 16)};
-                    uint32_t vc[2][2][D / 64];          // [half][token of the pair][word]
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const uint8_t* V = W + F::VC + hf * (64 * F::CB) + lane * (2 * F::CB);
-                        if constexpr (D == 128) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(V);
-                            vc[hf][0][0] = w.x; vc[hf][0][1] = w.y; vc[hf][1][0] = w.z; vc[hf][1][1] = w.w;
-                        } else {
-                            const uint2 w = *reinterpret_cast<const uint2*>(V);
-                            vc[hf][0][0] = w.x; vc[hf][1][0] = w.y;
-                        }
-                    }
-#pragma unroll
-                    for (int w = 0; w < D / 64; ++w) {
-                        uint32_t ev[2][4], od[2][4];   // pairs (token 2t, token 2t + 1) of the even and of the odd channels
+                        for (int n = 0; n < NB; ++n) s[blk][n][0] = s[blk][n][1] = s[blk][n][2] = s[blk][n][3] = 0.f;
+                        uint32_t code[2][D / 32], sc[2];   // sc: scales of the lane's two groups (D = 64: of its one)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            const uint32_t A = vc[hf][0][w], C = vc[hf][1][w];
-                            cvt_e2m1x8_f16((A & 0x0f0f0f0fu) | (C << 4 & 0xf0f0f0f0u), ev[hf]);
-                            cvt_e2m1x8_f16((A >> 4 & 0x0f0f0f0fu) | (C & 0xf0f0f0f0u), od[hf]);
+                            const int key = hf * 8 + g;
+                            if constexpr (D == 128) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(K + F::KC + key * 64 + t * 16);
+                                code[hf][0] = w.x; code[hf][1] = w.y; code[hf][2] = w.z; code[hf][3] = w.w;
+                                sc[hf] = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(K + F::KS + key * 8 + 2 * t));
+                            } else {
+                                const uint2 w = *reinterpret_cast<const uint2*>(K + F::KC + key * 32 + t * 8);
+                                code[hf][0] = w.x; code[hf][1] = w.y;
+                                sc[hf] = cvt_e4m3x2_f16x2(K[F::KS + key * 4 + t]);
+                            }
                         }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t a0 = hmul2_u32(ev[0][e], sv[0]), a1 = hmul2_u32(od[0][e], sv[0]);
-                            const uint32_t a2 = hmul2_u32(ev[1][e], sv[1]), a3 = hmul2_u32(od[1][e], sv[1]);
+                        for (int w = 0; w < D / 32; ++w) {
+                            uint32_t k0[4], k1[4];
+                            cvt_e2m1x8_f16(code[0][w], k0);
+                            cvt_e2m1x8_f16(code[1][w], k1);
 #pragma unroll
-                            for (int n = 0; n < NB; ++n) kv4_mma(acc[n][4 * w + e], a0, a1, a2, a3, pf[blk][n][0], pf[blk][n][1]);
-                            if constexpr (SPLIT) kv4_mma(acc[0][4 * w + e], a0, a1, a2, a3, pr[blk][0], pr[blk][1]);
+                            for (int e = 0; e < 4; ++e) {
+                                k0[e] = w < 2 ? hmul2_half<false>(k0[e], sc[0]) : hmul2_half<true>(k0[e], sc[0]);
+                                k1[e] = w < 2 ? hmul2_half<false>(k1[e], sc[1]) : hmul2_half<true>(k1[e], sc[1]);
+                            }
+                            kv4_mma(s[blk][0], k0[0], k1[0], k0[1], k1[1], qa[w].x, qa[w].y);
+                            if constexpr (MODE != KV4_8) kv4_mma(s[blk][NB - 1], k0[0], k1[0], k0[1], k1[1], qb[w].x, qb[w].y);
+                            kv4_mma(s[blk][0], k0[2], k1[2], k0[3], k1[3], qa[w].z, qa[w].w);
+                            if constexpr (MODE != KV4_8) kv4_mma(s[blk][NB - 1], k0[2], k1[2], k0[3], k1[3], qb[w].z, qb[w].w);
+                        }
+                    }
+                    // ---- running softmax ----
+                    const uint32_t miss = flags >> (8 + 2 * slot) & 3u;
+                    const bool masked = unit < see0 || unit >= see1 || miss != 0;
+                    if (masked) {
+#pragma unroll
+                        for (int a = 0; a < 2 * NB; ++a) {
+                            if constexpr (TREE) {
+                                uint64_t own;
+                                int low;
+                                tree_row(row_of(a), own, low);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (!sees_tree(own, low, unit * KV4_KEYS + i * 8 + g) || (miss >> (i >> 1) & 1u))
+                                        s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
+                                continue;
+                            }
+                            const int pos = row_pos(row_of(a));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int key = unit * KV4_KEYS + i * 8 + g;
+                                if (key > pos || (p.window > 0 && key <= pos - p.window) || (miss >> (i >> 1) & 1u))
+                                    s[i >> 1][a >> 1][2 * (i & 1) + (a & 1)] = -INFINITY;
+                            }
+                        }
+                    }
+                    float top[2 * NB];
+                    bool grow = false;
+#pragma unroll
+                    for (int a = 0; a < 2 * NB; ++a) {
+                        const int n = a >> 1, e = a & 1;
+                        top[a] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+                        if constexpr (NB == 1) grow |= top[a] > bar[a];
+                        else grow |= top[a] * rowf[row_of(a)] > m[a] + KV4_SLACK;
+                    }
+                    // rarely: a score above the running maximum by more than its slack
+                    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int a = 0; a < 2 * NB; ++a) {
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], o));
+                            const float c = rowf[row_of(a)];
+                            top[a] *= c;
+                            if (top[a] > m[a]) {
+                                if constexpr (NB == 1) bar[a] = (top[a] + KV4_SLACK) / c;
+                                const float f = ex2f(m[a] - top[a]);
+                                m[a] = top[a];
+                                l[a] *= f;
+#pragma unroll
+                                for (int j = 0; j < MT; ++j) {
+                                    acc[a >> 1][j][a & 1] *= f;
+                                    acc[a >> 1][j][2 + (a & 1)] *= f;
+                                }
+                            }
+                        }
+                    }
+                    uint32_t pf[2][NB][2], pr[SPLIT ? 2 : 1][2];   // B fragments of the probabilities, of their remainders
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        // both rows at once (packed fp32)
+                        const float2 c = *reinterpret_cast<const float2*>(rowf + row_of(2 * n));
+                        const float2 neg = make_float2(KV4_LIFT - m[2 * n], KV4_LIFT - m[2 * n + 1]);
+                        float2 sum = make_float2(l[2 * n], l[2 * n + 1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 e = __ffma2_rn(make_float2(s[i >> 1][n][2 * (i & 1)], s[i >> 1][n][2 * (i & 1) + 1]), c, neg);
+                            const float x0 = ex2f(e.x), x1 = ex2f(e.y);
+                            sum = __fadd2_rn(sum, make_float2(x0, x1));
+                            const __half2 hi = __floats2half2_rn(x0, x1);
+                            pf[i >> 1][n][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&hi));
+                            if constexpr (SPLIT) {
+                                const float2 f = __half22float2(hi);
+                                const __half2 rest = __floats2half2_rn(x0 - f.x, x1 - f.y);
+                                pr[i >> 1][i & 1] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&rest));
+                            }
+                        }
+                        l[2 * n] = sum.x;
+                        l[2 * n + 1] = sum.y;
+                    }
+                    // ---- values ----
+#pragma unroll
+                    for (int blk = 0; blk < 2; ++blk) {
+                        const uint8_t* W = B + blk * F::BLOCK;
+                        const int grp = g * (D / 8) / 16;       // the lane's channels are of one scale group
+                        uint32_t vs4 = *reinterpret_cast<const uint32_t*>(W + F::VS + (grp * 4 + t) * 4);
+                        if (masked) {
+                            // A token that some row does not see may hold anything, and 0 * NaN is NaN:
+                            // scales behind the end become 0, and so do NaN ones, whose channels of the
+                            // rows that do see them are then set by hand (a rare path).
+                            const int key0 = unit * KV4_KEYS + blk * 16, to = (miss >> blk & 1u) ? -1 : last_row_pos();
+                            bool nan = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = key0 + (e >> 1) * 8 + 2 * t + (e & 1);
+                                const bool bad = (vs4 >> (8 * e) & 0x7fu) == 0x7fu;
+                                if (key > to || bad) vs4 &= ~(0xffu << (8 * e));
+                                nan |= bad && key <= to;
+                            }
+                            if (__any_sync(0xffffffffu, nan)) {
+                                uint32_t hit = 0;
+#pragma unroll 1
+                                for (int w = 0; w < 16; ++w) {
+                                    if ((W[kv4_v_scale<D>(w, grp)] & 0x7f) != 0x7f || key0 + w > to) continue;
+#pragma unroll
+                                    for (int a = 0; a < 2 * NB; ++a) {
+                                        if constexpr (TREE) {
+                                            uint64_t own;
+                                            int low;
+                                            tree_row(row_of(a), own, low);
+                                            if (sees_tree(own, low, key0 + w)) hit |= 1u << a;
+                                            continue;
+                                        }
+                                        const int pos = row_pos(row_of(a));
+                                        if (key0 + w <= pos && (p.window <= 0 || key0 + w > pos - p.window)) hit |= 1u << a;
+                                    }
+                                }
+#pragma unroll
+                                for (int a = 0; a < 2 * NB; ++a)
+                                    if (hit >> a & 1u)
+#pragma unroll
+                                        for (int j = 0; j < MT; ++j) acc[a >> 1][j][a & 1] = acc[a >> 1][j][2 + (a & 1)] = NAN;
+                            }
+                        }
+                        const uint32_t sv[2] = {cvt_e4m3x2_f16x2(vs4 & 0xffffu), cvt_e4m3x2_f16x2(vs4 >> 16)};
+                        uint32_t vc[2][2][D / 64];          // [half][token of the pair][word]
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const uint8_t* V = W + F::VC + hf * (64 * F::CB) + lane * (2 * F::CB);
+                            if constexpr (D == 128) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(V);
+                                vc[hf][0][0] = w.x; vc[hf][0][1] = w.y; vc[hf][1][0] = w.z; vc[hf][1][1] = w.w;
+                            } else {
+                                const uint2 w = *reinterpret_cast<const uint2*>(V);
+                                vc[hf][0][0] = w.x; vc[hf][1][0] = w.y;
+                            }
+                        }
+#pragma unroll
+                        for (int w = 0; w < D / 64; ++w) {
+                            uint32_t ev[2][4], od[2][4];   // pairs (token 2t, token 2t + 1) of the even and of the odd channels
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const uint32_t A = vc[hf][0][w], C = vc[hf][1][w];
+                                cvt_e2m1x8_f16((A & 0x0f0f0f0fu) | (C << 4 & 0xf0f0f0f0u), ev[hf]);
+                                cvt_e2m1x8_f16((A >> 4 & 0x0f0f0f0fu) | (C & 0xf0f0f0f0u), od[hf]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t a0 = hmul2_u32(ev[0][e], sv[0]), a1 = hmul2_u32(od[0][e], sv[0]);
+                                const uint32_t a2 = hmul2_u32(ev[1][e], sv[1]), a3 = hmul2_u32(od[1][e], sv[1]);
+#pragma unroll
+                                for (int n = 0; n < NB; ++n) kv4_mma(acc[n][4 * w + e], a0, a1, a2, a3, pf[blk][n][0], pf[blk][n][1]);
+                                if constexpr (SPLIT) kv4_mma(acc[0][4 * w + e], a0, a1, a2, a3, pr[blk][0], pr[blk][1]);
+                            }
                         }
                     }
                 }
+                __syncwarp();
+                fetch(slot);
+                slot = slot + 1 == KV4_STAGES ? 0 : slot + 1;
             }
-            __syncwarp();
-            fetch(slot);
-            slot = slot + 1 == KV4_STAGES ? 0 : slot + 1;
+            if (!SPLIT || unit >= end) break;
+            if constexpr (SPLIT) {
+                // the products of the units to come start new sums
+                float f[2], lk[2];
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const float2 old = kept ? *reinterpret_cast<const float2*>(ml + (warp * KV4_ROWS + row_of(a)) * 2) : make_float2(-FLT_MAX, 0.f);
+                    f[a] = ex2f(old.x - m[a]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l[a] += __shfl_xor_sync(0xffffffffu, l[a], o);
+                    lk[a] = fmaf(old.y, f[a], l[a]);
+                    l[a] = 0.f;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    if (g == 0) *reinterpret_cast<float2*>(ml + (warp * KV4_ROWS + row_of(a)) * 2) = make_float2(m[a], lk[a]);
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        float4* to = kept_at(a, k);
+                        float4 v = make_float4(acc[0][2 * k][a], acc[0][2 * k][2 + a], acc[0][2 * k + 1][a], acc[0][2 * k + 1][2 + a]);
+                        if (kept) v = make_float4(fmaf(to->x, f[a], v.x), fmaf(to->y, f[a], v.y), fmaf(to->z, f[a], v.z), fmaf(to->w, f[a], v.w));
+                        *to = v;
+                        acc[0][2 * k][a] = acc[0][2 * k][2 + a] = acc[0][2 * k + 1][a] = acc[0][2 * k + 1][2 + a] = 0.f;
+                    }
+                }
+                __syncwarp();
+                kept = true;
+            }
         }
 
         // ---- the warps' sums of this part, joined in warp order ----
@@ -1153,6 +1197,20 @@ __global__ void __launch_bounds__(Kv4Shape<D, MODE>::THREADS, 2) kda_kv4_attend_
         for (int a = 0; a < 2 * NB; ++a) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[a] += __shfl_xor_sync(0xffffffffu, l[a], o);
+            if (SPLIT && kept) {
+                const float2 old = *reinterpret_cast<const float2*>(ml + (warp * KV4_ROWS + row_of(a)) * 2);
+                const float f = ex2f(old.x - m[a]);
+                l[a] = fmaf(old.y, f, l[a]);
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    const float4 v = *kept_at(a, k);
+                    acc[0][2 * k][a] = fmaf(v.x, f, acc[0][2 * k][a]);
+                    acc[0][2 * k][2 + a] = fmaf(v.y, f, acc[0][2 * k][2 + a]);
+                    acc[0][2 * k + 1][a] = fmaf(v.z, f, acc[0][2 * k + 1][a]);
+                    acc[0][2 * k + 1][2 + a] = fmaf(v.w, f, acc[0][2 * k + 1][2 + a]);
+                }
+                __syncwarp();
+            }
             if (g == 0) {
                 ml[(warp * KV4_ROWS + row_of(a)) * 2] = m[a];
                 ml[(warp * KV4_ROWS + row_of(a)) * 2 + 1] = l[a];

@@ -110,6 +110,58 @@ def test_wide_trees_whose_maximum_keeps_rising(lib, workspace, dim, dtype):
     assert ((got - want).abs() <= lim).all(), f"worst {((got - want).abs() / lim).max():.3g} of the bound"
 
 
+# -- up to 48 query rows a head: kda_kv4_attend's kernel, for fp16 and fp32 queries 32 units of 32 keys a warp and sum --------
+@pytest.mark.parametrize("ctx,dim,dtype,t,grp", [
+    (131000, 64, F32, 1, 8), (131000, 128, F32, 2, 4), (131000, 128, F16, 1, 1), (40000, 64, F16, 2, 3), (131000, 128, BF16, 2, 4),
+    # a warp's share at, one unit before and behind a move of the sums: eight warps (heads of 64) and six
+    (8190, 64, F32, 1, 8), (8191, 64, F32, 1, 8), (8192, 64, F32, 1, 8), (8447, 64, F32, 1, 8), (16400, 64, F32, 1, 8),
+    (6143, 128, F32, 1, 8), (6144, 128, F32, 1, 8), (6200, 128, F32, 1, 8), (6335, 128, F32, 1, 5), (12300, 128, F16, 1, 8),
+])
+@pytest.mark.parametrize("tree", [False, True])
+def test_few_rows(lib, workspace, ctx, dim, dtype, t, grp, tree):
+    n = 304
+    masks = ref.masks([ref.parents(t, "chain")] * n)
+    def call(pages, table, c, q, o, st):
+        if tree:
+            lib.kda_kv4_attend_tree(pages, table, c, q, masks, o, workspace, st, max_t=t)
+        else:
+            lib.kda_kv4_attend(pages, table, c, q, o, workspace, st, max_t=t)
+    # bf16 queries: one sum a warp, at least six warps, 2 additions a unit
+    additions = 32 * 4 if dtype != BF16 else 2 * ctx // 32 // 6
+    check(call, ctx, dim, dtype, t, grp, n, additions)
+    assert not workspace[:2048].any()
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -6, 0.0])
+@pytest.mark.parametrize("dim,t,grp", [(64, 1, 8), (128, 2, 2)])
+def test_few_rows_with_flat_scores(lib, workspace, dim, t, grp, gain):
+    """Small queries: little but the sums' own errors is left of the bound."""
+    call = lambda pages, table, c, q, o, st: lib.kda_kv4_attend(pages, table, c, q, o, workspace, st, max_t=t)  # noqa: E731
+    check(call, 131000, dim, F32, t, grp, 304, 32 * 4, gain)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, F32), (128, F16)])
+def test_few_rows_whose_maximum_keeps_rising(lib, workspace, dim, dtype):
+    ctx, t, grp, n = 30000, 2, 4, 304
+    full = -(-(ctx + t) // PAGE) * PAGE
+    g = torch.Generator().manual_seed(3)
+    base = torch.randn(1, 1, dim, generator=g)
+    gain = torch.linspace(0, 3, full).view(-1, 1, 1)
+    ck, sk = layer_ref.encode(base * gain + 0.1 * torch.randn(full, 1, dim, generator=g))
+    cv, sv = layer_ref.encode(torch.randn(full, 1, dim, generator=g))
+    pages = layer_ref.pack(ck, sk, cv, sv).view(1, -1, PAGE // 16, 18 * dim).transpose(0, 1).contiguous()
+    k, v = layer_ref.decode(ck, sk)[:ctx + t, 0], layer_ref.decode(cv, sv)[:ctx + t, 0]
+    q = (torch.randn(t, grp, dim, generator=g) + base).to(dtype)
+    want, err, big, top = reference(ctx, k, v, q, dim)
+    o, st = torch.full((n * t, grp, dim), float("nan"), dtype=dtype, device="cuda"), torch.zeros(1, dtype=I32, device="cuda")
+    table = torch.arange(pages.shape[0], dtype=I32).repeat(n, 1).cuda()
+    lib.kda_kv4_attend(pages.cuda(), table, torch.full((n,), ctx, dtype=I32, device="cuda"), q.repeat(n, 1, 1).cuda(), o, workspace, st, max_t=t)
+    assert st.item() == 0
+    lim = layer_ref.attend_tolerance(want, err, big, top, dtype, True) + 128 * 2.0 ** -24 * big.unsqueeze(-1)
+    got = o.cpu().double().view(n, t, grp, dim)
+    assert ((got - want).abs() <= lim).all(), f"worst {((got - want).abs() / lim).max():.3g} of the bound"
+
+
 def test_nan_and_windows_across_moves(lib, workspace):
     """A NaN value before the first move, seen by every row; and windows that begin behind it, which do not see it."""
     dim, ctx, n, grp = 64, 20000, 304, 4
