@@ -875,7 +875,9 @@ int kda_conv_step_tree(const kda_conv_window* win, const kda_conv_args* args, co
  * request's rows zero).  Otherwise args and checks as for the calls without a
  * tree, max_t <= KDA_TREE_MAX_TOKENS, workspace_bytes >=
  * KDA_KV4_TREE_WORKSPACE_BYTES (zeroed once; it may serve kda_kv4_attend too).
- * kda_kv4_attend_tree enqueues one kernel, or two in a row.
+ * kda_kv4_attend_tree enqueues one kernel, or two in a row (if only the second
+ * launch fails, the call returns KDA_ERR_LAUNCH with the first one enqueued, and
+ * rows that need the second are not written).
  */
 #define KDA_KV4_TREE_WORKSPACE_BYTES (64 << 20)
 int kda_kv4_append_tree(const kda_kv4_cache* cache, const kda_kv4_append_args* args, const uint64_t* tree, int32_t* dev_status,

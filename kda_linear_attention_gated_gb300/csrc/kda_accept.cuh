@@ -30,7 +30,7 @@ static_assert(ACC_SEGS == 64, "two pieces a lane");
 // A sum of two floats, hi + lo with |lo| at most half a step of hi: 48 bits.
 // fp64 runs at a 64th of the fp32 rate here (a version with the tests and the
 // scans in fp64: 70 us for 64 chains of 8 over 131072 tokens, where this takes
-// 25), and 32 bits lose the places next to a border between two tokens.
+// 26), and 32 bits lose the places next to a border between two tokens.
 struct Pair { float hi, lo; };
 // s += x (Knuth's exact sum of two floats; the errors add up in lo).  lo is a
 // plain float: a run of these has to be brought back into order by pair_norm
@@ -179,8 +179,8 @@ template <typename T, bool DRAWN> struct AcceptRow {
 //
 // Measured, us: a chain of 5, fp32, vocabulary 32000: 10.3 (8.7 on the GPU
 // alone: the launch, the barriers of the cluster, the draw's second look at a
-// piece); 64 chains of 8, 131072: 25.4, of which the 67 MB of the rows looked
-// at are 9.9 at the copy rate; 13 trees of up to 37, bf16, 50021: 23.6, passes
+// piece); 64 chains of 8, 131072: 26.2, of which the 67 MB of the rows looked
+// at are 9.9 at the copy rate; 13 trees of up to 37, bf16, 50021: 24, passes
 // one behind the other.  Warps mostly stand at barriers (the chain of a walk:
 // gather, pass, sum, pass, draw); the issue slots are used in 31 of 100 cycles.
 // Eight CTAs are the most that every cluster launch is granted.

@@ -593,6 +593,8 @@ struct Kv4Walk {
 //             probabilities into the same sums, so that products carry 22
 //             bits: fp16 and fp32 queries
 //   KV4_16    two times 8 rows as KV4_8: bf16 queries with more
+// KV4_REST also adds a warp's sums up in fp32 every few units (see KV4_CHAIN); a
+// single sum of bf16 queries loses 2^-13 over 131072 keys that six warps share.
 // In every mode a probability is also off by up to 2^-35 of the row's largest
 // (fp16's smallest steps, see KV4_LIFT).
 // P leaves the first product with keys along the lane's rows and enters the

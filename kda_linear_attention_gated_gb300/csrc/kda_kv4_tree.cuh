@@ -334,7 +334,9 @@ template <int D> struct KvtPart {
 // maximum and sum.  Codes times scales are exact in fp16; queries are scaled by a
 // power of two a row and rounded as in kda_kv4_attend_kernel, SPLIT: with their
 // remainders, and probabilities with theirs, as second operands into the same
-// sums.
+// sums.  The tensor cores' sums are added up in fp32 every few units (see
+// kvt_chain): in columns of tensor memory that are left, or, for bf16 queries
+// and heads of 128, in the part's place in the workspace.
 //
 // A unit of 64 keys is a step between two barriers of the CTA.  Behind the
 // first the control warp starts the last unit's P V and the unit's scores;
@@ -350,13 +352,14 @@ template <int D> struct KvtPart {
 // heads of 128, bf16: 126, where the products take 36.2 at the measured rate
 // and the codes 12.5; 32 of up to 16 tokens, 6 query heads on each of 8, 16383
 // keys at most: 88 (8.7 and 12.7; most of the 128 rows are empty, and warps
-// without any skip the softmax); 1 of 24, 131071 keys, 4 heads of 64, fp16: 86
-// (13.5 and 5.6).  The two CTAs of an SM issue in 48 of 100 cycles, 460
+// without any skip the softmax); 1 of 24, 131071 keys, 4 heads of 64, fp16: 84
+// (6.8 and 5.6).  The two CTAs of an SM issue in 48 of 100 cycles, 460
 // instructions a warp and unit, and the tensor cores are busy in 24: bound by a
 // unit's chain.  Of its 3300 cycles (heads of 128) a warp spends 600 at the
 // barrier, 780 on the next keys, 350 waiting for the last P V, 350 on values,
 // 180 waiting for scores, 430 on fetching and comparing them, 430 on
-// probabilities.  The first size on the way here: warp products of 16 rows 324;
+// probabilities.  A CTA's 54 units of the first size are 90 of its 126 us, the
+// rest its parts' beginnings and ends and the join.  The first size on the way here: warp products of 16 rows 324;
 // tensor cores, a barrier between any two steps 259; one barrier a unit, a warp
 // for copies and products 141; probabilities in tensor memory and two places for
 // keys 135; queries four rows at a time 131; P V before the scores, values

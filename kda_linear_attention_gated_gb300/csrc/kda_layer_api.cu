@@ -2,8 +2,10 @@
 // the 4-bit paged key/value cache and its attention, and the norms.  None of
 // them depends on the state pool's dtype; both library builds carry them.
 //
-// Host side: validate every argument synchronously and enqueue exactly one
-// kernel on the caller's stream.
+// Host side: validate every argument synchronously and enqueue one kernel on
+// the caller's stream; the attention of wide trees enqueues a second one behind
+// it, which joins parts (if that launch fails, the call says so with the first
+// one enqueued).
 #include <cuda_runtime.h>
 
 #include <algorithm>

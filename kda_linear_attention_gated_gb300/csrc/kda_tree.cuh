@@ -62,7 +62,7 @@ __device__ __forceinline__ float silu_short(float s) {
 // MB take 5.7 us at the copy rate: a CTA's loads all go out before its first
 // sum and its stores come after, so memory waits for the sums and the sums for
 // memory (issue slots in use in 37 of 100 cycles).  1 x 8 tokens: 3.1 us in a
-// graph, 9 through a call.  Vectors by threads of each, the first size: 64 x 4
+// graph, 9.5 to 11 through a call.  Vectors by threads of each, the first size: 64 x 4
 // 15.1, 64 x 2 20.4.  Every tap loaded from global memory as it is needed: 39;
 // weights fetched a channel a thread and rows through registers: 18.5.
 template <typename ET, int VC, int KWM>
@@ -294,8 +294,8 @@ template <typename ST> struct TreeSmem {
 // every state stored: 67.6, where its 219 MB take 32.3 at the copy rate.
 // Without its stores 51: twelve warps an SM (168 registers) issue in 45 of 100
 // cycles, a token's way being sums, shuffles and the next state one behind the
-// other.  One request of 8, fp32 pool: 10.8 (8.2 on the GPU alone, the loads
-// and three tokens in a row).  13 requests of up to 48, 6 heads of 96 x 80:
+// other.  One request of 8, fp32 pool: 10.6 to 12 (8.2 on the GPU alone, the
+// loads and three tokens in a row).  13 requests of up to 48, 6 heads of 96 x 80:
 // 56.3.  A child at a time, every tile as if it were ragged: 72 and 74 for the
 // first and the last; leaves like any other token, too: 92 and 89.
 template <typename ST, typename QT, int W, bool FULL>
